@@ -346,6 +346,107 @@ archead_status archead_build(int64_t V, int64_t d, int64_t k, int64_t r, int64_t
 archead_status archead_quantize(const double *x, int64_t rows, int64_t cols, int bits, int64_t group,
                                 int8_t *q, uint16_t *s, void *hip_stream);
 
+/* Element types of the post-training entry points below. */
+typedef enum archead_type {
+    ARCHEAD_F32 = 0,
+    ARCHEAD_BF16 = 1
+} archead_type;
+
+/*
+ * Post-training losses over logits (M rows of V logits, row stride ld
+ * elements, fp32 or bf16): what the head's logits go into when a model is
+ * scored or trained on its own answers.  With top = max_v y[v],
+ *   lse = top + log sum_v exp(y[v] - top),  logp = y[target] - lse,
+ * in natural logarithms, the log probabilities of archead_forward_ce (nll =
+ * -logp) for logits from anywhere: this head, a dense or 8-bit head, another
+ * GPU's shard gathered.
+ *
+ * Common to the three calls:
+ * logits     DEVICE, aligned to one element; ld >= V.  M <= 2^20, V < 2^31.
+ *            -inf logits (a vocabulary mask) have probability and gradient 0.
+ *            A row of -inf alone gives lse = -inf and logp = NaN; NaN or +inf
+ *            logits make the row's results NaN.
+ * targets    DEVICE int32 M.  A target outside [0, V) gives logp = NaN, and
+ *            NaN in the row's gradient; it is not an error.
+ * weights    DEVICE fp32 M.  A row of weight 0 carries no loss: its logits,
+ *            target and other inputs are not used (they may hold anything),
+ *            its logp is written as 0 and its gradient row as zeros.
+ * logp       DEVICE fp32 M, or NULL.
+ * dlogits    DEVICE M x V with row stride ldg, grad_type (fp32 or bf16,
+ *            rounded once), or NULL for the loss alone.  Every row is written
+ *            in full, nothing beyond column V.  May be logits itself (same
+ *            type and stride); otherwise it must not overlap them.
+ * grad_scale DEVICE fp32 scalar the gradient is multiplied by (the gradient
+ *            of what the loss goes into, a loss scale), or NULL for 1.
+ * ws         DEVICE workspace of at least archead_loss_workspace(M, V, P)
+ *            bytes (P = 0 without pairs), 16-byte aligned, contents
+ *            irrelevant.  It belongs to the call until the stream has passed
+ *            it: calls, or captured graphs, that may overlap need one each.
+ * The current device must be the one the buffers and hip_stream belong to.
+ * Work is enqueued, not waited for; nothing is allocated, so every call can
+ * be captured into a graph.  Statistics and sums are fp32 or wider, in a
+ * fixed order: equal calls give equal bits.
+ * Errors: negative sizes, missing pointers, unknown types, strides below V
+ * or a workspace too small -> ARCHEAD_EINVAL; sizes above the limits ->
+ * ARCHEAD_ESHAPE; both before anything is enqueued.
+ */
+archead_status archead_loss_workspace(int64_t M, int64_t V, int64_t P, uint64_t *bytes);
+
+/* archead_token_logp -- logp and lse of every row (either may be NULL, not
+ * both), e.g. the log probabilities of a rollout under a reference policy. */
+archead_status archead_token_logp(int64_t M, int64_t V, const void *logits, int type, int64_t ld,
+                                  const int32_t *targets, float *logp, float *lse, void *ws, uint64_t ws_bytes,
+                                  void *hip_stream);
+
+/*
+ * archead_policy_loss -- the clipped policy loss with a KL term, and its
+ * gradient by the logits:
+ *   rho_m  = exp(logp_m - old_logp_m)
+ *   loss   = sum_m weights_m ( -min(rho_m A_m, clip(rho_m, 1 - eps_low, 1 + eps_high) A_m)
+ *                              + beta (exp(r_m) - r_m - 1) ),   r_m = ref_logp_m - logp_m
+ *   dlogits[m, v] = c_m (1[v = target_m] - softmax(logits_m)[v]),
+ *   c_m    = weights_m ( -A_m rho_m [rho_m A_m <= clip(rho_m) A_m] + beta (1 - exp(r_m)) )
+ * The weights carry the normalisation (1 / tokens for a mean over tokens).
+ * A token whose clip is active and that has no KL term gets a zero row.
+ *
+ * old_logp, advantages   DEVICE fp32 M.  ref_logp  DEVICE fp32 M, required
+ * when beta > 0 and unused otherwise.  0 <= eps_low <= 1, eps_high >= 0,
+ * beta >= 0, all finite, else ARCHEAD_EINVAL.  loss  DEVICE fp32 scalar,
+ * written also for M = 0.
+ */
+archead_status archead_policy_loss(int64_t M, int64_t V, const void *logits, int type, int64_t ld,
+                                   const int32_t *targets, const float *old_logp, const float *ref_logp,
+                                   const float *advantages, const float *weights, float eps_low, float eps_high,
+                                   float beta, const float *grad_scale, float *loss, float *logp, void *dlogits,
+                                   int grad_type, int64_t ldg, void *ws, uint64_t ws_bytes, void *hip_stream);
+
+/*
+ * archead_preference_loss -- the preference loss of paired answers, and its
+ * gradient by the logits.  Answer i holds the rows offsets[i] .. offsets[i+1];
+ * pair p is the chosen answer 2p and the rejected answer 2p + 1.  With
+ *   s_i  = sum over the answer's rows of weights_m (logp_m - ref_logp_m)
+ *   h_p  = beta (s_2p - s_2p+1)
+ *   loss = 1/P sum_p [ -(1 - smoothing) log sigma(h_p) - smoothing log sigma(-h_p) ]
+ *   dlogits[m, v] = c_m (1[v = target_m] - softmax(logits_m)[v]),
+ *   c_m  = +-(beta / P) (sigma(h_p) - (1 - smoothing)) weights_m   (+ chosen, - rejected)
+ * Answers may be empty (s = 0) and of any lengths.
+ *
+ * P          pairs, 1 <= P <= 2^20.
+ * offsets    DEVICE int32 2P + 1, nondecreasing, within [0, M]; values that
+ *            break this are clamped to it (no access leaves the buffers) and
+ *            the results are unspecified.  Rows before offsets[0] and from
+ *            offsets[2P] on belong to no answer: as rows of weight 0.
+ * ref_logp   DEVICE fp32 M, or NULL for 0 (no reference policy).
+ * beta       finite and > 0; 0 <= smoothing < 1/2; else ARCHEAD_EINVAL.
+ * loss       DEVICE fp32 scalar; margins  DEVICE fp32 P (h_p), or NULL.
+ */
+archead_status archead_preference_loss(int64_t M, int64_t V, const void *logits, int type, int64_t ld,
+                                       const int32_t *targets, const float *weights, int64_t P,
+                                       const int32_t *offsets, const float *ref_logp, float beta, float smoothing,
+                                       const float *grad_scale, float *loss, float *margins, float *logp,
+                                       void *dlogits, int grad_type, int64_t ldg, void *ws, uint64_t ws_bytes,
+                                       void *hip_stream);
+
 /*
  * archead_packed_bytes -- eq 10 of the ARCHead paper: the sum over the
  * registered packed buffers of numel x element size (A5 counted at 5 bits,

@@ -41,6 +41,14 @@ SIGNATURES = {
     "archead_build": (ctypes.c_int, [_I64] * 6 + [_VP, _VP, ctypes.c_double, ctypes.c_double, ctypes.c_int,
                                                     ctypes.c_int, ctypes.c_uint64] + [_VP] * 10 + [_VP]),
     "archead_quantize": (ctypes.c_int, [_VP, _I64, _I64, ctypes.c_int, _I64, _VP, _VP, _VP]),
+    "archead_loss_workspace": (ctypes.c_int, [_I64, _I64, _I64, ctypes.POINTER(ctypes.c_uint64)]),
+    "archead_token_logp": (ctypes.c_int, [_I64, _I64, _VP, ctypes.c_int, _I64, _VP, _VP, _VP, _VP, ctypes.c_uint64,
+                                          _VP]),
+    "archead_policy_loss": (ctypes.c_int, [_I64, _I64, _VP, ctypes.c_int, _I64] + [_VP] * 5 +
+                            [ctypes.c_float] * 3 + [_VP] * 4 + [ctypes.c_int, _I64, _VP, ctypes.c_uint64, _VP]),
+    "archead_preference_loss": (ctypes.c_int, [_I64, _I64, _VP, ctypes.c_int, _I64, _VP, _VP, _I64, _VP, _VP,
+                                               ctypes.c_float, ctypes.c_float] + [_VP] * 5 +
+                                [ctypes.c_int, _I64, _VP, ctypes.c_uint64, _VP]),
     "archead_packed_bytes": (ctypes.c_int, [_VP, ctypes.POINTER(ctypes.c_uint64)]),
     "archead_device_bytes": (ctypes.c_int, [_VP, ctypes.POINTER(ctypes.c_uint64)]),
     "archead_free": (ctypes.c_int, [_VP]),

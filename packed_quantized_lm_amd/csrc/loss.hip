@@ -1,0 +1,663 @@
+// loss.hip -- token log probabilities and the two post-training losses over
+// logits, with the logits' gradient: the clipped policy loss with a KL term
+// and the preference loss over paired answers.
+//
+// Row m of the logits y (V wide, target t) has
+//   top = max_v y[v],  Z = sum_v exp(y[v] - top),  lse = top + log Z,
+//   logp = (y[t] - top) - log Z,  p[v] = exp(y[v] - top) / Z,
+// and both losses reach the logits through logp alone:
+//   dlogits[v] = c (1[v = t] - p[v]),   c = d loss / d logp[m].
+// Policy:     rho = exp(logp - old), kl = exp(ref - logp) - (ref - logp) - 1,
+//   loss = sum_m w (-min(rho A, clip(rho, 1 - el, 1 + eh) A) + beta kl),
+//   c = w (-A rho [the unclipped branch] + beta (1 - exp(ref - logp))).
+// Preference: with s_i = sum w (logp - ref) over answer i and, per pair,
+//   h = beta (s_chosen - s_rejected),
+//   loss = mean over pairs of -(1 - e) log sigma(h) - e log sigma(-h),
+//   c = +-beta/P (sigma(h) - (1 - e)) w  (+ for the chosen answer).
+//
+// Everything is bound by the logits' bytes: one read for the statistics (a
+// running maximum and sum, fp32), one more read with a write for the
+// gradient.  Every sum has a fixed order: repeated calls agree bit for bit.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <string>
+
+#include "api_internal.hpp"
+#include "archead.h"
+#include "device.hpp"
+
+namespace archead {
+namespace {
+
+constexpr int kNT = 256;            // threads of a slice's workgroup
+constexpr int kVec = 8;             // elements per thread and step
+constexpr int64_t kSliceMin = 4096; // smallest slice of a row
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// rows need not be aligned beyond one element (odd V): these vectors are
+// loaded and stored as 16 bytes from any element boundary
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint16_t u16x8u __attribute__((ext_vector_type(8), aligned(2)));
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+typedef __attribute__((ext_vector_type(2))) float f32x2;
+
+__device__ __forceinline__ void load8(const float *p, float v[kVec])
+{
+    const f32x4u a = *(const f32x4u *)p, b = *(const f32x4u *)(p + 4);
+    for (int i = 0; i < 4; ++i) {
+        v[i] = a[i];
+        v[4 + i] = b[i];
+    }
+}
+__device__ __forceinline__ void load8(const uint16_t *p, float v[kVec])
+{
+    const u16x8u a = *(const u16x8u *)p;
+    for (int i = 0; i < 8; ++i)
+        v[i] = __uint_as_float((uint32_t)a[i] << 16);
+}
+__device__ __forceinline__ float load1(const float *p) { return *p; }
+__device__ __forceinline__ float load1(const uint16_t *p) { return __uint_as_float((uint32_t)*p << 16); }
+
+// the gradient is rounded once, to the type the caller asked for
+__device__ __forceinline__ uint16_t to_bf16(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+__device__ __forceinline__ void store8(float *p, const float v[kVec])
+{
+    *(f32x4u *)p = f32x4u{v[0], v[1], v[2], v[3]};
+    *(f32x4u *)(p + 4) = f32x4u{v[4], v[5], v[6], v[7]};
+}
+__device__ __forceinline__ void store8(uint16_t *p, const float v[kVec])
+{
+    u16x8u o;
+    for (int i = 0; i < 8; i += 2) {
+        const uint32_t w = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v[i], v[i + 1]}, bf16x2));
+        o[i] = (uint16_t)w;
+        o[i + 1] = (uint16_t)(w >> 16);
+    }
+    *(u16x8u *)p = o;
+}
+__device__ __forceinline__ void store1(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store1(uint16_t *p, float v) { *p = to_bf16(v); }
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// running maximum and sum of exp(y - m); m = -inf and s = 0 when empty
+struct Stat {
+    float m, s;
+};
+
+// what exp is taken against: the maximum, or 0 while it is -inf (a row or
+// part of one whose entries are all -inf adds nothing, and -inf - -inf is
+// never formed)
+__device__ __forceinline__ float anchor(float m) { return m == -INFINITY ? 0.f : m; }
+
+__device__ __forceinline__ Stat merge(Stat a, Stat b)
+{
+    const float m = fmaxf(a.m, b.m), r = anchor(m);
+    return Stat{m, a.s * exp2_fast((a.m - r) * kLog2e) + b.s * exp2_fast((b.m - r) * kLog2e)};
+}
+
+__device__ __forceinline__ void add8(Stat &st, const float v[kVec])
+{
+    float m = st.m;
+    for (int i = 0; i < kVec; ++i)
+        m = fmaxf(m, v[i]);
+    const float r = anchor(m);
+    float s = st.s * exp2_fast((st.m - r) * kLog2e);
+    for (int i = 0; i < kVec; ++i)
+        s += exp2_fast((v[i] - r) * kLog2e);
+    st = Stat{m, s};
+}
+
+// statistics of y[0 .. n), one part per thread
+template <int NT, typename T> __device__ __forceinline__ Stat scan_part(const T *y, int64_t n)
+{
+    Stat st{-INFINITY, 0.f};
+    const int64_t nv = n / kVec;
+    int64_t q = threadIdx.x;
+    for (; q + 3 * NT < nv; q += 4 * NT) { // four loads in flight
+        float v[4][kVec];
+        for (int u = 0; u < 4; ++u)
+            load8(y + (q + u * NT) * kVec, v[u]);
+        for (int u = 0; u < 4; ++u)
+            add8(st, v[u]);
+    }
+    for (; q < nv; q += NT) {
+        float v[kVec];
+        load8(y + q * kVec, v);
+        add8(st, v);
+    }
+    const int64_t i = nv * kVec + threadIdx.x;
+    if (i < n)
+        st = merge(st, Stat{load1(y + i), 1.f});
+    return st;
+}
+
+// merge over the workgroup, the result in every thread
+template <int NT> __device__ __forceinline__ Stat block_merge(Stat st, Stat *red)
+{
+    for (int off = 32; off >= 1; off >>= 1)
+        st = merge(st, Stat{__shfl_xor(st.m, off), __shfl_xor(st.s, off)});
+    if ((threadIdx.x & 63) == 0)
+        red[threadIdx.x >> 6] = st;
+    __syncthreads();
+    st = red[0];
+    for (int w = 1; w < NT / 64; ++w)
+        st = merge(st, red[w]);
+    return st;
+}
+
+struct Rows {
+    int64_t M, V, ld;
+    const void *y;
+    const int32_t *targets;
+    const float *weights;   // null: every row counts
+    const int32_t *offsets; // preference: answer bounds, else null
+    int64_t n_off;
+    int64_t S, slice; // slices per row and their length
+};
+
+// a row that carries no loss is not read: its logits may hold anything
+__device__ __forceinline__ bool row_counts(const Rows &a, int64_t m)
+{
+    if (a.weights && a.weights[m] == 0.f)
+        return false;
+    if (a.offsets && (m < a.offsets[0] || m >= a.offsets[a.n_off - 1]))
+        return false;
+    return true;
+}
+
+template <typename T> __device__ __forceinline__ const T *row_ptr(const Rows &a, int64_t m)
+{
+    return (const T *)a.y + m * a.ld;
+}
+
+// log probability of row m's target; NaN for a target outside [0, V)
+template <typename T> __device__ __forceinline__ float row_logp(const Rows &a, int64_t m, Stat st)
+{
+    const int32_t t = a.targets[m];
+    if (t < 0 || t >= a.V)
+        return __builtin_nanf("");
+    return (load1(row_ptr<T>(a, m) + t) - st.m) - logf(st.s);
+}
+__device__ __forceinline__ float stat_lse(Stat st) { return st.m + logf(st.s); }
+
+__device__ __forceinline__ Stat merge_slices(const Stat *part, int64_t S)
+{
+    Stat st = part[0];
+    for (int64_t i = 1; i < S; ++i)
+        st = merge(st, part[i]);
+    return st;
+}
+
+// --- statistics: workgroup (row, slice) -> part[row][slice] -----------------
+template <typename T> __global__ __launch_bounds__(kNT) void stats_kernel(Rows a, Stat *part)
+{
+    __shared__ Stat red[kNT / 64];
+    const int64_t m = blockIdx.x / a.S, sl = blockIdx.x % a.S;
+    if (!row_counts(a, m))
+        return;
+    const int64_t v0 = sl * a.slice, n = min(a.slice, a.V - v0);
+    const Stat st = block_merge<kNT>(scan_part<kNT>(row_ptr<T>(a, m) + v0, n), red);
+    if (threadIdx.x == 0)
+        part[blockIdx.x] = st;
+}
+
+template <typename T>
+__global__ __launch_bounds__(kNT) void logp_kernel(Rows a, const Stat *part, float *logp, float *lse)
+{
+    const int64_t m = (int64_t)blockIdx.x * kNT + threadIdx.x;
+    if (m >= a.M)
+        return;
+    const Stat st = merge_slices(part + m * a.S, a.S);
+    if (logp)
+        logp[m] = row_logp<T>(a, m, st);
+    if (lse)
+        lse[m] = stat_lse(st);
+}
+
+// --- gradient of a slice -----------------------------------------------------
+template <typename G> __device__ __forceinline__ void zero_part(G *g, int64_t n)
+{
+    const float z[kVec] = {};
+    for (int64_t q = threadIdx.x; q < n / kVec; q += blockDim.x)
+        store8(g + q * kVec, z);
+    const int64_t i = n / kVec * kVec + threadIdx.x;
+    if (i < n)
+        store1(g + i, 0.f);
+}
+
+// g[i] = c (1[i = t] - exp(y[i] - m) / s) for i in [0, n); t relative to y
+template <int NT, typename T, typename G>
+__device__ __forceinline__ void grad_part(const T *y, G *g, int64_t n, int64_t t, float c, Stat st)
+{
+    const float r = anchor(st.m), k = -c / st.s;
+    auto one = [&](float v, int64_t i) {
+        const float x = k * exp2_fast((v - r) * kLog2e);
+        return i == t ? x + c : x;
+    };
+    const int64_t nv = n / kVec;
+    for (int64_t q = threadIdx.x; q < nv; q += NT) {
+        float v[kVec];
+        load8(y + q * kVec, v);
+        for (int i = 0; i < kVec; ++i)
+            v[i] = one(v[i], q * kVec + i);
+        store8(g + q * kVec, v);
+    }
+    const int64_t i = nv * kVec + threadIdx.x;
+    if (i < n)
+        store1(g + i, one(load1(y + i), i));
+}
+
+// dlogits of slice (row, sl): the row's statistics merged from part, its
+// coefficient from coef.  No logit outside the slice is read, so that the
+// gradient may be written over the logits.
+template <typename T, typename G>
+__global__ __launch_bounds__(kNT) void grad_kernel(Rows a, const Stat *part, const float *coef, const float *gscale,
+                                                   G *dy, int64_t ldg)
+{
+    const int64_t m = blockIdx.x / a.S, sl = blockIdx.x % a.S;
+    const int64_t v0 = sl * a.slice, n = min(a.slice, a.V - v0);
+    G *g = dy + m * ldg + v0;
+    float c = coef[m];
+    if (c == 0.f) { // a masked or clipped token: its logits are not read
+        zero_part(g, n);
+        return;
+    }
+    if (gscale)
+        c *= *gscale;
+    const Stat st = merge_slices(part + m * a.S, a.S);
+    grad_part<kNT>(row_ptr<T>(a, m) + v0, g, n, (int64_t)a.targets[m] - v0, c, st);
+}
+
+struct Policy {
+    const float *old_logp, *ref_logp, *adv;
+    float eps_low, eps_high, beta;
+};
+
+// one token's loss and its derivative by logp
+__device__ __forceinline__ float policy_token(const Policy &p, int64_t m, float w, float logp, float *c)
+{
+    const float A = p.adv[m], rho = expf(logp - p.old_logp[m]);
+    const float cl = fminf(fmaxf(rho, 1.f - p.eps_low), 1.f + p.eps_high);
+    float loss = -fminf(rho * A, cl * A);
+    float d = rho * A <= cl * A ? -A * rho : 0.f;
+    if (!(rho == rho)) // fmin and fmax drop a NaN
+        loss = d = rho;
+    if (p.beta != 0.f) { // without a KL term an infinite one is never formed
+        const float gap = p.ref_logp[m] - logp;
+        loss += p.beta * (expm1f(gap) - gap);
+        d -= p.beta * expm1f(gap);
+    }
+    *c = w * d;
+    return w * loss;
+}
+
+// --- sums in a fixed order ----------------------------------------------------
+constexpr int kSumNT = 1024;
+
+__device__ __forceinline__ double block_sum(double x, double *red)
+{
+    for (int off = 32; off >= 1; off >>= 1)
+        x += __shfl_xor(x, off);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0)
+        red[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = 0.;
+    for (int w = 0; w < (int)blockDim.x / 64; ++w)
+        x += red[w];
+    return x;
+}
+
+__global__ __launch_bounds__(kSumNT) void sum_kernel(const float *x, int64_t n, double scale, float *out)
+{
+    __shared__ double red[kSumNT / 64];
+    double s = 0.;
+    for (int64_t i = threadIdx.x; i < n; i += kSumNT)
+        s += x[i];
+    s = block_sum(s, red);
+    if (threadIdx.x == 0)
+        *out = (float)(s * scale);
+}
+
+// --- policy rows: logp, token loss and coefficient of every row -----------------
+template <typename T>
+__global__ __launch_bounds__(kNT) void policy_rows_kernel(Rows a, const Stat *part, Policy pol, float *logp,
+                                                          float *token, float *coef)
+{
+    const int64_t m = (int64_t)blockIdx.x * kNT + threadIdx.x;
+    if (m >= a.M)
+        return;
+    float lp = 0.f, loss = 0.f, c = 0.f;
+    if (row_counts(a, m)) {
+        lp = row_logp<T>(a, m, merge_slices(part + m * a.S, a.S));
+        loss = policy_token(pol, m, a.weights[m], lp, &c);
+    }
+    token[m] = loss;
+    coef[m] = c;
+    if (logp)
+        logp[m] = lp;
+}
+
+// --- preference pairs: workgroup p -> margin, pair loss, row coefficients ------
+template <typename T>
+__global__ __launch_bounds__(kNT) void pair_kernel(Rows a, const Stat *part, const float *ref, int64_t P, float beta,
+                                                   float smooth, float *logp, float *margins, float *pair,
+                                                   float *coef)
+{
+    __shared__ double red[kNT / 64];
+    const int64_t p = blockIdx.x;
+    // bounds are kept inside [0, M] and in order, whatever the offsets hold
+    int64_t b[3];
+    for (int i = 0; i < 3; ++i) {
+        b[i] = min(max((int64_t)a.offsets[2 * p + i], (int64_t)0), a.M);
+        if (i > 0)
+            b[i] = max(b[i], b[i - 1]);
+    }
+    double sum[2];
+    for (int i = 0; i < 2; ++i) {
+        double s = 0.;
+        for (int64_t m = b[i] + threadIdx.x; m < b[i + 1]; m += kNT) {
+            float lp = 0.f;
+            if (row_counts(a, m)) {
+                lp = row_logp<T>(a, m, merge_slices(part + m * a.S, a.S));
+                s += (double)a.weights[m] * ((double)lp - (double)(ref ? ref[m] : 0.f));
+            }
+            if (logp)
+                logp[m] = lp;
+        }
+        sum[i] = block_sum(s, red);
+    }
+    const float h = (float)((double)beta * (sum[0] - sum[1]));
+    const float e = expf(-fabsf(h)), sp = log1pf(e);               // log(1 + exp(-|h|))
+    const float sig = h >= 0.f ? 1.f / (1.f + e) : e / (1.f + e);  // sigma(h)
+    const float nsig = h >= 0.f ? e / (1.f + e) : 1.f / (1.f + e); // sigma(-h)
+    // sigma(h) - (1 - smooth) = smooth sigma(h) - (1 - smooth) sigma(-h)
+    const float slope = beta / (float)P * (smooth * sig - (1.f - smooth) * nsig);
+    for (int i = 0; i < 2; ++i)
+        for (int64_t m = b[i] + threadIdx.x; m < b[i + 1]; m += kNT)
+            coef[m] = row_counts(a, m) ? (i ? -slope : slope) * a.weights[m] : 0.f;
+    if (threadIdx.x == 0) {
+        pair[p] = (1.f - smooth) * (sp + fmaxf(-h, 0.f)) + smooth * (sp + fmaxf(h, 0.f));
+        if (margins)
+            margins[p] = h;
+    }
+}
+
+// rows outside every answer
+__global__ __launch_bounds__(kNT) void outside_kernel(Rows a, float *logp, float *coef)
+{
+    const int64_t m = (int64_t)blockIdx.x * kNT + threadIdx.x;
+    if (m < a.M && (m < a.offsets[0] || m >= a.offsets[a.n_off - 1])) {
+        coef[m] = 0.f;
+        if (logp)
+            logp[m] = 0.f;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+constexpr int64_t kMaxRows = int64_t(1) << 20;
+constexpr int64_t kTargetWg = 2048; // workgroups that fill the chip with slices
+
+void choose_slices(int64_t M, int64_t V, int64_t *S, int64_t *slice)
+{
+    int64_t s = std::max<int64_t>(1, kTargetWg / std::max<int64_t>(M, 1));
+    s = std::min(s, std::max<int64_t>(1, V / kSliceMin));
+    int64_t len = (V + s - 1) / s;
+    len = (len + kVec - 1) / kVec * kVec;
+    *slice = len;
+    *S = (V + len - 1) / len;
+}
+
+struct LossWs {
+    size_t part, token, coef, pair, total;
+};
+
+LossWs loss_ws(int64_t M, int64_t V, int64_t P)
+{
+    int64_t S, slice;
+    choose_slices(M, V, &S, &slice);
+    LossWs w;
+    size_t off = 0;
+    auto place = [&](size_t bytes) {
+        const size_t o = off;
+        off += (bytes + 255) / 256 * 256;
+        return o;
+    };
+    w.part = place(sizeof(Stat) * (size_t)(M * S));
+    w.token = place(4 * (size_t)M);
+    w.coef = place(4 * (size_t)M);
+    w.pair = place(4 * (size_t)P);
+    w.total = std::max<size_t>(off, 256);
+    return w;
+}
+
+archead_status check_common(int64_t M, int64_t V, const void *logits, int type, int64_t ld, const int32_t *targets,
+                            void *ws, size_t ws_bytes, int64_t P)
+{
+    if (M < 0)
+        return api_fail(ARCHEAD_EINVAL, "M < 0");
+    if (M > kMaxRows)
+        return api_fail(ARCHEAD_ESHAPE, "M above 2^20");
+    if (V < 1 || V >= (int64_t(1) << 31))
+        return api_fail(ARCHEAD_ESHAPE, "V must satisfy 1 <= V < 2^31");
+    if (type != ARCHEAD_F32 && type != ARCHEAD_BF16)
+        return api_fail(ARCHEAD_EINVAL, "logits must be ARCHEAD_F32 or ARCHEAD_BF16");
+    if (ld < V || ld > (int64_t(1) << 40))
+        return api_fail(ARCHEAD_EINVAL, "the row stride must lie in [V, 2^40]");
+    if (M > 0 && (!logits || !targets))
+        return api_fail(ARCHEAD_EINVAL, "logits and targets are required");
+    if (!ws || (uintptr_t)ws % 16)
+        return api_fail(ARCHEAD_EINVAL, "a 16-byte aligned workspace is required");
+    if (ws_bytes < loss_ws(M, V, P).total)
+        return api_fail(ARCHEAD_EINVAL, "the workspace is smaller than archead_loss_workspace asks for");
+    if ((uintptr_t)logits % (type == ARCHEAD_F32 ? 4 : 2))
+        return api_fail(ARCHEAD_EINVAL, "logits must be aligned to their element");
+    return ARCHEAD_OK;
+}
+
+archead_status check_grad(int64_t V, const void *logits, int type, int64_t ld, const void *dlogits, int grad_type,
+                          int64_t ldg)
+{
+    if (!dlogits)
+        return ARCHEAD_OK;
+    if (grad_type != ARCHEAD_F32 && grad_type != ARCHEAD_BF16)
+        return api_fail(ARCHEAD_EINVAL, "dlogits must be ARCHEAD_F32 or ARCHEAD_BF16");
+    if (ldg < V || ldg > (int64_t(1) << 40))
+        return api_fail(ARCHEAD_EINVAL, "the gradient's row stride must lie in [V, 2^40]");
+    if ((uintptr_t)dlogits % (grad_type == ARCHEAD_F32 ? 4 : 2))
+        return api_fail(ARCHEAD_EINVAL, "dlogits must be aligned to its element");
+    if (dlogits == logits && (grad_type != type || ldg != ld))
+        return api_fail(ARCHEAD_EINVAL, "a gradient in place needs the logits' type and row stride");
+    return ARCHEAD_OK;
+}
+
+archead_status launched(const char *what)
+{
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return api_fail(ARCHEAD_EHIP, std::string(what) + ": " + hipGetErrorString(e));
+    return ARCHEAD_OK;
+}
+
+Rows make_rows(int64_t M, int64_t V, const void *logits, int64_t ld, const int32_t *targets, const float *weights)
+{
+    Rows a{};
+    a.M = M;
+    a.V = V;
+    a.ld = ld;
+    a.y = logits;
+    a.targets = targets;
+    a.weights = weights;
+    choose_slices(M, V, &a.S, &a.slice);
+    return a;
+}
+
+template <typename T> void run_stats(const Rows &a, Stat *part, hipStream_t st)
+{
+    hipLaunchKernelGGL(stats_kernel<T>, dim3((unsigned)(a.M * a.S)), dim3(kNT), 0, st, a, part);
+}
+
+template <typename T>
+void run_grad(const Rows &a, const Stat *part, const float *coef, const float *gscale, void *dy, int grad_type,
+              int64_t ldg, hipStream_t st)
+{
+    const dim3 grid((unsigned)(a.M * a.S));
+    if (grad_type == ARCHEAD_F32)
+        hipLaunchKernelGGL((grad_kernel<T, float>), grid, dim3(kNT), 0, st, a, part, coef, gscale, (float *)dy, ldg);
+    else
+        hipLaunchKernelGGL((grad_kernel<T, uint16_t>), grid, dim3(kNT), 0, st, a, part, coef, gscale, (uint16_t *)dy,
+                           ldg);
+}
+
+struct Grad {
+    const float *scale;
+    void *dy;
+    int type;
+    int64_t ld;
+};
+
+template <typename T>
+void run_policy(const Rows &a, void *ws, const LossWs &L, const Policy &pol, float *logp, const Grad &g, hipStream_t st)
+{
+    Stat *part = (Stat *)((char *)ws + L.part);
+    float *token = (float *)((char *)ws + L.token), *coef = (float *)((char *)ws + L.coef);
+    run_stats<T>(a, part, st);
+    hipLaunchKernelGGL(policy_rows_kernel<T>, dim3((unsigned)((a.M + kNT - 1) / kNT)), dim3(kNT), 0, st, a, part, pol,
+                       logp, token, coef);
+    if (g.dy)
+        run_grad<T>(a, part, coef, g.scale, g.dy, g.type, g.ld, st);
+}
+
+template <typename T>
+void run_preference(const Rows &a, void *ws, const LossWs &L, const float *ref, int64_t P, float beta, float smoothing,
+                    float *logp, float *margins, const Grad &g, hipStream_t st)
+{
+    Stat *part = (Stat *)((char *)ws + L.part);
+    float *coef = (float *)((char *)ws + L.coef), *pair = (float *)((char *)ws + L.pair);
+    if (a.M > 0) {
+        hipLaunchKernelGGL(outside_kernel, dim3((unsigned)((a.M + kNT - 1) / kNT)), dim3(kNT), 0, st, a, logp, coef);
+        run_stats<T>(a, part, st);
+    }
+    hipLaunchKernelGGL(pair_kernel<T>, dim3((unsigned)P), dim3(kNT), 0, st, a, part, ref, P, beta, smoothing, logp,
+                       margins, pair, coef);
+    if (a.M > 0 && g.dy)
+        run_grad<T>(a, part, coef, g.scale, g.dy, g.type, g.ld, st);
+}
+
+} // namespace
+} // namespace archead
+
+using namespace archead;
+
+extern "C" archead_status archead_loss_workspace(int64_t M, int64_t V, int64_t P, uint64_t *bytes)
+{
+    if (!bytes)
+        return api_fail(ARCHEAD_EINVAL, "bytes is NULL");
+    if (M < 0 || P < 0)
+        return api_fail(ARCHEAD_EINVAL, "M < 0 or P < 0");
+    if (M > kMaxRows || P > kMaxRows || V < 1 || V >= (int64_t(1) << 31))
+        return api_fail(ARCHEAD_ESHAPE, "M, P <= 2^20 and 1 <= V < 2^31");
+    *bytes = loss_ws(M, V, P).total;
+    return ARCHEAD_OK;
+}
+
+extern "C" archead_status archead_token_logp(int64_t M, int64_t V, const void *logits, int type, int64_t ld,
+                                             const int32_t *targets, float *logp, float *lse, void *ws,
+                                             uint64_t ws_bytes, void *hip_stream)
+{
+    archead_status s = check_common(M, V, logits, type, ld, targets, ws, ws_bytes, 0);
+    if (s != ARCHEAD_OK)
+        return s;
+    if (M > 0 && !logp && !lse)
+        return api_fail(ARCHEAD_EINVAL, "logp and lse are both NULL");
+    if (M == 0)
+        return ARCHEAD_OK;
+    hipStream_t st = (hipStream_t)hip_stream;
+    const Rows a = make_rows(M, V, logits, ld, targets, nullptr);
+    Stat *part = (Stat *)((char *)ws + loss_ws(M, V, 0).part);
+    const dim3 grid((unsigned)((M + kNT - 1) / kNT));
+    if (type == ARCHEAD_F32) {
+        run_stats<float>(a, part, st);
+        hipLaunchKernelGGL(logp_kernel<float>, grid, dim3(kNT), 0, st, a, part, logp, lse);
+    } else {
+        run_stats<uint16_t>(a, part, st);
+        hipLaunchKernelGGL(logp_kernel<uint16_t>, grid, dim3(kNT), 0, st, a, part, logp, lse);
+    }
+    return launched("archead_token_logp");
+}
+
+extern "C" archead_status archead_policy_loss(int64_t M, int64_t V, const void *logits, int type, int64_t ld,
+                                              const int32_t *targets, const float *old_logp, const float *ref_logp,
+                                              const float *advantages, const float *weights, float eps_low,
+                                              float eps_high, float beta, const float *grad_scale, float *loss,
+                                              float *logp, void *dlogits, int grad_type, int64_t ldg, void *ws,
+                                              uint64_t ws_bytes, void *hip_stream)
+{
+    archead_status s = check_common(M, V, logits, type, ld, targets, ws, ws_bytes, 0);
+    if (s == ARCHEAD_OK)
+        s = check_grad(V, logits, type, ld, dlogits, grad_type, ldg);
+    if (s != ARCHEAD_OK)
+        return s;
+    if (!(eps_low >= 0.f && eps_low <= 1.f) || !(eps_high >= 0.f) || !std::isfinite(eps_high))
+        return api_fail(ARCHEAD_EINVAL, "0 <= eps_low <= 1 and a finite eps_high >= 0");
+    if (!(beta >= 0.f) || !std::isfinite(beta))
+        return api_fail(ARCHEAD_EINVAL, "beta must be finite and not negative");
+    if (!loss)
+        return api_fail(ARCHEAD_EINVAL, "loss is NULL");
+    if (M > 0 && (!old_logp || !advantages || !weights || (beta != 0.f && !ref_logp)))
+        return api_fail(ARCHEAD_EINVAL, "old_logp, advantages, weights and, with beta, ref_logp are required");
+    hipStream_t st = (hipStream_t)hip_stream;
+    const LossWs L = loss_ws(M, V, 0);
+    const Policy pol{old_logp, ref_logp, advantages, eps_low, eps_high, beta};
+    const Grad g{grad_scale, dlogits, grad_type, ldg};
+    const Rows a = make_rows(M, V, logits, ld, targets, weights);
+    if (M > 0 && type == ARCHEAD_F32)
+        run_policy<float>(a, ws, L, pol, logp, g, st);
+    else if (M > 0)
+        run_policy<uint16_t>(a, ws, L, pol, logp, g, st);
+    hipLaunchKernelGGL(sum_kernel, dim3(1), dim3(kSumNT), 0, st, (const float *)((char *)ws + L.token), M, 1.0, loss);
+    return launched("archead_policy_loss");
+}
+
+extern "C" archead_status archead_preference_loss(int64_t M, int64_t V, const void *logits, int type, int64_t ld,
+                                                  const int32_t *targets, const float *weights, int64_t P,
+                                                  const int32_t *offsets, const float *ref_logp, float beta,
+                                                  float smoothing, const float *grad_scale, float *loss,
+                                                  float *margins, float *logp, void *dlogits, int grad_type,
+                                                  int64_t ldg, void *ws, uint64_t ws_bytes, void *hip_stream)
+{
+    if (P < 1)
+        return api_fail(ARCHEAD_EINVAL, "P must be at least 1");
+    if (P > kMaxRows)
+        return api_fail(ARCHEAD_ESHAPE, "P above 2^20");
+    archead_status s = check_common(M, V, logits, type, ld, targets, ws, ws_bytes, P);
+    if (s == ARCHEAD_OK)
+        s = check_grad(V, logits, type, ld, dlogits, grad_type, ldg);
+    if (s != ARCHEAD_OK)
+        return s;
+    if (!(beta > 0.f) || !std::isfinite(beta))
+        return api_fail(ARCHEAD_EINVAL, "beta must be finite and positive");
+    if (!(smoothing >= 0.f && smoothing < 0.5f))
+        return api_fail(ARCHEAD_EINVAL, "0 <= smoothing < 1/2");
+    if (!loss || !offsets || (M > 0 && !weights))
+        return api_fail(ARCHEAD_EINVAL, "loss, offsets and weights are required");
+    hipStream_t st = (hipStream_t)hip_stream;
+    const LossWs L = loss_ws(M, V, P);
+    Rows a = make_rows(M, V, logits, ld, targets, weights);
+    a.offsets = offsets;
+    a.n_off = 2 * P + 1;
+    const Grad g{grad_scale, dlogits, grad_type, ldg};
+    if (type == ARCHEAD_F32)
+        run_preference<float>(a, ws, L, ref_logp, P, beta, smoothing, logp, margins, g, st);
+    else
+        run_preference<uint16_t>(a, ws, L, ref_logp, P, beta, smoothing, logp, margins, g, st);
+    hipLaunchKernelGGL(sum_kernel, dim3(1), dim3(kSumNT), 0, st, (const float *)((char *)ws + L.pair), P,
+                       1.0 / (double)P, loss);
+    return launched("archead_preference_loss");
+}
