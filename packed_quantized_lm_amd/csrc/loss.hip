@@ -32,10 +32,11 @@ namespace archead {
 namespace {
 
 constexpr int kNT = 256;            // threads of a slice's workgroup
+constexpr int kWide = 1024;         // threads of a long row's workgroup
 constexpr int kVec = 8;             // elements per thread and step
 constexpr int64_t kSliceMin = 4096; // smallest slice of a row
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLog2eLow = (float)(1.44269504088896340736 - (double)kLog2e);
 
 // rows need not be aligned beyond one element (odd V): these vectors are
 // loaded and stored as 16 bytes from any element boundary
@@ -44,19 +45,27 @@ typedef uint16_t u16x8u __attribute__((ext_vector_type(8), aligned(2)));
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
 typedef __attribute__((ext_vector_type(2))) float f32x2;
 
-__device__ __forceinline__ void load8(const float *p, float v[kVec])
+// eight elements as they lie in memory, and their values
+template <typename T> struct Raw;
+template <> struct Raw<float> {
+    f32x4u a, b;
+};
+template <> struct Raw<uint16_t> {
+    u16x8u a;
+};
+__device__ __forceinline__ Raw<float> load_raw(const float *p) { return {*(const f32x4u *)p, *(const f32x4u *)(p + 4)}; }
+__device__ __forceinline__ Raw<uint16_t> load_raw(const uint16_t *p) { return {*(const u16x8u *)p}; }
+__device__ __forceinline__ void values(const Raw<float> &r, float v[kVec])
 {
-    const f32x4u a = *(const f32x4u *)p, b = *(const f32x4u *)(p + 4);
     for (int i = 0; i < 4; ++i) {
-        v[i] = a[i];
-        v[4 + i] = b[i];
+        v[i] = r.a[i];
+        v[4 + i] = r.b[i];
     }
 }
-__device__ __forceinline__ void load8(const uint16_t *p, float v[kVec])
+__device__ __forceinline__ void values(const Raw<uint16_t> &r, float v[kVec])
 {
-    const u16x8u a = *(const u16x8u *)p;
     for (int i = 0; i < 8; ++i)
-        v[i] = __uint_as_float((uint32_t)a[i] << 16);
+        v[i] = __uint_as_float((uint32_t)r.a[i] << 16);
 }
 __device__ __forceinline__ float load1(const float *p) { return *p; }
 __device__ __forceinline__ float load1(const uint16_t *p) { return __uint_as_float((uint32_t)*p << 16); }
@@ -65,8 +74,8 @@ __device__ __forceinline__ float load1(const uint16_t *p) { return __uint_as_flo
 __device__ __forceinline__ uint16_t to_bf16(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
 __device__ __forceinline__ void store8(float *p, const float v[kVec])
 {
-    *(f32x4u *)p = f32x4u{v[0], v[1], v[2], v[3]};
-    *(f32x4u *)(p + 4) = f32x4u{v[4], v[5], v[6], v[7]};
+    __builtin_nontemporal_store(f32x4u{v[0], v[1], v[2], v[3]}, (f32x4u *)p);
+    __builtin_nontemporal_store(f32x4u{v[4], v[5], v[6], v[7]}, (f32x4u *)(p + 4));
 }
 __device__ __forceinline__ void store8(uint16_t *p, const float v[kVec])
 {
@@ -76,12 +85,19 @@ __device__ __forceinline__ void store8(uint16_t *p, const float v[kVec])
         o[i] = (uint16_t)w;
         o[i + 1] = (uint16_t)(w >> 16);
     }
-    *(u16x8u *)p = o;
+    __builtin_nontemporal_store(o, (u16x8u *)p);
 }
 __device__ __forceinline__ void store1(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store1(uint16_t *p, float v) { *p = to_bf16(v); }
 
-__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+// exp(x) for x <= 0 as exp2(x log2(e)).  log2(e) is taken in two parts: fp32's
+// alone is off by 1.3e-8 relative, which bends every term of a sum the same
+// way (measured: margins over 190 tokens five times further from their fp64
+// values).
+__device__ __forceinline__ float exp_neg(float x)
+{
+    return __builtin_amdgcn_exp2f(__builtin_fmaf(x, kLog2e, x * kLog2eLow));
+}
 
 // running maximum and sum of exp(y - m); m = -inf and s = 0 when empty
 struct Stat {
@@ -96,7 +112,7 @@ __device__ __forceinline__ float anchor(float m) { return m == -INFINITY ? 0.f :
 __device__ __forceinline__ Stat merge(Stat a, Stat b)
 {
     const float m = fmaxf(a.m, b.m), r = anchor(m);
-    return Stat{m, a.s * exp2_fast((a.m - r) * kLog2e) + b.s * exp2_fast((b.m - r) * kLog2e)};
+    return Stat{m, a.s * exp_neg(a.m - r) + b.s * exp_neg(b.m - r)};
 }
 
 __device__ __forceinline__ void add8(Stat &st, const float v[kVec])
@@ -105,28 +121,49 @@ __device__ __forceinline__ void add8(Stat &st, const float v[kVec])
     for (int i = 0; i < kVec; ++i)
         m = fmaxf(m, v[i]);
     const float r = anchor(m);
-    float s = st.s * exp2_fast((st.m - r) * kLog2e);
+    float e[kVec];
     for (int i = 0; i < kVec; ++i)
-        s += exp2_fast((v[i] - r) * kLog2e);
-    st = Stat{m, s};
+        e[i] = exp_neg(v[i] - r);
+    // pairwise: a thread's chain of additions is an eighth as long
+    const float add = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+    st = Stat{m, __builtin_fmaf(st.s, exp_neg(st.m - r), add)};
 }
 
-// statistics of y[0 .. n), one part per thread
-template <int NT, typename T> __device__ __forceinline__ Stat scan_part(const T *y, int64_t n)
+// Statistics of y[0 .. n), one part per thread.  The thread's first H vectors
+// stay in held, for the gradient that follows them.
+template <int NT, int H, typename T>
+__device__ __forceinline__ Stat scan_part(const T *y, int64_t n, Raw<T> (&held)[H > 0 ? H : 1])
 {
     Stat st{-INFINITY, 0.f};
     const int64_t nv = n / kVec;
     int64_t q = threadIdx.x;
-    for (; q + 3 * NT < nv; q += 4 * NT) { // four loads in flight
-        float v[4][kVec];
-        for (int u = 0; u < 4; ++u)
-            load8(y + (q + u * NT) * kVec, v[u]);
-        for (int u = 0; u < 4; ++u)
-            add8(st, v[u]);
+    if (H > 0 && nv > 0) {
+#pragma unroll
+        for (int j = 0; j < H; ++j) // all in flight; past the end the last vector again, not counted
+            held[j] = load_raw(y + min(q + j * NT, nv - 1) * kVec);
+#pragma unroll
+        for (int j = 0; j < H; ++j)
+            if (q + j * NT < nv) {
+                float v[kVec];
+                values(held[j], v);
+                add8(st, v);
+            }
+        q += H * NT;
     }
-    for (; q < nv; q += NT) {
+    for (; q + NT < nv; q += 4 * NT) { // four loads in flight, past the end as above
+        Raw<T> w[4];
+        for (int u = 0; u < 4; ++u)
+            w[u] = load_raw(y + min(q + u * NT, nv - 1) * kVec);
+        for (int u = 0; u < 4; ++u)
+            if (q + u * NT < nv) {
+                float v[kVec];
+                values(w[u], v);
+                add8(st, v);
+            }
+    }
+    if (q < nv) {
         float v[kVec];
-        load8(y + q * kVec, v);
+        values(load_raw(y + q * kVec), v);
         add8(st, v);
     }
     const int64_t i = nv * kVec + threadIdx.x;
@@ -184,25 +221,52 @@ template <typename T> __device__ __forceinline__ float row_logp(const Rows &a, i
 }
 __device__ __forceinline__ float stat_lse(Stat st) { return st.m + logf(st.s); }
 
+// the slices' parts of one row, eight loads in flight
 __device__ __forceinline__ Stat merge_slices(const Stat *part, int64_t S)
 {
-    Stat st = part[0];
-    for (int64_t i = 1; i < S; ++i)
-        st = merge(st, part[i]);
+    Stat st{-INFINITY, 0.f};
+    for (int64_t i = 0; i < S; i += 8) {
+        Stat p[8];
+        for (int u = 0; u < 8; ++u)
+            p[u] = part[min(i + u, S - 1)];
+        float m = st.m;
+        for (int u = 0; u < 8; ++u)
+            m = fmaxf(m, p[u].m);
+        const float r = anchor(m);
+        float s = st.s * exp_neg(st.m - r);
+        for (int u = 0; u < 8; ++u)
+            s += i + u < S ? p[u].s * exp_neg(p[u].m - r) : 0.f;
+        st = Stat{m, s};
+    }
     return st;
 }
 
-// --- statistics: workgroup (row, slice) -> part[row][slice] -----------------
-template <typename T> __global__ __launch_bounds__(kNT) void stats_kernel(Rows a, Stat *part)
+// --- statistics: workgroup (row, slice) -> part[row][slice]; with one slice
+// per row logp and lse (if not null) as well ---------------------------------------
+template <int NT, typename T>
+__global__ __launch_bounds__(NT) void stats_kernel(Rows a, Stat *part, float *logp, float *lse, float *coef)
 {
-    __shared__ Stat red[kNT / 64];
+    __shared__ Stat red[NT / 64];
     const int64_t m = blockIdx.x / a.S, sl = blockIdx.x % a.S;
-    if (!row_counts(a, m))
+    if (!row_counts(a, m)) {
+        if (sl == 0 && threadIdx.x == 0) { // no later kernel looks at a row outside every answer
+            if (logp)
+                logp[m] = 0.f;
+            if (coef)
+                coef[m] = 0.f;
+        }
         return;
+    }
     const int64_t v0 = sl * a.slice, n = min(a.slice, a.V - v0);
-    const Stat st = block_merge<kNT>(scan_part<kNT>(row_ptr<T>(a, m) + v0, n), red);
-    if (threadIdx.x == 0)
+    Raw<T> none[1];
+    const Stat st = block_merge<NT>(scan_part<NT, 0>(row_ptr<T>(a, m) + v0, n, none), red);
+    if (threadIdx.x == 0) {
         part[blockIdx.x] = st;
+        if (logp && a.S == 1)
+            logp[m] = row_logp<T>(a, m, st);
+        if (lse)
+            lse[m] = stat_lse(st);
+    }
 }
 
 template <typename T>
@@ -218,6 +282,41 @@ __global__ __launch_bounds__(kNT) void logp_kernel(Rows a, const Stat *part, flo
         lse[m] = stat_lse(st);
 }
 
+// --- sums in a fixed order ----------------------------------------------------
+struct Sum {
+    const float *x;
+    int64_t n;
+    double scale;
+    float *out;
+};
+
+template <int NT> __device__ __forceinline__ double block_sum(double x, double *red)
+{
+    for (int off = 32; off >= 1; off >>= 1)
+        x += __shfl_xor(x, off);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0)
+        red[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = 0.;
+    for (int w = 0; w < NT / 64; ++w)
+        x += red[w];
+    return x;
+}
+
+template <int NT> __device__ __forceinline__ void sum_all(const Sum &a)
+{
+    __shared__ double red[NT / 64];
+    double s = 0.;
+    for (int64_t i = threadIdx.x; i < a.n; i += NT)
+        s += a.x[i];
+    s = block_sum<NT>(s, red);
+    if (threadIdx.x == 0)
+        *a.out = (float)(s * a.scale);
+}
+
+__global__ __launch_bounds__(kWide) void sum_kernel(Sum a) { sum_all<kWide>(a); }
+
 // --- gradient of a slice -----------------------------------------------------
 template <typename G> __device__ __forceinline__ void zero_part(G *g, int64_t n)
 {
@@ -230,35 +329,61 @@ template <typename G> __device__ __forceinline__ void zero_part(G *g, int64_t n)
 }
 
 // g[i] = c (1[i = t] - exp(y[i] - m) / s) for i in [0, n); t relative to y
-template <int NT, typename T, typename G>
-__device__ __forceinline__ void grad_part(const T *y, G *g, int64_t n, int64_t t, float c, Stat st)
+template <int NT, int H, typename T, typename G>
+__device__ __forceinline__ void grad_part(const T *y, G *g, int64_t n, int64_t t, float c, Stat st,
+                                          const Raw<T> (&held)[H > 0 ? H : 1])
 {
     const float r = anchor(st.m), k = -c / st.s;
-    auto one = [&](float v, int64_t i) {
-        const float x = k * exp2_fast((v - r) * kLog2e);
-        return i == t ? x + c : x;
-    };
-    const int64_t nv = n / kVec;
-    for (int64_t q = threadIdx.x; q < nv; q += NT) {
+    auto put = [&](const Raw<T> &w, int64_t q) {
         float v[kVec];
-        load8(y + q * kVec, v);
+        values(w, v);
         for (int i = 0; i < kVec; ++i)
-            v[i] = one(v[i], q * kVec + i);
+            v[i] = k * exp_neg(v[i] - r);
+        if (t >> 3 == q)
+            for (int i = 0; i < kVec; ++i)
+                v[i] += (t & 7) == i ? c : 0.f;
         store8(g + q * kVec, v);
+    };
+    static_assert(kVec == 8, "t >> 3");
+    const int64_t nv = n / kVec;
+    int64_t q = threadIdx.x;
+    if (H > 0 && nv > 0) {
+#pragma unroll
+        for (int j = 0; j < H; ++j)
+            if (q + j * NT < nv)
+                put(held[j], q + j * NT);
+        q += H * NT;
     }
+    for (; q + NT < nv; q += 4 * NT) {
+        Raw<T> w[4];
+        for (int u = 0; u < 4; ++u)
+            w[u] = load_raw(y + min(q + u * NT, nv - 1) * kVec);
+        for (int u = 0; u < 4; ++u)
+            if (q + u * NT < nv)
+                put(w[u], q + u * NT);
+    }
+    if (q < nv)
+        put(load_raw(y + q * kVec), q);
     const int64_t i = nv * kVec + threadIdx.x;
-    if (i < n)
-        store1(g + i, one(load1(y + i), i));
+    if (i < n) {
+        const float x = k * exp_neg(load1(y + i) - r);
+        store1(g + i, i == t ? x + c : x);
+    }
 }
 
 // dlogits of slice (row, sl): the row's statistics merged from part, its
 // coefficient from coef.  No logit outside the slice is read, so that the
-// gradient may be written over the logits.
+// gradient may be written over the logits.  The first workgroup also sums
+// the loss, which saves a launch.
 template <typename T, typename G>
 __global__ __launch_bounds__(kNT) void grad_kernel(Rows a, const Stat *part, const float *coef, const float *gscale,
-                                                   G *dy, int64_t ldg)
+                                                   G *dy, int64_t ldg, Sum total)
 {
-    const int64_t m = blockIdx.x / a.S, sl = blockIdx.x % a.S;
+    if (blockIdx.x == 0)
+        sum_all<kNT>(total);
+    // last rows first: the statistics read them last, and what the memory-side
+    // cache (256 MB) still holds of them is not fetched again
+    const int64_t b = gridDim.x - 1 - (int64_t)blockIdx.x, m = b / a.S, sl = b % a.S;
     const int64_t v0 = sl * a.slice, n = min(a.slice, a.V - v0);
     G *g = dy + m * ldg + v0;
     float c = coef[m];
@@ -269,7 +394,8 @@ __global__ __launch_bounds__(kNT) void grad_kernel(Rows a, const Stat *part, con
     if (gscale)
         c *= *gscale;
     const Stat st = merge_slices(part + m * a.S, a.S);
-    grad_part<kNT>(row_ptr<T>(a, m) + v0, g, n, (int64_t)a.targets[m] - v0, c, st);
+    const Raw<T> none[1] = {};
+    grad_part<kNT, 0>(row_ptr<T>(a, m) + v0, g, n, (int64_t)a.targets[m] - v0, c, st, none);
 }
 
 struct Policy {
@@ -295,32 +421,43 @@ __device__ __forceinline__ float policy_token(const Policy &p, int64_t m, float 
     return w * loss;
 }
 
-// --- sums in a fixed order ----------------------------------------------------
-constexpr int kSumNT = 1024;
-
-__device__ __forceinline__ double block_sum(double x, double *red)
+// The policy loss of a whole row in one workgroup: statistics, loss,
+// coefficient and gradient.  The gradient's second pass finds the row in
+// registers (the first H vectors of each thread) and in the caches.
+template <int NT, int H, typename T, typename G>
+__global__ __launch_bounds__(NT) void policy_row_kernel(Rows a, Policy pol, const float *gscale, float *logp,
+                                                        float *token, G *dy, int64_t ldg)
 {
-    for (int off = 32; off >= 1; off >>= 1)
-        x += __shfl_xor(x, off);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0)
-        red[threadIdx.x >> 6] = x;
-    __syncthreads();
-    x = 0.;
-    for (int w = 0; w < (int)blockDim.x / 64; ++w)
-        x += red[w];
-    return x;
-}
-
-__global__ __launch_bounds__(kSumNT) void sum_kernel(const float *x, int64_t n, double scale, float *out)
-{
-    __shared__ double red[kSumNT / 64];
-    double s = 0.;
-    for (int64_t i = threadIdx.x; i < n; i += kSumNT)
-        s += x[i];
-    s = block_sum(s, red);
-    if (threadIdx.x == 0)
-        *out = (float)(s * scale);
+    __shared__ Stat red[NT / 64];
+    const int64_t m = blockIdx.x;
+    float lp = 0.f, loss = 0.f, c = 0.f;
+    Stat st{0.f, 1.f};
+    Raw<T> held[H > 0 ? H : 1];
+    const T *y = row_ptr<T>(a, m);
+    int64_t t = -1;
+    if (row_counts(a, m)) {
+        t = a.targets[m];
+        // read before the barrier: the gradient may be written over it
+        const float yt = t >= 0 && t < a.V ? load1(y + t) : __builtin_nanf("");
+        st = block_merge<NT>(scan_part<NT, H>(y, a.V, held), red);
+        lp = (yt - st.m) - logf(st.s);
+        loss = policy_token(pol, m, a.weights[m], lp, &c);
+    }
+    if (threadIdx.x == 0) {
+        token[m] = loss;
+        if (logp)
+            logp[m] = lp;
+    }
+    if (!dy)
+        return;
+    G *g = dy + m * ldg;
+    if (c == 0.f) {
+        zero_part(g, a.V);
+        return;
+    }
+    if (gscale)
+        c *= *gscale;
+    grad_part<NT, H>(y, g, a.V, t, c, st, held);
 }
 
 // --- policy rows: logp, token loss and coefficient of every row -----------------
@@ -369,7 +506,7 @@ __global__ __launch_bounds__(kNT) void pair_kernel(Rows a, const Stat *part, con
             if (logp)
                 logp[m] = lp;
         }
-        sum[i] = block_sum(s, red);
+        sum[i] = block_sum<kNT>(s, red);
     }
     const float h = (float)((double)beta * (sum[0] - sum[1]));
     const float e = expf(-fabsf(h)), sp = log1pf(e);               // log(1 + exp(-|h|))
@@ -387,31 +524,37 @@ __global__ __launch_bounds__(kNT) void pair_kernel(Rows a, const Stat *part, con
     }
 }
 
-// rows outside every answer
-__global__ __launch_bounds__(kNT) void outside_kernel(Rows a, float *logp, float *coef)
-{
-    const int64_t m = (int64_t)blockIdx.x * kNT + threadIdx.x;
-    if (m < a.M && (m < a.offsets[0] || m >= a.offsets[a.n_off - 1])) {
-        coef[m] = 0.f;
-        if (logp)
-            logp[m] = 0.f;
-    }
-}
-
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 constexpr int64_t kMaxRows = int64_t(1) << 20;
-constexpr int64_t kTargetWg = 2048; // workgroups that fill the chip with slices
+constexpr int64_t kTargetWg = 4096; // workgroups that fill the chip with slices
+constexpr int64_t kHoldMin = 4096;  // row length from which a row's workgroup keeps logits in registers
+constexpr int64_t kCu = 256;        // compute units
 
+// Slices of a row: enough workgroups to fill the chip evenly, each with at
+// least kSliceMin logits, in whole steps of a workgroup.
 void choose_slices(int64_t M, int64_t V, int64_t *S, int64_t *slice)
 {
     int64_t s = std::max<int64_t>(1, kTargetWg / std::max<int64_t>(M, 1));
     s = std::min(s, std::max<int64_t>(1, V / kSliceMin));
     int64_t len = (V + s - 1) / s;
-    len = (len + kVec - 1) / kVec * kVec;
+    len = (len + kNT * kVec - 1) / (kNT * kVec) * (kNT * kVec);
     *slice = len;
     *S = (V + len - 1) / len;
+}
+
+// Whether the policy loss runs as one workgroup per row (the logits read from
+// HBM once) rather than in slices (read twice).  A long row's workgroup fills
+// a compute unit, so the rows go in rounds of kCu, and a round that is mostly
+// empty costs more than the second read: at V = 151936 a round takes 50 us
+// and the slices 0.25 us a row + 8 us, which cross at 0.7 of a round filled.
+bool whole_rows(int64_t M, int64_t V)
+{
+    if (V <= 4 * kNT * kVec)
+        return true; // several rows fit a compute unit
+    const int64_t rounds = (M + kCu - 1) / kCu;
+    return 10 * M >= 7 * rounds * kCu;
 }
 
 struct LossWs {
@@ -498,21 +641,24 @@ Rows make_rows(int64_t M, int64_t V, const void *logits, int64_t ld, const int32
     return a;
 }
 
-template <typename T> void run_stats(const Rows &a, Stat *part, hipStream_t st)
+template <typename T>
+void run_stats(const Rows &a, Stat *part, float *logp, float *lse, float *coef, hipStream_t st)
 {
-    hipLaunchKernelGGL(stats_kernel<T>, dim3((unsigned)(a.M * a.S)), dim3(kNT), 0, st, a, part);
+    hipLaunchKernelGGL((stats_kernel<kNT, T>), dim3((unsigned)(a.M * a.S)), dim3(kNT), 0, st, a, part, logp, lse, coef);
 }
 
-template <typename T>
-void run_grad(const Rows &a, const Stat *part, const float *coef, const float *gscale, void *dy, int grad_type,
-              int64_t ldg, hipStream_t st)
+template <typename T> void run_logp(const Rows &a, Stat *part, float *logp, float *lse, hipStream_t st)
 {
-    const dim3 grid((unsigned)(a.M * a.S));
-    if (grad_type == ARCHEAD_F32)
-        hipLaunchKernelGGL((grad_kernel<T, float>), grid, dim3(kNT), 0, st, a, part, coef, gscale, (float *)dy, ldg);
-    else
-        hipLaunchKernelGGL((grad_kernel<T, uint16_t>), grid, dim3(kNT), 0, st, a, part, coef, gscale, (uint16_t *)dy,
-                           ldg);
+    const bool whole = a.S == 1;
+    run_stats<T>(a, part, whole ? logp : nullptr, whole ? lse : nullptr, nullptr, st);
+    if (!whole)
+        hipLaunchKernelGGL(logp_kernel<T>, dim3((unsigned)((a.M + kNT - 1) / kNT)), dim3(kNT), 0, st, a, part, logp,
+                           lse);
+}
+
+void run_sum(const float *x, int64_t n, double scale, float *out, hipStream_t st)
+{
+    hipLaunchKernelGGL(sum_kernel, dim3(1), dim3(kWide), 0, st, Sum{x, n, scale, out});
 }
 
 struct Grad {
@@ -523,31 +669,85 @@ struct Grad {
 };
 
 template <typename T>
-void run_policy(const Rows &a, void *ws, const LossWs &L, const Policy &pol, float *logp, const Grad &g, hipStream_t st)
+void run_grad(const Rows &a, const Stat *part, const float *coef, const Grad &g, const Sum &total, hipStream_t st)
+{
+    const dim3 grid((unsigned)(a.M * a.S));
+    if (g.type == ARCHEAD_F32)
+        hipLaunchKernelGGL((grad_kernel<T, float>), grid, dim3(kNT), 0, st, a, part, coef, g.scale, (float *)g.dy, g.ld,
+                           total);
+    else
+        hipLaunchKernelGGL((grad_kernel<T, uint16_t>), grid, dim3(kNT), 0, st, a, part, coef, g.scale,
+                           (uint16_t *)g.dy, g.ld, total);
+}
+
+template <int NT, int H, typename T>
+void run_policy_rows(const Rows &a, const Policy &pol, float *logp, float *token, const Grad &g, hipStream_t st)
+{
+    if (g.type == ARCHEAD_F32)
+        hipLaunchKernelGGL((policy_row_kernel<NT, H, T, float>), dim3((unsigned)a.M), dim3(NT), 0, st, a, pol, g.scale,
+                           logp, token, (float *)g.dy, g.ld);
+    else
+        hipLaunchKernelGGL((policy_row_kernel<NT, H, T, uint16_t>), dim3((unsigned)a.M), dim3(NT), 0, st, a, pol,
+                           g.scale, logp, token, (uint16_t *)g.dy, g.ld);
+}
+
+// Threads and held vectors by the row's length: as many vectors held as the
+// row fills (a vector past its end is a wasted load: V = 50021 in bf16 took
+// 128 us with 16 held of which 6 are filled, 102 us with none) and the
+// registers of 1024 threads allow.  2048 rows of 151936 fp32 logits with a
+// bf16 gradient: 400 us with eight held, 486 us with none.
+template <typename T>
+void run_policy_whole(const Rows &a, const Policy &pol, float *logp, float *token, const Grad &g, hipStream_t st)
+{
+    const int64_t narrow = (a.V + kNT * kVec - 1) / (kNT * kVec), wide = (a.V + kWide * kVec - 1) / (kWide * kVec);
+    if (!g.dy || a.V < kHoldMin)
+        run_policy_rows<kNT, 0, T>(a, pol, logp, token, g, st);
+    else if (narrow <= 4)
+        run_policy_rows<kNT, 4, T>(a, pol, logp, token, g, st);
+    else if (wide < 4)
+        run_policy_rows<kWide, 2, T>(a, pol, logp, token, g, st);
+    else if (wide < 8)
+        run_policy_rows<kWide, 4, T>(a, pol, logp, token, g, st);
+    else if (sizeof(T) == 4 || wide < 16)
+        run_policy_rows<kWide, 8, T>(a, pol, logp, token, g, st);
+    else
+        run_policy_rows<kWide, 16, T>(a, pol, logp, token, g, st);
+}
+
+template <typename T>
+void run_policy(const Rows &a, void *ws, const LossWs &L, const Policy &pol, float *loss, float *logp, const Grad &g,
+                hipStream_t st)
 {
     Stat *part = (Stat *)((char *)ws + L.part);
     float *token = (float *)((char *)ws + L.token), *coef = (float *)((char *)ws + L.coef);
-    run_stats<T>(a, part, st);
+    if (whole_rows(a.M, a.V)) {
+        run_policy_whole<T>(a, pol, logp, token, g, st);
+        run_sum(token, a.M, 1.0, loss, st);
+        return;
+    }
+    run_stats<T>(a, part, nullptr, nullptr, nullptr, st);
     hipLaunchKernelGGL(policy_rows_kernel<T>, dim3((unsigned)((a.M + kNT - 1) / kNT)), dim3(kNT), 0, st, a, part, pol,
                        logp, token, coef);
     if (g.dy)
-        run_grad<T>(a, part, coef, g.scale, g.dy, g.type, g.ld, st);
+        run_grad<T>(a, part, coef, g, Sum{token, a.M, 1.0, loss}, st);
+    else
+        run_sum(token, a.M, 1.0, loss, st);
 }
 
 template <typename T>
 void run_preference(const Rows &a, void *ws, const LossWs &L, const float *ref, int64_t P, float beta, float smoothing,
-                    float *logp, float *margins, const Grad &g, hipStream_t st)
+                    float *loss, float *logp, float *margins, const Grad &g, hipStream_t st)
 {
     Stat *part = (Stat *)((char *)ws + L.part);
     float *coef = (float *)((char *)ws + L.coef), *pair = (float *)((char *)ws + L.pair);
-    if (a.M > 0) {
-        hipLaunchKernelGGL(outside_kernel, dim3((unsigned)((a.M + kNT - 1) / kNT)), dim3(kNT), 0, st, a, logp, coef);
-        run_stats<T>(a, part, st);
-    }
+    if (a.M > 0)
+        run_stats<T>(a, part, logp, nullptr, coef, st);
     hipLaunchKernelGGL(pair_kernel<T>, dim3((unsigned)P), dim3(kNT), 0, st, a, part, ref, P, beta, smoothing, logp,
                        margins, pair, coef);
     if (a.M > 0 && g.dy)
-        run_grad<T>(a, part, coef, g.scale, g.dy, g.type, g.ld, st);
+        run_grad<T>(a, part, coef, g, Sum{pair, P, 1.0 / (double)P, loss}, st);
+    else
+        run_sum(pair, P, 1.0 / (double)P, loss, st);
 }
 
 } // namespace
@@ -581,14 +781,10 @@ extern "C" archead_status archead_token_logp(int64_t M, int64_t V, const void *l
     hipStream_t st = (hipStream_t)hip_stream;
     const Rows a = make_rows(M, V, logits, ld, targets, nullptr);
     Stat *part = (Stat *)((char *)ws + loss_ws(M, V, 0).part);
-    const dim3 grid((unsigned)((M + kNT - 1) / kNT));
-    if (type == ARCHEAD_F32) {
-        run_stats<float>(a, part, st);
-        hipLaunchKernelGGL(logp_kernel<float>, grid, dim3(kNT), 0, st, a, part, logp, lse);
-    } else {
-        run_stats<uint16_t>(a, part, st);
-        hipLaunchKernelGGL(logp_kernel<uint16_t>, grid, dim3(kNT), 0, st, a, part, logp, lse);
-    }
+    if (type == ARCHEAD_F32)
+        run_logp<float>(a, part, logp, lse, st);
+    else
+        run_logp<uint16_t>(a, part, logp, lse, st);
     return launched("archead_token_logp");
 }
 
@@ -618,10 +814,11 @@ extern "C" archead_status archead_policy_loss(int64_t M, int64_t V, const void *
     const Grad g{grad_scale, dlogits, grad_type, ldg};
     const Rows a = make_rows(M, V, logits, ld, targets, weights);
     if (M > 0 && type == ARCHEAD_F32)
-        run_policy<float>(a, ws, L, pol, logp, g, st);
+        run_policy<float>(a, ws, L, pol, loss, logp, g, st);
     else if (M > 0)
-        run_policy<uint16_t>(a, ws, L, pol, logp, g, st);
-    hipLaunchKernelGGL(sum_kernel, dim3(1), dim3(kSumNT), 0, st, (const float *)((char *)ws + L.token), M, 1.0, loss);
+        run_policy<uint16_t>(a, ws, L, pol, loss, logp, g, st);
+    else
+        run_sum(nullptr, 0, 1.0, loss, st);
     return launched("archead_policy_loss");
 }
 
@@ -654,10 +851,8 @@ extern "C" archead_status archead_preference_loss(int64_t M, int64_t V, const vo
     a.n_off = 2 * P + 1;
     const Grad g{grad_scale, dlogits, grad_type, ldg};
     if (type == ARCHEAD_F32)
-        run_preference<float>(a, ws, L, ref_logp, P, beta, smoothing, logp, margins, g, st);
+        run_preference<float>(a, ws, L, ref_logp, P, beta, smoothing, loss, logp, margins, g, st);
     else
-        run_preference<uint16_t>(a, ws, L, ref_logp, P, beta, smoothing, logp, margins, g, st);
-    hipLaunchKernelGGL(sum_kernel, dim3(1), dim3(kSumNT), 0, st, (const float *)((char *)ws + L.pair), P,
-                       1.0 / (double)P, loss);
+        run_preference<uint16_t>(a, ws, L, ref_logp, P, beta, smoothing, loss, logp, margins, g, st);
     return launched("archead_preference_loss");
 }

@@ -23,16 +23,26 @@ def _type_code(dtype, name):
 
 
 @contextlib.contextmanager
-def on_stream(device, stream):
-    """Makes device current and stream (default: that device's current one)
-    the stream of the allocations inside; yields the hipStream_t."""
+def _entered(device, stream):
     import torch
     with torch.cuda.device(device):
         s = torch.cuda.current_stream(device) if stream is None else stream
         if s.device != device:
             raise ValueError(f"the stream belongs to {s.device}, the tensors live on {device}")
         with torch.cuda.stream(s):
-            yield ctypes.c_void_p(s.cuda_stream)
+            yield s.cuda_stream
+
+
+def on_stream(device, stream, call):
+    """call(hipStream_t) with device current and stream (default: that
+    device's current one) the stream of the allocations inside."""
+    import torch
+    # entering torch's device and stream contexts costs 10 us, more than the
+    # smallest calls: they are skipped where they would change nothing
+    if stream is None and device.index == torch.cuda.current_device():
+        return call(torch.cuda.current_stream(device).cuda_stream)
+    with _entered(device, stream) as st:
+        return call(st)
 
 
 def need_rows(t, name, dtypes, shape, device):
@@ -56,7 +66,13 @@ def need_rows(t, name, dtypes, shape, device):
 
 
 def ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+def _need_vector(t, name, dtype, n, device):
+    # what a sound call costs is this one line; _need says what is wrong with another
+    if not (hasattr(t, "dtype") and t.dtype == dtype and t.shape == (n,) and t.device == device and t.is_contiguous()):
+        _need(t, name, (dtype,), (n,), device)
 
 
 def _logit_args(logits, targets, **vectors):
@@ -69,10 +85,10 @@ def _logit_args(logits, targets, **vectors):
         raise ValueError("logits need at least one column")
     code = _type_code(logits.dtype, "logits")
     ld = need_rows(logits, "logits", (logits.dtype,), (M, V), logits.device)
-    _need(targets, "targets", (torch.int32,), (M,), logits.device)
+    _need_vector(targets, "targets", torch.int32, M, logits.device)
     for name, t in vectors.items():
         if t is not None:
-            _need(t, name, (torch.float32,), (M,), logits.device)
+            _need_vector(t, name, torch.float32, M, logits.device)
     return M, V, code, ld
 
 
@@ -102,12 +118,16 @@ def token_logp(logits, targets, stream=None):
     the log-normaliser of every row of logits (fp32 or bf16, M x V)."""
     import torch
     M, V, code, ld = _logit_args(logits, targets)
-    with on_stream(logits.device, stream) as st:
-        out = torch.empty((2, M), dtype=torch.float32, device=logits.device)
-        ws, n = _workspace(M, V, 0, logits.device)
-        _check(load_library().archead_token_logp(M, V, ptr(logits), code, ld, ptr(targets), ptr(out[0]), ptr(out[1]),
+    dev = logits.device
+
+    def call(st):
+        logp = torch.empty((M,), dtype=torch.float32, device=dev)
+        lse = torch.empty((M,), dtype=torch.float32, device=dev)
+        ws, n = _workspace(M, V, 0, dev)
+        _check(load_library().archead_token_logp(M, V, ptr(logits), code, ld, ptr(targets), ptr(logp), ptr(lse),
                                                  ptr(ws), n, st), "archead_token_logp")
-    return out[0], out[1]
+        return logp, lse
+    return on_stream(dev, stream, call)
 
 
 def policy_loss(logits, targets, old_logp, advantages, weights, ref_logp=None, beta: float = 0.0,
@@ -127,7 +147,8 @@ def policy_loss(logits, targets, old_logp, advantages, weights, ref_logp=None, b
             raise ValueError(f"{name} is required")
     if grad_scale is not None:
         _need(grad_scale, "grad_scale", (torch.float32,), (), dev)
-    with on_stream(dev, stream) as st:
+
+    def call(st):
         dy, gcode, ldg = _gradient(logits, M, V, grad_dtype, dlogits)
         loss = torch.empty((), dtype=torch.float32, device=dev)
         logp = torch.empty((M,), dtype=torch.float32, device=dev)
@@ -136,7 +157,8 @@ def policy_loss(logits, targets, old_logp, advantages, weights, ref_logp=None, b
             M, V, ptr(logits), code, ld, ptr(targets), ptr(old_logp), ptr(ref_logp), ptr(advantages), ptr(weights),
             float(eps_low), float(eps_high), float(beta), ptr(grad_scale), ptr(loss), ptr(logp), ptr(dy), gcode, ldg,
             ptr(ws), n, st), "archead_policy_loss")
-    return loss, logp, dy
+        return loss, logp, dy
+    return on_stream(dev, stream, call)
 
 
 def preference_loss(logits, targets, weights, offsets, ref_logp=None, beta: float = 0.1, smoothing: float = 0.0,
@@ -156,7 +178,8 @@ def preference_loss(logits, targets, weights, offsets, ref_logp=None, beta: floa
     P = (int(offsets.shape[0]) - 1) // 2
     if grad_scale is not None:
         _need(grad_scale, "grad_scale", (torch.float32,), (), dev)
-    with on_stream(dev, stream) as st:
+
+    def call(st):
         dy, gcode, ldg = _gradient(logits, M, V, grad_dtype, dlogits)
         loss = torch.empty((), dtype=torch.float32, device=dev)
         margins = torch.empty((P,), dtype=torch.float32, device=dev)
@@ -166,4 +189,5 @@ def preference_loss(logits, targets, weights, offsets, ref_logp=None, beta: floa
             M, V, ptr(logits), code, ld, ptr(targets), ptr(weights), P, ptr(offsets), ptr(ref_logp), float(beta),
             float(smoothing), ptr(grad_scale), ptr(loss), ptr(margins), ptr(logp), ptr(dy), gcode, ldg, ptr(ws), n,
             st), "archead_preference_loss")
-    return loss, margins, logp, dy
+        return loss, margins, logp, dy
+    return on_stream(dev, stream, call)
