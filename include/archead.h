@@ -448,6 +448,53 @@ archead_status archead_preference_loss(int64_t M, int64_t V, const void *logits,
                                        void *hip_stream);
 
 /*
+ * archead_fp8_quantize -- a matrix in 8-bit floating point (e4m3, OCP: largest
+ * value 448) with a scale for each block of 128: of 128 columns of one row
+ * (block_rows = 1, for activations) or of 128 x 128 (block_rows = 128, for
+ * weights); the last block of a row or column may be smaller.  A block with
+ * largest magnitude a has the scale s = a / 448 in fp32 (at least 2^-126; 0
+ * for a block of zeros, whose codes are 0), and its codes are the e4m3 values
+ * nearest to the exact quotients x / s, ties to even.  A NaN has the code of
+ * NaN; an infinity makes its block's scale infinite and its products NaN.
+ *
+ * x    DEVICE rows x cols, fp32 or bf16 (type), row stride ldx elements,
+ *      aligned to its element.  rows < 2^31; cols a multiple of 16 (the
+ *      product reads rows in 16-byte pieces) up to 2^20; rows times blocks at
+ *      most 2^34; else ARCHEAD_ESHAPE.
+ * q    DEVICE codes, rows x cols bytes, row stride ldq bytes; q and ldq
+ *      multiples of 16.
+ * s    DEVICE fp32.  block_rows = 1: s[b * lds + row] for block b of a row
+ *      (the product reads neighbouring rows' scales of one block together),
+ *      lds >= rows; block_rows = 128: s[(row / 128) * lds + b], lds >=
+ *      ceil(cols / 128).
+ * The current device must be the one the buffers and hip_stream belong to.
+ * Enqueued, not waited for; nothing is allocated (graph capture is fine).
+ */
+archead_status archead_fp8_quantize(int64_t rows, int64_t cols, const void *x, int type, int64_t ldx, int block_rows,
+                                    uint8_t *q, int64_t ldq, float *s, int64_t lds, void *hip_stream);
+
+/*
+ * archead_fp8_matmul -- out = A B^T of two such matrices: A (M x K, scales
+ * per row and block) and B (N x K, scales per 128 x 128 block), an output
+ * head's hidden states and its weights:
+ *   out[m, n] = sum_b sA[b, m] sB[n / 128, b] sum_{k in block b} A[m, k] B[n, k]
+ * The codes' products enter the sums exactly; sums are fp32; out is rounded
+ * once to its type.
+ *
+ * M <= 2^20, N < 2^31, K a multiple of 16 in [16, 2^20]; else ARCHEAD_ESHAPE.
+ * A, B   DEVICE e4m3 codes, 16-byte aligned, row strides lda, ldb >= K
+ *        multiples of 16.  Bytes of a row past K are not used.
+ * sA     DEVICE fp32, sA[b * ldsa + m], ldsa >= M.
+ * sB     DEVICE fp32, sB[(n / 128) * ldsb + b], ldsb >= ceil(K / 128).
+ * out    DEVICE M x N, fp32 or bf16 (out_type), row stride ldo >= N elements.
+ * M = 0 or N = 0 succeeds without work.  Stream behaviour as
+ * archead_fp8_quantize; equal calls give equal bits.
+ */
+archead_status archead_fp8_matmul(int64_t M, int64_t N, int64_t K, const uint8_t *A, int64_t lda, const float *sA,
+                                  int64_t ldsa, const uint8_t *B, int64_t ldb, const float *sB, int64_t ldsb,
+                                  void *out, int out_type, int64_t ldo, void *hip_stream);
+
+/*
  * archead_packed_bytes -- eq 10 of the ARCHead paper: the sum over the
  * registered packed buffers of numel x element size (A5 counted at 5 bits,
  * R4 at 4 bits, int8 fields at 8, scales at 16; each buffer rounded up to a

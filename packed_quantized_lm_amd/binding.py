@@ -49,6 +49,10 @@ SIGNATURES = {
     "archead_preference_loss": (ctypes.c_int, [_I64, _I64, _VP, ctypes.c_int, _I64, _VP, _VP, _I64, _VP, _VP,
                                                ctypes.c_float, ctypes.c_float] + [_VP] * 5 +
                                 [ctypes.c_int, _I64, _VP, ctypes.c_uint64, _VP]),
+    "archead_fp8_quantize": (ctypes.c_int, [_I64, _I64, _VP, ctypes.c_int, _I64, ctypes.c_int, _VP, _I64, _VP, _I64,
+                                            _VP]),
+    "archead_fp8_matmul": (ctypes.c_int, [_I64] * 3 + [_VP, _I64, _VP, _I64, _VP, _I64, _VP, _I64, _VP, ctypes.c_int,
+                                                       _I64, _VP]),
     "archead_packed_bytes": (ctypes.c_int, [_VP, ctypes.POINTER(ctypes.c_uint64)]),
     "archead_device_bytes": (ctypes.c_int, [_VP, ctypes.POINTER(ctypes.c_uint64)]),
     "archead_free": (ctypes.c_int, [_VP]),
