@@ -452,9 +452,10 @@ archead_status archead_preference_loss(int64_t M, int64_t V, const void *logits,
  * value 448) with a scale for each block of 128: of 128 columns of one row
  * (block_rows = 1, for activations) or of 128 x 128 (block_rows = 128, for
  * weights); the last block of a row or column may be smaller.  A block with
- * largest magnitude a has the scale s = a / 448 in fp32 (at least 2^-126; 0
- * for a block of zeros, whose codes are 0), and its codes are the e4m3 values
- * nearest to the exact quotients x / s, ties to even.  A NaN has the code of
+ * largest magnitude a has the scale s = a * (1 / 448), the reciprocal and the
+ * product rounded to fp32 (at least 2^-126; 0 for a block of zeros, whose codes
+ * are 0), and its codes are the e4m3 values nearest to the exact quotients
+ * x / s, ties to even.  A NaN has the code of
  * NaN; an infinity makes its block's scale infinite and its products NaN.
  *
  * x    DEVICE rows x cols, fp32 or bf16 (type), row stride ldx elements,
@@ -478,8 +479,10 @@ archead_status archead_fp8_quantize(int64_t rows, int64_t cols, const void *x, i
  * per row and block) and B (N x K, scales per 128 x 128 block), an output
  * head's hidden states and its weights:
  *   out[m, n] = sum_b sA[b, m] sB[n / 128, b] sum_{k in block b} A[m, k] B[n, k]
- * The codes' products enter the sums exactly; sums are fp32; out is rounded
- * once to its type.
+ * The codes' products enter the sums exactly, and sums are fp32; only with a
+ * bf16 out and M > 64 do products 2^13 below the largest of their group of
+ * eight lose bits (the fp8 matrix instruction's adder; 1e-4 of a typical
+ * result).  out is rounded once to its type.
  *
  * M <= 2^20, N < 2^31, K a multiple of 16 in [16, 2^20]; else ARCHEAD_ESHAPE.
  * A, B   DEVICE e4m3 codes, 16-byte aligned, row strides lda, ldb >= K

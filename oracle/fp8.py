@@ -1,7 +1,7 @@
 """Matrices in e4m3 with a scale per block of 128, and their product -- TEST
 INFRASTRUCTURE.
 
-Defined in include/archead.h: s = fp32(amax / 448), at least 2^-126 (0 for a
+Defined in include/archead.h: s = fp32(amax * fp32(1 / 448)), at least 2^-126 (0 for a
 block of zeros); codes nearest to the exact quotient, ties to even.  Quotients
 are taken in fp64: x has at most 24 significant bits and s 24, so a quotient
 that is no tie lies at least 2^-50 of itself away from one, and fp64 tells.
@@ -39,7 +39,7 @@ def encode(q: np.ndarray) -> np.ndarray:
 def scale_of(amax: np.ndarray) -> np.ndarray:
     """fp32 scales of blocks with these largest magnitudes (exact in fp32)."""
     a = np.asarray(amax, dtype=np.float32)
-    s = np.maximum(a / np.float32(448), np.float32(2.0 ** -126))
+    s = np.maximum(a * (np.float32(1) / np.float32(448)), np.float32(2.0 ** -126))
     return np.where(a > 0, s, np.float32(0))
 
 

@@ -2,7 +2,8 @@
 // each block of 128, and the product of two of them: an 8-bit output head.
 //
 // Quantiser: a block (128 columns of one row, or 128 x 128) gets
-//   s = amax / 448 in fp32 (448 is e4m3's largest value), at least 2^-126;
+//   s = amax * (1 / 448), both factors and the product in fp32 (448 is e4m3's
+//   largest value), at least 2^-126;
 //   code = the e4m3 value nearest to the exact quotient x / s, ties to even.
 // Product: out[m, n] = sum_b sA[b, m] sB[n / 128, b] P_b[m, n],
 //   P_b[m, n] = sum over the 128 columns of block b of A8[m, k] B8[n, k].
@@ -49,7 +50,7 @@ __device__ __forceinline__ void load8(const uint16_t *p, float v[8])
 
 __device__ __forceinline__ float block_scale(float amax)
 {
-    return amax > 0.f ? fmaxf(amax / kE4m3Max, 1.17549435e-38f) : 0.f;
+    return amax > 0.f ? fmaxf(amax * (1.f / kE4m3Max), 1.17549435e-38f) : 0.f;
 }
 
 // x / s with the last bit set where the quotient is not exact, so that the
@@ -178,9 +179,11 @@ __device__ __forceinline__ f16x8 halves(uint32_t lo, uint32_t hi)
 
 // c + the product of 16 rows' 128 columns with 16 others', 32 bytes a lane.
 // The products are taken in fp16 matrix instructions, which add them in full
-// fp32: the fp8 forms align each group of eight products to its largest and
-// drop what lies 2^14 below (measured: 2e-5 of the terms' magnitudes, which
-// shows in an fp32 result).
+// fp32.  The fp8 forms align each group of eight products to its largest and
+// cut off what lies 2^13 below it (measured: 2e-5 of the terms' magnitudes,
+// 1e-4 of a typical result), which would show in an fp32 result; a bf16
+// result, rounded at 2^-8, hides it, and there the tiles for many rows use
+// them (2048 x 151936 x 4096: 1.85 ms against 2.58 in fp16).
 __device__ __forceinline__ f32x4 block_product(i32x8 a, i32x8 b, f32x4 c)
 {
     for (int i = 0; i < 8; i += 2)
@@ -214,30 +217,280 @@ __device__ __forceinline__ i32x8 join(i32x4 a, i32x4 b)
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// One wave per 16 x 16 tile of the output.  The weights are the A operand, so
-// that a lane's four results are consecutive columns of one output row.  Lane
-// l takes bytes 16 (l / 16) .. +15 of both halves of a block's 128 columns:
-// any order of the columns serves as long as both operands share it.
-template <typename O> __global__ __launch_bounds__(64) void product_simple_kernel(ProdArgs a)
+// ---------------------------------------------------------------------------
+// Few rows (M <= 16): the weights are streamed once, which bounds it.  The
+// workgroups of 4 waves stay and take every gridDim-th block of 16 weight
+// rows; each wave takes a quarter of the row block's column blocks, and the
+// waves' sums meet in LDS.  Each wave keeps kDepth column blocks (2 KiB of
+// weights each) in flight, across the row blocks' ends.  The weights are the A
+// operand, so that a lane's four results are consecutive columns of one output
+// row.  Lane l takes bytes 16 (l / 16) .. +15 of both halves of a block's 128
+// columns: any order of the columns serves as long as both operands share it.
+// The hidden states' codes lie in LDS where they fit, M K <= 64 KiB: read
+// through the caches they pass at the weights' own rate (M = 16, N = 151936,
+// K = 4096: 163 us against 138).
+// ---------------------------------------------------------------------------
+constexpr int kSkinnyM = 16, kSkinnyWaves = 4, kDepth = 4;
+constexpr int64_t kSkinnyX = 64 << 10;   // LDS for the hidden states' codes, two workgroups a compute unit
+constexpr int64_t kSkinnyGrid = 256 * 4; // workgroups: four a compute unit
+
+template <bool XL, typename O> __global__ __launch_bounds__(kSkinnyWaves * 64) void product_skinny_kernel(ProdArgs a)
 {
-    const int lane = threadIdx.x, q = lane >> 4;
-    const int64_t nt = (a.N + 15) / 16;
-    const int64_t n0 = (blockIdx.x % nt) * 16, m0 = (blockIdx.x / nt) * 16;
-    const uint8_t *w = a.B + min(n0 + (lane & 15), a.N - 1) * a.ldb;
-    const int64_t m = m0 + (lane & 15), mc = min(m, a.M - 1);
-    const uint8_t *x = a.A + mc * a.lda;
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    const int64_t nb = (a.K + kBlk - 1) / kBlk;
-    for (int64_t b = 0; b < nb; ++b) {
-        const int64_t c = b * kBlk + 16 * q;
-        const f32x4 p = block_product(join(piece(w, c, a.K), piece(w, c + 64, a.K)),
-                                      join(piece(x, c, a.K), piece(x, c + 64, a.K)), f32x4{0.f, 0.f, 0.f, 0.f});
-        const float sc = a.sA[b * a.ldsa + mc] * a.sB[n0 / kBlk * a.ldsb + b];
-        for (int i = 0; i < 4; ++i)
-            acc[i] = __builtin_fmaf(p[i], sc, acc[i]);
+    __shared__ f32x4 part[2][kSkinnyWaves][64];
+    extern __shared__ i32x4 xs[]; // XL: A's pieces [block][half][quarter][row], zeros past K
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, q = lane >> 4, r = lane & 15;
+    const int64_t nb = (a.K + kBlk - 1) / kBlk, per = (nb + kSkinnyWaves - 1) / kSkinnyWaves;
+    const int64_t nrb = (a.N + 15) / 16;
+    const int64_t m = min((int64_t)r, a.M - 1);
+    const uint8_t *x = a.A + m * a.lda;
+    if (XL) {
+        for (int64_t i = threadIdx.x; i < nb * 8 * a.M; i += kSkinnyWaves * 64)
+            xs[i] = piece(a.A + i % a.M * a.lda, i / a.M * 16, a.K);
+        __syncthreads();
     }
-    if (m < a.M)
-        put4((O *)a.out + m * a.ldo + n0 + 4 * q, acc, a.N - n0 - 4 * q);
+    struct Unit {
+        i32x4 w0, w1, x0, x1;
+        float s, sx;
+        int xb;
+    } u[kDepth];
+    // the next column block to load: number j of this wave's in row block rb
+    int64_t rb = blockIdx.x, j = 0;
+    const uint8_t *w = a.B + min(rb * 16 + r, a.N - 1) * a.ldb;
+    const float *sw = a.sB + rb / (kBlk / 16) * a.ldsb;
+    auto load = [&](Unit &v) {
+        if (rb < nrb) {
+            const int64_t b = wv * per + j, c = b * kBlk + 16 * q, bc = min(b, nb - 1);
+            v.w0 = piece(w, c, a.K);
+            v.w1 = piece(w, c + 64, a.K);
+            if (XL) {
+                v.xb = (int)bc;
+            } else {
+                v.x0 = piece(x, c, a.K);
+                v.x1 = piece(x, c + 64, a.K);
+            }
+            v.sx = a.sA[bc * a.ldsa + m];
+            v.s = b < nb ? sw[bc] : 0.f;
+            if (b >= nb)
+                v.sx = 0.f;
+            if (++j == per) {
+                j = 0;
+                rb += gridDim.x;
+                w = a.B + min(rb * 16 + r, a.N - 1) * a.ldb;
+                sw = a.sB + min(rb, nrb - 1) / (kBlk / 16) * a.ldsb;
+            }
+        }
+    };
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d)
+        load(u[d]);
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    int64_t done = 0, at = blockIdx.x;
+    int par = 0;
+    const int64_t mine = ((nrb - blockIdx.x + gridDim.x - 1) / gridDim.x) * per; // column blocks of this wave
+    for (int64_t i = 0; i < mine; i += kDepth) {
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) {
+            if (i + d < mine) {
+                if (XL) {
+                    const int at_x = (u[d].xb * 8 + q) * (int)a.M + (int)m;
+                    u[d].x0 = xs[at_x];
+                    u[d].x1 = xs[at_x + 4 * (int)a.M];
+                }
+                const f32x4 p = block_product(join(u[d].w0, u[d].w1), join(u[d].x0, u[d].x1),
+                                              f32x4{0.f, 0.f, 0.f, 0.f});
+                const float f = u[d].s * u[d].sx;
+                for (int e = 0; e < 4; ++e)
+                    acc[e] = __builtin_fmaf(p[e], f, acc[e]);
+                load(u[d]);
+                if (++done == per) { // the row block's end: the four sums in wave order
+                    part[par][wv][lane] = acc;
+                    // LDS alone has to be waited for: the loads stay in flight
+                    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+                    __builtin_amdgcn_s_barrier();
+                    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+                    // wave 0 writes; the other buffer's readers are two barriers behind
+                    if (wv == 0) {
+                        for (int v = 1; v < kSkinnyWaves; ++v)
+                            acc += part[par][v][lane];
+                        const int64_t c = at * 16 + 4 * q;
+                        if (r < a.M)
+                            put4((O *)a.out + r * a.ldo + c, acc, a.N - c);
+                    }
+                    acc = f32x4{0.f, 0.f, 0.f, 0.f};
+                    done = 0;
+                    at += gridDim.x;
+                    par ^= 1;
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: tiles of BM output rows x 256 columns, 8 waves as 2 x 4, each
+// [BM / 2 x 64].  A stage is one block of 128 columns of both operands, copied
+// straight into LDS as codes (16-byte pieces, a row's pieces exchanged by the
+// row's low bits so that the reads of eight neighbouring rows fall on
+// different banks) while the other buffer is worked on; the block's sums are
+// scaled into the accumulator in fp32.
+// ---------------------------------------------------------------------------
+constexpr int kBN = 256;
+__device__ const u32x4 kNothing = {0u, 0u, 0u, 0u}; // what a piece past K is copied from
+
+template <int BM> struct Tile {
+    static constexpr int rows = BM + kBN, codes = rows * kBlk / 4;
+    // The rows' scales lie behind the codes, but with BM = 64, where two
+    // workgroups share a compute unit's LDS only without them, in registers.
+    static constexpr bool reg = BM == 64;
+    static constexpr int words = codes + (reg ? 0 : BM);            // LDS of a stage
+    static constexpr int copies = rows / 8 / 8;                     // 1 KiB copies per wave and stage
+    static constexpr int mt = BM / 32, nt = 4;                      // 16 x 16 tiles per wave
+};
+
+template <int BM, bool F8, typename O>
+__global__ __launch_bounds__(512, BM == 64 ? 4 : 2) void product_tile_kernel(ProdArgs a)
+{
+    using T = Tile<BM>;
+    // two stage buffers, each the codes and then the rows' scales
+    __shared__ __attribute__((aligned(16))) uint32_t smem[2 * T::words];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, q = lane >> 4, r = lane & 15;
+    // Workgroup b runs on XCD b mod 8: an XCD takes every eighth column tile
+    // and all row tiles of it in turn, so that the weights pass through one L2.
+    const int64_t n_mt = (a.M + BM - 1) / BM, n_nt = (a.N + kBN - 1) / kBN;
+    const int64_t id = blockIdx.x >> 3, ni = (id / n_mt) * 8 + (blockIdx.x & 7), mi = id % n_mt;
+    if (ni >= n_nt)
+        return;
+    const int64_t m0 = mi * BM, n0 = ni * kBN;
+    const int64_t nb = (a.K + kBlk - 1) / kBlk;
+
+    // copy c of this wave: LDS rows 8 (8 c + wv) .. +7 (rows 0 .. BM-1 from A,
+    // the rest from B), lane l piece l % 8 of row l / 8
+    const int wm = (wv >> 2) * (BM / 2), wn = (wv & 3) * 64;
+    float sn[T::mt], sc[T::mt]; // T::reg: the next stage's row scales and this one's
+    auto fill = [&](int at, int64_t b) { // at: the buffer's first word
+        int l8 = lane >> 3;
+        if (BM > 128)
+            asm volatile("" : "+v"(l8)); // addresses formed anew: kept, they take 32 registers
+        const int64_t col = b * kBlk + 16 * ((lane & 7) ^ l8); // row & 7 = l8
+#pragma unroll
+        for (int c = 0; c < T::copies; ++c) {
+            const int row = 8 * (8 * c + wv) + l8;
+            const uint8_t *p = 64 * c < BM ? a.A + min(m0 + row, a.M - 1) * a.lda
+                                           : a.B + min(n0 + row - BM, a.N - 1) * a.ldb;
+            lds_dma16<false>(col < a.K ? p + col : (const uint8_t *)&kNothing, &smem[at + (8 * c + wv) * 256]);
+        }
+        if constexpr (T::reg)
+            for (int t = 0; t < T::mt; ++t)
+                sn[t] = a.sA[b * a.ldsa + min(m0 + wm + 16 * t + r, a.M - 1)];
+        else if (wv < BM / 64)
+            lds_dma4(a.sA + b * a.ldsa + min(m0 + 64 * wv + lane, a.M - 1), &smem[at + T::codes + 64 * wv]);
+    };
+    const float *sw = a.sB + min((n0 + wn) / kBlk, (a.N - 1) / kBlk) * a.ldsb;
+    // the two pieces of a lane's 32 bytes of one row
+    const int p0 = 4 * (q ^ (r & 7)), p1 = 4 * ((q + 4) ^ (r & 7));
+    const int f0 = r * 32 + p0, f1 = r * 32 + p1;
+    auto frag = [&](int at, int row) {
+        return join(*(const i32x4 *)&smem[at + f0 + row * 32], *(const i32x4 *)&smem[at + f1 + row * 32]);
+    };
+    auto row_scale = [&](int at, int t) {
+        return T::reg ? sc[t] : __uint_as_float(smem[at + T::codes + wm + 16 * t + r]);
+    };
+    f32x4 acc[T::mt][4];
+    for (int t = 0; t < T::mt; ++t)
+        for (int n = 0; n < 4; ++n)
+            acc[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // The scheduler is held to one row tile at a time: left alone it loads all
+    // tiles' operands first and spills the accumulator.
+    auto work = [&](int at, float f) {
+        float s = row_scale(at, 0) * f;
+        if constexpr (F8) {
+            i32x8 x = frag(at, wm);
+            i32x8 w[4];
+            for (int n = 0; n < 4; ++n)
+                w[n] = frag(at, BM + wn + 16 * n);
+#pragma unroll
+            for (int t = 0; t < T::mt; ++t) {
+                const i32x8 xt = x;
+                const float st = s;
+                if (t + 1 < T::mt) {
+                    x = frag(at, wm + 16 * (t + 1));
+                    s = row_scale(at, t + 1) * f;
+                }
+                f32x4 p[4];
+                for (int n = 0; n < 4; ++n)
+                    p[n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[n], xt, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0,
+                                                                            0, 0, 0, 0);
+                for (int n = 0; n < 4; ++n)
+                    for (int i = 0; i < 4; ++i)
+                        acc[t][n][i] = __builtin_fmaf(p[n][i], st, acc[t][n][i]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
+            // the operand with fewer tiles stays in registers as fp16, the
+            // other's tiles pass (all fit only that way beside the accumulator)
+            constexpr bool hold_x = T::mt < 4;
+            constexpr int nh = hold_x ? T::mt : 4, np = hold_x ? 4 : T::mt;
+            const int h0 = hold_x ? wm : BM + wn, s0 = hold_x ? BM + wn : wm;
+            f16x8 held[nh][4];
+            i32x8 next = frag(at, s0);
+            float sh[nh];
+            for (int n = 0; n < nh; ++n) {
+                const i32x8 c = frag(at, h0 + 16 * n);
+                for (int h = 0; h < 4; ++h)
+                    held[n][h] = halves(c[2 * h], c[2 * h + 1]);
+                if (hold_x)
+                    sh[n] = row_scale(at, n) * f;
+            }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int t = 0; t < np; ++t) {
+                const i32x8 c = next;
+                const float st = s;
+                if (t + 1 < np) {
+                    next = frag(at, s0 + 16 * (t + 1));
+                    if (!hold_x)
+                        s = row_scale(at, t + 1) * f;
+                }
+                f32x4 p[nh] = {};
+                for (int h = 0; h < 4; ++h) {
+                    const f16x8 y = halves(c[2 * h], c[2 * h + 1]);
+                    for (int n = 0; n < nh; ++n)
+                        p[n] = hold_x ? __builtin_amdgcn_mfma_f32_16x16x32_f16(y, held[n][h], p[n], 0, 0, 0)
+                                      : __builtin_amdgcn_mfma_f32_16x16x32_f16(held[n][h], y, p[n], 0, 0, 0);
+                }
+                for (int n = 0; n < nh; ++n)
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (hold_x)
+                            acc[n][t][i] = __builtin_fmaf(p[n][i], sh[n], acc[n][t][i]);
+                        else
+                            acc[t][n][i] = __builtin_fmaf(p[n][i], st, acc[t][n][i]);
+                    }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    };
+    fill(0, 0);
+    for (int64_t b = 0; b < nb; ++b) {
+        const int cur = (b & 1) * T::words;
+        const float f = sw[b];
+        wait_vm_all();
+        __syncthreads(); // this stage is filled, and everyone is done with the other buffer
+        if constexpr (T::reg)
+            for (int t = 0; t < T::mt; ++t)
+                sc[t] = sn[t];
+        if (b + 1 < nb)
+            fill(T::words - cur, b + 1);
+        work(cur, f);
+    }
+    for (int t = 0; t < T::mt; ++t) {
+        const int64_t m = m0 + wm + 16 * t + r;
+        for (int n = 0; n < 4; ++n) {
+            const int64_t c = n0 + wn + 16 * n + 4 * q;
+            if (m < a.M)
+                put4((O *)a.out + m * a.ldo + c, acc[t][n], a.N - c);
+        }
+    }
 }
 
 archead_status launched(const char *what)
@@ -249,6 +502,38 @@ archead_status launched(const char *what)
 }
 
 bool bad_rows(const void *p, int64_t ld, int64_t cols) { return (uintptr_t)p % 16 || ld % 16 || ld < cols; }
+
+template <typename O> void run_skinny(const ProdArgs &a, hipStream_t st)
+{
+    const dim3 grid((unsigned)std::min<int64_t>((a.N + 15) / 16, kSkinnyGrid));
+    const int64_t lds = (a.K + kBlk - 1) / kBlk * kBlk * a.M;
+    if (lds <= kSkinnyX)
+        hipLaunchKernelGGL((product_skinny_kernel<true, O>), grid, dim3(kSkinnyWaves * 64), (size_t)lds, st, a);
+    else
+        hipLaunchKernelGGL((product_skinny_kernel<false, O>), grid, dim3(kSkinnyWaves * 64), 0, st, a);
+}
+
+template <int BM, typename O> void run_tile(const ProdArgs &a, hipStream_t st)
+{
+    const int64_t n_mt = (a.M + BM - 1) / BM, n_nt = (a.N + kBN - 1) / kBN;
+    const dim3 grid((unsigned)((n_nt + 7) / 8 * 8 * n_mt));
+    hipLaunchKernelGGL((product_tile_kernel<BM, sizeof(O) == 2 && (BM > 64), O>), grid, dim3(512), 0, st, a);
+}
+
+template <typename O> archead_status run_product(const ProdArgs &a, hipStream_t st)
+{
+    if (((a.N + kBN - 1) / kBN + 8) * ((a.M + 63) / 64) >= int64_t(1) << 31)
+        return api_fail(ARCHEAD_ESHAPE, "product too large");
+    if (a.M <= kSkinnyM)
+        run_skinny<O>(a, st);
+    else if (a.M <= 64)
+        run_tile<64, O>(a, st);
+    else if (a.M <= 256 || sizeof(O) == 4)
+        run_tile<128, O>(a, st);
+    else if constexpr (sizeof(O) == 2)
+        run_tile<256, O>(a, st);
+    return launched("archead_fp8_matmul");
+}
 
 } // namespace
 } // namespace archead
@@ -322,12 +607,7 @@ extern "C" archead_status archead_fp8_matmul(int64_t M, int64_t N, int64_t K, co
         return api_fail(ARCHEAD_EINVAL, "out must be aligned to its element");
     hipStream_t st = (hipStream_t)hip_stream;
     const ProdArgs a{M, N, K, lda, ldb, ldo, ldsa, ldsb, A, B, sA, sB, out};
-    const int64_t tiles = (M + 15) / 16 * ((N + 15) / 16);
-    if (tiles >= (int64_t(1) << 31))
-        return api_fail(ARCHEAD_ESHAPE, "product too large");
     if (out_type == ARCHEAD_F32)
-        hipLaunchKernelGGL(product_simple_kernel<float>, dim3((unsigned)tiles), dim3(64), 0, st, a);
-    else
-        hipLaunchKernelGGL(product_simple_kernel<uint16_t>, dim3((unsigned)tiles), dim3(64), 0, st, a);
-    return launched("archead_fp8_matmul");
+        return run_product<float>(a, st);
+    return run_product<uint16_t>(a, st);
 }

@@ -4,7 +4,11 @@ The quantiser is exact: equal codes and scales.  The product sums n = K terms
 in fp32 in some order, each addition rounded or truncated (2^-23 of what has
 been added so far, at most the sum of the terms' magnitudes), and takes three
 roundings per block for the scales: |error| <= (K + 8) 2^-23 sum |terms|,
-and half a step of the output's type.
+and half a step of the output's type.  With more than 64 rows and a bf16
+result the products are formed by the fp8 matrix instruction, which aligns
+each group of eight to its largest and cuts the others off at 2^-13 of it: a
+group loses less than 7 2^-13 of its largest term, so all of them lose at most
+7 2^-13 sum |terms|.
 """
 import numpy as np
 import pytest
@@ -14,6 +18,11 @@ from oracle import fp8
 
 pytestmark = pytest.mark.gpu
 HALF = {"float32": 2.0 ** -24, "bfloat16": 2.0 ** -8}
+
+
+def tolerance(M, K, dtype, want, terms):
+    cut = 7 * 2.0 ** -13 if dtype == "bfloat16" and M > 64 else 0.0
+    return ((K + 8) * 2.0 ** -23 + cut) * terms + HALF[dtype] * np.abs(want)
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -126,7 +135,7 @@ def test_product(M, N, K, dtype):
     got = fp8_matmul(ta, dev(sa), tb, dev(sb), out=buf[:, :N])
     assert (buf[:, N:] == 7.0).all()
     err = np.abs(got.double().cpu().numpy() - want)
-    tol = (K + 8) * 2.0 ** -23 * terms + HALF[dtype] * np.abs(want)
+    tol = tolerance(M, K, dtype, want, terms)
     assert (err <= tol).all(), (err / tol).max()
     again = fp8_matmul(ta, dev(sa), tb, dev(sb), out_dtype=getattr(torch, dtype))
     assert torch.equal(again, got)
