@@ -353,6 +353,47 @@ typedef enum archead_type {
 } archead_type;
 
 /*
+ * archead_reserve_backward -- prepare a handle for archead_backward: the
+ * packed codes are laid out a second time on the device, by vocabulary rows
+ * (about the packed head's size again, 1.3 times at d / g = 32), and a
+ * workspace for M_max rows at a time is allocated (at most 2048; a call with
+ * more goes in parts).  Waits until both are ready.  Called again it only ever
+ * enlarges the workspace; calls of archead_backward on the handle that are
+ * still running elsewhere must have ended then.
+ * M_max < 1 -> ARCHEAD_EINVAL; M_max > 2^20, or a head whose second layout
+ * passes 2^31 KiB -> ARCHEAD_ESHAPE; a stream being captured -> ARCHEAD_EINVAL;
+ * no memory -> ARCHEAD_ENOMEM, with the handle as it was.  archead_device_bytes
+ * counts both; archead_free releases them.
+ */
+archead_status archead_reserve_backward(archead_t h, int64_t M_max, void *hip_stream);
+
+/*
+ * archead_backward -- the gradient of a loss by the hidden states, through the
+ * frozen head: with G = dlogits (for instance of archead_policy_loss) and
+ * W_hat of eq 6,
+ *   dX[m, j] = sum_v G[m, v] W_hat[v, j],
+ * evaluated factored, like the forward.  archead_reserve_backward first, else
+ * ARCHEAD_EINVAL.
+ *
+ * M        0 <= M <= 2^20 rows (0 is a no-op that succeeds).
+ * dlogits  DEVICE M x V, fp32 or bf16 (type), row stride ld >= V elements,
+ *          aligned to its element.
+ * dX       DEVICE bf16, M x d row-major, written in full.
+ * Numerics: row m of G enters as fp16, scaled by a power of two that puts its
+ * largest entry into [2^14, 2^15) (bf16 entries within 2^28 of it exactly, fp32
+ * ones rounded to 11 bits); the residual's and the low-rank codes times their
+ * scales are rounded once to fp16; sums are fp32; the low-rank factors T, U
+ * enter their second product with 16 significant bits; dX is rounded once.
+ * A NaN or infinity in row m of G makes row m of dX NaN and no other.
+ * Enqueued on hip_stream, not waited for; nothing is allocated, so the call can
+ * be captured.  The calls of one handle share its backward workspace: enqueue
+ * them (and replay graphs that hold them) on one stream, or order them with
+ * events.  It is another workspace than the forward's.
+ */
+archead_status archead_backward(archead_t h, int64_t M, const void *dlogits, int type, int64_t ld, void *dX,
+                                void *hip_stream);
+
+/*
  * Post-training losses over logits (M rows of V logits, row stride ld
  * elements, fp32 or bf16): what the head's logits go into when a model is
  * scored or trained on its own answers.  With top = max_v y[v],

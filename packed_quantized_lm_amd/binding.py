@@ -53,6 +53,8 @@ SIGNATURES = {
                                             _VP]),
     "archead_fp8_matmul": (ctypes.c_int, [_I64] * 3 + [_VP, _I64, _VP, _I64, _VP, _I64, _VP, _I64, _VP, ctypes.c_int,
                                                        _I64, _VP]),
+    "archead_reserve_backward": (ctypes.c_int, [_VP, _I64, _VP]),
+    "archead_backward": (ctypes.c_int, [_VP, _I64, _VP, ctypes.c_int, _I64, _VP, _VP]),
     "archead_packed_bytes": (ctypes.c_int, [_VP, ctypes.POINTER(ctypes.c_uint64)]),
     "archead_device_bytes": (ctypes.c_int, [_VP, ctypes.POINTER(ctypes.c_uint64)]),
     "archead_free": (ctypes.c_int, [_VP]),
@@ -331,6 +333,32 @@ class PackedHead:
         argmax = torch.empty((M,), dtype=torch.int32, device=X.device) if want_argmax else None
         self.forward_into(X, logits, argmax, path=path, stream=stream)
         return logits, argmax
+
+    def reserve_backward(self, M_max: int, stream=None):
+        """Prepare backward() for up to M_max rows at a time (archead_reserve_backward)."""
+        _check(load_library().archead_reserve_backward(self.handle, int(M_max), _stream_handle(stream)),
+               "archead_reserve_backward")
+
+    def backward(self, dlogits, dX=None, stream=None):
+        """dX = dlogits W_hat, bf16 M x d: the gradient by the hidden states of a
+        loss whose gradient by the logits (fp32 or bf16 M x V, rows may be
+        strided) is dlogits.  reserve_backward first."""
+        import torch
+        from .losses import _type_code, need_rows, on_stream, ptr
+        if not isinstance(dlogits, torch.Tensor) or dlogits.dim() != 2 or dlogits.shape[1] != self.V:
+            raise ValueError(f"dlogits must be an M x {self.V} tensor")
+        dev, M = dlogits.device, int(dlogits.shape[0])
+        code = _type_code(dlogits.dtype, "dlogits")
+        ld = need_rows(dlogits, "dlogits", (dlogits.dtype,), (M, self.V), dev)
+        if dX is not None:
+            _need(dX, "dX", (torch.bfloat16,), (M, self.d), dev)
+
+        def call(st):
+            out = torch.empty((M, self.d), dtype=torch.bfloat16, device=dev) if dX is None else dX
+            _check(load_library().archead_backward(self.handle, M, ptr(dlogits), code, ld, ptr(out), st),
+                   "archead_backward")
+            return out
+        return on_stream(dev, stream, call)
 
     def close(self):
         if self._h is not None:

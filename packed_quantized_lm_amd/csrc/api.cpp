@@ -61,6 +61,7 @@ struct archead_head {
     size_t ws_bytes;
     int64_t ws_M;       // largest M the workspace holds
     int device;
+    BackwardState *bw;  // null until archead_reserve_backward
 };
 
 namespace {
@@ -254,6 +255,16 @@ archead_status handle_device(archead_t h, int *device)
     return ARCHEAD_OK;
 }
 
+archead_status backward_slot(archead_t h, const DevHead **dev, BackwardState ***slot, int *device)
+{
+    const archead_status st = handle_device(h, device);
+    if (st != ARCHEAD_OK)
+        return st;
+    *dev = &h->dev;
+    *slot = &h->bw;
+    return ARCHEAD_OK;
+}
+
 size_t workspace_bytes(archead_t h, int64_t M, size_t *zero_head, size_t *zero_tail)
 {
     const WsLayout L = ws_layout(h->s, std::max<int64_t>(M, 1));
@@ -385,6 +396,7 @@ archead_status archead_pack_load(int64_t V, int64_t d, int64_t k, int64_t r, int
     h->ws_bytes = 0;
     h->ws_M = 0;
     h->device = dev;
+    h->bw = nullptr;
     st = grow_workspace(h, 1, stream);
     if (st == ARCHEAD_OK && hipStreamSynchronize(stream) != hipSuccess)
         st = fail(ARCHEAD_EHIP, "workspace set-up did not complete");
@@ -657,7 +669,7 @@ archead_status archead_device_bytes(archead_t h, uint64_t *bytes)
     g_err.clear();
     if (!live(h) || !bytes)
         return fail(ARCHEAD_EINVAL, "invalid handle or NULL output");
-    *bytes = h->block_bytes + h->ws_bytes;
+    *bytes = h->block_bytes + h->ws_bytes + backward_bytes(h->bw);
     return ARCHEAD_OK;
 }
 
@@ -678,6 +690,7 @@ archead_status archead_free(archead_t h)
         (void)hipFree(h->ws);
     if (h->block)
         (void)hipFree(h->block);
+    backward_release(h->bw);
     h->magic = 0;
     delete h;
     if (e != hipSuccess)

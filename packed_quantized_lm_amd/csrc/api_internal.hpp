@@ -1,6 +1,7 @@
 // api_internal.hpp -- what api.cpp lends to the other host-side entry points
 // of the library (the no-allocation forward in noalloc.hip, the construction
-// in build.hip).
+// in build.hip, the backward in backward.hip, the losses in loss.hip and the
+// 8-bit head in fp8.hip).
 #pragma once
 #include <string>
 
@@ -15,6 +16,16 @@ archead_status api_fail(archead_status s, const std::string &msg);
 // device allocation of the library larger than that is refused (the caller
 // reports ARCHEAD_ENOMEM, as for a failed hipMalloc) before any HIP call.
 bool alloc_refused(size_t bytes);
+
+// What archead_backward keeps on a handle: the codes laid out a second time and
+// its workspace (backward.hip).  Null until archead_reserve_backward.
+struct BackwardState;
+struct DevHead;
+void backward_release(BackwardState *b);
+size_t backward_bytes(const BackwardState *b);
+// ARCHEAD_OK, the handle's device view, where it keeps that state, and its
+// device; or ARCHEAD_EINVAL for a bad handle
+archead_status backward_slot(archead_t h, const DevHead **dev, BackwardState ***slot, int *device);
 
 // ARCHEAD_OK and the device the handle lives on, or ARCHEAD_EINVAL for a bad handle
 archead_status handle_device(archead_t h, int *device);

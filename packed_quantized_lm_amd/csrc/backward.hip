@@ -1,0 +1,842 @@
+// backward.hip -- the packed head's gradient by its hidden states,
+//   dX[m, j] = sum_v G[m, v] W_hat[v, j],   G = dlogits,
+// with W_hat in its stored fields (eq 6 and the text after eq 7 of the
+// ARCHead paper; the head itself is frozen), again without a dense W_hat:
+//   dX = G (sR o R4) + (T sB) B8 + sum_grp (U sD_grp) D8_grp,
+//   T = G (sA o A5),  U = G (sC o C8).
+//
+// Everything that sums over the vocabulary is one kind of product: rows of G
+// against 4-bit codes with a scale per (v, 32 columns).  R4 is that already; a
+// 5-bit core code a = 2 h + b and an 8-bit correction code c = 16 h + l are
+// two such columns each.  The codes are laid out a second time, eight
+// vocabulary rows of one column to a dword (the forward's layout holds eight
+// columns of one row), so that a dword is one lane's matrix operand.
+//
+//   amax, convert  G 2^f_m as fp16 rows, f_m putting row m's largest entry
+//                  into [2^14, 2^15): exact for bf16 G within 2^28 of it
+//   tile kernel    [BM rows x 256 columns] over a range of the vocabulary,
+//                  first for the columns of T and U, then for dX's
+//   sums           T sB and U from their ranges, fp32
+//   finish         dX's ranges + the products with B8 and D8, one rounding
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <new>
+#include <string>
+
+#include "api_internal.hpp"
+#include "archead.h"
+#include "device.hpp"
+
+namespace archead {
+namespace {
+
+constexpr int kVC = 128;    // vocabulary rows per stage ("chunk")
+constexpr int kJT = 256;    // columns per tile
+constexpr int kUnit = 32;   // columns that share a scale
+constexpr int64_t kChunkM = 2048; // most rows of G held at a time
+
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint16_t u16x8u __attribute__((ext_vector_type(8), aligned(2)));
+typedef uint16_t u16x4u __attribute__((ext_vector_type(4), aligned(2)));
+
+// Columns of the second layout: dX's d columns, then the tile-aligned columns
+// of T and U by units of 32: kst units of h and kst of b for the core, rst of
+// h and rst of l for the correction.
+struct Cols {
+    int64_t d, kst, rst;
+    __host__ __device__ int64_t main_tiles() const { return (d + kJT - 1) / kJT; }
+    __host__ __device__ int64_t low_units() const { return 2 * (kst + rst); }
+    __host__ __device__ int64_t low_tiles() const { return (low_units() * kUnit + kJT - 1) / kJT; }
+    __host__ __device__ int64_t tiles() const { return main_tiles() + low_tiles(); }
+};
+Cols cols_of(const Shape &s) { return Cols{s.d, s.kst(), s.rst()}; }
+
+// ---------------------------------------------------------------------------
+// The second layout (once per head)
+//   codes uint32 [chunk][tile * 16 + block][64 lanes][4]: lane l holds column
+//         l % 16 of the 16-column block, dword s the chunk's rows
+//         32 s + 8 (l / 16) + e, e = 0 .. 7, offset binary, in the nibble order
+//         of the first layout
+//   sc    fp16 [chunk][tile * 8 + unit][128 rows], scale 2^E, the exponents E
+//         (ex: residual, core, correction) putting the field's largest scaled
+//         value below 2^15
+//   b8t, d8t  int8 [d][kpad], [d][rpad]: B8 and D8 by columns
+// ---------------------------------------------------------------------------
+struct Layout {
+    DevHead h;
+    Cols c;
+    int64_t nvc;
+    uint32_t *codes;
+    uint16_t *sc;
+    int8_t *b8t, *d8t;
+    uint32_t *peak; // largest |sR|, |sA|, |sC| as fp32 bits
+    int32_t *ex;
+};
+
+__global__ __launch_bounds__(256) void peak_kernel(Layout a)
+{
+    const int which = blockIdx.y;
+    const uint16_t *p = which == 0 ? a.h.sr : which == 1 ? a.h.sa : a.h.sc;
+    const int64_t n = which == 0 ? (int64_t)a.h.s.n_sr() : (int64_t)a.h.s.n_rows();
+    float m = 0.f;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const float f = fabsf(h2f(p[i]));
+        m = f <= 65504.f ? fmaxf(m, f) : m; // NaN and Inf scales only propagate
+    }
+    for (int off = 32; off >= 1; off >>= 1)
+        m = fmaxf(m, __shfl_xor(m, off));
+    if ((threadIdx.x & 63) == 0)
+        atomicMax(a.peak + which, __float_as_uint(m)); // any order gives the same maximum
+}
+
+__global__ void exponent_kernel(Layout a)
+{
+    const int w = threadIdx.x;
+    if (w >= 3)
+        return;
+    const float m = __uint_as_float(a.peak[w]) * (w == 0 ? 1.f : w == 1 ? 2.f : 16.f);
+    a.ex[w] = m > 0.f ? 11 - ilogbf(m) : 0; // scales below 2^12, codes up to 8 times that
+}
+
+// residual code (offset binary) of row v, column j in the first layout
+__device__ __forceinline__ uint32_t r4_code(const DevHead &h, int64_t v, int64_t j)
+{
+    const int64_t lane = (v & 15) + 16 * ((j >> 3) & 3);
+    const uint32_t w = h.r4[(((j >> 7) * h.s.nvb() + (v >> 4)) * 64 + lane) * 4 + ((j >> 5) & 3)];
+    const int e = (int)(j & 7);
+    return w >> (4 * ((e >> 1) + 4 * (e & 1))) & 15u;
+}
+// core code + 16, correction code + 128
+__device__ __forceinline__ uint32_t a5_code(const DevHead &h, int64_t v, int64_t i)
+{
+    const int64_t ks = i >> 5, q = ks % 3, lane = (v & 15) + 16 * ((i >> 3) & 3);
+    const uint32_t *c = h.lr + (((ks / 3) * h.s.nvb() + (v >> 4)) * 64 + lane) * 4;
+    const int e = (int)(i & 7);
+    const uint32_t nib = c[q] >> (4 * ((e >> 1) + 4 * (e & 1))) & 15u;
+    return nib | (c[3] >> ((4 + 4 * q + (e >> 1) + 16 * (e & 1)) & 31) & 1u) << 4;
+}
+__device__ __forceinline__ uint32_t c8_code(const DevHead &h, int64_t v, int64_t i)
+{
+    const int64_t ks = i >> 5, lane = (v & 15) + 16 * ((i >> 3) & 3);
+    const uint32_t *c = h.lr + (((h.s.lr_na() + ks / 2) * h.s.nvb() + (v >> 4)) * 64 + lane) * 4;
+    return c[2 * (ks & 1) + ((i >> 2) & 1)] >> (8 * (i & 3)) & 255u;
+}
+
+// what a column of the low-rank tiles stands for: part 0 / 1 the core's h / b,
+// 2 / 3 the correction's h / l, -1 padding; i the factor's column
+__device__ __forceinline__ int low_part(const Cols &c, int64_t unit)
+{
+    return unit < c.kst ? 0 : unit < 2 * c.kst ? 1 : unit < 2 * c.kst + c.rst ? 2 : unit < c.low_units() ? 3 : -1;
+}
+__device__ __forceinline__ int64_t low_first(const Cols &c, int part)
+{
+    return part == 0 ? 0 : part == 1 ? c.kst : part == 2 ? 2 * c.kst : 2 * c.kst + c.rst;
+}
+
+// one dword of codes per thread
+__global__ __launch_bounds__(256) void codes_kernel(Layout a, int64_t nblk)
+{
+    const int64_t vc = blockIdx.x / nblk, blk = blockIdx.x % nblk; // chunk, 16-column block
+    const int lane = threadIdx.x >> 2, s = threadIdx.x & 3;
+    const int64_t j = blk * 16 + (lane & 15), main = a.c.main_tiles() * kJT;
+    int part = 4; // residual
+    int64_t i = j;
+    if (j >= main) {
+        const int64_t unit = (j - main) / kUnit;
+        part = low_part(a.c, unit);
+        i = part < 0 ? 0 : (unit - low_first(a.c, part)) * kUnit + (j & 31);
+    }
+    uint32_t w = 0;
+    for (int e = 0; e < 8; ++e) {
+        const int64_t v = vc * kVC + 32 * s + 8 * (lane >> 4) + e;
+        uint32_t u = 8;
+        if (v < a.h.s.nvb() * kVB) { // the first layout's padding rows hold codes of zero
+            if (part == 4)
+                u = j < a.h.s.d ? r4_code(a.h, v, j) : 8u;
+            else if (part == 0)
+                u = a5_code(a.h, v, i) >> 1; // (a + 16) / 2 = h + 8
+            else if (part == 1)
+                u = a5_code(a.h, v, i) & 1u; // b, without an offset
+            else if (part == 2)
+                u = c8_code(a.h, v, i) >> 4; // (c + 128) / 16 = h + 8
+            else if (part == 3)
+                u = c8_code(a.h, v, i) & 15u; // l, without an offset
+        }
+        w |= u << (4 * ((e >> 1) + 4 * (e & 1)));
+    }
+    a.codes[((vc * a.c.tiles() * 16 + blk) * 64 + lane) * 4 + s] = w;
+}
+
+__global__ __launch_bounds__(128) void scales_kernel(Layout a, int64_t nunit)
+{
+    const int64_t vc = blockIdx.x / nunit, unit = blockIdx.x % nunit, v = vc * kVC + threadIdx.x;
+    const int64_t main = a.c.main_tiles() * (kJT / kUnit);
+    float f = 0.f;
+    if (v < a.h.s.V) {
+        if (unit < main) {
+            if (unit * kUnit < a.h.s.d)
+                f = ldexpf(h2f(a.h.sr[((v >> 4) * a.h.s.G() + unit * kUnit / a.h.s.g) * kVB + (v & 15)]), a.ex[0]);
+        } else {
+            const int part = low_part(a.c, unit - main);
+            if (part == 0 || part == 1)
+                f = ldexpf(h2f(a.h.sa[v]), a.ex[1] + (part == 0 ? 1 : 0));
+            else if (part == 2 || part == 3)
+                f = ldexpf(h2f(a.h.sc[v]), a.ex[2] + (part == 2 ? 4 : 0));
+        }
+    }
+    a.sc[(vc * a.c.tiles() * (kJT / kUnit) + unit) * kVC + threadIdx.x] =
+        __builtin_bit_cast(uint16_t, (_Float16)f);
+}
+
+__global__ __launch_bounds__(256) void columns_kernel(const int8_t *x, int64_t rows, int64_t d, int64_t pad, int8_t *out)
+{
+    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < d * pad; t += (int64_t)gridDim.x * 256) {
+        const int64_t j = t / pad, i = t % pad;
+        out[t] = i < rows ? x[i * d + j] : (int8_t)0;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// G 2^f_m as fp16
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void load8(const float *p, float v[8])
+{
+    const f32x4u a = *(const f32x4u *)p, b = *(const f32x4u *)(p + 4);
+    for (int i = 0; i < 4; ++i) {
+        v[i] = a[i];
+        v[4 + i] = b[i];
+    }
+}
+__device__ __forceinline__ void load8(const uint16_t *p, float v[8])
+{
+    const u16x8u a = *(const u16x8u *)p;
+    for (int i = 0; i < 8; ++i)
+        v[i] = __uint_as_float((uint32_t)a[i] << 16);
+}
+__device__ __forceinline__ float load1(const float *p) { return *p; }
+__device__ __forceinline__ float load1(const uint16_t *p) { return __uint_as_float((uint32_t)*p << 16); }
+
+struct GArgs {
+    const void *g;
+    int64_t M, V, ld, Vp;  // Vp: V rounded up to chunks
+    int64_t S, slice;      // slices of a row
+    float *amax;           // [M][S]
+    uint16_t *g16;         // [M][Vp]
+    float *unscale;        // [M] 2^-f_m
+};
+
+template <typename T> __device__ __forceinline__ void load8_edge(const T *row, int64_t v, int64_t V, float x[8])
+{
+    if (v + 8 <= V) {
+        load8(row + v, x);
+        return;
+    }
+    for (int i = 0; i < 8; ++i)
+        x[i] = v + i < V ? load1(row + v + i) : 0.f;
+}
+
+template <typename T> __global__ __launch_bounds__(256) void amax_kernel(GArgs a)
+{
+    __shared__ float red[4];
+    const int64_t m = blockIdx.x / a.S, sl = blockIdx.x % a.S;
+    const T *row = (const T *)a.g + m * a.ld;
+    float mx = 0.f;
+    const int64_t end = min((sl + 1) * a.slice, a.V);
+    for (int64_t v = sl * a.slice + 8 * threadIdx.x; v < end; v += 256 * 8) {
+        float x[8];
+        load8_edge(row, v, a.V, x);
+        for (int i = 0; i < 8; ++i)
+            mx = fmaxf(mx, fabsf(x[i]));
+    }
+    for (int off = 32; off >= 1; off >>= 1)
+        mx = fmaxf(mx, __shfl_xor(mx, off));
+    if ((threadIdx.x & 63) == 0)
+        red[threadIdx.x >> 6] = mx;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        a.amax[blockIdx.x] = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+}
+
+template <typename T> __global__ __launch_bounds__(256) void convert_kernel(GArgs a)
+{
+    const int64_t m = blockIdx.x / a.S, sl = blockIdx.x % a.S;
+    const T *row = (const T *)a.g + m * a.ld;
+    float mx = 0.f;
+    for (int64_t i = 0; i < a.S; ++i)
+        mx = fmaxf(mx, a.amax[m * a.S + i]);
+    int f = 0;
+    if (mx > 0.f && mx <= 3.4028235e38f) {
+        f = 14 - ilogbf(mx);
+        f = f > 126 ? 126 : f;
+    }
+    if (sl == 0 && threadIdx.x == 0)
+        a.unscale[m] = ldexpf(1.f, -f);
+    const float up = ldexpf(1.f, f);
+    uint16_t *out = a.g16 + m * a.Vp;
+    const int64_t end = min((sl + 1) * a.slice, a.Vp);
+    for (int64_t v = sl * a.slice + 8 * threadIdx.x; v < end; v += 256 * 8) {
+        float x[8];
+        load8_edge(row, v, a.V, x);
+        f16x8 o;
+        for (int i = 0; i < 8; ++i)
+            o[i] = (_Float16)(x[i] * up);
+        *(f16x8 *)(out + v) = o;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// tile kernel
+// ---------------------------------------------------------------------------
+struct TileArgs {
+    const uint16_t *g16;
+    const float *unscale;
+    const uint32_t *codes;
+    const uint16_t *sc;
+    const int32_t *ex;
+    int64_t M, Vp, nvc, tiles; // tiles: of the whole layout
+    int64_t t0, n_jt, n_mt, S; // this launch: first tile, column tiles, row tiles, vocabulary ranges
+    Cols c;
+    int low;                   // the tiles of T and U
+    float *part;               // [S][M][n_jt * 256]
+};
+
+// Eight codes of a lane as fp16 q S: the codes spliced into 1024 + u (and
+// 1024 + 16 u), exact integers after one add (one fma), one rounding in the
+// product with the scales.  off0 = -(1024 + offset), off1 = -(64 + offset).
+__device__ __forceinline__ f16x8 dequant(uint32_t w, u32x4 s, uint32_t magic, f16x2 off0, f16x2 off1)
+{
+    const f16x2 sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
+    const uint32_t w8 = w >> 8;
+    auto h = [](uint32_t x) { return __builtin_bit_cast(f16x2, x); };
+    const f16x2 a = (h((w & 0x000F000Fu) | magic) + off0) * h(s.x);
+    const f16x2 b = __builtin_elementwise_fma(h((w & 0x00F000F0u) | magic), sixteenth, off1) * h(s.y);
+    const f16x2 c = (h((w8 & 0x000F000Fu) | magic) + off0) * h(s.z);
+    const f16x2 d = __builtin_elementwise_fma(h((w8 & 0x00F000F0u) | magic), sixteenth, off1) * h(s.w);
+    return f16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+template <int BM> struct BTile {
+    static constexpr int wm = BM == 128 ? 2 : 1, wj = 8 / wm;      // waves along rows and columns
+    static constexpr int mt = BM / wm / 16, jb = kJT / wj / 16;    // 16 x 16 tiles per wave
+    static constexpr int gw = BM * kVC / 2, cw = 16 * 256, sw = 8 * kVC / 2; // words of a stage: G, codes, scales
+    static constexpr int words = gw + cw + sw;
+};
+
+template <int BM> __global__ __launch_bounds__(512) void tile_kernel(TileArgs a)
+{
+    using T = BTile<BM>;
+    __shared__ __attribute__((aligned(16))) uint32_t smem[2 * T::words];
+    const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // Workgroup b runs on XCD b mod 8; an XCD takes a contiguous run of
+    // (range, row tile, column tile), column tiles fastest, so that the rows
+    // of G pass through one L2 for all column tiles.
+    const int64_t total = a.S * a.n_mt * a.n_jt, per = (total + 7) / 8;
+    const int64_t id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((int64_t)(blockIdx.x >> 3) >= per || id >= total)
+        return;
+    const int64_t jt = id % a.n_jt, mi = id / a.n_jt % a.n_mt, sp = id / a.n_jt / a.n_mt;
+    const int64_t m0 = mi * BM, tile = a.t0 + jt;
+    const int64_t c0 = a.nvc * sp / a.S, c1 = a.nvc * (sp + 1) / a.S;
+    const int wm0 = wv / T::wj * (BM / T::wm), wj0 = wv % T::wj * T::jb; // first row, first 16-column block
+
+    auto fill = [&](int at, int64_t vc) {
+        // G: 1 KiB copies of 4 rows x 256 bytes, 16-byte pieces exchanged by
+        // the row's low bits so that eight rows' reads fall on different banks
+#pragma unroll
+        for (int c = 0; c < BM / 32; ++c) {
+            const int row = 4 * (8 * c + wv) + q;
+            const uint16_t *p = a.g16 + min(m0 + row, a.M - 1) * a.Vp + vc * kVC + 8 * (r ^ (row & 7));
+            lds_dma16<false>(p, &smem[at + (8 * c + wv) * 256]);
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            lds_dma16<false>(a.codes + ((vc * a.tiles + tile) * 16 + 8 * c + wv) * 256 + lane * 4,
+                             &smem[at + T::gw + (8 * c + wv) * 256]);
+        if (wv < 2)
+            lds_dma16<false>(a.sc + ((vc * a.tiles + tile) * 8 + 4 * wv) * kVC + lane * 8,
+                             &smem[at + T::gw + T::cw + wv * 256]);
+    };
+    const uint32_t magic = vgpr_const(kF16Magic);
+    // offset-binary codes but for the low parts of core and correction
+    f16x2 off0[T::jb / 2], off1[T::jb / 2];
+    for (int u = 0; u < T::jb / 2; ++u) {
+        const int part = a.low ? low_part(a.c, jt * 8 + (wj0 >> 1) + u) : 0;
+        const float o = part == 1 || part == 3 ? 0.f : 8.f;
+        off0[u] = f16x2{(_Float16)(-1024.f - o), (_Float16)(-1024.f - o)};
+        off1[u] = f16x2{(_Float16)(-64.f - o), (_Float16)(-64.f - o)};
+    }
+    f32x4 acc[T::mt][T::jb];
+    for (int t = 0; t < T::mt; ++t)
+        for (int n = 0; n < T::jb; ++n)
+            acc[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    auto work = [&](int at) {
+        u32x4 c[T::jb];
+        for (int n = 0; n < T::jb; ++n)
+            c[n] = *(const u32x4 *)&smem[at + T::gw + (wj0 + n) * 256 + lane * 4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            f16x8 w[T::jb];
+            for (int u = 0; u < T::jb / 2; ++u) {
+                const u32x4 sc = *(const u32x4 *)&smem[at + T::gw + T::cw + ((wj0 >> 1) + u) * (kVC / 2) + 16 * s + 4 * q];
+                w[2 * u] = dequant(c[2 * u][s], sc, magic, off0[u], off1[u]);
+                w[2 * u + 1] = dequant(c[2 * u + 1][s], sc, magic, off0[u], off1[u]);
+            }
+            for (int t = 0; t < T::mt; ++t) {
+                const int row = wm0 + 16 * t + r; // row & 7 = r & 7
+                const f16x8 g = *(const f16x8 *)&smem[at + row * (kVC / 2) + 4 * ((4 * s + q) ^ (r & 7))];
+                for (int n = 0; n < T::jb; ++n)
+                    acc[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[n], g, acc[t][n], 0, 0, 0);
+            }
+        }
+    };
+    if (c0 < c1)
+        fill(0, c0);
+    for (int64_t vc = c0; vc < c1; ++vc) {
+        const int cur = (vc - c0) & 1 ? T::words : 0;
+        wait_vm_all();
+        __syncthreads(); // this stage is filled, and everyone is done with the other buffer
+        if (vc + 1 < c1)
+            fill(T::words - cur, vc + 1);
+        work(cur);
+    }
+    // lane: row m = r of each row tile, four consecutive columns
+    for (int n = 0; n < T::jb; ++n) {
+        const int part = a.low ? low_part(a.c, jt * 8 + ((wj0 + n) >> 1)) : 4;
+        const float down = ldexpf(1.f, -a.ex[part == 4 ? 0 : part <= 1 ? 1 : 2]);
+        for (int t = 0; t < T::mt; ++t) {
+            const int64_t m = m0 + wm0 + 16 * t + r;
+            if (m < a.M) {
+                f32x4 o = acc[t][n];
+                const float un = a.unscale[m];
+                for (int i = 0; i < 4; ++i)
+                    o[i] = o[i] * down * un;
+                *(f32x4 *)(a.part + (sp * a.M + m) * a.n_jt * kJT + jt * kJT + (wj0 + n) * 16 + 4 * q) = o;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// T sB and U: the ranges' sums of the two halves of every column
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void low_sum_kernel(const float *part, int64_t M, int64_t S, Cols c, int64_t k,
+                                                      int64_t r, const float *sb, float *tu)
+{
+    const int64_t kp = c.kst * kUnit, rp = c.rst * kUnit, w = kp + rp, pitch = c.low_tiles() * kJT;
+    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (t >= M * w)
+        return;
+    const int64_t m = t / w, i = t % w;
+    const bool core = i < kp;
+    const int64_t hi = core ? i : 2 * kp + (i - kp), lo = hi + (core ? kp : rp);
+    float s = 0.f;
+    for (int64_t p = 0; p < S; ++p) {
+        const float *x = part + (p * M + m) * pitch;
+        s += x[hi] + x[lo];
+    }
+    tu[t] = core ? (i < k ? s * sb[i] : 0.f) : (i - kp < r ? s : 0.f);
+}
+
+// ---------------------------------------------------------------------------
+// finish: one wave per [64 rows x 16 columns]
+// ---------------------------------------------------------------------------
+struct FinishArgs {
+    int64_t M, d, k, r, G, g, S, pitch; // pitch: columns of a range's rows
+    Cols c;
+    const float *part, *tu, *sd;
+    const int8_t *b8t, *d8t;
+    uint16_t *dx;
+};
+
+// eight int8 in order as exact bf16
+__device__ __forceinline__ bf16x8 codes_bf16(const int8_t *p)
+{
+    const u32x2 w = *(const u32x2 *)p;
+    return as_bf16x8(c8_bf16(u32x2{w.x ^ 0x80808080u, w.y ^ 0x80808080u}));
+}
+
+__global__ __launch_bounds__(256) void finish_kernel(FinishArgs a)
+{
+    const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
+    const int64_t blocks = a.d / 16, id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t j0 = id % blocks * 16, m0 = id / blocks * 64;
+    if (m0 >= a.M)
+        return;
+    const int64_t kp = a.c.kst * kUnit, rp = a.c.rst * kUnit, w = kp + rp;
+    f32x4 acc[4];
+    const float *tu[4];
+    for (int t = 0; t < 4; ++t) {
+        const int64_t m = min(m0 + 16 * t + r, a.M - 1);
+        acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int64_t p = 0; p < a.S; ++p) // the ranges in order
+            acc[t] += *(const f32x4 *)(a.part + (p * a.M + m) * a.pitch + j0 + 4 * q);
+        tu[t] = a.tu + m * w + 8 * q;
+    }
+    // x in two bf16 parts (16 significant bits) against the exact codes
+    auto add = [&](f32x4 &c, bf16x8 code, const float x[8]) {
+        bf16x8 hi, lo;
+        for (int e = 0; e < 8; ++e) {
+            hi[e] = (__bf16)x[e];
+            lo[e] = (__bf16)(x[e] - (float)hi[e]);
+        }
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(code, hi, c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(code, lo, c, 0, 0, 0);
+    };
+    for (int64_t i = 0; i < kp; i += kUnit) {
+        const bf16x8 code = codes_bf16(a.b8t + (j0 + r) * kp + i + 8 * q);
+        for (int t = 0; t < 4; ++t) {
+            float x[8];
+            load8(tu[t] + i, x);
+            add(acc[t], code, x);
+        }
+    }
+    for (int64_t i = 0; i < rp; i += kUnit) {
+        const bf16x8 code = codes_bf16(a.d8t + (j0 + r) * rp + i + 8 * q);
+        float sd[8]; // the 16 columns share a group
+        for (int e = 0; e < 8; ++e)
+            sd[e] = i + 8 * q + e < a.r ? a.sd[(i + 8 * q + e) * a.G + j0 / a.g] : 0.f;
+        for (int t = 0; t < 4; ++t) {
+            float x[8];
+            load8(tu[t] + kp + i, x);
+            for (int e = 0; e < 8; ++e)
+                x[e] *= sd[e];
+            add(acc[t], code, x);
+        }
+    }
+    for (int t = 0; t < 4; ++t) {
+        const int64_t m = m0 + 16 * t + r;
+        if (m < a.M) {
+            u16x4u o;
+            for (int i = 0; i < 4; ++i)
+                o[i] = __builtin_bit_cast(uint16_t, (__bf16)acc[t][i]);
+            *(u16x4u *)(a.dx + m * a.d + j0 + 4 * q) = o;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+
+struct Plan {
+    int64_t n_mt, Sl, Sm; // row tiles, vocabulary ranges of the low-rank and the main launch
+    int bm;
+};
+
+// Row tile by the rows there are; ranges so that the workgroups come to
+// about kWg, each with at least kMinChunks chunks.
+constexpr int64_t kWg = 512, kMinChunks = 8;
+
+Plan plan_of(const Cols &c, int64_t M, int64_t nvc)
+{
+    Plan p;
+    p.bm = M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    p.n_mt = (M + p.bm - 1) / p.bm;
+    auto ranges = [&](int64_t tiles) {
+        const int64_t t = std::max<int64_t>(tiles * p.n_mt, 1);
+        return std::max<int64_t>(1, std::min<int64_t>(kWg / t, std::max<int64_t>(1, nvc / kMinChunks)));
+    };
+    p.Sl = ranges(c.low_tiles());
+    p.Sm = ranges(c.main_tiles());
+    return p;
+}
+
+struct BwWs {
+    size_t g16, amax, unscale, low, tu, part, total;
+};
+constexpr int64_t kAmaxSlices = 64;
+
+// Fits every call of up to rows rows: with more than one range, ranges x
+// tiles x row tiles stays within kWg, so the parts within kWg tiles.
+BwWs bw_ws(const Shape &s, int64_t rows)
+{
+    const Cols c = cols_of(s);
+    const int64_t nvc = (s.V + kVC - 1) / kVC;
+    auto parts = [&](int64_t tiles) {
+        const int64_t one = rows * tiles * kJT, all = one * std::max<int64_t>(1, nvc / kMinChunks);
+        return std::max(one, std::min(all, kWg * 128 * kJT));
+    };
+    BwWs w;
+    size_t off = 0;
+    auto place = [&](size_t bytes) {
+        const size_t o = off;
+        off += up(std::max<size_t>(bytes, 16));
+        return o;
+    };
+    w.g16 = place(size_t(rows) * nvc * kVC * 2);
+    w.amax = place(size_t(rows) * kAmaxSlices * 4);
+    w.unscale = place(size_t(rows) * 4);
+    w.low = place(size_t(parts(c.low_tiles())) * 4);
+    w.tu = place(size_t(rows) * (c.kst + c.rst) * kUnit * 4);
+    w.part = place(size_t(parts(c.main_tiles())) * 4);
+    w.total = off;
+    return w;
+}
+
+} // namespace
+
+struct BackwardState {
+    void *block; // the second layout
+    size_t block_bytes;
+    uint32_t *codes;
+    uint16_t *sc;
+    int8_t *b8t, *d8t;
+    int32_t *ex;
+    void *ws;
+    size_t ws_bytes;
+    int64_t rows; // rows the workspace holds
+};
+
+void backward_release(BackwardState *b)
+{
+    if (!b)
+        return;
+    if (b->ws)
+        (void)hipFree(b->ws);
+    if (b->block)
+        (void)hipFree(b->block);
+    delete b;
+}
+
+size_t backward_bytes(const BackwardState *b) { return b ? b->block_bytes + b->ws_bytes : 0; }
+
+namespace {
+
+#define BW_TRY(expr)                                                                               \
+    do {                                                                                           \
+        hipError_t e_ = (expr);                                                                    \
+        if (e_ != hipSuccess)                                                                      \
+            return api_fail(ARCHEAD_EHIP, std::string(#expr) + ": " + hipGetErrorString(e_));      \
+    } while (0)
+
+archead_status device_alloc(void **p, size_t bytes, const char *what)
+{
+    *p = nullptr;
+    if (alloc_refused(bytes))
+        return api_fail(ARCHEAD_ENOMEM, std::string(what) + " of " + std::to_string(bytes) +
+                                            " bytes refused (ARCHEAD_TEST_ALLOC_LIMIT)");
+    const hipError_t e = hipMalloc(p, bytes);
+    if (e != hipSuccess) {
+        *p = nullptr;
+        return api_fail(ARCHEAD_ENOMEM, std::string("hipMalloc of the ") + what + ": " + hipGetErrorString(e));
+    }
+    return ARCHEAD_OK;
+}
+
+// lays the codes out a second time into a fresh block
+archead_status lay_out(const DevHead &h, BackwardState *b, hipStream_t st)
+{
+    Layout a{};
+    a.h = h;
+    a.c = cols_of(h.s);
+    a.nvc = (h.s.V + kVC - 1) / kVC;
+    const int64_t nblk = a.c.tiles() * 16, nunit = a.c.tiles() * (kJT / kUnit);
+    if (a.nvc * nblk >= int64_t(1) << 31)
+        return api_fail(ARCHEAD_ESHAPE, "head too large for the backward's layout");
+    size_t off = 0;
+    auto place = [&](size_t bytes) {
+        const size_t o = off;
+        off += up(std::max<size_t>(bytes, 16));
+        return o;
+    };
+    const size_t kp = a.c.kst * kUnit, rp = a.c.rst * kUnit;
+    const size_t o_codes = place(size_t(a.nvc) * nblk * 1024), o_sc = place(size_t(a.nvc) * nunit * kVC * 2);
+    const size_t o_b8 = place(h.s.d * kp), o_d8 = place(h.s.d * rp), o_ex = place(64);
+    archead_status s = device_alloc(&b->block, off, "backward layout");
+    if (s != ARCHEAD_OK)
+        return s;
+    b->block_bytes = off;
+    char *p = (char *)b->block;
+    a.codes = b->codes = (uint32_t *)(p + o_codes);
+    a.sc = b->sc = (uint16_t *)(p + o_sc);
+    a.b8t = b->b8t = (int8_t *)(p + o_b8);
+    a.d8t = b->d8t = (int8_t *)(p + o_d8);
+    a.ex = b->ex = (int32_t *)(p + o_ex);
+    a.peak = (uint32_t *)(p + o_ex + 32);
+    BW_TRY(hipMemsetAsync(p + o_ex, 0, 64, st)); // never under capture (checked by the caller)
+    hipLaunchKernelGGL(peak_kernel, dim3(256, 3), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(exponent_kernel, dim3(1), dim3(64), 0, st, a);
+    hipLaunchKernelGGL(codes_kernel, dim3((unsigned)(a.nvc * nblk)), dim3(256), 0, st, a, nblk);
+    hipLaunchKernelGGL(scales_kernel, dim3((unsigned)(a.nvc * nunit)), dim3(kVC), 0, st, a, nunit);
+    if (kp)
+        hipLaunchKernelGGL(columns_kernel, dim3(1024), dim3(256), 0, st, h.b8, h.s.k, h.s.d, (int64_t)kp, a.b8t);
+    if (rp)
+        hipLaunchKernelGGL(columns_kernel, dim3(1024), dim3(256), 0, st, h.d8, h.s.r, h.s.d, (int64_t)rp, a.d8t);
+    BW_TRY(hipGetLastError());
+    return ARCHEAD_OK;
+}
+
+template <int BM> void launch_tiles(const TileArgs &a, hipStream_t st)
+{
+    const int64_t per = (a.S * a.n_mt * a.n_jt + 7) / 8;
+    hipLaunchKernelGGL(tile_kernel<BM>, dim3((unsigned)(per * 8)), dim3(512), 0, st, a);
+}
+
+void run_tiles(int bm, const TileArgs &a, hipStream_t st)
+{
+    if (bm == 32)
+        launch_tiles<32>(a, st);
+    else if (bm == 64)
+        launch_tiles<64>(a, st);
+    else
+        launch_tiles<128>(a, st);
+}
+
+// up to b.rows rows of G
+void backward_rows(const DevHead &h, const BackwardState &b, int64_t M, const void *g, int type, int64_t ld,
+                   uint16_t *dx, hipStream_t st)
+{
+    const Shape &s = h.s;
+    const Cols c = cols_of(s);
+    const BwWs L = bw_ws(s, b.rows);
+    char *ws = (char *)b.ws;
+    const int64_t nvc = (s.V + kVC - 1) / kVC;
+    GArgs ga{};
+    ga.g = g;
+    ga.M = M;
+    ga.V = s.V;
+    ga.ld = ld;
+    ga.Vp = nvc * kVC;
+    const int64_t step = 256 * 8; // a workgroup's elements per step
+    ga.S = std::max<int64_t>(1, std::min<int64_t>({kAmaxSlices, 2048 / std::max<int64_t>(M, 1), ga.Vp / step}));
+    ga.slice = (ga.Vp + ga.S * step - 1) / (ga.S * step) * step;
+    ga.S = (ga.Vp + ga.slice - 1) / ga.slice;
+    ga.amax = (float *)(ws + L.amax);
+    ga.g16 = (uint16_t *)(ws + L.g16);
+    ga.unscale = (float *)(ws + L.unscale);
+    const dim3 grid((unsigned)(M * ga.S));
+    if (type == ARCHEAD_F32) {
+        hipLaunchKernelGGL(amax_kernel<float>, grid, dim3(256), 0, st, ga);
+        hipLaunchKernelGGL(convert_kernel<float>, grid, dim3(256), 0, st, ga);
+    } else {
+        hipLaunchKernelGGL(amax_kernel<uint16_t>, grid, dim3(256), 0, st, ga);
+        hipLaunchKernelGGL(convert_kernel<uint16_t>, grid, dim3(256), 0, st, ga);
+    }
+    const Plan p = plan_of(c, M, nvc);
+    TileArgs t{};
+    t.g16 = ga.g16;
+    t.unscale = ga.unscale;
+    t.codes = b.codes;
+    t.sc = b.sc;
+    t.ex = b.ex;
+    t.M = M;
+    t.Vp = ga.Vp;
+    t.nvc = nvc;
+    t.tiles = c.tiles();
+    t.n_mt = p.n_mt;
+    t.c = c;
+    float *low = (float *)(ws + L.low), *tu = (float *)(ws + L.tu), *part = (float *)(ws + L.part);
+    if (c.low_tiles() > 0) {
+        t.t0 = c.main_tiles();
+        t.n_jt = c.low_tiles();
+        t.S = p.Sl;
+        t.low = 1;
+        t.part = low;
+        run_tiles(p.bm, t, st);
+        const int64_t n = M * (c.kst + c.rst) * kUnit;
+        hipLaunchKernelGGL(low_sum_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, low, M, p.Sl, c, s.k,
+                           s.r, h.sb, tu);
+    }
+    t.t0 = 0;
+    t.n_jt = c.main_tiles();
+    t.S = p.Sm;
+    t.low = 0;
+    t.part = part;
+    run_tiles(p.bm, t, st);
+    const FinishArgs f{M, s.d, s.k, s.r, s.G(), s.g, p.Sm, c.main_tiles() * kJT, c, part, tu, h.sd, b.b8t, b.d8t, dx};
+    const int64_t waves = (M + 63) / 64 * (s.d / 16);
+    hipLaunchKernelGGL(finish_kernel, dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, f);
+}
+
+} // namespace
+} // namespace archead
+
+using namespace archead;
+
+extern "C" archead_status archead_reserve_backward(archead_t h, int64_t M_max, void *hip_stream)
+{
+    const DevHead *dev = nullptr;
+    BackwardState **slot = nullptr;
+    int device = 0;
+    archead_status s = backward_slot(h, &dev, &slot, &device);
+    if (s != ARCHEAD_OK)
+        return s;
+    if (M_max < 1)
+        return api_fail(ARCHEAD_EINVAL, "M_max must be at least 1");
+    if (M_max > int64_t(1) << 20)
+        return api_fail(ARCHEAD_ESHAPE, "M_max above 2^20");
+    const int64_t rows = std::min(M_max, kChunkM);
+    if (*slot && (*slot)->rows >= rows)
+        return ARCHEAD_OK;
+    hipStream_t st = (hipStream_t)hip_stream;
+    BW_TRY(hipSetDevice(device));
+    hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
+    BW_TRY(hipStreamIsCapturing(st, &cap));
+    if (cap != hipStreamCaptureStatusNone)
+        return api_fail(ARCHEAD_EINVAL, "archead_reserve_backward allocates: call it before the capture");
+    // a state of its own until all of it is there
+    BackwardState *b = *slot ? *slot : new (std::nothrow) BackwardState();
+    if (!b)
+        return api_fail(ARCHEAD_ENOMEM, "host allocation failed");
+    void *ws = nullptr;
+    const size_t bytes = bw_ws(dev->s, rows).total;
+    s = device_alloc(&ws, bytes, "backward workspace");
+    if (s == ARCHEAD_OK && !b->block)
+        s = lay_out(*dev, b, st);
+    if (s == ARCHEAD_OK && hipStreamSynchronize(st) != hipSuccess)
+        s = api_fail(ARCHEAD_EHIP, "the backward's layout did not complete");
+    if (s != ARCHEAD_OK) {
+        if (ws)
+            (void)hipFree(ws);
+        if (!*slot)
+            backward_release(b);
+        return s;
+    }
+    if (b->ws)
+        (void)hipFree(b->ws); // waits for the device
+    b->ws = ws;
+    b->ws_bytes = bytes;
+    b->rows = rows;
+    *slot = b;
+    return ARCHEAD_OK;
+}
+
+extern "C" archead_status archead_backward(archead_t h, int64_t M, const void *dlogits, int type, int64_t ld, void *dX,
+                                           void *hip_stream)
+{
+    const DevHead *dev = nullptr;
+    BackwardState **slot = nullptr;
+    int device = 0;
+    archead_status s = backward_slot(h, &dev, &slot, &device);
+    if (s != ARCHEAD_OK)
+        return s;
+    if (M < 0)
+        return api_fail(ARCHEAD_EINVAL, "M < 0");
+    if (M > int64_t(1) << 20)
+        return api_fail(ARCHEAD_ESHAPE, "M above 2^20");
+    if (type != ARCHEAD_F32 && type != ARCHEAD_BF16)
+        return api_fail(ARCHEAD_EINVAL, "dlogits must be ARCHEAD_F32 or ARCHEAD_BF16");
+    if (ld < dev->s.V || ld > int64_t(1) << 40)
+        return api_fail(ARCHEAD_EINVAL, "the row stride must lie in [V, 2^40]");
+    if (M == 0)
+        return ARCHEAD_OK;
+    if (!dlogits || !dX)
+        return api_fail(ARCHEAD_EINVAL, "dlogits and dX are required");
+    if ((uintptr_t)dlogits % (type == ARCHEAD_F32 ? 4 : 2) || (uintptr_t)dX % 2)
+        return api_fail(ARCHEAD_EINVAL, "dlogits and dX must be aligned to their elements");
+    if (!*slot)
+        return api_fail(ARCHEAD_EINVAL, "call archead_reserve_backward first");
+    BW_TRY(hipSetDevice(device));
+    const BackwardState &b = **slot;
+    const size_t esz = type == ARCHEAD_F32 ? 4 : 2;
+    for (int64_t m = 0; m < M; m += b.rows)
+        backward_rows(*dev, b, std::min(b.rows, M - m), (const char *)dlogits + size_t(m) * ld * esz, type, ld,
+                      (uint16_t *)dX + m * dev->s.d, (hipStream_t)hip_stream);
+    BW_TRY(hipGetLastError());
+    return ARCHEAD_OK;
+}
