@@ -421,33 +421,60 @@ template <int BM> __global__ __launch_bounds__(512) void tile_kernel(TileArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// T sB and U: the ranges' sums of the two halves of every column
+// T sB and U: the ranges' sums of the two halves of every column.  T sB is
+// left in two bf16 parts (16 significant bits), as the finish multiplies it.
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void low_sum_kernel(const float *part, int64_t M, int64_t S, Cols c, int64_t k,
-                                                      int64_t r, const float *sb, float *tu)
+struct LowArgs {
+    int64_t M, S, k, r;
+    Cols c;
+    const float *part, *sb;
+    uint16_t *thi, *tlo; // [M][kp]
+    float *u;            // [M][rp]
+};
+
+constexpr int kLowLanes = 8; // threads that share a column's ranges
+
+__global__ __launch_bounds__(256) void low_sum_kernel(LowArgs a)
 {
-    const int64_t kp = c.kst * kUnit, rp = c.rst * kUnit, w = kp + rp, pitch = c.low_tiles() * kJT;
-    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (t >= M * w)
-        return;
+    const int64_t kp = a.c.kst * kUnit, rp = a.c.rst * kUnit, w = kp + rp, pitch = a.c.low_tiles() * kJT;
+    // thread (column, share): 32 columns of one row per workgroup (w is a multiple of 32)
+    const int64_t t = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
+    const int sh = threadIdx.x >> 5;
     const int64_t m = t / w, i = t % w;
+    __shared__ float red[kLowLanes][32];
     const bool core = i < kp;
     const int64_t hi = core ? i : 2 * kp + (i - kp), lo = hi + (core ? kp : rp);
     float s = 0.f;
-    for (int64_t p = 0; p < S; ++p) {
-        const float *x = part + (p * M + m) * pitch;
+#pragma unroll 4
+    for (int64_t p = sh; p < a.S; p += kLowLanes) {
+        const float *x = a.part + (p * a.M + m) * pitch;
         s += x[hi] + x[lo];
     }
-    tu[t] = core ? (i < k ? s * sb[i] : 0.f) : (i - kp < r ? s : 0.f);
+    red[sh][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (sh)
+        return;
+    s = 0.f;
+    for (int p = 0; p < kLowLanes; ++p)
+        s += red[p][threadIdx.x];
+    if (core) {
+        const float x = i < a.k ? s * a.sb[i] : 0.f;
+        const __bf16 h = (__bf16)x;
+        a.thi[m * kp + i] = __builtin_bit_cast(uint16_t, h);
+        a.tlo[m * kp + i] = __builtin_bit_cast(uint16_t, (__bf16)(x - (float)h));
+    } else {
+        a.u[m * rp + i - kp] = i - kp < a.r ? s : 0.f;
+    }
 }
 
 // ---------------------------------------------------------------------------
-// finish: one wave per [64 rows x 16 columns]
+// finish: one wave per [16 NT rows x 16 columns]
 // ---------------------------------------------------------------------------
 struct FinishArgs {
     int64_t M, d, k, r, G, g, S, pitch; // pitch: columns of a range's rows
     Cols c;
-    const float *part, *tu, *sd;
+    const float *part, *u, *sd;
+    const uint16_t *thi, *tlo;
     const int8_t *b8t, *d8t;
     uint16_t *dx;
 };
@@ -459,39 +486,31 @@ __device__ __forceinline__ bf16x8 codes_bf16(const int8_t *p)
     return as_bf16x8(c8_bf16(u32x2{w.x ^ 0x80808080u, w.y ^ 0x80808080u}));
 }
 
-__global__ __launch_bounds__(256) void finish_kernel(FinishArgs a)
+template <int NT> __global__ __launch_bounds__(256) void finish_kernel(FinishArgs a)
 {
     const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
     const int64_t blocks = a.d / 16, id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int64_t j0 = id % blocks * 16, m0 = id / blocks * 64;
+    const int64_t j0 = id % blocks * 16, m0 = id / blocks * 16 * NT;
     if (m0 >= a.M)
         return;
-    const int64_t kp = a.c.kst * kUnit, rp = a.c.rst * kUnit, w = kp + rp;
-    f32x4 acc[4];
-    const float *tu[4];
-    for (int t = 0; t < 4; ++t) {
-        const int64_t m = min(m0 + 16 * t + r, a.M - 1);
+    const int64_t kp = a.c.kst * kUnit, rp = a.c.rst * kUnit;
+    f32x4 acc[NT];
+    int64_t m[NT];
+    for (int t = 0; t < NT; ++t) {
+        m[t] = min(m0 + 16 * t + r, a.M - 1);
         acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        for (int64_t p = 0; p < a.S; ++p) // the ranges in order
-            acc[t] += *(const f32x4 *)(a.part + (p * a.M + m) * a.pitch + j0 + 4 * q);
-        tu[t] = a.tu + m * w + 8 * q;
+        const float *p = a.part + m[t] * a.pitch + j0 + 4 * q;
+#pragma unroll 8
+        for (int64_t i = 0; i < a.S; ++i) // the ranges in order
+            acc[t] += *(const f32x4 *)(p + i * a.M * a.pitch);
     }
-    // x in two bf16 parts (16 significant bits) against the exact codes
-    auto add = [&](f32x4 &c, bf16x8 code, const float x[8]) {
-        bf16x8 hi, lo;
-        for (int e = 0; e < 8; ++e) {
-            hi[e] = (__bf16)x[e];
-            lo[e] = (__bf16)(x[e] - (float)hi[e]);
-        }
-        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(code, hi, c, 0, 0, 0);
-        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(code, lo, c, 0, 0, 0);
-    };
+#pragma unroll 2
     for (int64_t i = 0; i < kp; i += kUnit) {
         const bf16x8 code = codes_bf16(a.b8t + (j0 + r) * kp + i + 8 * q);
-        for (int t = 0; t < 4; ++t) {
-            float x[8];
-            load8(tu[t] + i, x);
-            add(acc[t], code, x);
+        for (int t = 0; t < NT; ++t) {
+            const int64_t at = m[t] * kp + i + 8 * q;
+            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(code, *(const bf16x8 *)(a.thi + at), acc[t], 0, 0, 0);
+            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(code, *(const bf16x8 *)(a.tlo + at), acc[t], 0, 0, 0);
         }
     }
     for (int64_t i = 0; i < rp; i += kUnit) {
@@ -499,23 +518,26 @@ __global__ __launch_bounds__(256) void finish_kernel(FinishArgs a)
         float sd[8]; // the 16 columns share a group
         for (int e = 0; e < 8; ++e)
             sd[e] = i + 8 * q + e < a.r ? a.sd[(i + 8 * q + e) * a.G + j0 / a.g] : 0.f;
-        for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < NT; ++t) {
             float x[8];
-            load8(tu[t] + kp + i, x);
-            for (int e = 0; e < 8; ++e)
+            load8(a.u + m[t] * rp + i + 8 * q, x);
+            bf16x8 hi, lo; // U sD in two bf16 parts against the exact codes
+            for (int e = 0; e < 8; ++e) {
                 x[e] *= sd[e];
-            add(acc[t], code, x);
+                hi[e] = (__bf16)x[e];
+                lo[e] = (__bf16)(x[e] - (float)hi[e]);
+            }
+            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(code, hi, acc[t], 0, 0, 0);
+            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(code, lo, acc[t], 0, 0, 0);
         }
     }
-    for (int t = 0; t < 4; ++t) {
-        const int64_t m = m0 + 16 * t + r;
-        if (m < a.M) {
+    for (int t = 0; t < NT; ++t)
+        if (m0 + 16 * t + r < a.M) {
             u16x4u o;
             for (int i = 0; i < 4; ++i)
                 o[i] = __builtin_bit_cast(uint16_t, (__bf16)acc[t][i]);
-            *(u16x4u *)(a.dx + m * a.d + j0 + 4 * q) = o;
+            *(u16x4u *)(a.dx + m[t] * a.d + j0 + 4 * q) = o;
         }
-    }
 }
 
 // ---------------------------------------------------------------------------
@@ -528,18 +550,31 @@ struct Plan {
     int bm;
 };
 
-// Row tile by the rows there are; ranges so that the workgroups come to
-// about kWg, each with at least kMinChunks chunks.
-constexpr int64_t kWg = 512, kMinChunks = 8;
+// Row tile by the rows there are.  Ranges: the vocabulary is cut so that the
+// workgroups fill the compute units' places (by LDS: one of 128 rows, two of
+// 64, three of 32) in whole rounds: of up to kRounds rounds the count whose
+// share of idle places and of stages past the first fill is least.
+constexpr int64_t kCu = 256, kMaxWg = 1024, kMinChunks = 8;
 
 Plan plan_of(const Cols &c, int64_t M, int64_t nvc)
 {
     Plan p;
     p.bm = M <= 32 ? 32 : M <= 64 ? 64 : 128;
     p.n_mt = (M + p.bm - 1) / p.bm;
+    const int64_t places = kCu * (p.bm == 32 ? 3 : p.bm == 64 ? 2 : 1);
     auto ranges = [&](int64_t tiles) {
-        const int64_t t = std::max<int64_t>(tiles * p.n_mt, 1);
-        return std::max<int64_t>(1, std::min<int64_t>(kWg / t, std::max<int64_t>(1, nvc / kMinChunks)));
+        const int64_t t = std::max<int64_t>(tiles * p.n_mt, 1), most = std::max<int64_t>(1, nvc / kMinChunks);
+        int64_t best = 1;
+        double least = 1e300;
+        for (int64_t S = 1; S <= most && (S == 1 || S * t <= kMaxWg); ++S) {
+            // rounds of a range's chunks, each with about two stages of latency
+            const double cost = double((S * t + places - 1) / places) * (double((nvc + S - 1) / S) + 2.0);
+            if (cost < least * 0.995) {
+                least = cost;
+                best = S;
+            }
+        }
+        return best;
     };
     p.Sl = ranges(c.low_tiles());
     p.Sm = ranges(c.main_tiles());
@@ -547,19 +582,19 @@ Plan plan_of(const Cols &c, int64_t M, int64_t nvc)
 }
 
 struct BwWs {
-    size_t g16, amax, unscale, low, tu, part, total;
+    size_t g16, amax, unscale, low, thi, tlo, u, part, total;
 };
 constexpr int64_t kAmaxSlices = 64;
 
 // Fits every call of up to rows rows: with more than one range, ranges x
-// tiles x row tiles stays within kWg, so the parts within kWg tiles.
+// tiles x row tiles stays within kMaxWg, so the parts within kMaxWg tiles.
 BwWs bw_ws(const Shape &s, int64_t rows)
 {
     const Cols c = cols_of(s);
     const int64_t nvc = (s.V + kVC - 1) / kVC;
     auto parts = [&](int64_t tiles) {
         const int64_t one = rows * tiles * kJT, all = one * std::max<int64_t>(1, nvc / kMinChunks);
-        return std::max(one, std::min(all, kWg * 128 * kJT));
+        return std::max(one, std::min(all, kMaxWg * 128 * kJT));
     };
     BwWs w;
     size_t off = 0;
@@ -572,7 +607,9 @@ BwWs bw_ws(const Shape &s, int64_t rows)
     w.amax = place(size_t(rows) * kAmaxSlices * 4);
     w.unscale = place(size_t(rows) * 4);
     w.low = place(size_t(parts(c.low_tiles())) * 4);
-    w.tu = place(size_t(rows) * (c.kst + c.rst) * kUnit * 4);
+    w.thi = place(size_t(rows) * c.kst * kUnit * 2);
+    w.tlo = place(size_t(rows) * c.kst * kUnit * 2);
+    w.u = place(size_t(rows) * c.rst * kUnit * 4);
     w.part = place(size_t(parts(c.main_tiles())) * 4);
     w.total = off;
     return w;
@@ -730,7 +767,8 @@ void backward_rows(const DevHead &h, const BackwardState &b, int64_t M, const vo
     t.tiles = c.tiles();
     t.n_mt = p.n_mt;
     t.c = c;
-    float *low = (float *)(ws + L.low), *tu = (float *)(ws + L.tu), *part = (float *)(ws + L.part);
+    float *low = (float *)(ws + L.low), *u = (float *)(ws + L.u), *part = (float *)(ws + L.part);
+    uint16_t *thi = (uint16_t *)(ws + L.thi), *tlo = (uint16_t *)(ws + L.tlo);
     if (c.low_tiles() > 0) {
         t.t0 = c.main_tiles();
         t.n_jt = c.low_tiles();
@@ -738,9 +776,8 @@ void backward_rows(const DevHead &h, const BackwardState &b, int64_t M, const vo
         t.low = 1;
         t.part = low;
         run_tiles(p.bm, t, st);
-        const int64_t n = M * (c.kst + c.rst) * kUnit;
-        hipLaunchKernelGGL(low_sum_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, low, M, p.Sl, c, s.k,
-                           s.r, h.sb, tu);
+        const LowArgs l{M, p.Sl, s.k, s.r, c, low, h.sb, thi, tlo, u};
+        hipLaunchKernelGGL(low_sum_kernel, dim3((unsigned)(M * (c.kst + c.rst))), dim3(256), 0, st, l);
     }
     t.t0 = 0;
     t.n_jt = c.main_tiles();
@@ -748,9 +785,15 @@ void backward_rows(const DevHead &h, const BackwardState &b, int64_t M, const vo
     t.low = 0;
     t.part = part;
     run_tiles(p.bm, t, st);
-    const FinishArgs f{M, s.d, s.k, s.r, s.G(), s.g, p.Sm, c.main_tiles() * kJT, c, part, tu, h.sd, b.b8t, b.d8t, dx};
-    const int64_t waves = (M + 63) / 64 * (s.d / 16);
-    hipLaunchKernelGGL(finish_kernel, dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, f);
+    const FinishArgs f{M, s.d, s.k, s.r, s.G(), s.g, p.Sm, c.main_tiles() * kJT, c, part, u, h.sd, thi, tlo,
+                       b.b8t, b.d8t, dx};
+    if (M <= 256) { // few rows: more waves, for the latency of the ranges' loads
+        const int64_t waves = (M + 15) / 16 * (s.d / 16);
+        hipLaunchKernelGGL(finish_kernel<1>, dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, f);
+    } else {
+        const int64_t waves = (M + 63) / 64 * (s.d / 16);
+        hipLaunchKernelGGL(finish_kernel<4>, dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, f);
+    }
 }
 
 } // namespace
