@@ -355,7 +355,7 @@ typedef enum archead_type {
 /*
  * archead_reserve_backward -- prepare a handle for archead_backward: the
  * packed codes are laid out a second time on the device, by vocabulary rows
- * (about the packed head's size again, 1.3 times at d / g = 32), and a
+ * (about the packed head's size again), and a
  * workspace for M_max rows at a time is allocated (at most 2048; a call with
  * more goes in parts).  Waits until both are ready.  Called again it only ever
  * enlarges the workspace; calls of archead_backward on the handle that are

@@ -6,11 +6,11 @@
 //   T = G (sA o A5),  U = G (sC o C8).
 //
 // Everything that sums over the vocabulary is one kind of product: rows of G
-// against 4-bit codes with a scale per (v, 32 columns).  R4 is that already; a
-// 5-bit core code a = 2 h + b and an 8-bit correction code c = 16 h + l are
-// two such columns each.  The codes are laid out a second time, eight
-// vocabulary rows of one column to a dword (the forward's layout holds eight
-// columns of one row), so that a dword is one lane's matrix operand.
+// against integer codes with a scale per (v, 32 columns): R4's 4-bit codes, and
+// A5's and C8's as bytes.  The codes are laid out a second time, eight
+// vocabulary rows of one column beside each other (the forward's layout holds
+// eight columns of one row), so that a dword of nibbles, or two of bytes, is one
+// lane's matrix operand.
 //
 //   amax, convert  G 2^f_m as fp16 rows, f_m putting row m's largest entry
 //                  into [2^14, 2^15): exact for bf16 G within 2^28 of it
@@ -41,35 +41,34 @@ typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint16_t u16x8u __attribute__((ext_vector_type(8), aligned(2)));
 typedef uint16_t u16x4u __attribute__((ext_vector_type(4), aligned(2)));
 
-// Columns of the second layout: dX's d columns, then the tile-aligned columns
-// of T and U by units of 32: kst units of h and kst of b for the core, rst of
-// h and rst of l for the correction.
+// Columns of the second layout: dX's d columns, and the columns of T and U by
+// units of 32: kst units of the core, then rst of the correction.
 struct Cols {
     int64_t d, kst, rst;
     __host__ __device__ int64_t main_tiles() const { return (d + kJT - 1) / kJT; }
-    __host__ __device__ int64_t low_units() const { return 2 * (kst + rst); }
+    __host__ __device__ int64_t low_units() const { return kst + rst; }
     __host__ __device__ int64_t low_tiles() const { return (low_units() * kUnit + kJT - 1) / kJT; }
-    __host__ __device__ int64_t tiles() const { return main_tiles() + low_tiles(); }
 };
 Cols cols_of(const Shape &s) { return Cols{s.d, s.kst(), s.rst()}; }
 
 // ---------------------------------------------------------------------------
 // The second layout (once per head)
-//   codes uint32 [chunk][tile * 16 + block][64 lanes][4]: lane l holds column
-//         l % 16 of the 16-column block, dword s the chunk's rows
-//         32 s + 8 (l / 16) + e, e = 0 .. 7, offset binary, in the nibble order
-//         of the first layout
-//   sc    fp16 [chunk][tile * 8 + unit][128 rows], scale 2^E, the exponents E
-//         (ex: residual, core, correction) putting the field's largest scaled
-//         value below 2^15
+//   codes uint32 [chunk][16-column block][64 lanes][4]: lane l holds column
+//         l % 16 of the block, dword s the chunk's rows 32 s + 8 (l / 16) + e,
+//         e = 0 .. 7, offset binary, in the nibble order of the first layout
+//   low   uint32 [chunk][block][2][64 lanes][4]: the same rows of a core or
+//         correction column as bytes a + 16 or c + 128, dwords 2 s and 2 s + 1 of
+//         a lane in half s / 2
+//   sc, lsc  fp16 [chunk][unit][128 rows], scale 2^E, the exponents E (ex:
+//         residual, core, correction) keeping every code times scale below 2^15
 //   b8t, d8t  int8 [d][kpad], [d][rpad]: B8 and D8 by columns
 // ---------------------------------------------------------------------------
 struct Layout {
     DevHead h;
     Cols c;
     int64_t nvc;
-    uint32_t *codes;
-    uint16_t *sc;
+    uint32_t *codes, *low;
+    uint16_t *sc, *lsc;
     int8_t *b8t, *d8t;
     uint32_t *peak; // largest |sR|, |sA|, |sC| as fp32 bits
     int32_t *ex;
@@ -97,7 +96,7 @@ __global__ void exponent_kernel(Layout a)
     if (w >= 3)
         return;
     const float m = __uint_as_float(a.peak[w]) * (w == 0 ? 1.f : w == 1 ? 2.f : 16.f);
-    a.ex[w] = m > 0.f ? 11 - ilogbf(m) : 0; // scales below 2^12, codes up to 8 times that
+    a.ex[w] = m > 0.f ? 11 - ilogbf(m) : 0; // codes reach 8, 16 and 128
 }
 
 // residual code (offset binary) of row v, column j in the first layout
@@ -124,70 +123,60 @@ __device__ __forceinline__ uint32_t c8_code(const DevHead &h, int64_t v, int64_t
     return c[2 * (ks & 1) + ((i >> 2) & 1)] >> (8 * (i & 3)) & 255u;
 }
 
-// what a column of the low-rank tiles stands for: part 0 / 1 the core's h / b,
-// 2 / 3 the correction's h / l, -1 padding; i the factor's column
-__device__ __forceinline__ int low_part(const Cols &c, int64_t unit)
-{
-    return unit < c.kst ? 0 : unit < 2 * c.kst ? 1 : unit < 2 * c.kst + c.rst ? 2 : unit < c.low_units() ? 3 : -1;
-}
-__device__ __forceinline__ int64_t low_first(const Cols &c, int part)
-{
-    return part == 0 ? 0 : part == 1 ? c.kst : part == 2 ? 2 * c.kst : 2 * c.kst + c.rst;
-}
-
-// one dword of codes per thread
+// one dword of nibbles per thread
 __global__ __launch_bounds__(256) void codes_kernel(Layout a, int64_t nblk)
 {
     const int64_t vc = blockIdx.x / nblk, blk = blockIdx.x % nblk; // chunk, 16-column block
     const int lane = threadIdx.x >> 2, s = threadIdx.x & 3;
-    const int64_t j = blk * 16 + (lane & 15), main = a.c.main_tiles() * kJT;
-    int part = 4; // residual
-    int64_t i = j;
-    if (j >= main) {
-        const int64_t unit = (j - main) / kUnit;
-        part = low_part(a.c, unit);
-        i = part < 0 ? 0 : (unit - low_first(a.c, part)) * kUnit + (j & 31);
-    }
+    const int64_t j = blk * 16 + (lane & 15);
     uint32_t w = 0;
     for (int e = 0; e < 8; ++e) {
         const int64_t v = vc * kVC + 32 * s + 8 * (lane >> 4) + e;
-        uint32_t u = 8;
-        if (v < a.h.s.nvb() * kVB) { // the first layout's padding rows hold codes of zero
-            if (part == 4)
-                u = j < a.h.s.d ? r4_code(a.h, v, j) : 8u;
-            else if (part == 0)
-                u = a5_code(a.h, v, i) >> 1; // (a + 16) / 2 = h + 8
-            else if (part == 1)
-                u = a5_code(a.h, v, i) & 1u; // b, without an offset
-            else if (part == 2)
-                u = c8_code(a.h, v, i) >> 4; // (c + 128) / 16 = h + 8
-            else if (part == 3)
-                u = c8_code(a.h, v, i) & 15u; // l, without an offset
-        }
+        // the first layout's padding rows hold codes of zero
+        const uint32_t u = v < a.h.s.nvb() * kVB && j < a.h.s.d ? r4_code(a.h, v, j) : 8u;
         w |= u << (4 * ((e >> 1) + 4 * (e & 1)));
     }
-    a.codes[((vc * a.c.tiles() * 16 + blk) * 64 + lane) * 4 + s] = w;
+    a.codes[((vc * nblk + blk) * 64 + lane) * 4 + s] = w;
+}
+
+// one dword of bytes per thread
+__global__ __launch_bounds__(512) void low_codes_kernel(Layout a, int64_t nblk)
+{
+    const int64_t vc = blockIdx.x / nblk, blk = blockIdx.x % nblk;
+    const int half = threadIdx.x >> 8, lane = threadIdx.x >> 2 & 63, dw = threadIdx.x & 3;
+    const int64_t unit = blk / 2, i = (blk & 1) * 16 + (lane & 15);
+    uint32_t w = 0;
+    for (int e = 0; e < 4; ++e) {
+        const int64_t v = vc * kVC + 32 * (2 * half + (dw >> 1)) + 8 * (lane >> 4) + 4 * (dw & 1) + e;
+        const bool in = v < a.h.s.nvb() * kVB;
+        uint32_t u = unit < a.c.kst ? 16u : 128u;
+        if (in && unit < a.c.kst)
+            u = a5_code(a.h, v, unit * kUnit + i);
+        else if (in && unit < a.c.low_units())
+            u = c8_code(a.h, v, (unit - a.c.kst) * kUnit + i);
+        w |= u << (8 * e);
+    }
+    a.low[(((vc * nblk + blk) * 2 + half) * 64 + lane) * 4 + dw] = w;
 }
 
 __global__ __launch_bounds__(128) void scales_kernel(Layout a, int64_t nunit)
 {
     const int64_t vc = blockIdx.x / nunit, unit = blockIdx.x % nunit, v = vc * kVC + threadIdx.x;
-    const int64_t main = a.c.main_tiles() * (kJT / kUnit);
     float f = 0.f;
-    if (v < a.h.s.V) {
-        if (unit < main) {
-            if (unit * kUnit < a.h.s.d)
-                f = ldexpf(h2f(a.h.sr[((v >> 4) * a.h.s.G() + unit * kUnit / a.h.s.g) * kVB + (v & 15)]), a.ex[0]);
-        } else {
-            const int part = low_part(a.c, unit - main);
-            if (part == 0 || part == 1)
-                f = ldexpf(h2f(a.h.sa[v]), a.ex[1] + (part == 0 ? 1 : 0));
-            else if (part == 2 || part == 3)
-                f = ldexpf(h2f(a.h.sc[v]), a.ex[2] + (part == 2 ? 4 : 0));
-        }
-    }
-    a.sc[(vc * a.c.tiles() * (kJT / kUnit) + unit) * kVC + threadIdx.x] =
-        __builtin_bit_cast(uint16_t, (_Float16)f);
+    if (v < a.h.s.V && unit * kUnit < a.h.s.d)
+        f = ldexpf(h2f(a.h.sr[((v >> 4) * a.h.s.G() + unit * kUnit / a.h.s.g) * kVB + (v & 15)]), a.ex[0]);
+    a.sc[(vc * nunit + unit) * kVC + threadIdx.x] = __builtin_bit_cast(uint16_t, (_Float16)f);
+}
+
+__global__ __launch_bounds__(128) void low_scales_kernel(Layout a, int64_t nunit)
+{
+    const int64_t vc = blockIdx.x / nunit, unit = blockIdx.x % nunit, v = vc * kVC + threadIdx.x;
+    float f = 0.f;
+    if (v < a.h.s.V && unit < a.c.kst)
+        f = ldexpf(h2f(a.h.sa[v]), a.ex[1]);
+    else if (v < a.h.s.V && unit < a.c.low_units())
+        f = ldexpf(h2f(a.h.sc[v]), a.ex[2]);
+    a.lsc[(vc * nunit + unit) * kVC + threadIdx.x] = __builtin_bit_cast(uint16_t, (_Float16)f);
 }
 
 __global__ __launch_bounds__(256) void columns_kernel(const int8_t *x, int64_t rows, int64_t d, int64_t pad, int8_t *out)
@@ -295,38 +284,51 @@ struct TileArgs {
     const uint32_t *codes;
     const uint16_t *sc;
     const int32_t *ex;
-    int64_t M, Vp, nvc, tiles; // tiles: of the whole layout
-    int64_t t0, n_jt, n_mt, S; // this launch: first tile, column tiles, row tiles, vocabulary ranges
-    Cols c;
-    int low;                   // the tiles of T and U
-    float *part;               // [S][M][n_jt * 256]
+    int64_t M, Vp, nvc;
+    int64_t n_jt, n_mt, S; // column tiles, row tiles, vocabulary ranges
+    int64_t kst, units;    // core units and all units of the low-rank columns
+    float *part;           // [S][M][n_jt * 256]
 };
 
-// Eight codes of a lane as fp16 q S: the codes spliced into 1024 + u (and
+__device__ __forceinline__ f16x2 as_h2(uint32_t x) { return __builtin_bit_cast(f16x2, x); }
+
+// Eight nibbles of a lane as fp16 q S: the codes spliced into 1024 + u (and
 // 1024 + 16 u), exact integers after one add (one fma), one rounding in the
-// product with the scales.  off0 = -(1024 + offset), off1 = -(64 + offset).
-__device__ __forceinline__ f16x8 dequant(uint32_t w, u32x4 s, uint32_t magic, f16x2 off0, f16x2 off1)
+// product with the scales.
+__device__ __forceinline__ f16x8 dequant4(uint32_t w, u32x4 s, uint32_t magic)
 {
+    const f16x2 off0 = {(_Float16)-1032.f, (_Float16)-1032.f}, off1 = {(_Float16)-72.f, (_Float16)-72.f};
     const f16x2 sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
     const uint32_t w8 = w >> 8;
-    auto h = [](uint32_t x) { return __builtin_bit_cast(f16x2, x); };
-    const f16x2 a = (h((w & 0x000F000Fu) | magic) + off0) * h(s.x);
-    const f16x2 b = __builtin_elementwise_fma(h((w & 0x00F000F0u) | magic), sixteenth, off1) * h(s.y);
-    const f16x2 c = (h((w8 & 0x000F000Fu) | magic) + off0) * h(s.z);
-    const f16x2 d = __builtin_elementwise_fma(h((w8 & 0x00F000F0u) | magic), sixteenth, off1) * h(s.w);
+    const f16x2 a = (as_h2((w & 0x000F000Fu) | magic) + off0) * as_h2(s.x);
+    const f16x2 b = __builtin_elementwise_fma(as_h2((w & 0x00F000F0u) | magic), sixteenth, off1) * as_h2(s.y);
+    const f16x2 c = (as_h2((w8 & 0x000F000Fu) | magic) + off0) * as_h2(s.z);
+    const f16x2 d = __builtin_elementwise_fma(as_h2((w8 & 0x00F000F0u) | magic), sixteenth, off1) * as_h2(s.w);
     return f16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
-template <int BM> struct BTile {
+// eight bytes likewise; off = -(1024 + the codes' offset)
+__device__ __forceinline__ f16x8 dequant8(uint32_t w0, uint32_t w1, u32x4 s, uint32_t magic, f16x2 off)
+{
+    // bytes 2 p, 2 p + 1 of a dword into the low bytes of its two halves
+    const f16x2 a = (as_h2(__builtin_amdgcn_perm(0u, w0, 0x0c010c00u) | magic) + off) * as_h2(s.x);
+    const f16x2 b = (as_h2(__builtin_amdgcn_perm(0u, w0, 0x0c030c02u) | magic) + off) * as_h2(s.y);
+    const f16x2 c = (as_h2(__builtin_amdgcn_perm(0u, w1, 0x0c010c00u) | magic) + off) * as_h2(s.z);
+    const f16x2 d = (as_h2(__builtin_amdgcn_perm(0u, w1, 0x0c030c02u) | magic) + off) * as_h2(s.w);
+    return f16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+template <int BM, bool LOW> struct BTile {
     static constexpr int wm = BM == 128 ? 2 : 1, wj = 8 / wm;      // waves along rows and columns
     static constexpr int mt = BM / wm / 16, jb = kJT / wj / 16;    // 16 x 16 tiles per wave
-    static constexpr int gw = BM * kVC / 2, cw = 16 * 256, sw = 8 * kVC / 2; // words of a stage: G, codes, scales
+    static constexpr int bw = LOW ? 512 : 256;                     // words of a 16-column block's codes
+    static constexpr int gw = BM * kVC / 2, cw = 16 * bw, sw = 8 * kVC / 2; // words of a stage: G, codes, scales
     static constexpr int words = gw + cw + sw;
 };
 
-template <int BM> __global__ __launch_bounds__(512) void tile_kernel(TileArgs a)
+template <int BM, bool LOW> __global__ __launch_bounds__(512) void tile_kernel(TileArgs a)
 {
-    using T = BTile<BM>;
+    using T = BTile<BM, LOW>;
     __shared__ __attribute__((aligned(16))) uint32_t smem[2 * T::words];
     const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -335,10 +337,10 @@ template <int BM> __global__ __launch_bounds__(512) void tile_kernel(TileArgs a)
     // of G pass through one L2 for all column tiles.
     const int64_t total = a.S * a.n_mt * a.n_jt, per = (total + 7) / 8;
     const int64_t id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if ((int64_t)(blockIdx.x >> 3) >= per || id >= total)
+    if (id >= total)
         return;
     const int64_t jt = id % a.n_jt, mi = id / a.n_jt % a.n_mt, sp = id / a.n_jt / a.n_mt;
-    const int64_t m0 = mi * BM, tile = a.t0 + jt;
+    const int64_t m0 = mi * BM;
     const int64_t c0 = a.nvc * sp / a.S, c1 = a.nvc * (sp + 1) / a.S;
     const int wm0 = wv / T::wj * (BM / T::wm), wj0 = wv % T::wj * T::jb; // first row, first 16-column block
 
@@ -352,21 +354,21 @@ template <int BM> __global__ __launch_bounds__(512) void tile_kernel(TileArgs a)
             lds_dma16<false>(p, &smem[at + (8 * c + wv) * 256]);
         }
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-            lds_dma16<false>(a.codes + ((vc * a.tiles + tile) * 16 + 8 * c + wv) * 256 + lane * 4,
+        for (int c = 0; c < T::cw / 2048; ++c)
+            lds_dma16<false>(a.codes + (vc * a.n_jt + jt) * T::cw + (8 * c + wv) * 256 + lane * 4,
                              &smem[at + T::gw + (8 * c + wv) * 256]);
         if (wv < 2)
-            lds_dma16<false>(a.sc + ((vc * a.tiles + tile) * 8 + 4 * wv) * kVC + lane * 8,
+            lds_dma16<false>(a.sc + ((vc * a.n_jt + jt) * 8 + 4 * wv) * kVC + lane * 8,
                              &smem[at + T::gw + T::cw + wv * 256]);
     };
     const uint32_t magic = vgpr_const(kF16Magic);
-    // offset-binary codes but for the low parts of core and correction
-    f16x2 off0[T::jb / 2], off1[T::jb / 2];
+    f16x2 off[T::jb / 2]; // LOW: a core's or a correction's byte offset
+    bool idle = LOW;      // and whether this wave's columns are padding only
     for (int u = 0; u < T::jb / 2; ++u) {
-        const int part = a.low ? low_part(a.c, jt * 8 + (wj0 >> 1) + u) : 0;
-        const float o = part == 1 || part == 3 ? 0.f : 8.f;
-        off0[u] = f16x2{(_Float16)(-1024.f - o), (_Float16)(-1024.f - o)};
-        off1[u] = f16x2{(_Float16)(-64.f - o), (_Float16)(-64.f - o)};
+        const int64_t unit = jt * 8 + (wj0 >> 1) + u;
+        const _Float16 o = (_Float16)(LOW && unit < a.kst ? -1040.f : -1152.f);
+        off[u] = f16x2{o, o};
+        idle = idle && unit >= a.units;
     }
     f32x4 acc[T::mt][T::jb];
     for (int t = 0; t < T::mt; ++t)
@@ -375,15 +377,24 @@ template <int BM> __global__ __launch_bounds__(512) void tile_kernel(TileArgs a)
 
     auto work = [&](int at) {
         u32x4 c[T::jb];
-        for (int n = 0; n < T::jb; ++n)
-            c[n] = *(const u32x4 *)&smem[at + T::gw + (wj0 + n) * 256 + lane * 4];
+        if constexpr (!LOW)
+            for (int n = 0; n < T::jb; ++n)
+                c[n] = *(const u32x4 *)&smem[at + T::gw + (wj0 + n) * 256 + lane * 4];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
+            if constexpr (LOW)
+                if ((s & 1) == 0)
+                    for (int n = 0; n < T::jb; ++n)
+                        c[n] = *(const u32x4 *)&smem[at + T::gw + (wj0 + n) * 512 + (s >> 1) * 256 + lane * 4];
             f16x8 w[T::jb];
             for (int u = 0; u < T::jb / 2; ++u) {
                 const u32x4 sc = *(const u32x4 *)&smem[at + T::gw + T::cw + ((wj0 >> 1) + u) * (kVC / 2) + 16 * s + 4 * q];
-                w[2 * u] = dequant(c[2 * u][s], sc, magic, off0[u], off1[u]);
-                w[2 * u + 1] = dequant(c[2 * u + 1][s], sc, magic, off0[u], off1[u]);
+                for (int n = 2 * u; n < 2 * u + 2; ++n) {
+                    if constexpr (LOW)
+                        w[n] = dequant8(c[n][2 * (s & 1)], c[n][2 * (s & 1) + 1], sc, magic, off[u]);
+                    else
+                        w[n] = dequant4(c[n][s], sc, magic);
+                }
             }
             for (int t = 0; t < T::mt; ++t) {
                 const int row = wm0 + 16 * t + r; // row & 7 = r & 7
@@ -401,12 +412,14 @@ template <int BM> __global__ __launch_bounds__(512) void tile_kernel(TileArgs a)
         __syncthreads(); // this stage is filled, and everyone is done with the other buffer
         if (vc + 1 < c1)
             fill(T::words - cur, vc + 1);
-        work(cur);
+        if (!LOW || !idle)
+            work(cur);
     }
+    if (idle)
+        return;
     // lane: row m = r of each row tile, four consecutive columns
     for (int n = 0; n < T::jb; ++n) {
-        const int part = a.low ? low_part(a.c, jt * 8 + ((wj0 + n) >> 1)) : 4;
-        const float down = ldexpf(1.f, -a.ex[part == 4 ? 0 : part <= 1 ? 1 : 2]);
+        const float down = ldexpf(1.f, -a.ex[!LOW ? 0 : jt * 8 + ((wj0 + n) >> 1) < a.kst ? 1 : 2]);
         for (int t = 0; t < T::mt; ++t) {
             const int64_t m = m0 + wm0 + 16 * t + r;
             if (m < a.M) {
@@ -421,8 +434,8 @@ template <int BM> __global__ __launch_bounds__(512) void tile_kernel(TileArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// T sB and U: the ranges' sums of the two halves of every column.  T sB is
-// left in two bf16 parts (16 significant bits), as the finish multiplies it.
+// T sB and U: the ranges' sums.  T sB is left in two bf16 parts (16
+// significant bits), as the finish multiplies it.
 // ---------------------------------------------------------------------------
 struct LowArgs {
     int64_t M, S, k, r;
@@ -443,13 +456,10 @@ __global__ __launch_bounds__(256) void low_sum_kernel(LowArgs a)
     const int64_t m = t / w, i = t % w;
     __shared__ float red[kLowLanes][32];
     const bool core = i < kp;
-    const int64_t hi = core ? i : 2 * kp + (i - kp), lo = hi + (core ? kp : rp);
     float s = 0.f;
 #pragma unroll 4
-    for (int64_t p = sh; p < a.S; p += kLowLanes) {
-        const float *x = a.part + (p * a.M + m) * pitch;
-        s += x[hi] + x[lo];
-    }
+    for (int64_t p = sh; p < a.S; p += kLowLanes)
+        s += a.part[(p * a.M + m) * pitch + i];
     red[sh][threadIdx.x & 31] = s;
     __syncthreads();
     if (sh)
@@ -468,7 +478,7 @@ __global__ __launch_bounds__(256) void low_sum_kernel(LowArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// finish: one wave per [16 NT rows x 16 columns]
+// finish: one wave per [16 NT rows x 16 NJ columns]
 // ---------------------------------------------------------------------------
 struct FinishArgs {
     int64_t M, d, k, r, G, g, S, pitch; // pitch: columns of a range's rows
@@ -486,58 +496,74 @@ __device__ __forceinline__ bf16x8 codes_bf16(const int8_t *p)
     return as_bf16x8(c8_bf16(u32x2{w.x ^ 0x80808080u, w.y ^ 0x80808080u}));
 }
 
-template <int NT> __global__ __launch_bounds__(256) void finish_kernel(FinishArgs a)
+template <int NT, int NJ> __global__ __launch_bounds__(256) void finish_kernel(FinishArgs a)
 {
     const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
-    const int64_t blocks = a.d / 16, id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int64_t j0 = id % blocks * 16, m0 = id / blocks * 16 * NT;
+    const int64_t blocks = a.d / (16 * NJ), id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t j0 = id % blocks * 16 * NJ, m0 = id / blocks * 16 * NT;
     if (m0 >= a.M)
         return;
     const int64_t kp = a.c.kst * kUnit, rp = a.c.rst * kUnit;
-    f32x4 acc[NT];
+    f32x4 acc[NT][NJ];
     int64_t m[NT];
     for (int t = 0; t < NT; ++t) {
         m[t] = min(m0 + 16 * t + r, a.M - 1);
-        acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const float *p = a.part + m[t] * a.pitch + j0 + 4 * q;
-#pragma unroll 8
-        for (int64_t i = 0; i < a.S; ++i) // the ranges in order
-            acc[t] += *(const f32x4 *)(p + i * a.M * a.pitch);
+        for (int n = 0; n < NJ; ++n) {
+            acc[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
+            const float *p = a.part + m[t] * a.pitch + j0 + 16 * n + 4 * q;
+#pragma unroll(NJ > 1 ? 1 : 8)
+            for (int64_t i = 0; i < a.S; ++i) // the ranges in order
+                acc[t][n] += *(const f32x4 *)(p + i * a.M * a.pitch);
+        }
     }
-#pragma unroll 2
+#pragma unroll(NJ > 1 ? 1 : 2)
     for (int64_t i = 0; i < kp; i += kUnit) {
-        const bf16x8 code = codes_bf16(a.b8t + (j0 + r) * kp + i + 8 * q);
+        bf16x8 code[NJ];
+        for (int n = 0; n < NJ; ++n)
+            code[n] = codes_bf16(a.b8t + (j0 + 16 * n + r) * kp + i + 8 * q);
         for (int t = 0; t < NT; ++t) {
             const int64_t at = m[t] * kp + i + 8 * q;
-            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(code, *(const bf16x8 *)(a.thi + at), acc[t], 0, 0, 0);
-            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(code, *(const bf16x8 *)(a.tlo + at), acc[t], 0, 0, 0);
-        }
-    }
-    for (int64_t i = 0; i < rp; i += kUnit) {
-        const bf16x8 code = codes_bf16(a.d8t + (j0 + r) * rp + i + 8 * q);
-        float sd[8]; // the 16 columns share a group
-        for (int e = 0; e < 8; ++e)
-            sd[e] = i + 8 * q + e < a.r ? a.sd[(i + 8 * q + e) * a.G + j0 / a.g] : 0.f;
-        for (int t = 0; t < NT; ++t) {
-            float x[8];
-            load8(a.u + m[t] * rp + i + 8 * q, x);
-            bf16x8 hi, lo; // U sD in two bf16 parts against the exact codes
-            for (int e = 0; e < 8; ++e) {
-                x[e] *= sd[e];
-                hi[e] = (__bf16)x[e];
-                lo[e] = (__bf16)(x[e] - (float)hi[e]);
+            const bf16x8 hi = *(const bf16x8 *)(a.thi + at), lo = *(const bf16x8 *)(a.tlo + at);
+            for (int n = 0; n < NJ; ++n) {
+                acc[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(code[n], hi, acc[t][n], 0, 0, 0);
+                acc[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(code[n], lo, acc[t][n], 0, 0, 0);
             }
-            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(code, hi, acc[t], 0, 0, 0);
-            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(code, lo, acc[t], 0, 0, 0);
         }
     }
-    for (int t = 0; t < NT; ++t)
-        if (m0 + 16 * t + r < a.M) {
-            u16x4u o;
-            for (int i = 0; i < 4; ++i)
-                o[i] = __builtin_bit_cast(uint16_t, (__bf16)acc[t][i]);
-            *(u16x4u *)(a.dx + m[t] * a.d + j0 + 4 * q) = o;
+    // U sD in two bf16 parts against the exact codes; NJ pairs of 16 columns
+    // share a group by twos (groups are multiples of 32 columns)
+    constexpr int NP = NJ > 1 ? 2 : 1;
+    for (int64_t i = 0; i < rp; i += kUnit)
+        for (int p = 0; p < NJ; p += NP) {
+            bf16x8 code[NP];
+            for (int n = 0; n < NP; ++n)
+                code[n] = codes_bf16(a.d8t + (j0 + 16 * (p + n) + r) * rp + i + 8 * q);
+            float sd[8];
+            for (int e = 0; e < 8; ++e)
+                sd[e] = i + 8 * q + e < a.r ? a.sd[(i + 8 * q + e) * a.G + (j0 + 16 * p) / a.g] : 0.f;
+            for (int t = 0; t < NT; ++t) {
+                float x[8];
+                load8(a.u + m[t] * rp + i + 8 * q, x);
+                bf16x8 hi, lo;
+                for (int e = 0; e < 8; ++e) {
+                    x[e] *= sd[e];
+                    hi[e] = (__bf16)x[e];
+                    lo[e] = (__bf16)(x[e] - (float)hi[e]);
+                }
+                for (int n = 0; n < NP; ++n) {
+                    acc[t][p + n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(code[n], hi, acc[t][p + n], 0, 0, 0);
+                    acc[t][p + n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(code[n], lo, acc[t][p + n], 0, 0, 0);
+                }
+            }
         }
+    for (int t = 0; t < NT; ++t)
+        if (m0 + 16 * t + r < a.M)
+            for (int n = 0; n < NJ; ++n) {
+                u16x4u o;
+                for (int i = 0; i < 4; ++i)
+                    o[i] = __builtin_bit_cast(uint16_t, (__bf16)acc[t][n][i]);
+                *(u16x4u *)(a.dx + m[t] * a.d + j0 + 16 * n + 4 * q) = o;
+            }
 }
 
 // ---------------------------------------------------------------------------
@@ -552,8 +578,8 @@ struct Plan {
 
 // Row tile by the rows there are.  Ranges: the vocabulary is cut so that the
 // workgroups fill the compute units' places (by LDS: one of 128 rows, two of
-// 64, three of 32) in whole rounds: of up to kRounds rounds the count whose
-// share of idle places and of stages past the first fill is least.
+// 64, three of 32; one of the low-rank columns, whose codes are wider) in whole
+// rounds: the count whose rounds, with two stages of latency each, are shortest.
 constexpr int64_t kCu = 256, kMaxWg = 1024, kMinChunks = 8;
 
 Plan plan_of(const Cols &c, int64_t M, int64_t nvc)
@@ -561,8 +587,7 @@ Plan plan_of(const Cols &c, int64_t M, int64_t nvc)
     Plan p;
     p.bm = M <= 32 ? 32 : M <= 64 ? 64 : 128;
     p.n_mt = (M + p.bm - 1) / p.bm;
-    const int64_t places = kCu * (p.bm == 32 ? 3 : p.bm == 64 ? 2 : 1);
-    auto ranges = [&](int64_t tiles) {
+    auto ranges = [&](int64_t tiles, int64_t places) {
         const int64_t t = std::max<int64_t>(tiles * p.n_mt, 1), most = std::max<int64_t>(1, nvc / kMinChunks);
         int64_t best = 1;
         double least = 1e300;
@@ -576,8 +601,8 @@ Plan plan_of(const Cols &c, int64_t M, int64_t nvc)
         }
         return best;
     };
-    p.Sl = ranges(c.low_tiles());
-    p.Sm = ranges(c.main_tiles());
+    p.Sl = ranges(c.low_tiles(), kCu);
+    p.Sm = ranges(c.main_tiles(), kCu * (p.bm == 32 ? 3 : p.bm == 64 ? 2 : 1));
     return p;
 }
 
@@ -620,8 +645,8 @@ BwWs bw_ws(const Shape &s, int64_t rows)
 struct BackwardState {
     void *block; // the second layout
     size_t block_bytes;
-    uint32_t *codes;
-    uint16_t *sc;
+    uint32_t *codes, *low;
+    uint16_t *sc, *lsc;
     int8_t *b8t, *d8t;
     int32_t *ex;
     void *ws;
@@ -672,8 +697,9 @@ archead_status lay_out(const DevHead &h, BackwardState *b, hipStream_t st)
     a.h = h;
     a.c = cols_of(h.s);
     a.nvc = (h.s.V + kVC - 1) / kVC;
-    const int64_t nblk = a.c.tiles() * 16, nunit = a.c.tiles() * (kJT / kUnit);
-    if (a.nvc * nblk >= int64_t(1) << 31)
+    const int64_t nblk = a.c.main_tiles() * 16, nunit = a.c.main_tiles() * (kJT / kUnit);
+    const int64_t lblk = a.c.low_tiles() * 16, lunit = a.c.low_tiles() * (kJT / kUnit);
+    if (a.nvc * std::max(nblk, lblk) >= int64_t(1) << 31)
         return api_fail(ARCHEAD_ESHAPE, "head too large for the backward's layout");
     size_t off = 0;
     auto place = [&](size_t bytes) {
@@ -683,6 +709,7 @@ archead_status lay_out(const DevHead &h, BackwardState *b, hipStream_t st)
     };
     const size_t kp = a.c.kst * kUnit, rp = a.c.rst * kUnit;
     const size_t o_codes = place(size_t(a.nvc) * nblk * 1024), o_sc = place(size_t(a.nvc) * nunit * kVC * 2);
+    const size_t o_low = place(size_t(a.nvc) * lblk * 2048), o_lsc = place(size_t(a.nvc) * lunit * kVC * 2);
     const size_t o_b8 = place(h.s.d * kp), o_d8 = place(h.s.d * rp), o_ex = place(64);
     archead_status s = device_alloc(&b->block, off, "backward layout");
     if (s != ARCHEAD_OK)
@@ -691,6 +718,8 @@ archead_status lay_out(const DevHead &h, BackwardState *b, hipStream_t st)
     char *p = (char *)b->block;
     a.codes = b->codes = (uint32_t *)(p + o_codes);
     a.sc = b->sc = (uint16_t *)(p + o_sc);
+    a.low = b->low = (uint32_t *)(p + o_low);
+    a.lsc = b->lsc = (uint16_t *)(p + o_lsc);
     a.b8t = b->b8t = (int8_t *)(p + o_b8);
     a.d8t = b->d8t = (int8_t *)(p + o_d8);
     a.ex = b->ex = (int32_t *)(p + o_ex);
@@ -700,6 +729,10 @@ archead_status lay_out(const DevHead &h, BackwardState *b, hipStream_t st)
     hipLaunchKernelGGL(exponent_kernel, dim3(1), dim3(64), 0, st, a);
     hipLaunchKernelGGL(codes_kernel, dim3((unsigned)(a.nvc * nblk)), dim3(256), 0, st, a, nblk);
     hipLaunchKernelGGL(scales_kernel, dim3((unsigned)(a.nvc * nunit)), dim3(kVC), 0, st, a, nunit);
+    if (lblk) {
+        hipLaunchKernelGGL(low_codes_kernel, dim3((unsigned)(a.nvc * lblk)), dim3(512), 0, st, a, lblk);
+        hipLaunchKernelGGL(low_scales_kernel, dim3((unsigned)(a.nvc * lunit)), dim3(kVC), 0, st, a, lunit);
+    }
     if (kp)
         hipLaunchKernelGGL(columns_kernel, dim3(1024), dim3(256), 0, st, h.b8, h.s.k, h.s.d, (int64_t)kp, a.b8t);
     if (rp)
@@ -708,20 +741,15 @@ archead_status lay_out(const DevHead &h, BackwardState *b, hipStream_t st)
     return ARCHEAD_OK;
 }
 
-template <int BM> void launch_tiles(const TileArgs &a, hipStream_t st)
+template <bool LOW> void run_tiles(int bm, const TileArgs &a, hipStream_t st)
 {
-    const int64_t per = (a.S * a.n_mt * a.n_jt + 7) / 8;
-    hipLaunchKernelGGL(tile_kernel<BM>, dim3((unsigned)(per * 8)), dim3(512), 0, st, a);
-}
-
-void run_tiles(int bm, const TileArgs &a, hipStream_t st)
-{
+    const dim3 grid((unsigned)((a.S * a.n_mt * a.n_jt + 7) / 8 * 8));
     if (bm == 32)
-        launch_tiles<32>(a, st);
+        hipLaunchKernelGGL((tile_kernel<32, LOW>), grid, dim3(512), 0, st, a);
     else if (bm == 64)
-        launch_tiles<64>(a, st);
+        hipLaunchKernelGGL((tile_kernel<64, LOW>), grid, dim3(512), 0, st, a);
     else
-        launch_tiles<128>(a, st);
+        hipLaunchKernelGGL((tile_kernel<128, LOW>), grid, dim3(512), 0, st, a);
 }
 
 // up to b.rows rows of G
@@ -758,41 +786,39 @@ void backward_rows(const DevHead &h, const BackwardState &b, int64_t M, const vo
     TileArgs t{};
     t.g16 = ga.g16;
     t.unscale = ga.unscale;
-    t.codes = b.codes;
-    t.sc = b.sc;
     t.ex = b.ex;
     t.M = M;
     t.Vp = ga.Vp;
     t.nvc = nvc;
-    t.tiles = c.tiles();
     t.n_mt = p.n_mt;
-    t.c = c;
+    t.kst = c.kst;
+    t.units = c.low_units();
     float *low = (float *)(ws + L.low), *u = (float *)(ws + L.u), *part = (float *)(ws + L.part);
     uint16_t *thi = (uint16_t *)(ws + L.thi), *tlo = (uint16_t *)(ws + L.tlo);
     if (c.low_tiles() > 0) {
-        t.t0 = c.main_tiles();
+        t.codes = b.low;
+        t.sc = b.lsc;
         t.n_jt = c.low_tiles();
         t.S = p.Sl;
-        t.low = 1;
         t.part = low;
-        run_tiles(p.bm, t, st);
+        run_tiles<true>(p.bm, t, st);
         const LowArgs l{M, p.Sl, s.k, s.r, c, low, h.sb, thi, tlo, u};
         hipLaunchKernelGGL(low_sum_kernel, dim3((unsigned)(M * (c.kst + c.rst))), dim3(256), 0, st, l);
     }
-    t.t0 = 0;
+    t.codes = b.codes;
+    t.sc = b.sc;
     t.n_jt = c.main_tiles();
     t.S = p.Sm;
-    t.low = 0;
     t.part = part;
-    run_tiles(p.bm, t, st);
+    run_tiles<false>(p.bm, t, st);
     const FinishArgs f{M, s.d, s.k, s.r, s.G(), s.g, p.Sm, c.main_tiles() * kJT, c, part, u, h.sd, thi, tlo,
                        b.b8t, b.d8t, dx};
     if (M <= 256) { // few rows: more waves, for the latency of the ranges' loads
         const int64_t waves = (M + 15) / 16 * (s.d / 16);
-        hipLaunchKernelGGL(finish_kernel<1>, dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, f);
+        hipLaunchKernelGGL((finish_kernel<1, 1>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, f);
     } else {
-        const int64_t waves = (M + 63) / 64 * (s.d / 16);
-        hipLaunchKernelGGL(finish_kernel<4>, dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, f);
+        const int64_t waves = (M + 63) / 64 * (s.d / 64);
+        hipLaunchKernelGGL((finish_kernel<4, 4>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, f);
     }
 }
 

@@ -5,9 +5,7 @@ Tolerance: a code times its scale is rounded once to fp16 (2^-11 of it), fp32
 entries of G too (bf16 ones are exact within 2^28 of the row's largest, below
 that off by 2^-39 of it); a sum of n terms in fp32, each addition rounded or
 truncated, is off by n 2^-23 of the terms' magnitudes; T and U carry 16 bits
-into the second product (2^-16); dX is rounded once (2^-8).  A core code a
-enters as 2 h + b and a correction code c as 16 h + l: the parts' magnitudes
-are at most |a| + 2 and |c| + 30.
+into the second product (2^-16); dX is rounded once (2^-8).
 """
 import numpy as np
 import pytest
@@ -33,12 +31,12 @@ def half(bits):
 
 
 def magnitudes(f):
-    """|sR R4|, the core's two factors' and the correction's, in the parts they enter by."""
+    """|sR R4|, the core's two factors' and the correction's."""
     R = np.abs(layout.unpack_r4(f["R4"], f["d"]).astype(float))
     R = R * np.repeat(np.abs(half(f["sR"])), f["g"], axis=1)
-    A = (np.abs(f["A5"].astype(float)) + 2) * np.abs(half(f["sA"]))[:, None]
+    A = np.abs(f["A5"].astype(float)) * np.abs(half(f["sA"]))[:, None]
     B = np.abs(f["B8"].astype(float)) * np.abs(half(f["sB"]))[:, None]
-    C = (np.abs(f["C8"].astype(float)) + 30) * np.abs(half(f["sC"]))[:, None]
+    C = np.abs(f["C8"].astype(float)) * np.abs(half(f["sC"]))[:, None]
     D = np.abs(f["D8"].astype(float)) * np.repeat(np.abs(half(f["sD"])), f["g"], axis=1)
     return R, A, B, C, D
 
