@@ -24,6 +24,7 @@
 #include <cmath>
 #include <new>
 #include <string>
+#include <type_traits>
 
 #include "api_internal.hpp"
 #include "archead.h"
@@ -33,7 +34,8 @@ namespace archead {
 namespace {
 
 constexpr int kVC = 128;    // vocabulary rows per stage ("chunk")
-constexpr int kJT = 256;    // columns per tile
+constexpr int kJT = 256;    // columns per tile of dX
+constexpr int kLT = 128;    // columns per tile of T and U
 constexpr int kUnit = 32;   // columns that share a scale
 constexpr int64_t kChunkM = 2048; // most rows of G held at a time
 
@@ -47,7 +49,7 @@ struct Cols {
     int64_t d, kst, rst;
     __host__ __device__ int64_t main_tiles() const { return (d + kJT - 1) / kJT; }
     __host__ __device__ int64_t low_units() const { return kst + rst; }
-    __host__ __device__ int64_t low_tiles() const { return (low_units() * kUnit + kJT - 1) / kJT; }
+    __host__ __device__ int64_t low_tiles() const { return (low_units() * kUnit + kLT - 1) / kLT; }
 };
 Cols cols_of(const Shape &s) { return Cols{s.d, s.kst(), s.rst()}; }
 
@@ -216,6 +218,12 @@ struct GArgs {
     float *unscale;        // [M] 2^-f_m
 };
 
+// f_m: mx 2^f in [2^14, 2^15) (0 for a row of zeros or with an infinity)
+__device__ __forceinline__ int row_exponent(float mx)
+{
+    return mx > 0.f && mx <= 3.4028235e38f ? min(14 - ilogbf(mx), 126) : 0;
+}
+
 template <typename T> __device__ __forceinline__ void load8_edge(const T *row, int64_t v, int64_t V, float x[8])
 {
     if (v + 8 <= V) {
@@ -255,17 +263,73 @@ template <typename T> __global__ __launch_bounds__(256) void convert_kernel(GArg
     float mx = 0.f;
     for (int64_t i = 0; i < a.S; ++i)
         mx = fmaxf(mx, a.amax[m * a.S + i]);
-    int f = 0;
-    if (mx > 0.f && mx <= 3.4028235e38f) {
-        f = 14 - ilogbf(mx);
-        f = f > 126 ? 126 : f;
-    }
+    const int f = row_exponent(mx);
     if (sl == 0 && threadIdx.x == 0)
         a.unscale[m] = ldexpf(1.f, -f);
     const float up = ldexpf(1.f, f);
     uint16_t *out = a.g16 + m * a.Vp;
     const int64_t end = min((sl + 1) * a.slice, a.Vp);
     for (int64_t v = sl * a.slice + 8 * threadIdx.x; v < end; v += 256 * 8) {
+        float x[8];
+        load8_edge(row, v, a.V, x);
+        f16x8 o;
+        for (int i = 0; i < 8; ++i)
+            o[i] = (_Float16)(x[i] * up);
+        *(f16x8 *)(out + v) = o;
+    }
+}
+
+// Both in one pass over a row, a workgroup each: the second half finds the
+// row's first H vectors of each thread in registers, the rest in the caches.
+constexpr int kWide = 1024;
+template <int H, typename T> __global__ __launch_bounds__(kWide) void convert_row_kernel(GArgs a)
+{
+    __shared__ float red[kWide / 64];
+    const int64_t m = blockIdx.x;
+    const T *row = (const T *)a.g + m * a.ld;
+    typedef T Raw __attribute__((ext_vector_type(8), aligned(sizeof(T))));
+    Raw held[H];
+    const int64_t nv = a.V / 8; // whole vectors; the rest of the row is one step of the loop below
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+        held[h] = nv ? *(const Raw *)(row + min((int64_t)threadIdx.x + h * kWide, nv - 1) * 8) : Raw{};
+    auto value = [](T x) { return load1(&x); };
+    float mx = 0.f;
+#pragma unroll
+    for (int h = 0; h < H; ++h) // past the end the last vector again: the maximum stays
+        for (int i = 0; i < 8; ++i)
+            mx = fmaxf(mx, fabsf(value(held[h][i])));
+    for (int64_t v = 8 * ((int64_t)threadIdx.x + H * kWide); v < a.V; v += 8 * kWide) {
+        float x[8];
+        load8_edge(row, v, a.V, x);
+        for (int i = 0; i < 8; ++i)
+            mx = fmaxf(mx, fabsf(x[i]));
+    }
+    if (nv < H * kWide && threadIdx.x < a.V - nv * 8)
+        mx = fmaxf(mx, fabsf(load1(row + nv * 8 + threadIdx.x)));
+    for (int off = 32; off >= 1; off >>= 1)
+        mx = fmaxf(mx, __shfl_xor(mx, off));
+    if ((threadIdx.x & 63) == 0)
+        red[threadIdx.x >> 6] = mx;
+    __syncthreads();
+    for (int w = 0; w < kWide / 64; ++w)
+        mx = fmaxf(mx, red[w]);
+    const int f = row_exponent(mx);
+    if (threadIdx.x == 0)
+        a.unscale[m] = ldexpf(1.f, -f);
+    const float up = ldexpf(1.f, f);
+    uint16_t *out = a.g16 + m * a.Vp;
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+        const int64_t v = threadIdx.x + h * kWide;
+        if (v < nv) {
+            f16x8 o;
+            for (int i = 0; i < 8; ++i)
+                o[i] = (_Float16)(value(held[h][i]) * up);
+            *(f16x8 *)(out + 8 * v) = o;
+        }
+    }
+    for (int64_t v = 8 * (threadIdx.x + min((int64_t)H * kWide, nv)); v < a.Vp; v += 8 * kWide) {
         float x[8];
         load8_edge(row, v, a.V, x);
         f16x8 o;
@@ -287,7 +351,7 @@ struct TileArgs {
     int64_t M, Vp, nvc;
     int64_t n_jt, n_mt, S; // column tiles, row tiles, vocabulary ranges
     int64_t kst, units;    // core units and all units of the low-rank columns
-    float *part;           // [S][M][n_jt * 256]
+    float *part;           // [S][M][columns of the tiles]
 };
 
 __device__ __forceinline__ f16x2 as_h2(uint32_t x) { return __builtin_bit_cast(f16x2, x); }
@@ -319,17 +383,23 @@ __device__ __forceinline__ f16x8 dequant8(uint32_t w0, uint32_t w1, u32x4 s, uin
 }
 
 template <int BM, bool LOW> struct BTile {
-    static constexpr int wm = BM == 128 ? 2 : 1, wj = 8 / wm;      // waves along rows and columns
-    static constexpr int mt = BM / wm / 16, jb = kJT / wj / 16;    // 16 x 16 tiles per wave
+    static constexpr int wm = BM >= 128 ? 2 : 1, wj = 8 / wm;      // waves along rows and columns
+    // vocabulary rows of G per stage: half a chunk where a whole one of 256
+    // rows would not fit twice; codes and scales come by whole chunks
+    static constexpr int gv = BM == 256 ? kVC / 2 : kVC, parts = kVC / gv;
+    static constexpr int jt = LOW ? kLT : kJT;
+    static constexpr int mt = BM / wm / 16, jb = jt / wj / 16;     // 16 x 16 tiles per wave
+    static constexpr int un = jb > 1 ? jb / 2 : 1;                 // units of 32 columns per wave
     static constexpr int bw = LOW ? 512 : 256;                     // words of a 16-column block's codes
-    static constexpr int gw = BM * kVC / 2, cw = 16 * bw, sw = 8 * kVC / 2; // words of a stage: G, codes, scales
-    static constexpr int words = gw + cw + sw;
+    static constexpr int su = jt / kUnit;                          // units of a tile
+    static constexpr int gw = BM * gv / 2, cw = jt / 16 * bw, sw = su * kVC / 2; // words of a buffer: G, codes, scales
+    static constexpr int kw = cw + sw, words = 2 * (gw + kw);      // G twice, codes with scales twice
 };
 
 template <int BM, bool LOW> __global__ __launch_bounds__(512) void tile_kernel(TileArgs a)
 {
     using T = BTile<BM, LOW>;
-    __shared__ __attribute__((aligned(16))) uint32_t smem[2 * T::words];
+    __shared__ __attribute__((aligned(16))) uint32_t smem[T::words];
     const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // Workgroup b runs on XCD b mod 8; an XCD takes a contiguous run of
@@ -344,28 +414,37 @@ template <int BM, bool LOW> __global__ __launch_bounds__(512) void tile_kernel(T
     const int64_t c0 = a.nvc * sp / a.S, c1 = a.nvc * (sp + 1) / a.S;
     const int wm0 = wv / T::wj * (BM / T::wm), wj0 = wv % T::wj * T::jb; // first row, first 16-column block
 
-    auto fill = [&](int at, int64_t vc) {
-        // G: 1 KiB copies of 4 rows x 256 bytes, 16-byte pieces exchanged by
-        // the row's low bits so that eight rows' reads fall on different banks
+    // Stage i of this range: G's vocabulary rows T::gv i .., and with every
+    // T::parts-th stage a chunk's codes.  G comes in 1 KiB copies of rows of
+    // 2 T::gv bytes, 16-byte pieces exchanged by the row's low bits so that
+    // eight rows' reads fall on different banks.
+    constexpr int pieces = T::gv / 8, rows = 64 / pieces; // of a row; of a copy
+    auto fill = [&](int64_t i) {
+        const int g = (int)(i & 1) * T::gw;
+        const uint16_t *v = a.g16 + c0 * kVC + i * T::gv;
 #pragma unroll
-        for (int c = 0; c < BM / 32; ++c) {
-            const int row = 4 * (8 * c + wv) + q;
-            const uint16_t *p = a.g16 + min(m0 + row, a.M - 1) * a.Vp + vc * kVC + 8 * (r ^ (row & 7));
-            lds_dma16<false>(p, &smem[at + (8 * c + wv) * 256]);
+        for (int c = 0; c < T::gw / 2048; ++c) {
+            const int row = rows * (8 * c + wv) + lane / pieces;
+            lds_dma16<false>(v + min(m0 + row, a.M - 1) * a.Vp + 8 * ((lane % pieces) ^ (row & 7)),
+                             &smem[g + (8 * c + wv) * 256]);
         }
+        if (i % T::parts == 0) {
+            const int64_t vc = c0 + i / T::parts;
+            const int k = 2 * T::gw + (int)(i / T::parts & 1) * T::kw;
 #pragma unroll
-        for (int c = 0; c < T::cw / 2048; ++c)
-            lds_dma16<false>(a.codes + (vc * a.n_jt + jt) * T::cw + (8 * c + wv) * 256 + lane * 4,
-                             &smem[at + T::gw + (8 * c + wv) * 256]);
-        if (wv < 2)
-            lds_dma16<false>(a.sc + ((vc * a.n_jt + jt) * 8 + 4 * wv) * kVC + lane * 8,
-                             &smem[at + T::gw + T::cw + wv * 256]);
+            for (int c = 0; c < T::cw / 2048; ++c)
+                lds_dma16<false>(a.codes + (vc * a.n_jt + jt) * T::cw + (8 * c + wv) * 256 + lane * 4,
+                                 &smem[k + (8 * c + wv) * 256]);
+            if (wv < T::sw / 256)
+                lds_dma16<false>(a.sc + ((vc * a.n_jt + jt) * T::su + 4 * wv) * kVC + lane * 8,
+                                 &smem[k + T::cw + wv * 256]);
+        }
     };
     const uint32_t magic = vgpr_const(kF16Magic);
-    f16x2 off[T::jb / 2]; // LOW: a core's or a correction's byte offset
-    bool idle = LOW;      // and whether this wave's columns are padding only
-    for (int u = 0; u < T::jb / 2; ++u) {
-        const int64_t unit = jt * 8 + (wj0 >> 1) + u;
+    f16x2 off[T::un]; // LOW: a core's or a correction's byte offset
+    bool idle = LOW;  // and whether this wave's columns are padding only
+    for (int u = 0; u < T::un; ++u) {
+        const int64_t unit = jt * T::su + (wj0 >> 1) + u;
         const _Float16 o = (_Float16)(LOW && unit < a.kst ? -1040.f : -1152.f);
         off[u] = f16x2{o, o};
         idle = idle && unit >= a.units;
@@ -375,21 +454,23 @@ template <int BM, bool LOW> __global__ __launch_bounds__(512) void tile_kernel(T
         for (int n = 0; n < T::jb; ++n)
             acc[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    auto work = [&](int at) {
-        u32x4 c[T::jb];
-        if constexpr (!LOW)
+    u32x4 c[T::jb];
+    // the 32-row steps of part h of a chunk
+    auto work = [&](int g, int k, auto part) {
+        constexpr int h = decltype(part)::value;
+        if constexpr (!LOW && h == 0)
             for (int n = 0; n < T::jb; ++n)
-                c[n] = *(const u32x4 *)&smem[at + T::gw + (wj0 + n) * 256 + lane * 4];
+                c[n] = *(const u32x4 *)&smem[k + (wj0 + n) * 256 + lane * 4];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
+        for (int s = h * 4 / T::parts; s < (h + 1) * 4 / T::parts; ++s) {
             if constexpr (LOW)
                 if ((s & 1) == 0)
                     for (int n = 0; n < T::jb; ++n)
-                        c[n] = *(const u32x4 *)&smem[at + T::gw + (wj0 + n) * 512 + (s >> 1) * 256 + lane * 4];
+                        c[n] = *(const u32x4 *)&smem[k + (wj0 + n) * 512 + (s >> 1) * 256 + lane * 4];
             f16x8 w[T::jb];
-            for (int u = 0; u < T::jb / 2; ++u) {
-                const u32x4 sc = *(const u32x4 *)&smem[at + T::gw + T::cw + ((wj0 >> 1) + u) * (kVC / 2) + 16 * s + 4 * q];
-                for (int n = 2 * u; n < 2 * u + 2; ++n) {
+            for (int u = 0; u < T::un; ++u) {
+                const u32x4 sc = *(const u32x4 *)&smem[k + T::cw + ((wj0 >> 1) + u) * (kVC / 2) + 16 * s + 4 * q];
+                for (int n = 2 * u; n < 2 * u + 2 && n < T::jb; ++n) {
                     if constexpr (LOW)
                         w[n] = dequant8(c[n][2 * (s & 1)], c[n][2 * (s & 1) + 1], sc, magic, off[u]);
                     else
@@ -398,28 +479,35 @@ template <int BM, bool LOW> __global__ __launch_bounds__(512) void tile_kernel(T
             }
             for (int t = 0; t < T::mt; ++t) {
                 const int row = wm0 + 16 * t + r; // row & 7 = r & 7
-                const f16x8 g = *(const f16x8 *)&smem[at + row * (kVC / 2) + 4 * ((4 * s + q) ^ (r & 7))];
+                const f16x8 x = *(const f16x8 *)&smem[g + row * (T::gv / 2) + 4 * ((4 * (s % (4 / T::parts)) + q) ^ (r & 7))];
                 for (int n = 0; n < T::jb; ++n)
-                    acc[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[n], g, acc[t][n], 0, 0, 0);
+                    acc[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[n], x, acc[t][n], 0, 0, 0);
             }
         }
     };
-    if (c0 < c1)
-        fill(0, c0);
-    for (int64_t vc = c0; vc < c1; ++vc) {
-        const int cur = (vc - c0) & 1 ? T::words : 0;
-        wait_vm_all();
-        __syncthreads(); // this stage is filled, and everyone is done with the other buffer
-        if (vc + 1 < c1)
-            fill(T::words - cur, vc + 1);
-        if (!LOW || !idle)
-            work(cur);
+    const int64_t stages = (c1 - c0) * T::parts;
+    if (stages > 0)
+        fill(0);
+    for (int64_t i = 0; i < stages; i += T::parts) {
+        const int k = 2 * T::gw + (int)(i / T::parts & 1) * T::kw;
+        auto stage = [&](auto part) {
+            const int64_t j = i + decltype(part)::value;
+            wait_vm_all();
+            __syncthreads(); // this stage is filled, and everyone is done with the other buffers
+            if (j + 1 < stages)
+                fill(j + 1);
+            if (!LOW || !idle)
+                work((int)(j & 1) * T::gw, k, part);
+        };
+        stage(std::integral_constant<int, 0>{});
+        if constexpr (T::parts == 2)
+            stage(std::integral_constant<int, 1>{});
     }
     if (idle)
         return;
     // lane: row m = r of each row tile, four consecutive columns
     for (int n = 0; n < T::jb; ++n) {
-        const float down = ldexpf(1.f, -a.ex[!LOW ? 0 : jt * 8 + ((wj0 + n) >> 1) < a.kst ? 1 : 2]);
+        const float down = ldexpf(1.f, -a.ex[!LOW ? 0 : jt * T::su + ((wj0 + n) >> 1) < a.kst ? 1 : 2]);
         for (int t = 0; t < T::mt; ++t) {
             const int64_t m = m0 + wm0 + 16 * t + r;
             if (m < a.M) {
@@ -427,7 +515,7 @@ template <int BM, bool LOW> __global__ __launch_bounds__(512) void tile_kernel(T
                 const float un = a.unscale[m];
                 for (int i = 0; i < 4; ++i)
                     o[i] = o[i] * down * un;
-                *(f32x4 *)(a.part + (sp * a.M + m) * a.n_jt * kJT + jt * kJT + (wj0 + n) * 16 + 4 * q) = o;
+                *(f32x4 *)(a.part + ((sp * a.M + m) * a.n_jt + jt) * T::jt + (wj0 + n) * 16 + 4 * q) = o;
             }
         }
     }
@@ -449,7 +537,7 @@ constexpr int kLowLanes = 8; // threads that share a column's ranges
 
 __global__ __launch_bounds__(256) void low_sum_kernel(LowArgs a)
 {
-    const int64_t kp = a.c.kst * kUnit, rp = a.c.rst * kUnit, w = kp + rp, pitch = a.c.low_tiles() * kJT;
+    const int64_t kp = a.c.kst * kUnit, rp = a.c.rst * kUnit, w = kp + rp, pitch = a.c.low_tiles() * kLT;
     // thread (column, share): 32 columns of one row per workgroup (w is a multiple of 32)
     const int64_t t = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
     const int sh = threadIdx.x >> 5;
@@ -571,39 +659,42 @@ template <int NT, int NJ> __global__ __launch_bounds__(256) void finish_kernel(F
 // ---------------------------------------------------------------------------
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
+struct Launch {
+    int bm;          // rows of a tile
+    int64_t n_mt, S; // row tiles, vocabulary ranges
+};
 struct Plan {
-    int64_t n_mt, Sl, Sm; // row tiles, vocabulary ranges of the low-rank and the main launch
-    int bm;
+    Launch low, main;
 };
 
 // Row tile by the rows there are.  Ranges: the vocabulary is cut so that the
 // workgroups fill the compute units' places (by LDS: one of 128 rows, two of
-// 64, three of 32; one of the low-rank columns, whose codes are wider) in whole
-// rounds: the count whose rounds, with two stages of latency each, are shortest.
+// 64, three of 32) in whole rounds: the count whose rounds, with two stages of latency each, are shortest.
 constexpr int64_t kCu = 256, kMaxWg = 1024, kMinChunks = 8;
+constexpr int64_t kWideM = 256; // rows from which dX's tiles have 256
+
+Launch launch_of(int64_t M, int64_t tiles, int64_t nvc, bool low)
+{
+    Launch p;
+    p.bm = M <= 32 ? 32 : M <= 64 ? 64 : low || M < kWideM ? 128 : 256;
+    p.n_mt = (M + p.bm - 1) / p.bm;
+    const int64_t places = kCu * (p.bm == 32 ? 3 : p.bm == 64 ? 2 : 1);
+    const int64_t t = std::max<int64_t>(tiles * p.n_mt, 1), most = std::max<int64_t>(1, nvc / kMinChunks);
+    double least = 1e300;
+    p.S = 1;
+    for (int64_t S = 1; S <= most && (S == 1 || S * t <= kMaxWg); ++S) {
+        const double cost = double((S * t + places - 1) / places) * (double((nvc + S - 1) / S) + 2.0);
+        if (cost < least * 0.995) {
+            least = cost;
+            p.S = S;
+        }
+    }
+    return p;
+}
 
 Plan plan_of(const Cols &c, int64_t M, int64_t nvc)
 {
-    Plan p;
-    p.bm = M <= 32 ? 32 : M <= 64 ? 64 : 128;
-    p.n_mt = (M + p.bm - 1) / p.bm;
-    auto ranges = [&](int64_t tiles, int64_t places) {
-        const int64_t t = std::max<int64_t>(tiles * p.n_mt, 1), most = std::max<int64_t>(1, nvc / kMinChunks);
-        int64_t best = 1;
-        double least = 1e300;
-        for (int64_t S = 1; S <= most && (S == 1 || S * t <= kMaxWg); ++S) {
-            // rounds of a range's chunks, each with about two stages of latency
-            const double cost = double((S * t + places - 1) / places) * (double((nvc + S - 1) / S) + 2.0);
-            if (cost < least * 0.995) {
-                least = cost;
-                best = S;
-            }
-        }
-        return best;
-    };
-    p.Sl = ranges(c.low_tiles(), kCu);
-    p.Sm = ranges(c.main_tiles(), kCu * (p.bm == 32 ? 3 : p.bm == 64 ? 2 : 1));
-    return p;
+    return Plan{launch_of(M, c.low_tiles(), nvc, true), launch_of(M, c.main_tiles(), nvc, false)};
 }
 
 struct BwWs {
@@ -619,7 +710,7 @@ BwWs bw_ws(const Shape &s, int64_t rows)
     const int64_t nvc = (s.V + kVC - 1) / kVC;
     auto parts = [&](int64_t tiles) {
         const int64_t one = rows * tiles * kJT, all = one * std::max<int64_t>(1, nvc / kMinChunks);
-        return std::max(one, std::min(all, kMaxWg * 128 * kJT));
+        return std::max(one, std::min(all, kMaxWg * 256 * kJT));
     };
     BwWs w;
     size_t off = 0;
@@ -698,7 +789,7 @@ archead_status lay_out(const DevHead &h, BackwardState *b, hipStream_t st)
     a.c = cols_of(h.s);
     a.nvc = (h.s.V + kVC - 1) / kVC;
     const int64_t nblk = a.c.main_tiles() * 16, nunit = a.c.main_tiles() * (kJT / kUnit);
-    const int64_t lblk = a.c.low_tiles() * 16, lunit = a.c.low_tiles() * (kJT / kUnit);
+    const int64_t lblk = a.c.low_tiles() * (kLT / 16), lunit = a.c.low_tiles() * (kLT / kUnit);
     if (a.nvc * std::max(nblk, lblk) >= int64_t(1) << 31)
         return api_fail(ARCHEAD_ESHAPE, "head too large for the backward's layout");
     size_t off = 0;
@@ -748,8 +839,10 @@ template <bool LOW> void run_tiles(int bm, const TileArgs &a, hipStream_t st)
         hipLaunchKernelGGL((tile_kernel<32, LOW>), grid, dim3(512), 0, st, a);
     else if (bm == 64)
         hipLaunchKernelGGL((tile_kernel<64, LOW>), grid, dim3(512), 0, st, a);
-    else
+    else if (LOW || bm == 128)
         hipLaunchKernelGGL((tile_kernel<128, LOW>), grid, dim3(512), 0, st, a);
+    else if constexpr (!LOW)
+        hipLaunchKernelGGL((tile_kernel<256, LOW>), grid, dim3(512), 0, st, a);
 }
 
 // up to b.rows rows of G
@@ -775,7 +868,13 @@ void backward_rows(const DevHead &h, const BackwardState &b, int64_t M, const vo
     ga.g16 = (uint16_t *)(ws + L.g16);
     ga.unscale = (float *)(ws + L.unscale);
     const dim3 grid((unsigned)(M * ga.S));
-    if (type == ARCHEAD_F32) {
+    // long rows enough to fill most of a round of compute units: one pass each
+    const bool whole = s.V >= kWide * 8 && 10 * M >= 7 * ((M + kCu - 1) / kCu * kCu);
+    if (whole && type == ARCHEAD_F32)
+        hipLaunchKernelGGL((convert_row_kernel<8, float>), dim3((unsigned)M), dim3(kWide), 0, st, ga);
+    else if (whole)
+        hipLaunchKernelGGL((convert_row_kernel<12, uint16_t>), dim3((unsigned)M), dim3(kWide), 0, st, ga);
+    else if (type == ARCHEAD_F32) {
         hipLaunchKernelGGL(amax_kernel<float>, grid, dim3(256), 0, st, ga);
         hipLaunchKernelGGL(convert_kernel<float>, grid, dim3(256), 0, st, ga);
     } else {
@@ -790,7 +889,6 @@ void backward_rows(const DevHead &h, const BackwardState &b, int64_t M, const vo
     t.M = M;
     t.Vp = ga.Vp;
     t.nvc = nvc;
-    t.n_mt = p.n_mt;
     t.kst = c.kst;
     t.units = c.low_units();
     float *low = (float *)(ws + L.low), *u = (float *)(ws + L.u), *part = (float *)(ws + L.part);
@@ -799,21 +897,23 @@ void backward_rows(const DevHead &h, const BackwardState &b, int64_t M, const vo
         t.codes = b.low;
         t.sc = b.lsc;
         t.n_jt = c.low_tiles();
-        t.S = p.Sl;
+        t.n_mt = p.low.n_mt;
+        t.S = p.low.S;
         t.part = low;
-        run_tiles<true>(p.bm, t, st);
-        const LowArgs l{M, p.Sl, s.k, s.r, c, low, h.sb, thi, tlo, u};
+        run_tiles<true>(p.low.bm, t, st);
+        const LowArgs l{M, p.low.S, s.k, s.r, c, low, h.sb, thi, tlo, u};
         hipLaunchKernelGGL(low_sum_kernel, dim3((unsigned)(M * (c.kst + c.rst))), dim3(256), 0, st, l);
     }
     t.codes = b.codes;
     t.sc = b.sc;
     t.n_jt = c.main_tiles();
-    t.S = p.Sm;
+    t.n_mt = p.main.n_mt;
+    t.S = p.main.S;
     t.part = part;
-    run_tiles<false>(p.bm, t, st);
-    const FinishArgs f{M, s.d, s.k, s.r, s.G(), s.g, p.Sm, c.main_tiles() * kJT, c, part, u, h.sd, thi, tlo,
+    run_tiles<false>(p.main.bm, t, st);
+    const FinishArgs f{M, s.d, s.k, s.r, s.G(), s.g, p.main.S, c.main_tiles() * kJT, c, part, u, h.sd, thi, tlo,
                        b.b8t, b.d8t, dx};
-    if (M <= 256) { // few rows: more waves, for the latency of the ranges' loads
+    if (M <= 512) { // few rows: more waves, for the latency of the ranges' loads
         const int64_t waves = (M + 15) / 16 * (s.d / 16);
         hipLaunchKernelGGL((finish_kernel<1, 1>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, f);
     } else {

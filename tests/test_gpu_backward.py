@@ -80,7 +80,7 @@ def gradient(M, V, seed, dtype="bfloat16", pad=0, kind="softmax"):
 SHAPES = [(16, 128, 0, 0, 32, 1), (1, 128, 5, 3, 128, 2), (37, 256, 16, 4, 64, 3), (130, 384, 0, 8, 96, 5),
           (1000, 128, 33, 0, 128, 16), (2049, 640, 40, 20, 32, 33), (517, 256, 7, 70, 256, 64),
           (3001, 512, 256, 64, 128, 65), (777, 1024, 100, 16, 64, 129), (300, 256, 16, 16, 128, 257),
-          (5003, 384, 24, 12, 32, 31)]
+          (5003, 384, 24, 12, 32, 31), (9001, 128, 8, 4, 128, 200), (16411, 128, 40, 0, 64, 256), (140003, 128, 0, 8, 64, 180)]
 
 
 @pytest.mark.parametrize("V,d,k,r,g,M", SHAPES)
