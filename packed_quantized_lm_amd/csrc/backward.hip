@@ -566,7 +566,9 @@ __global__ __launch_bounds__(256) void low_sum_kernel(LowArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// finish: one wave per [16 NT rows x 16 NJ columns]
+// finish: one wave per [16 NT rows x 16 NJ columns], or with few rows (SPLIT)
+// a workgroup's four waves, each with every fourth range and 32 columns of the
+// factors: the loads' latency is what such a call waits for
 // ---------------------------------------------------------------------------
 struct FinishArgs {
     int64_t M, d, k, r, G, g, S, pitch; // pitch: columns of a range's rows
@@ -584,10 +586,14 @@ __device__ __forceinline__ bf16x8 codes_bf16(const int8_t *p)
     return as_bf16x8(c8_bf16(u32x2{w.x ^ 0x80808080u, w.y ^ 0x80808080u}));
 }
 
-template <int NT, int NJ> __global__ __launch_bounds__(256) void finish_kernel(FinishArgs a)
+template <int NT, int NJ, bool SPLIT> __global__ __launch_bounds__(256) void finish_kernel(FinishArgs a)
 {
+    __shared__ f32x4 red[SPLIT ? 3 : 1][64];
     const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
-    const int64_t blocks = a.d / (16 * NJ), id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int wv = threadIdx.x >> 6;
+    constexpr int step = SPLIT ? 4 : 1;
+    const int first = SPLIT ? wv : 0;
+    const int64_t blocks = a.d / (16 * NJ), id = SPLIT ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + wv;
     const int64_t j0 = id % blocks * 16 * NJ, m0 = id / blocks * 16 * NT;
     if (m0 >= a.M)
         return;
@@ -600,12 +606,12 @@ template <int NT, int NJ> __global__ __launch_bounds__(256) void finish_kernel(F
             acc[t][n] = f32x4{0.f, 0.f, 0.f, 0.f};
             const float *p = a.part + m[t] * a.pitch + j0 + 16 * n + 4 * q;
 #pragma unroll(NJ > 1 ? 1 : 8)
-            for (int64_t i = 0; i < a.S; ++i) // the ranges in order
+            for (int64_t i = first; i < a.S; i += step) // the ranges in order
                 acc[t][n] += *(const f32x4 *)(p + i * a.M * a.pitch);
         }
     }
 #pragma unroll(NJ > 1 ? 1 : 2)
-    for (int64_t i = 0; i < kp; i += kUnit) {
+    for (int64_t i = first * kUnit; i < kp; i += step * kUnit) {
         bf16x8 code[NJ];
         for (int n = 0; n < NJ; ++n)
             code[n] = codes_bf16(a.b8t + (j0 + 16 * n + r) * kp + i + 8 * q);
@@ -621,7 +627,7 @@ template <int NT, int NJ> __global__ __launch_bounds__(256) void finish_kernel(F
     // U sD in two bf16 parts against the exact codes; NJ pairs of 16 columns
     // share a group by twos (groups are multiples of 32 columns)
     constexpr int NP = NJ > 1 ? 2 : 1;
-    for (int64_t i = 0; i < rp; i += kUnit)
+    for (int64_t i = first * kUnit; i < rp; i += step * kUnit)
         for (int p = 0; p < NJ; p += NP) {
             bf16x8 code[NP];
             for (int n = 0; n < NP; ++n)
@@ -644,6 +650,16 @@ template <int NT, int NJ> __global__ __launch_bounds__(256) void finish_kernel(F
                 }
             }
         }
+    if constexpr (SPLIT) {
+        static_assert(NT == 1 && NJ == 1, "one tile per workgroup");
+        if (wv)
+            red[wv - 1][lane] = acc[0][0];
+        __syncthreads();
+        if (wv)
+            return;
+        for (int w = 0; w < 3; ++w)
+            acc[0][0] += red[w][lane];
+    }
     for (int t = 0; t < NT; ++t)
         if (m0 + 16 * t + r < a.M)
             for (int n = 0; n < NJ; ++n) {
@@ -670,7 +686,7 @@ struct Plan {
 // Row tile by the rows there are.  Ranges: the vocabulary is cut so that the
 // workgroups fill the compute units' places (by LDS: one of 128 rows, two of
 // 64, three of 32) in whole rounds: the count whose rounds, with two stages of latency each, are shortest.
-constexpr int64_t kCu = 256, kMaxWg = 1024, kMinChunks = 8;
+constexpr int64_t kCu = 256, kMaxWg = 1024, kMinChunks = 2;
 constexpr int64_t kWideM = 256; // rows from which dX's tiles have 256
 
 Launch launch_of(int64_t M, int64_t tiles, int64_t nvc, bool low)
@@ -913,13 +929,15 @@ void backward_rows(const DevHead &h, const BackwardState &b, int64_t M, const vo
     run_tiles<false>(p.main.bm, t, st);
     const FinishArgs f{M, s.d, s.k, s.r, s.G(), s.g, p.main.S, c.main_tiles() * kJT, c, part, u, h.sd, thi, tlo,
                        b.b8t, b.d8t, dx};
-    if (M <= 512) { // few rows: more waves, for the latency of the ranges' loads
-        const int64_t waves = (M + 15) / 16 * (s.d / 16);
-        hipLaunchKernelGGL((finish_kernel<1, 1>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, f);
-    } else {
-        const int64_t waves = (M + 63) / 64 * (s.d / 64);
-        hipLaunchKernelGGL((finish_kernel<4, 4>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, f);
-    }
+    // by measurement at d = 4096: four waves a tile 9 us against 14 at M = 16,
+    // 17 against 13 at M = 64; 16 x 16 a wave 41 us against 46 at M = 512
+    const int64_t tiles = (M + 15) / 16 * (s.d / 16), waves = (M + 63) / 64 * (s.d / 64);
+    if (tiles <= 512)
+        hipLaunchKernelGGL((finish_kernel<1, 1, true>), dim3((unsigned)tiles), dim3(256), 0, st, f);
+    else if (M <= 512)
+        hipLaunchKernelGGL((finish_kernel<1, 1, false>), dim3((unsigned)((tiles + 3) / 4)), dim3(256), 0, st, f);
+    else
+        hipLaunchKernelGGL((finish_kernel<4, 4, false>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, f);
 }
 
 } // namespace
