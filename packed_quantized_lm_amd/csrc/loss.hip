@@ -211,15 +211,17 @@ template <typename T> __device__ __forceinline__ const T *row_ptr(const Rows &a,
     return (const T *)a.y + m * a.ld;
 }
 
-// log probability of row m's target; NaN for a target outside [0, V)
-template <typename T> __device__ __forceinline__ float row_logp(const Rows &a, int64_t m, Stat st)
+// Log probability of row m's target; NaN for a target outside [0, V).  A row's
+// few scalars are taken in fp64: log Z in fp32 alone is off by up to 5e-7, which
+// the losses' differences of log probabilities would keep.
+template <typename T> __device__ __forceinline__ double row_logp(const Rows &a, int64_t m, Stat st)
 {
     const int32_t t = a.targets[m];
     if (t < 0 || t >= a.V)
-        return __builtin_nanf("");
-    return (load1(row_ptr<T>(a, m) + t) - st.m) - logf(st.s);
+        return __builtin_nan("");
+    return ((double)load1(row_ptr<T>(a, m) + t) - (double)st.m) - log((double)st.s);
 }
-__device__ __forceinline__ float stat_lse(Stat st) { return st.m + logf(st.s); }
+__device__ __forceinline__ float stat_lse(Stat st) { return (float)((double)st.m + log((double)st.s)); }
 
 // the slices' parts of one row, eight loads in flight
 __device__ __forceinline__ Stat merge_slices(const Stat *part, int64_t S)
@@ -263,7 +265,7 @@ __global__ __launch_bounds__(NT) void stats_kernel(Rows a, Stat *part, float *lo
     if (threadIdx.x == 0) {
         part[blockIdx.x] = st;
         if (logp && a.S == 1)
-            logp[m] = row_logp<T>(a, m, st);
+            logp[m] = (float)row_logp<T>(a, m, st);
         if (lse)
             lse[m] = stat_lse(st);
     }
@@ -277,7 +279,7 @@ __global__ __launch_bounds__(kNT) void logp_kernel(Rows a, const Stat *part, flo
         return;
     const Stat st = merge_slices(part + m * a.S, a.S);
     if (logp)
-        logp[m] = row_logp<T>(a, m, st);
+        logp[m] = (float)row_logp<T>(a, m, st);
     if (lse)
         lse[m] = stat_lse(st);
 }
@@ -404,21 +406,21 @@ struct Policy {
 };
 
 // one token's loss and its derivative by logp
-__device__ __forceinline__ float policy_token(const Policy &p, int64_t m, float w, float logp, float *c)
+__device__ __forceinline__ float policy_token(const Policy &p, int64_t m, float w, double logp, float *c)
 {
-    const float A = p.adv[m], rho = expf(logp - p.old_logp[m]);
-    const float cl = fminf(fmaxf(rho, 1.f - p.eps_low), 1.f + p.eps_high);
-    float loss = -fminf(rho * A, cl * A);
-    float d = rho * A <= cl * A ? -A * rho : 0.f;
+    const double A = p.adv[m], rho = exp(logp - (double)p.old_logp[m]);
+    const double cl = fmin(fmax(rho, 1. - (double)p.eps_low), 1. + (double)p.eps_high);
+    double loss = -fmin(rho * A, cl * A);
+    double d = rho * A <= cl * A ? -A * rho : 0.;
     if (!(rho == rho)) // fmin and fmax drop a NaN
         loss = d = rho;
     if (p.beta != 0.f) { // without a KL term an infinite one is never formed
-        const float gap = p.ref_logp[m] - logp;
-        loss += p.beta * (expm1f(gap) - gap);
-        d -= p.beta * expm1f(gap);
+        const double gap = (double)p.ref_logp[m] - logp, e = expm1(gap);
+        loss += (double)p.beta * (e - gap);
+        d -= (double)p.beta * e;
     }
-    *c = w * d;
-    return w * loss;
+    *c = (float)(w * d);
+    return (float)(w * loss);
 }
 
 // The policy loss of a whole row in one workgroup: statistics, loss,
@@ -430,24 +432,32 @@ __global__ __launch_bounds__(NT) void policy_row_kernel(Rows a, Policy pol, cons
 {
     __shared__ Stat red[NT / 64];
     const int64_t m = blockIdx.x;
-    float lp = 0.f, loss = 0.f, c = 0.f;
+    __shared__ float coef;
     Stat st{0.f, 1.f};
     Raw<T> held[H > 0 ? H : 1];
     const T *y = row_ptr<T>(a, m);
     int64_t t = -1;
-    if (row_counts(a, m)) {
+    float lp = 0.f, loss = 0.f, c = 0.f;
+    const bool counts = row_counts(a, m);
+    if (counts) {
         t = a.targets[m];
-        // read before the barrier: the gradient may be written over it
+        // read before the barriers: the gradient may be written over it
         const float yt = t >= 0 && t < a.V ? load1(y + t) : __builtin_nanf("");
         st = block_merge<NT>(scan_part<NT, H>(y, a.V, held), red);
-        lp = (yt - st.m) - logf(st.s);
-        loss = policy_token(pol, m, a.weights[m], lp, &c);
+        if (threadIdx.x < 64) { // one wave: fp64 is slow
+            const double lp64 = ((double)yt - (double)st.m) - log((double)st.s);
+            lp = (float)lp64;
+            loss = policy_token(pol, m, a.weights[m], lp64, &c);
+        }
     }
     if (threadIdx.x == 0) {
         token[m] = loss;
+        coef = c;
         if (logp)
             logp[m] = lp;
     }
+    __syncthreads();
+    c = coef;
     if (!dy)
         return;
     G *g = dy + m * ldg;
@@ -470,8 +480,9 @@ __global__ __launch_bounds__(kNT) void policy_rows_kernel(Rows a, const Stat *pa
         return;
     float lp = 0.f, loss = 0.f, c = 0.f;
     if (row_counts(a, m)) {
-        lp = row_logp<T>(a, m, merge_slices(part + m * a.S, a.S));
-        loss = policy_token(pol, m, a.weights[m], lp, &c);
+        const double lp64 = row_logp<T>(a, m, merge_slices(part + m * a.S, a.S));
+        lp = (float)lp64;
+        loss = policy_token(pol, m, a.weights[m], lp64, &c);
     }
     token[m] = loss;
     coef[m] = c;
@@ -498,29 +509,29 @@ __global__ __launch_bounds__(kNT) void pair_kernel(Rows a, const Stat *part, con
     for (int i = 0; i < 2; ++i) {
         double s = 0.;
         for (int64_t m = b[i] + threadIdx.x; m < b[i + 1]; m += kNT) {
-            float lp = 0.f;
+            double lp = 0.;
             if (row_counts(a, m)) {
                 lp = row_logp<T>(a, m, merge_slices(part + m * a.S, a.S));
-                s += (double)a.weights[m] * ((double)lp - (double)(ref ? ref[m] : 0.f));
+                s += (double)a.weights[m] * (lp - (double)(ref ? ref[m] : 0.f));
             }
             if (logp)
-                logp[m] = lp;
+                logp[m] = (float)lp;
         }
         sum[i] = block_sum<kNT>(s, red);
     }
-    const float h = (float)((double)beta * (sum[0] - sum[1]));
-    const float e = expf(-fabsf(h)), sp = log1pf(e);               // log(1 + exp(-|h|))
-    const float sig = h >= 0.f ? 1.f / (1.f + e) : e / (1.f + e);  // sigma(h)
-    const float nsig = h >= 0.f ? e / (1.f + e) : 1.f / (1.f + e); // sigma(-h)
+    const double h = (double)beta * (sum[0] - sum[1]), sm = smooth;
+    const double e = exp(-fabs(h)), sp = log1p(e);             // log(1 + exp(-|h|))
+    const double up = 1. / (1. + e), down = e / (1. + e);      // sigma(|h|), sigma(-|h|)
     // sigma(h) - (1 - smooth) = smooth sigma(h) - (1 - smooth) sigma(-h)
-    const float slope = beta / (float)P * (smooth * sig - (1.f - smooth) * nsig);
+    const double slope = (double)beta / (double)P * (sm * (h >= 0. ? up : down) - (1. - sm) * (h >= 0. ? down : up));
     for (int i = 0; i < 2; ++i)
         for (int64_t m = b[i] + threadIdx.x; m < b[i + 1]; m += kNT)
-            coef[m] = row_counts(a, m) ? (i ? -slope : slope) * a.weights[m] : 0.f;
+            coef[m] = row_counts(a, m) ? (float)((i ? -slope : slope) * a.weights[m]) : 0.f;
     if (threadIdx.x == 0) {
-        pair[p] = (1.f - smooth) * (sp + fmaxf(-h, 0.f)) + smooth * (sp + fmaxf(h, 0.f));
+        const double over = h != h ? h : fmax(h, 0.), under = h != h ? h : fmax(-h, 0.); // a NaN stays
+        pair[p] = (float)((1. - sm) * (sp + under) + sm * (sp + over));
         if (margins)
-            margins[p] = h;
+            margins[p] = (float)h;
     }
 }
 
@@ -708,10 +719,11 @@ void run_policy_whole(const Rows &a, const Policy &pol, float *logp, float *toke
         run_policy_rows<kWide, 2, T>(a, pol, logp, token, g, st);
     else if (wide < 8)
         run_policy_rows<kWide, 4, T>(a, pol, logp, token, g, st);
-    else if (sizeof(T) == 4 || wide < 16)
-        run_policy_rows<kWide, 8, T>(a, pol, logp, token, g, st);
+    else if constexpr (sizeof(T) == 2)
+        wide < 16 ? run_policy_rows<kWide, 8, T>(a, pol, logp, token, g, st)
+                  : run_policy_rows<kWide, 16, T>(a, pol, logp, token, g, st);
     else
-        run_policy_rows<kWide, 16, T>(a, pol, logp, token, g, st);
+        run_policy_rows<kWide, 8, T>(a, pol, logp, token, g, st);
 }
 
 template <typename T>

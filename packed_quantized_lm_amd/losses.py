@@ -38,9 +38,10 @@ def on_stream(device, stream, call):
     device's current one) the stream of the allocations inside."""
     import torch
     # entering torch's device and stream contexts costs 10 us, more than the
-    # smallest calls: they are skipped where they would change nothing
+    # smallest calls, and a Stream object 2 us: both are skipped where they
+    # would change nothing
     if stream is None and device.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream(device).cuda_stream)
+        return call(torch._C._cuda_getCurrentRawStream(device.index))
     with _entered(device, stream) as st:
         return call(st)
 
@@ -151,7 +152,7 @@ def policy_loss(logits, targets, old_logp, advantages, weights, ref_logp=None, b
     def call(st):
         dy, gcode, ldg = _gradient(logits, M, V, grad_dtype, dlogits)
         loss = torch.empty((), dtype=torch.float32, device=dev)
-        logp = torch.empty((M,), dtype=torch.float32, device=dev)
+        logp = torch.empty(M, dtype=torch.float32, device=dev)
         ws, n = _workspace(M, V, 0, dev)
         _check(load_library().archead_policy_loss(
             M, V, ptr(logits), code, ld, ptr(targets), ptr(old_logp), ptr(ref_logp), ptr(advantages), ptr(weights),
