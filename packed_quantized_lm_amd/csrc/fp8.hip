@@ -232,7 +232,8 @@ __device__ __forceinline__ i32x8 join(i32x4 a, i32x4 b)
 // ---------------------------------------------------------------------------
 constexpr int kSkinnyM = 16, kSkinnyWaves = 4, kDepth = 4;
 constexpr int64_t kSkinnyX = 64 << 10;   // LDS for the hidden states' codes, two workgroups a compute unit
-constexpr int64_t kSkinnyGrid = 256 * 4; // workgroups: four a compute unit
+constexpr int64_t kCu = 256;
+constexpr int64_t kSkinnyGrid = kCu * 4; // workgroups: four a compute unit
 
 template <bool XL, typename O> __global__ __launch_bounds__(kSkinnyWaves * 64) void product_skinny_kernel(ProdArgs a)
 {
@@ -327,45 +328,45 @@ template <bool XL, typename O> __global__ __launch_bounds__(kSkinnyWaves * 64) v
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: tiles of BM output rows x 256 columns, 8 waves as 2 x 4, each
-// [BM / 2 x 64].  A stage is one block of 128 columns of both operands, copied
+// Many rows: tiles of BM output rows x BN columns, each wave [BM / 2 x 64].  A stage is one block of 128 columns of both operands, copied
 // straight into LDS as codes (16-byte pieces, a row's pieces exchanged by the
 // row's low bits so that the reads of eight neighbouring rows fall on
 // different banks) while the other buffer is worked on; the block's sums are
 // scaled into the accumulator in fp32.
 // ---------------------------------------------------------------------------
-constexpr int kBN = 256;
 __device__ const u32x4 kNothing = {0u, 0u, 0u, 0u}; // what a piece past K is copied from
 
-template <int BM> struct Tile {
-    static constexpr int rows = BM + kBN, codes = rows * kBlk / 4;
+template <int BM, int BN> struct Tile {
+    static constexpr int waves = BN / 32;                           // two along the rows, each 64 columns
+    static constexpr int rows = BM + BN, codes = rows * kBlk / 4;
     // The rows' scales lie behind the codes, but with BM = 64, where two
     // workgroups share a compute unit's LDS only without them, in registers.
     static constexpr bool reg = BM == 64;
     static constexpr int words = codes + (reg ? 0 : BM);            // LDS of a stage
-    static constexpr int copies = rows / 8 / 8;                     // 1 KiB copies per wave and stage
+    static constexpr int copies = rows / 8 / waves;                 // 1 KiB copies per wave and stage
     static constexpr int mt = BM / 32, nt = 4;                      // 16 x 16 tiles per wave
+    static constexpr int wgs = words * 8 <= 80 * 1024 ? 2 : 1;      // workgroups a compute unit holds
 };
 
-template <int BM, bool F8, typename O>
-__global__ __launch_bounds__(512, BM == 64 ? 4 : 2) void product_tile_kernel(ProdArgs a)
+template <int BM, int BN, bool F8, typename O>
+__global__ __launch_bounds__((BN * 2), (Tile<BM, BN>::wgs * BN / 128)) void product_tile_kernel(ProdArgs a)
 {
-    using T = Tile<BM>;
+    using T = Tile<BM, BN>;
     // two stage buffers, each the codes and then the rows' scales
     __shared__ __attribute__((aligned(16))) uint32_t smem[2 * T::words];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, q = lane >> 4, r = lane & 15;
     // Workgroup b runs on XCD b mod 8: an XCD takes every eighth column tile
     // and all row tiles of it in turn, so that the weights pass through one L2.
-    const int64_t n_mt = (a.M + BM - 1) / BM, n_nt = (a.N + kBN - 1) / kBN;
+    const int64_t n_mt = (a.M + BM - 1) / BM, n_nt = (a.N + BN - 1) / BN;
     const int64_t id = blockIdx.x >> 3, ni = (id / n_mt) * 8 + (blockIdx.x & 7), mi = id % n_mt;
     if (ni >= n_nt)
         return;
-    const int64_t m0 = mi * BM, n0 = ni * kBN;
+    const int64_t m0 = mi * BM, n0 = ni * BN;
     const int64_t nb = (a.K + kBlk - 1) / kBlk;
 
-    // copy c of this wave: LDS rows 8 (8 c + wv) .. +7 (rows 0 .. BM-1 from A,
-    // the rest from B), lane l piece l % 8 of row l / 8
-    const int wm = (wv >> 2) * (BM / 2), wn = (wv & 3) * 64;
+    // copy c of this wave: LDS rows 8 (waves c + wv) .. +7 (rows 0 .. BM-1 from
+    // A, the rest from B), lane l piece l % 8 of row l / 8
+    const int wm = wv / (BN / 64) * (BM / 2), wn = wv % (BN / 64) * 64;
     float sn[T::mt], sc[T::mt]; // T::reg: the next stage's row scales and this one's
     auto fill = [&](int at, int64_t b) { // at: the buffer's first word
         int l8 = lane >> 3;
@@ -374,10 +375,10 @@ __global__ __launch_bounds__(512, BM == 64 ? 4 : 2) void product_tile_kernel(Pro
         const int64_t col = b * kBlk + 16 * ((lane & 7) ^ l8); // row & 7 = l8
 #pragma unroll
         for (int c = 0; c < T::copies; ++c) {
-            const int row = 8 * (8 * c + wv) + l8;
-            const uint8_t *p = 64 * c < BM ? a.A + min(m0 + row, a.M - 1) * a.lda
+            const int row = 8 * (T::waves * c + wv) + l8;
+            const uint8_t *p = 8 * T::waves * c < BM ? a.A + min(m0 + row, a.M - 1) * a.lda
                                            : a.B + min(n0 + row - BM, a.N - 1) * a.ldb;
-            lds_dma16<false>(col < a.K ? p + col : (const uint8_t *)&kNothing, &smem[at + (8 * c + wv) * 256]);
+            lds_dma16<false>(col < a.K ? p + col : (const uint8_t *)&kNothing, &smem[at + (T::waves * c + wv) * 256]);
         }
         if constexpr (T::reg)
             for (int t = 0; t < T::mt; ++t)
@@ -513,25 +514,40 @@ template <typename O> void run_skinny(const ProdArgs &a, hipStream_t st)
         hipLaunchKernelGGL((product_skinny_kernel<false, O>), grid, dim3(kSkinnyWaves * 64), 0, st, a);
 }
 
-template <int BM, typename O> void run_tile(const ProdArgs &a, hipStream_t st)
+template <int BM, int BN, typename O> void run_tile(const ProdArgs &a, hipStream_t st)
 {
-    const int64_t n_mt = (a.M + BM - 1) / BM, n_nt = (a.N + kBN - 1) / kBN;
+    const int64_t n_mt = (a.M + BM - 1) / BM, n_nt = (a.N + BN - 1) / BN;
     const dim3 grid((unsigned)((n_nt + 7) / 8 * 8 * n_mt));
-    hipLaunchKernelGGL((product_tile_kernel<BM, sizeof(O) == 2 && (BM > 64), O>), grid, dim3(512), 0, st, a);
+    hipLaunchKernelGGL((product_tile_kernel<BM, BN, sizeof(O) == 2 && (BM > 64), O>), grid, dim3(BN * 2), 0, st, a);
 }
 
 template <typename O> archead_status run_product(const ProdArgs &a, hipStream_t st)
 {
-    if (((a.N + kBN - 1) / kBN + 8) * ((a.M + 63) / 64) >= int64_t(1) << 31)
+    if (((a.N + 127) / 128 + 8) * ((a.M + 63) / 64) >= int64_t(1) << 31)
         return api_fail(ARCHEAD_ESHAPE, "product too large");
     if (a.M <= kSkinnyM)
         run_skinny<O>(a, st);
     else if (a.M <= 64)
-        run_tile<64, O>(a, st);
-    else if (a.M <= 256 || sizeof(O) == 4)
-        run_tile<128, O>(a, st);
-    else if constexpr (sizeof(O) == 2)
-        run_tile<256, O>(a, st);
+        run_tile<64, 256, O>(a, st);
+    else {
+        // Tiles by the rounds they take over kCu compute units, in units of a
+        // 128 x 256 tile: two of 128 x 128 run beside each other there (333 x
+        // 50021 x 2576, bf16: 119 us against 138; 1000 x 4096 x 4096, fp32: 53
+        // against 70), but move more per product (2048 x 151936 x 4096, fp32:
+        // 2.80 ms against 2.67); 256 x 256, bf16 only, is the most economical
+        // (1.95 ms against 2.14) and the coarsest.
+        auto rounds = [&](int64_t bm, int64_t bn) {
+            return double(((a.M + bm - 1) / bm * ((a.N + bn - 1) / bn) + kCu - 1) / kCu);
+        };
+        const double small = 0.53 * rounds(128, 128), mid = rounds(128, 256), large = 1.75 * rounds(256, 256);
+        if (sizeof(O) == 2 && large < small && large < mid) {
+            if constexpr (sizeof(O) == 2)
+                run_tile<256, 256, O>(a, st);
+        } else if (small < mid)
+            run_tile<128, 128, O>(a, st);
+        else
+            run_tile<128, 256, O>(a, st);
+    }
     return launched("archead_fp8_matmul");
 }
 
