@@ -527,7 +527,8 @@ archead_status archead_fp8_quantize(int64_t rows, int64_t cols, const void *x, i
  *
  * M <= 2^20, N < 2^31, K a multiple of 16 in [16, 2^20]; else ARCHEAD_ESHAPE.
  * A, B   DEVICE e4m3 codes, 16-byte aligned, row strides lda, ldb >= K
- *        multiples of 16.  Bytes of a row past K are not used.
+ *        multiples of 16 below 2^23 (else ARCHEAD_ESHAPE).  Bytes of a row
+ *        past K are not used.
  * sA     DEVICE fp32, sA[b * ldsa + m], ldsa >= M.
  * sB     DEVICE fp32, sB[(n / 128) * ldsb + b], ldsb >= ceil(K / 128).
  * out    DEVICE M x N, fp32 or bf16 (out_type), row stride ldo >= N elements.

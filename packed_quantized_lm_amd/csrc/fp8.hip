@@ -29,6 +29,7 @@ typedef uint16_t u16x8u __attribute__((ext_vector_type(8), aligned(2)));
 
 constexpr int kBlk = 128; // columns (and weight rows) that share a scale
 constexpr float kE4m3Max = 448.f;
+constexpr int64_t kMaxStride = int64_t(1) << 23; // of A and B: a tile's offsets fit 32 bits
 
 // ---------------------------------------------------------------------------
 // quantiser
@@ -354,7 +355,8 @@ __global__ __launch_bounds__((BN * 2), (Tile<BM, BN>::wgs * BN / 128)) void prod
     using T = Tile<BM, BN>;
     // two stage buffers, each the codes and then the rows' scales
     __shared__ __attribute__((aligned(16))) uint32_t smem[2 * T::words];
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, q = lane >> 4, r = lane & 15;
+    const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // Workgroup b runs on XCD b mod 8: an XCD takes every eighth column tile
     // and all row tiles of it in turn, so that the weights pass through one L2.
     const int64_t n_mt = (a.M + BM - 1) / BM, n_nt = (a.N + BN - 1) / BN;
@@ -367,18 +369,30 @@ __global__ __launch_bounds__((BN * 2), (Tile<BM, BN>::wgs * BN / 128)) void prod
     // copy c of this wave: LDS rows 8 (waves c + wv) .. +7 (rows 0 .. BM-1 from
     // A, the rest from B), lane l piece l % 8 of row l / 8
     const int wm = wv / (BN / 64) * (BM / 2), wn = wv % (BN / 64) * 64;
+    const int col = 16 * ((lane & 7) ^ (lane >> 3)); // row & 7 = lane / 8
+    const uint8_t *baseA = a.A + m0 * a.lda, *baseB = a.B + n0 * a.ldb;
+    uint32_t off[T::copies]; // byte offsets from them: row strides are below 2^23
+#pragma unroll
+    for (int c = 0; c < T::copies; ++c) {
+        const int row = 8 * (T::waves * c + wv) + (lane >> 3);
+        off[c] = (8 * T::waves * c < BM ? (uint32_t)min((int64_t)row, a.M - 1 - m0) * (uint32_t)a.lda
+                                        : (uint32_t)min((int64_t)row - BM, a.N - 1 - n0) * (uint32_t)a.ldb) + col;
+    }
+    const uint32_t lds0 = lds_address(smem);
     float sn[T::mt], sc[T::mt]; // T::reg: the next stage's row scales and this one's
     auto fill = [&](int at, int64_t b) { // at: the buffer's first word
-        int l8 = lane >> 3;
-        if (BM > 128)
-            asm volatile("" : "+v"(l8)); // addresses formed anew: kept, they take 32 registers
-        const int64_t col = b * kBlk + 16 * ((lane & 7) ^ l8); // row & 7 = l8
+        const int64_t k0 = b * kBlk;
+        if (k0 + kBlk <= a.K) {
 #pragma unroll
-        for (int c = 0; c < T::copies; ++c) {
-            const int row = 8 * (T::waves * c + wv) + l8;
-            const uint8_t *p = 8 * T::waves * c < BM ? a.A + min(m0 + row, a.M - 1) * a.lda
-                                           : a.B + min(n0 + row - BM, a.N - 1) * a.ldb;
-            lds_dma16<false>(col < a.K ? p + col : (const uint8_t *)&kNothing, &smem[at + (T::waves * c + wv) * 256]);
+            for (int c = 0; c < T::copies; ++c)
+                lds_dma16_from((8 * T::waves * c < BM ? baseA : baseB) + k0, off[c],
+                               lds0 + 4 * (at + (T::waves * c + wv) * 256));
+        } else { // the last, shorter block: zeros past K
+#pragma unroll
+            for (int c = 0; c < T::copies; ++c) {
+                const uint8_t *p = (8 * T::waves * c < BM ? baseA : baseB) + k0 + off[c];
+                lds_dma16<false>(k0 + col < a.K ? p : (const uint8_t *)&kNothing, &smem[at + (T::waves * c + wv) * 256]);
+            }
         }
         if constexpr (T::reg)
             for (int t = 0; t < T::mt; ++t)
@@ -617,6 +631,8 @@ extern "C" archead_status archead_fp8_matmul(int64_t M, int64_t N, int64_t K, co
         return ARCHEAD_OK;
     if (!A || !sA || !B || !sB || !out)
         return api_fail(ARCHEAD_EINVAL, "A, sA, B, sB and out are required");
+    if (lda >= kMaxStride || ldb >= kMaxStride)
+        return api_fail(ARCHEAD_ESHAPE, "row strides of A and B must lie below 2^23 bytes");
     if (bad_rows(A, lda, K) || bad_rows(B, ldb, K))
         return api_fail(ARCHEAD_EINVAL, "A, B and their row strides must be multiples of 16 bytes, strides at least K");
     if ((uintptr_t)out % (out_type == ARCHEAD_F32 ? 4 : 2))

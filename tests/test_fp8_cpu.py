@@ -42,7 +42,8 @@ def _mm(lib, M=4, N=8, K=64, a=B, lda=64, sa=B, ldsa=4, b=B, ldb=64, sb=B, ldsb=
     (dict(ldo=7), binding.EINVAL), (dict(a=None), binding.EINVAL), (dict(sa=None), binding.EINVAL),
     (dict(b=None), binding.EINVAL), (dict(sb=None), binding.EINVAL), (dict(out=None), binding.EINVAL),
     (dict(a=ODD), binding.EINVAL), (dict(b=ODD), binding.EINVAL), (dict(lda=72), binding.EINVAL),
-    (dict(ldb=48), binding.EINVAL), (dict(out=ctypes.c_void_p(4098)), binding.EINVAL)])
+    (dict(ldb=48), binding.EINVAL), (dict(lda=1 << 23), binding.ESHAPE), (dict(ldb=1 << 23), binding.ESHAPE),
+    (dict(out=ctypes.c_void_p(4098)), binding.EINVAL)])
 def test_matmul_refusals(lib, over, status):
     assert _mm(lib, **over) == status
     assert lib.archead_last_error().decode()
