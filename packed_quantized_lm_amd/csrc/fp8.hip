@@ -457,6 +457,17 @@ __global__ __launch_bounds__((BN * 2), (Tile<BM, BN>::wgs * BN / 128)) void prod
                 if (hold_x)
                     sh[n] = row_scale(at, n) * f;
             }
+            f32x4 pp[2][nh];
+            float s1 = 0.f;
+            auto add = [&](int t, float st) {
+                for (int n = 0; n < nh; ++n)
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (hold_x)
+                            acc[n][t][i] = __builtin_fmaf(pp[t & 1][n][i], sh[n], acc[n][t][i]);
+                        else
+                            acc[t][n][i] = __builtin_fmaf(pp[t & 1][n][i], st, acc[t][n][i]);
+                    }
+            };
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int t = 0; t < np; ++t) {
@@ -467,22 +478,21 @@ __global__ __launch_bounds__((BN * 2), (Tile<BM, BN>::wgs * BN / 128)) void prod
                     if (!hold_x)
                         s = row_scale(at, t + 1) * f;
                 }
-                f32x4 p[nh] = {};
+                f32x4 (&p)[nh] = pp[t & 1];
+                for (int n = 0; n < nh; ++n)
+                    p[n] = f32x4{0.f, 0.f, 0.f, 0.f};
                 for (int h = 0; h < 4; ++h) {
                     const f16x8 y = halves(c[2 * h], c[2 * h + 1]);
                     for (int n = 0; n < nh; ++n)
                         p[n] = hold_x ? __builtin_amdgcn_mfma_f32_16x16x32_f16(y, held[n][h], p[n], 0, 0, 0)
                                       : __builtin_amdgcn_mfma_f32_16x16x32_f16(held[n][h], y, p[n], 0, 0, 0);
                 }
-                for (int n = 0; n < nh; ++n)
-                    for (int i = 0; i < 4; ++i) {
-                        if constexpr (hold_x)
-                            acc[n][t][i] = __builtin_fmaf(p[n][i], sh[n], acc[n][t][i]);
-                        else
-                            acc[t][n][i] = __builtin_fmaf(p[n][i], st, acc[t][n][i]);
-                    }
+                if (t > 0)
+                    add(t - 1, s1);
+                s1 = st;
                 __builtin_amdgcn_sched_barrier(0);
             }
+            add(np - 1, s1);
         }
     };
     fill(0, 0);
