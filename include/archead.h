@@ -360,8 +360,8 @@ typedef enum archead_type {
  * more goes in parts).  Waits until both are ready.  Called again it only ever
  * enlarges the workspace; calls of archead_backward on the handle that are
  * still running elsewhere must have ended then.
- * M_max < 1 -> ARCHEAD_EINVAL; M_max > 2^20, or a head whose second layout
- * passes 2^31 KiB -> ARCHEAD_ESHAPE; a stream being captured -> ARCHEAD_EINVAL;
+ * M_max < 1 -> ARCHEAD_EINVAL; M_max > 2^20, V > 2^22, or a head whose second
+ * layout passes 2^31 KiB -> ARCHEAD_ESHAPE; a stream being captured -> ARCHEAD_EINVAL;
  * no memory -> ARCHEAD_ENOMEM, with the handle as it was.  archead_device_bytes
  * counts both; archead_free releases them.
  */

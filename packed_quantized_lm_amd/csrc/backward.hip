@@ -38,6 +38,7 @@ constexpr int kJT = 256;    // columns per tile of dX
 constexpr int kLT = 128;    // columns per tile of T and U
 constexpr int kUnit = 32;   // columns that share a scale
 constexpr int64_t kChunkM = 2048; // most rows of G held at a time
+constexpr int64_t kMaxV = int64_t(1) << 22; // a tile's offsets into G fit 32 bits
 
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint16_t u16x8u __attribute__((ext_vector_type(8), aligned(2)));
@@ -418,26 +419,29 @@ template <int BM, bool LOW> __global__ __launch_bounds__(512) void tile_kernel(T
     // T::parts-th stage a chunk's codes.  G comes in 1 KiB copies of rows of
     // 2 T::gv bytes, 16-byte pieces exchanged by the row's low bits so that
     // eight rows' reads fall on different banks.
-    constexpr int pieces = T::gv / 8, rows = 64 / pieces; // of a row; of a copy
-    auto fill = [&](int64_t i) {
-        const int g = (int)(i & 1) * T::gw;
-        const uint16_t *v = a.g16 + c0 * kVC + i * T::gv;
+    constexpr int pieces = T::gv / 8, rows = 64 / pieces, copies = T::gw / 2048; // of a row; of a copy; per wave
+    const uint16_t *gbase = a.g16 + m0 * a.Vp + c0 * kVC;
+    uint32_t goff[copies]; // byte offsets from it: rows are shorter than 2^24 bytes
 #pragma unroll
-        for (int c = 0; c < T::gw / 2048; ++c) {
-            const int row = rows * (8 * c + wv) + lane / pieces;
-            lds_dma16<false>(v + min(m0 + row, a.M - 1) * a.Vp + 8 * ((lane % pieces) ^ (row & 7)),
-                             &smem[g + (8 * c + wv) * 256]);
-        }
+    for (int c = 0; c < copies; ++c) {
+        const int row = rows * (8 * c + wv) + lane / pieces;
+        goff[c] = (uint32_t)min((int64_t)row, a.M - 1 - m0) * (uint32_t)(2 * a.Vp) +
+                  16 * ((lane % pieces) ^ (row & 7));
+    }
+    const uint32_t lds0 = lds_address(smem), lane16 = 16 * lane;
+    auto fill = [&](int64_t i) {
+        const uint32_t g = lds0 + 4 * (uint32_t)((int)(i & 1) * T::gw);
+#pragma unroll
+        for (int c = 0; c < copies; ++c)
+            lds_dma16_from(gbase + i * T::gv, goff[c], g + 1024 * (8 * c + wv));
         if (i % T::parts == 0) {
-            const int64_t vc = c0 + i / T::parts;
-            const int k = 2 * T::gw + (int)(i / T::parts & 1) * T::kw;
+            const int64_t at = (c0 + i / T::parts) * a.n_jt + jt;
+            const uint32_t k = lds0 + 4 * (uint32_t)(2 * T::gw + (int)(i / T::parts & 1) * T::kw);
 #pragma unroll
             for (int c = 0; c < T::cw / 2048; ++c)
-                lds_dma16<false>(a.codes + (vc * a.n_jt + jt) * T::cw + (8 * c + wv) * 256 + lane * 4,
-                                 &smem[k + (8 * c + wv) * 256]);
+                lds_dma16_from(a.codes + at * T::cw + (8 * c + wv) * 256, lane16, k + 1024 * (8 * c + wv));
             if (wv < T::sw / 256)
-                lds_dma16<false>(a.sc + ((vc * a.n_jt + jt) * T::su + 4 * wv) * kVC + lane * 8,
-                                 &smem[k + T::cw + wv * 256]);
+                lds_dma16_from(a.sc + (at * T::su + 4 * wv) * kVC, lane16, k + 4 * T::cw + 1024 * wv);
         }
     };
     const uint32_t magic = vgpr_const(kF16Magic);
@@ -957,6 +961,8 @@ extern "C" archead_status archead_reserve_backward(archead_t h, int64_t M_max, v
         return api_fail(ARCHEAD_EINVAL, "M_max must be at least 1");
     if (M_max > int64_t(1) << 20)
         return api_fail(ARCHEAD_ESHAPE, "M_max above 2^20");
+    if (dev->s.V > kMaxV)
+        return api_fail(ARCHEAD_ESHAPE, "the backward takes V up to 2^22");
     const int64_t rows = std::min(M_max, kChunkM);
     if (*slot && (*slot)->rows >= rows)
         return ARCHEAD_OK;
