@@ -384,7 +384,8 @@ __device__ __forceinline__ f16x8 dequant8(uint32_t w0, uint32_t w1, u32x4 s, uin
 }
 
 template <int BM, bool LOW> struct BTile {
-    static constexpr int wm = BM >= 128 ? 2 : 1, wj = 8 / wm;      // waves along rows and columns
+    // waves along rows and columns: each 64 columns of dX, at least 32 of T and U
+    static constexpr int wm = BM == 256 && LOW ? 4 : BM >= 128 ? 2 : 1, wj = 8 / wm;
     // vocabulary rows of G per stage: half a chunk where a whole one of 256
     // rows would not fit twice; codes and scales come by whole chunks
     static constexpr int gv = BM == 256 ? kVC / 2 : kVC, parts = kVC / gv;
@@ -691,12 +692,12 @@ struct Plan {
 // workgroups fill the compute units' places (by LDS: one of 128 rows, two of
 // 64, three of 32) in whole rounds: the count whose rounds, with two stages of latency each, are shortest.
 constexpr int64_t kCu = 256, kMaxWg = 1024, kMinChunks = 2;
-constexpr int64_t kWideM = 256; // rows from which dX's tiles have 256
+constexpr int64_t kWideM = 256; // rows from which tiles have 256
 
-Launch launch_of(int64_t M, int64_t tiles, int64_t nvc, bool low)
+Launch launch_of(int64_t M, int64_t tiles, int64_t nvc)
 {
     Launch p;
-    p.bm = M <= 32 ? 32 : M <= 64 ? 64 : low || M < kWideM ? 128 : 256;
+    p.bm = M <= 32 ? 32 : M <= 64 ? 64 : M < kWideM ? 128 : 256;
     p.n_mt = (M + p.bm - 1) / p.bm;
     const int64_t places = kCu * (p.bm == 32 ? 3 : p.bm == 64 ? 2 : 1);
     const int64_t t = std::max<int64_t>(tiles * p.n_mt, 1), most = std::max<int64_t>(1, nvc / kMinChunks);
@@ -714,7 +715,7 @@ Launch launch_of(int64_t M, int64_t tiles, int64_t nvc, bool low)
 
 Plan plan_of(const Cols &c, int64_t M, int64_t nvc)
 {
-    return Plan{launch_of(M, c.low_tiles(), nvc, true), launch_of(M, c.main_tiles(), nvc, false)};
+    return Plan{launch_of(M, c.low_tiles(), nvc), launch_of(M, c.main_tiles(), nvc)};
 }
 
 struct BwWs {
@@ -859,9 +860,9 @@ template <bool LOW> void run_tiles(int bm, const TileArgs &a, hipStream_t st)
         hipLaunchKernelGGL((tile_kernel<32, LOW>), grid, dim3(512), 0, st, a);
     else if (bm == 64)
         hipLaunchKernelGGL((tile_kernel<64, LOW>), grid, dim3(512), 0, st, a);
-    else if (LOW || bm == 128)
+    else if (bm == 128)
         hipLaunchKernelGGL((tile_kernel<128, LOW>), grid, dim3(512), 0, st, a);
-    else if constexpr (!LOW)
+    else
         hipLaunchKernelGGL((tile_kernel<256, LOW>), grid, dim3(512), 0, st, a);
 }
 
