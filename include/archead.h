@@ -1,5 +1,8 @@
 /*
- * archead.h -- C ABI of the packed ARCHead LM-head forward for MI355X (gfx950).
+ * archead.h -- C ABI of the packed ARCHead LM-head for MI355X (gfx950): its
+ * forward with what follows it at inference, its construction, and what a model
+ * is scored and trained with through it (losses over logits, the gradient by
+ * the hidden states, an 8-bit head to hold it against).
  *
  * The operation (ARCHead paper, "Activation-Metric Residual Correction for
  * LLM Output Heads", section 3.2):
@@ -358,8 +361,9 @@ typedef enum archead_type {
  * (about the packed head's size again), and a
  * workspace for M_max rows at a time is allocated (at most 2048; a call with
  * more goes in parts).  Waits until both are ready.  Called again it only ever
- * enlarges the workspace; calls of archead_backward on the handle that are
- * still running elsewhere must have ended then.
+ * enlarges the workspace, into new memory: no call of archead_backward on the
+ * handle may then be running elsewhere, and graphs that captured one before
+ * must not be replayed any more.
  * M_max < 1 -> ARCHEAD_EINVAL; M_max > 2^20, V > 2^22, or a head whose second
  * layout passes 2^31 KiB -> ARCHEAD_ESHAPE; a stream being captured -> ARCHEAD_EINVAL;
  * no memory -> ARCHEAD_ENOMEM, with the handle as it was.  archead_device_bytes
@@ -384,7 +388,8 @@ archead_status archead_reserve_backward(archead_t h, int64_t M_max, void *hip_st
  * ones rounded to 11 bits); the residual's and the low-rank codes times their
  * scales are rounded once to fp16; sums are fp32; the low-rank factors T, U
  * enter their second product with 16 significant bits; dX is rounded once.
- * A NaN or infinity in row m of G makes row m of dX NaN and no other.
+ * A NaN or infinity in row m of G makes row m of dX NaN or infinite and no
+ * other.
  * Enqueued on hip_stream, not waited for; nothing is allocated, so the call can
  * be captured.  The calls of one handle share its backward workspace: enqueue
  * them (and replay graphs that hold them) on one stream, or order them with

@@ -130,7 +130,7 @@ _FIELD_DTYPES = [("A5", np.int8), ("sA", np.uint16), ("B8", np.int8), ("sB", np.
 
 
 class PackedHead:
-    """A packed ARCHead head resident on the current HIP device."""
+    """A packed ARCHead head resident on the HIP device current at its construction."""
 
     def __init__(self, fields: dict, stream=None):
         lib = load_library()
@@ -145,6 +145,8 @@ class PackedHead:
                                    _stream_handle(stream), ctypes.byref(handle))
         _check(st, "archead_pack_load")
         self._h = handle
+        import torch
+        self.device = torch.device("cuda", torch.cuda.current_device())
 
     @property
     def handle(self):
@@ -336,8 +338,10 @@ class PackedHead:
 
     def reserve_backward(self, M_max: int, stream=None):
         """Prepare backward() for up to M_max rows at a time (archead_reserve_backward)."""
-        _check(load_library().archead_reserve_backward(self.handle, int(M_max), _stream_handle(stream)),
-               "archead_reserve_backward")
+        from .losses import on_stream
+        h = self.handle
+        on_stream(self.device, stream, lambda st: _check(
+            load_library().archead_reserve_backward(h, int(M_max), st), "archead_reserve_backward"))
 
     def backward(self, dlogits, dX=None, stream=None):
         """dX = dlogits W_hat, bf16 M x d: the gradient by the hidden states of a
@@ -347,7 +351,7 @@ class PackedHead:
         from .losses import _type_code, need_rows, on_stream, ptr
         if not isinstance(dlogits, torch.Tensor) or dlogits.dim() != 2 or dlogits.shape[1] != self.V:
             raise ValueError(f"dlogits must be an M x {self.V} tensor")
-        dev, M = dlogits.device, int(dlogits.shape[0])
+        dev, M, h = self.device, int(dlogits.shape[0]), self.handle
         code = _type_code(dlogits.dtype, "dlogits")
         ld = need_rows(dlogits, "dlogits", (dlogits.dtype,), (M, self.V), dev)
         if dX is not None:
@@ -355,8 +359,7 @@ class PackedHead:
 
         def call(st):
             out = torch.empty((M, self.d), dtype=torch.bfloat16, device=dev) if dX is None else dX
-            _check(load_library().archead_backward(self.handle, M, ptr(dlogits), code, ld, ptr(out), st),
-                   "archead_backward")
+            _check(load_library().archead_backward(h, M, ptr(dlogits), code, ld, ptr(out), st), "archead_backward")
             return out
         return on_stream(dev, stream, call)
 

@@ -218,6 +218,21 @@ def test_a_refused_reserve_leaves_the_handle_as_it_was(monkeypatch):
     head.close()
 
 
+def test_offsets_past_32_bits():
+    """Rows of dlogits 2^29 elements apart: the last ones past 2^32 elements."""
+    import torch
+    from packed_quantized_lm_amd import PackedHead
+    f = random_small_head(1000, 128, 8, 8, 32, 1, seed=12)
+    head = PackedHead(f)
+    head.reserve_backward(4)
+    M, far = 10, 1 << 29
+    flat = torch.zeros((M - 1) * far + 1000, dtype=torch.bfloat16, device="cuda")
+    G = flat.as_strided((M, 1000), (far, 1))
+    G.copy_(gradient(M, 1000, 3))
+    assert torch.equal(head.backward(G), head.backward(G.contiguous()))
+    head.close()
+
+
 def test_binding_refuses_bad_tensors():
     import torch
     from packed_quantized_lm_amd import PackedHead
