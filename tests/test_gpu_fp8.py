@@ -108,7 +108,8 @@ def test_nan_and_infinity():
 
 SHAPES = [(1, 1, 16), (1, 37, 48), (2, 16, 128), (5, 129, 144), (16, 300, 256), (17, 40, 1040), (33, 1000, 400),
           (64, 257, 512), (65, 130, 272), (127, 515, 640), (128, 256, 256), (129, 257, 384), (200, 700, 1168),
-          (300, 1100, 2064), (513, 300, 128), (1, 5000, 4096), (7, 3001, 2576)]
+          (300, 1100, 2064), (513, 300, 128), (1, 5000, 4096), (7, 3001, 2576), (16, 300, 4096),
+          (9, 200, 16400), (130, 4097, 1024), (600, 2500, 144)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -183,6 +184,20 @@ def test_head_empty_sizes_streams_and_graphs():
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(out, head.forward(X))
+
+
+def test_offsets_past_32_bits():
+    """Rows of out that lie 2^26 elements apart: the last ones past 2^32."""
+    import torch
+    from packed_quantized_lm_amd import Fp8Head
+    head = Fp8Head(torch.randn(300, 64, device="cuda"))
+    for M in (17, 70):
+        X = torch.randn(M, 64, device="cuda")
+        flat = torch.zeros(M * (1 << 26) + 512, dtype=torch.bfloat16, device="cuda")
+        out = flat.as_strided((M, 300), (1 << 26, 1))
+        head.forward(X, out=out)
+        assert torch.equal(out.contiguous(), head.forward(X, out_dtype=torch.bfloat16))
+        del flat, out
 
 
 def test_binding_refuses_bad_tensors():

@@ -301,6 +301,24 @@ def test_graph_capture_replays():
         torch.cuda.synchronize()
 
 
+def test_offsets_past_32_bits():
+    """Rows 2^29 elements apart: the last ones past 2^32 elements."""
+    import torch
+    from packed_quantized_lm_amd import policy_loss, token_logp
+    M, V, far = 10, 9001, 1 << 29
+    flat = torch.zeros((M - 1) * far + V, dtype=torch.bfloat16, device="cuda")
+    y = flat.as_strided((M, V), (far, 1))
+    y.copy_(torch.randn(M, V))
+    t = torch.randint(0, V, (M,), dtype=torch.int32, device="cuda")
+    v = torch.ones(M, device="cuda")
+    near = y.contiguous()
+    for a, b in zip(token_logp(y, t), token_logp(near, t)):
+        assert torch.equal(a, b)
+    want = policy_loss(near, t, v, v, v, grad_dtype=torch.bfloat16)
+    got = policy_loss(y, t, v, v, v, dlogits=y)  # in place, far apart
+    assert torch.equal(got[0], want[0]) and torch.equal(y.contiguous(), want[2])
+
+
 def test_binding_refuses_bad_tensors():
     import torch
     from packed_quantized_lm_amd import policy_loss, preference_loss, token_logp
