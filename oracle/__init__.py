@@ -29,6 +29,9 @@ softmax  log-normaliser lse = log sum_v exp(logits) and cross-entropy
          lse - logit[target] of the logits (abstract and section 1: the
          logits feed the softmax; the head is judged by cross-entropy and
          perplexity)
+losses   token log probabilities, the clipped policy loss with a KL term and
+         the preference loss over logits, with the logits' gradients
+fp8      matrices in e4m3 with a scale per block of 128, and their product
 
 Parity pins (what each function is checked against, in tests/):
   quant   -- closed-form bounds |x - s q| <= s/2, ranges, idempotence, and
@@ -44,6 +47,10 @@ Parity pins (what each function is checked against, in tests/):
   softmax -- closed forms (equal logits: ln V; V = 1; two-way softplus),
              shift invariance, softmax sums to one, math.fsum brute force on
              tiny rows, scipy's logsumexp at overflow-prone magnitudes
+  losses  -- gradients against central differences of the losses, closed forms
+             (equal logits, no margin), the cross-entropy above
+  fp8     -- every e4m3 code against torch's, ties and ends, the nearest code by
+             exact fractions, products of small integers
   packer  -- correction: Eckart-Young-Mirsky tail energy, brute force over
              random and grid rank-r candidates, the eigenvector route, the
              p = 1/2 identity with eq 1, the isotropic (C = I) reduction;
