@@ -506,8 +506,8 @@ archead_status archead_preference_loss(int64_t M, int64_t V, const void *logits,
  *
  * x    DEVICE rows x cols, fp32 or bf16 (type), row stride ldx elements,
  *      aligned to its element.  rows < 2^31; cols a multiple of 16 (the
- *      product reads rows in 16-byte pieces) up to 2^20; rows times blocks at
- *      most 2^34; else ARCHEAD_ESHAPE.
+ *      product reads rows in 16-byte pieces) up to 2^20; rows times blocks below
+ *      2^28; else ARCHEAD_ESHAPE.
  * q    DEVICE codes, rows x cols bytes, row stride ldq bytes; q and ldq
  *      multiples of 16.
  * s    DEVICE fp32.  block_rows = 1: s[b * lds + row] for block b of a row
@@ -530,7 +530,8 @@ archead_status archead_fp8_quantize(int64_t rows, int64_t cols, const void *x, i
  * eight lose bits (the fp8 matrix instruction's adder; 1e-4 of a typical
  * result).  out is rounded once to its type.
  *
- * M <= 2^20, N < 2^31, K a multiple of 16 in [16, 2^20]; else ARCHEAD_ESHAPE.
+ * M <= 2^20, N <= 2^30, M N <= 2^36, K a multiple of 16 in [16, 2^20]; else
+ * ARCHEAD_ESHAPE.
  * A, B   DEVICE e4m3 codes, 16-byte aligned, row strides lda, ldb >= K
  *        multiples of 16 below 2^23 (else ARCHEAD_ESHAPE).  Bytes of a row
  *        past K are not used.

@@ -126,10 +126,10 @@ __device__ __forceinline__ uint32_t c8_code(const DevHead &h, int64_t v, int64_t
     return c[2 * (ks & 1) + ((i >> 2) & 1)] >> (8 * (i & 3)) & 255u;
 }
 
-// one dword of nibbles per thread
+// one dword of nibbles per thread; workgroup (block, chunk), at most 2^15 chunks
 __global__ __launch_bounds__(256) void codes_kernel(Layout a, int64_t nblk)
 {
-    const int64_t vc = blockIdx.x / nblk, blk = blockIdx.x % nblk; // chunk, 16-column block
+    const int64_t vc = blockIdx.y, blk = blockIdx.x; // chunk, 16-column block
     const int lane = threadIdx.x >> 2, s = threadIdx.x & 3;
     const int64_t j = blk * 16 + (lane & 15);
     uint32_t w = 0;
@@ -145,7 +145,7 @@ __global__ __launch_bounds__(256) void codes_kernel(Layout a, int64_t nblk)
 // one dword of bytes per thread
 __global__ __launch_bounds__(512) void low_codes_kernel(Layout a, int64_t nblk)
 {
-    const int64_t vc = blockIdx.x / nblk, blk = blockIdx.x % nblk;
+    const int64_t vc = blockIdx.y, blk = blockIdx.x;
     const int half = threadIdx.x >> 8, lane = threadIdx.x >> 2 & 63, dw = threadIdx.x & 3;
     const int64_t unit = blk / 2, i = (blk & 1) * 16 + (lane & 15);
     uint32_t w = 0;
@@ -164,7 +164,7 @@ __global__ __launch_bounds__(512) void low_codes_kernel(Layout a, int64_t nblk)
 
 __global__ __launch_bounds__(128) void scales_kernel(Layout a, int64_t nunit)
 {
-    const int64_t vc = blockIdx.x / nunit, unit = blockIdx.x % nunit, v = vc * kVC + threadIdx.x;
+    const int64_t vc = blockIdx.y, unit = blockIdx.x, v = vc * kVC + threadIdx.x;
     float f = 0.f;
     if (v < a.h.s.V && unit * kUnit < a.h.s.d)
         f = ldexpf(h2f(a.h.sr[((v >> 4) * a.h.s.G() + unit * kUnit / a.h.s.g) * kVB + (v & 15)]), a.ex[0]);
@@ -173,7 +173,7 @@ __global__ __launch_bounds__(128) void scales_kernel(Layout a, int64_t nunit)
 
 __global__ __launch_bounds__(128) void low_scales_kernel(Layout a, int64_t nunit)
 {
-    const int64_t vc = blockIdx.x / nunit, unit = blockIdx.x % nunit, v = vc * kVC + threadIdx.x;
+    const int64_t vc = blockIdx.y, unit = blockIdx.x, v = vc * kVC + threadIdx.x;
     float f = 0.f;
     if (v < a.h.s.V && unit < a.c.kst)
         f = ldexpf(h2f(a.h.sa[v]), a.ex[1]);
@@ -839,11 +839,11 @@ archead_status lay_out(const DevHead &h, BackwardState *b, hipStream_t st)
     BW_TRY(hipMemsetAsync(p + o_ex, 0, 64, st)); // never under capture (checked by the caller)
     hipLaunchKernelGGL(peak_kernel, dim3(256, 3), dim3(256), 0, st, a);
     hipLaunchKernelGGL(exponent_kernel, dim3(1), dim3(64), 0, st, a);
-    hipLaunchKernelGGL(codes_kernel, dim3((unsigned)(a.nvc * nblk)), dim3(256), 0, st, a, nblk);
-    hipLaunchKernelGGL(scales_kernel, dim3((unsigned)(a.nvc * nunit)), dim3(kVC), 0, st, a, nunit);
+    hipLaunchKernelGGL(codes_kernel, dim3((unsigned)nblk, (unsigned)a.nvc), dim3(256), 0, st, a, nblk);
+    hipLaunchKernelGGL(scales_kernel, dim3((unsigned)nunit, (unsigned)a.nvc), dim3(kVC), 0, st, a, nunit);
     if (lblk) {
-        hipLaunchKernelGGL(low_codes_kernel, dim3((unsigned)(a.nvc * lblk)), dim3(512), 0, st, a, lblk);
-        hipLaunchKernelGGL(low_scales_kernel, dim3((unsigned)(a.nvc * lunit)), dim3(kVC), 0, st, a, lunit);
+        hipLaunchKernelGGL(low_codes_kernel, dim3((unsigned)lblk, (unsigned)a.nvc), dim3(512), 0, st, a, lblk);
+        hipLaunchKernelGGL(low_scales_kernel, dim3((unsigned)lunit, (unsigned)a.nvc), dim3(kVC), 0, st, a, lunit);
     }
     if (kp)
         hipLaunchKernelGGL(columns_kernel, dim3(1024), dim3(256), 0, st, h.b8, h.s.k, h.s.d, (int64_t)kp, a.b8t);

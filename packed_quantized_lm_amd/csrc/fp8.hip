@@ -547,8 +547,6 @@ template <int BM, int BN, typename O> void run_tile(const ProdArgs &a, hipStream
 
 template <typename O> archead_status run_product(const ProdArgs &a, hipStream_t st)
 {
-    if (((a.N + 127) / 128 + 8) * ((a.M + 63) / 64) >= int64_t(1) << 31)
-        return api_fail(ARCHEAD_ESHAPE, "product too large");
     if (a.M <= kSkinnyM)
         run_skinny<O>(a, st);
     else if (a.M <= 64)
@@ -586,9 +584,10 @@ extern "C" archead_status archead_fp8_quantize(int64_t rows, int64_t cols, const
 {
     if (rows < 0)
         return api_fail(ARCHEAD_EINVAL, "rows < 0");
+    // a launch holds fewer than 2^32 threads, 16 a row block
     if (rows >= (int64_t(1) << 31) || cols < 16 || cols % 16 || cols > (int64_t(1) << 20) ||
-        rows * ((cols + kBlk - 1) / kBlk) > (int64_t(1) << 34))
-        return api_fail(ARCHEAD_ESHAPE, "rows < 2^31, cols a multiple of 16 in [16, 2^20], at most 2^34 row blocks");
+        rows * ((cols + kBlk - 1) / kBlk) >= (int64_t(1) << 28))
+        return api_fail(ARCHEAD_ESHAPE, "rows < 2^31, cols a multiple of 16 in [16, 2^20], fewer than 2^28 row blocks");
     if (type != ARCHEAD_F32 && type != ARCHEAD_BF16)
         return api_fail(ARCHEAD_EINVAL, "x must be ARCHEAD_F32 or ARCHEAD_BF16");
     if (block_rows != 1 && block_rows != kBlk)
@@ -630,8 +629,10 @@ extern "C" archead_status archead_fp8_matmul(int64_t M, int64_t N, int64_t K, co
 {
     if (M < 0 || N < 0)
         return api_fail(ARCHEAD_EINVAL, "M < 0 or N < 0");
-    if (M > (int64_t(1) << 20) || N >= (int64_t(1) << 31) || K < 16 || K % 16 || K > (int64_t(1) << 20))
-        return api_fail(ARCHEAD_ESHAPE, "M <= 2^20, N < 2^31 and K a multiple of 16 in [16, 2^20]");
+    // a launch holds fewer than 2^32 threads: the tiles have one for 32 elements or more
+    if (M > (int64_t(1) << 20) || N > (int64_t(1) << 30) || M * N > (int64_t(1) << 36) || K < 16 || K % 16 ||
+        K > (int64_t(1) << 20))
+        return api_fail(ARCHEAD_ESHAPE, "M <= 2^20, N <= 2^30, M N <= 2^36 and K a multiple of 16 in [16, 2^20]");
     if (out_type != ARCHEAD_F32 && out_type != ARCHEAD_BF16)
         return api_fail(ARCHEAD_EINVAL, "out must be ARCHEAD_F32 or ARCHEAD_BF16");
     const int64_t nb = (K + kBlk - 1) / kBlk;

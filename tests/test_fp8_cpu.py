@@ -22,6 +22,7 @@ def _quant(lib, rows=4, cols=64, x=B, type=0, ldx=64, br=1, q=B, ldq=64, s=B, ld
     (dict(rows=-1), binding.EINVAL), (dict(rows=1 << 31), binding.ESHAPE), (dict(cols=24), binding.ESHAPE),
     (dict(cols=0), binding.ESHAPE), (dict(cols=(1 << 20) + 16), binding.ESHAPE),
     (dict(rows=(1 << 31) - 1, cols=1 << 20, ldx=1 << 20, ldq=1 << 20, lds=1 << 31), binding.ESHAPE),
+    (dict(rows=1 << 28, lds=1 << 28), binding.ESHAPE), (dict(rows=1 << 21, br=128, cols=1 << 14, ldx=1 << 14, ldq=1 << 14), binding.ESHAPE),
     (dict(type=2), binding.EINVAL), (dict(br=64), binding.EINVAL), (dict(ldx=63), binding.EINVAL),
     (dict(lds=3), binding.EINVAL), (dict(br=128, lds=0), binding.EINVAL), (dict(x=None), binding.EINVAL),
     (dict(q=None), binding.EINVAL), (dict(s=None), binding.EINVAL), (dict(q=ODD), binding.EINVAL),
@@ -38,6 +39,8 @@ def _mm(lib, M=4, N=8, K=64, a=B, lda=64, sa=B, ldsa=4, b=B, ldb=64, sb=B, ldsb=
 @pytest.mark.parametrize("over,status", [
     (dict(M=-1), binding.EINVAL), (dict(N=-1), binding.EINVAL), (dict(M=(1 << 20) + 1), binding.ESHAPE),
     (dict(N=1 << 31), binding.ESHAPE), (dict(K=0), binding.ESHAPE), (dict(K=24), binding.ESHAPE),
+    (dict(N=(1 << 30) + 1, ldo=1 << 31), binding.ESHAPE),
+    (dict(M=1 << 20, N=(1 << 16) + 1, ldsa=1 << 20, ldo=1 << 17), binding.ESHAPE),
     (dict(type=7), binding.EINVAL), (dict(ldsa=3), binding.EINVAL), (dict(ldsb=0), binding.EINVAL),
     (dict(ldo=7), binding.EINVAL), (dict(a=None), binding.EINVAL), (dict(sa=None), binding.EINVAL),
     (dict(b=None), binding.EINVAL), (dict(sb=None), binding.EINVAL), (dict(out=None), binding.EINVAL),
