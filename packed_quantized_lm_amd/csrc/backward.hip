@@ -385,7 +385,7 @@ __device__ __forceinline__ f16x8 dequant8(uint32_t w0, uint32_t w1, u32x4 s, uin
 
 template <int BM, bool LOW> struct BTile {
     // waves along rows and columns: each 64 columns of dX, at least 32 of T and U
-    static constexpr int wm = BM == 256 && LOW ? 4 : BM >= 128 ? 2 : 1, wj = 8 / wm;
+    static constexpr int wm = BM == 256 ? LOW ? 4 : 2 : 1, wj = 8 / wm;
     // vocabulary rows of G per stage: half a chunk where a whole one of 256
     // rows would not fit twice; codes and scales come by whole chunks
     static constexpr int gv = BM == 256 ? kVC / 2 : kVC, parts = kVC / gv;
@@ -688,26 +688,39 @@ struct Plan {
     Launch low, main;
 };
 
-// Row tile by the rows there are.  Ranges: the vocabulary is cut so that the
-// workgroups fill the compute units' places (by LDS: one of 128 rows, two of
-// 64, three of 32) in whole rounds: the count whose rounds, with two stages of latency each, are shortest.
+// Row tiles and ranges by the time a launch is expected to take.  Ranges: the
+// vocabulary is cut so that the workgroups fill the compute units' places (by
+// LDS: one of 256 rows, two of 64, three of 32) in whole rounds, each with two
+// stages of latency, against the ranges' sums written and read.  Tiles: 32 rows
+// as far as they go; beyond, 256 rows take 3.5 us a chunk on a full chip and 64
+// rows 2.2, so that 64 win where 256 would be mostly empty (260 rows of 151936 x
+// 4096: 509 us against 613; 512 rows: 790 against 695) or need more ranges
+// (1000 rows of 30011 x 640: 156 against 198).
 constexpr int64_t kCu = 256, kMaxWg = 1024, kMinChunks = 2;
-constexpr int64_t kWideM = 256; // rows from which tiles have 256
+struct TileKind {
+    int rows, places; // places on a compute unit
+    double us;        // a chunk's time with all places taken
+};
+constexpr TileKind kTiles[] = {{32, 3, 2.6}, {64, 2, 2.2}, {256, 1, 3.5}};
+constexpr double kSumRate = 4e6; // bytes a us
 
-Launch launch_of(int64_t M, int64_t tiles, int64_t nvc)
+Launch launch_of(int64_t M, int64_t tiles, int64_t tile_cols, int64_t nvc)
 {
-    Launch p;
-    p.bm = M <= 32 ? 32 : M <= 64 ? 64 : M < kWideM ? 128 : 256;
-    p.n_mt = (M + p.bm - 1) / p.bm;
-    const int64_t places = kCu * (p.bm == 32 ? 3 : p.bm == 64 ? 2 : 1);
-    const int64_t t = std::max<int64_t>(tiles * p.n_mt, 1), most = std::max<int64_t>(1, nvc / kMinChunks);
+    Launch p{};
     double least = 1e300;
-    p.S = 1;
-    for (int64_t S = 1; S <= most && (S == 1 || S * t <= kMaxWg); ++S) {
-        const double cost = double((S * t + places - 1) / places) * (double((nvc + S - 1) / S) + 2.0);
-        if (cost < least * 0.995) {
-            least = cost;
-            p.S = S;
+    for (const TileKind &k : kTiles) {
+        if ((k.rows == 32) != (M <= 32))
+            continue;
+        const int64_t n_mt = (M + k.rows - 1) / k.rows, t = std::max<int64_t>(tiles * n_mt, 1);
+        const int64_t places = kCu * k.places, most = std::max<int64_t>(1, nvc / kMinChunks);
+        const double sums = double(M) * double(tiles * tile_cols) * 8 / kSumRate;
+        for (int64_t S = 1; S <= most && (S == 1 || S * t <= kMaxWg); ++S) {
+            const double cost = double((S * t + places - 1) / places) * (double((nvc + S - 1) / S) + 2.0) * k.us +
+                                double(S) * sums;
+            if (cost < least * 0.995) {
+                least = cost;
+                p = Launch{k.rows, n_mt, S};
+            }
         }
     }
     return p;
@@ -715,7 +728,7 @@ Launch launch_of(int64_t M, int64_t tiles, int64_t nvc)
 
 Plan plan_of(const Cols &c, int64_t M, int64_t nvc)
 {
-    return Plan{launch_of(M, c.low_tiles(), nvc), launch_of(M, c.main_tiles(), nvc)};
+    return Plan{launch_of(M, c.low_tiles(), kLT, nvc), launch_of(M, c.main_tiles(), kJT, nvc)};
 }
 
 struct BwWs {
@@ -860,8 +873,6 @@ template <bool LOW> void run_tiles(int bm, const TileArgs &a, hipStream_t st)
         hipLaunchKernelGGL((tile_kernel<32, LOW>), grid, dim3(512), 0, st, a);
     else if (bm == 64)
         hipLaunchKernelGGL((tile_kernel<64, LOW>), grid, dim3(512), 0, st, a);
-    else if (bm == 128)
-        hipLaunchKernelGGL((tile_kernel<128, LOW>), grid, dim3(512), 0, st, a);
     else
         hipLaunchKernelGGL((tile_kernel<256, LOW>), grid, dim3(512), 0, st, a);
 }
