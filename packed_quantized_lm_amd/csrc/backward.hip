@@ -14,8 +14,8 @@
 //
 //   amax, convert  G 2^f_m as fp16 rows, f_m putting row m's largest entry
 //                  into [2^14, 2^15): exact for bf16 G within 2^28 of it
-//   tile kernel    [BM rows x 256 columns] over a range of the vocabulary,
-//                  first for the columns of T and U, then for dX's
+//   tile kernel    [BM rows x 256 columns of dX, 128 of T and U] over a range
+//                  of the vocabulary
 //   sums           T sB and U from their ranges, fp32
 //   finish         dX's ranges + the products with B8 and D8, one rounding
 #include <hip/hip_runtime.h>
@@ -398,17 +398,19 @@ template <int BM, bool LOW> struct BTile {
     static constexpr int kw = cw + sw, words = 2 * (gw + kw);      // G twice, codes with scales twice
 };
 
-template <int BM, bool LOW> __global__ __launch_bounds__(512) void tile_kernel(TileArgs a)
+// workgroup wg of a's tiles
+template <int BM, bool LOW, int N>
+__device__ __forceinline__ void tile_of(const TileArgs &a, uint32_t (&smem)[N], int64_t wg)
 {
     using T = BTile<BM, LOW>;
-    __shared__ __attribute__((aligned(16))) uint32_t smem[T::words];
+    static_assert(T::words <= N, "LDS");
     const int lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // Workgroup b runs on XCD b mod 8; an XCD takes a contiguous run of
+    // Workgroup wg runs on XCD wg mod 8; an XCD takes a contiguous run of
     // (range, row tile, column tile), column tiles fastest, so that the rows
     // of G pass through one L2 for all column tiles.
     const int64_t total = a.S * a.n_mt * a.n_jt, per = (total + 7) / 8;
-    const int64_t id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    const int64_t id = (wg & 7) * per + (wg >> 3);
     if (id >= total)
         return;
     const int64_t jt = id % a.n_jt, mi = id / a.n_jt % a.n_mt, sp = id / a.n_jt / a.n_mt;
@@ -524,6 +526,18 @@ template <int BM, bool LOW> __global__ __launch_bounds__(512) void tile_kernel(T
             }
         }
     }
+}
+
+// T's and U's tiles, the first low_groups workgroups (a multiple of 8), and dX's
+// behind them
+template <int BM> __global__ __launch_bounds__(512) void tile_kernel(TileArgs low, TileArgs main, uint32_t low_groups)
+{
+    constexpr int words = std::max(BTile<BM, true>::words, BTile<BM, false>::words);
+    __shared__ __attribute__((aligned(16))) uint32_t smem[words];
+    if (blockIdx.x < low_groups)
+        tile_of<BM, true>(low, smem, blockIdx.x);
+    else
+        tile_of<BM, false>(main, smem, blockIdx.x - low_groups);
 }
 
 // ---------------------------------------------------------------------------
@@ -680,12 +694,9 @@ template <int NT, int NJ, bool SPLIT> __global__ __launch_bounds__(256) void fin
 // ---------------------------------------------------------------------------
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
-struct Launch {
-    int bm;          // rows of a tile
-    int64_t n_mt, S; // row tiles, vocabulary ranges
-};
 struct Plan {
-    Launch low, main;
+    int bm;            // rows of a tile
+    int64_t low, main; // vocabulary ranges of T's and U's tiles, and of dX's
 };
 
 // Row tiles and ranges by the time a launch is expected to take.  Ranges: the
@@ -704,31 +715,40 @@ struct TileKind {
 constexpr TileKind kTiles[] = {{32, 3, 2.6}, {64, 2, 2.2}, {256, 1, 3.5}};
 constexpr double kSumRate = 4e6; // bytes a us
 
-Launch launch_of(int64_t M, int64_t tiles, int64_t tile_cols, int64_t nvc)
+// the best ranges for tiles of one kind, and their time
+double ranges_of(const TileKind &k, int64_t M, int64_t tiles, int64_t tile_cols, int64_t nvc, int64_t *ranges)
 {
-    Launch p{};
+    const int64_t t = std::max<int64_t>(tiles * ((M + k.rows - 1) / k.rows), 1);
+    const int64_t places = kCu * k.places, most = std::max<int64_t>(1, nvc / kMinChunks);
+    const double sums = double(M) * double(tiles * tile_cols) * 8 / kSumRate;
     double least = 1e300;
-    for (const TileKind &k : kTiles) {
-        if ((k.rows == 32) != (M <= 32))
-            continue;
-        const int64_t n_mt = (M + k.rows - 1) / k.rows, t = std::max<int64_t>(tiles * n_mt, 1);
-        const int64_t places = kCu * k.places, most = std::max<int64_t>(1, nvc / kMinChunks);
-        const double sums = double(M) * double(tiles * tile_cols) * 8 / kSumRate;
-        for (int64_t S = 1; S <= most && (S == 1 || S * t <= kMaxWg); ++S) {
-            const double cost = double((S * t + places - 1) / places) * (double((nvc + S - 1) / S) + 2.0) * k.us +
-                                double(S) * sums;
-            if (cost < least * 0.995) {
-                least = cost;
-                p = Launch{k.rows, n_mt, S};
-            }
+    for (int64_t S = 1; S <= most && (S == 1 || S * t <= kMaxWg); ++S) {
+        const double cost = double((S * t + places - 1) / places) * (double((nvc + S - 1) / S) + 2.0) * k.us +
+                            double(S) * sums;
+        if (cost < least * 0.995) {
+            least = cost;
+            *ranges = S;
         }
     }
-    return p;
+    return least;
 }
 
 Plan plan_of(const Cols &c, int64_t M, int64_t nvc)
 {
-    return Plan{launch_of(M, c.low_tiles(), kLT, nvc), launch_of(M, c.main_tiles(), kJT, nvc)};
+    Plan best{};
+    double least = 1e300;
+    for (const TileKind &k : kTiles) {
+        if ((k.rows == 32) != (M <= 32))
+            continue;
+        Plan p{k.rows, 1, 1};
+        const double cost = ranges_of(k, M, c.main_tiles(), kJT, nvc, &p.main) +
+                            (c.low_tiles() ? ranges_of(k, M, c.low_tiles(), kLT, nvc, &p.low) : 0.);
+        if (cost < least) {
+            least = cost;
+            best = p;
+        }
+    }
+    return best;
 }
 
 struct BwWs {
@@ -866,15 +886,29 @@ archead_status lay_out(const DevHead &h, BackwardState *b, hipStream_t st)
     return ARCHEAD_OK;
 }
 
-template <bool LOW> void run_tiles(int bm, const TileArgs &a, hipStream_t st)
+// Neither kind of tile waits for the other, and a launch of both saves the end
+// of one: 1 row of 151936 x 4096 98 us against 106, 133 rows of 30011 x 640 44
+// against 47.  Where both would come in several rounds they get in each other's
+// way (2048 rows of 151936 x 4096: 2.61 ms together, 2.55 apart; 300 rows of
+// 50257 x 1280: 100 us, 94).
+void run_tiles(int bm, const TileArgs &low, const TileArgs &main, hipStream_t st)
 {
-    const dim3 grid((unsigned)((a.S * a.n_mt * a.n_jt + 7) / 8 * 8));
-    if (bm == 32)
-        hipLaunchKernelGGL((tile_kernel<32, LOW>), grid, dim3(512), 0, st, a);
-    else if (bm == 64)
-        hipLaunchKernelGGL((tile_kernel<64, LOW>), grid, dim3(512), 0, st, a);
-    else
-        hipLaunchKernelGGL((tile_kernel<256, LOW>), grid, dim3(512), 0, st, a);
+    auto groups = [](const TileArgs &a) { return (uint32_t)((a.S * a.n_mt * a.n_jt + 7) / 8 * 8); };
+    auto launch = [&](uint32_t n, uint32_t grid) {
+        if (bm == 32)
+            hipLaunchKernelGGL(tile_kernel<32>, dim3(grid), dim3(512), 0, st, low, main, n);
+        else if (bm == 64)
+            hipLaunchKernelGGL(tile_kernel<64>, dim3(grid), dim3(512), 0, st, low, main, n);
+        else
+            hipLaunchKernelGGL(tile_kernel<256>, dim3(grid), dim3(512), 0, st, low, main, n);
+    };
+    const uint32_t n = groups(low), all = n + groups(main), places = (uint32_t)kCu * (bm == 64 ? 2 : 1);
+    if (n == 0 || bm == 32 || all <= places + places / 2)
+        launch(n, all);
+    else {
+        launch(n, n);
+        launch(0, all - n);
+    }
 }
 
 // up to b.rows rows of G
@@ -914,36 +948,35 @@ void backward_rows(const DevHead &h, const BackwardState &b, int64_t M, const vo
         hipLaunchKernelGGL(convert_kernel<uint16_t>, grid, dim3(256), 0, st, ga);
     }
     const Plan p = plan_of(c, M, nvc);
-    TileArgs t{};
-    t.g16 = ga.g16;
-    t.unscale = ga.unscale;
-    t.ex = b.ex;
-    t.M = M;
-    t.Vp = ga.Vp;
-    t.nvc = nvc;
-    t.kst = c.kst;
-    t.units = c.low_units();
     float *low = (float *)(ws + L.low), *u = (float *)(ws + L.u), *part = (float *)(ws + L.part);
     uint16_t *thi = (uint16_t *)(ws + L.thi), *tlo = (uint16_t *)(ws + L.tlo);
+    TileArgs tl{};
+    tl.g16 = ga.g16;
+    tl.unscale = ga.unscale;
+    tl.ex = b.ex;
+    tl.M = M;
+    tl.Vp = ga.Vp;
+    tl.nvc = nvc;
+    tl.kst = c.kst;
+    tl.units = c.low_units();
+    tl.n_mt = (M + p.bm - 1) / p.bm;
+    TileArgs tm = tl;
+    tl.codes = b.low;
+    tl.sc = b.lsc;
+    tl.n_jt = c.low_tiles();
+    tl.S = p.low;
+    tl.part = low;
+    tm.codes = b.codes;
+    tm.sc = b.sc;
+    tm.n_jt = c.main_tiles();
+    tm.S = p.main;
+    tm.part = part;
+    run_tiles(p.bm, tl, tm, st);
     if (c.low_tiles() > 0) {
-        t.codes = b.low;
-        t.sc = b.lsc;
-        t.n_jt = c.low_tiles();
-        t.n_mt = p.low.n_mt;
-        t.S = p.low.S;
-        t.part = low;
-        run_tiles<true>(p.low.bm, t, st);
-        const LowArgs l{M, p.low.S, s.k, s.r, c, low, h.sb, thi, tlo, u};
+        const LowArgs l{M, p.low, s.k, s.r, c, low, h.sb, thi, tlo, u};
         hipLaunchKernelGGL(low_sum_kernel, dim3((unsigned)(M * (c.kst + c.rst))), dim3(256), 0, st, l);
     }
-    t.codes = b.codes;
-    t.sc = b.sc;
-    t.n_jt = c.main_tiles();
-    t.n_mt = p.main.n_mt;
-    t.S = p.main.S;
-    t.part = part;
-    run_tiles<false>(p.main.bm, t, st);
-    const FinishArgs f{M, s.d, s.k, s.r, s.G(), s.g, p.main.S, c.main_tiles() * kJT, c, part, u, h.sd, thi, tlo,
+    const FinishArgs f{M, s.d, s.k, s.r, s.G(), s.g, p.main, c.main_tiles() * kJT, c, part, u, h.sd, thi, tlo,
                        b.b8t, b.d8t, dx};
     // by measurement at d = 4096: four waves a tile 9 us against 14 at M = 16,
     // 17 against 13 at M = 64; 16 x 16 a wave 41 us against 46 at M = 512
