@@ -130,9 +130,10 @@ __device__ __forceinline__ void add8(Stat &st, const float v[kVec])
 }
 
 // Statistics of y[0 .. n), one part per thread.  The thread's first H vectors
-// stay in held, for the gradient that follows them.
-template <int NT, int H, typename T>
-__device__ __forceinline__ Stat scan_part(const T *y, int64_t n, Raw<T> (&held)[H > 0 ? H : 1])
+// stay in held and its next L in its places of more (LDS), for the gradient that
+// follows them.
+template <int NT, int H, int L, typename T>
+__device__ __forceinline__ Stat scan_part(const T *y, int64_t n, Raw<T> (&held)[H > 0 ? H : 1], Raw<T> *more)
 {
     Stat st{-INFINITY, 0.f};
     const int64_t nv = n / kVec;
@@ -149,6 +150,21 @@ __device__ __forceinline__ Stat scan_part(const T *y, int64_t n, Raw<T> (&held)[
                 add8(st, v);
             }
         q += H * NT;
+    }
+    if (L > 0 && nv > 0) {
+        Raw<T> w[L > 0 ? L : 1];
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+            w[j] = load_raw(y + min(q + j * NT, nv - 1) * kVec);
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+            if (q + j * NT < nv) {
+                float v[kVec];
+                values(w[j], v);
+                add8(st, v);
+                more[j * NT + threadIdx.x] = w[j]; // read back by this thread alone
+            }
+        q += L * NT;
     }
     for (; q + NT < nv; q += 4 * NT) { // four loads in flight, past the end as above
         Raw<T> w[4];
@@ -261,7 +277,7 @@ __global__ __launch_bounds__(NT) void stats_kernel(Rows a, Stat *part, float *lo
     }
     const int64_t v0 = sl * a.slice, n = min(a.slice, a.V - v0);
     Raw<T> none[1];
-    const Stat st = block_merge<NT>(scan_part<NT, 0>(row_ptr<T>(a, m) + v0, n, none), red);
+    const Stat st = block_merge<NT>(scan_part<NT, 0, 0, T>(row_ptr<T>(a, m) + v0, n, none, nullptr), red);
     if (threadIdx.x == 0) {
         part[blockIdx.x] = st;
         if (logp && a.S == 1)
@@ -331,9 +347,9 @@ template <typename G> __device__ __forceinline__ void zero_part(G *g, int64_t n)
 }
 
 // g[i] = c (1[i = t] - exp(y[i] - m) / s) for i in [0, n); t relative to y
-template <int NT, int H, typename T, typename G>
+template <int NT, int H, int L, typename T, typename G>
 __device__ __forceinline__ void grad_part(const T *y, G *g, int64_t n, int64_t t, float c, Stat st,
-                                          const Raw<T> (&held)[H > 0 ? H : 1])
+                                          const Raw<T> (&held)[H > 0 ? H : 1], const Raw<T> *more)
 {
     const float r = anchor(st.m), k = -c / st.s;
     auto put = [&](const Raw<T> &w, int64_t q) {
@@ -355,6 +371,12 @@ __device__ __forceinline__ void grad_part(const T *y, G *g, int64_t n, int64_t t
             if (q + j * NT < nv)
                 put(held[j], q + j * NT);
         q += H * NT;
+    }
+    if (L > 0 && nv > 0) {
+        for (int j = 0; j < L; ++j)
+            if (q + j * NT < nv)
+                put(more[j * NT + threadIdx.x], q + j * NT);
+        q += L * NT;
     }
     for (; q + NT < nv; q += 4 * NT) {
         Raw<T> w[4];
@@ -397,7 +419,7 @@ __global__ __launch_bounds__(kNT) void grad_kernel(Rows a, const Stat *part, con
         c *= *gscale;
     const Stat st = merge_slices(part + m * a.S, a.S);
     const Raw<T> none[1] = {};
-    grad_part<kNT, 0>(row_ptr<T>(a, m) + v0, g, n, (int64_t)a.targets[m] - v0, c, st, none);
+    grad_part<kNT, 0, 0, T>(row_ptr<T>(a, m) + v0, g, n, (int64_t)a.targets[m] - v0, c, st, none, nullptr);
 }
 
 struct Policy {
@@ -425,8 +447,9 @@ __device__ __forceinline__ float policy_token(const Policy &p, int64_t m, float 
 
 // The policy loss of a whole row in one workgroup: statistics, loss,
 // coefficient and gradient.  The gradient's second pass finds the row in
-// registers (the first H vectors of each thread) and in the caches.
-template <int NT, int H, typename T, typename G>
+// registers (the first H vectors of each thread), in LDS (the next L) and in the
+// caches.
+template <int NT, int H, int L, typename T, typename G>
 __global__ __launch_bounds__(NT) void policy_row_kernel(Rows a, Policy pol, const float *gscale, float *logp,
                                                         float *token, G *dy, int64_t ldg)
 {
@@ -435,6 +458,7 @@ __global__ __launch_bounds__(NT) void policy_row_kernel(Rows a, Policy pol, cons
     __shared__ float coef;
     Stat st{0.f, 1.f};
     Raw<T> held[H > 0 ? H : 1];
+    __shared__ Raw<T> more[L > 0 ? L * NT : 1];
     const T *y = row_ptr<T>(a, m);
     int64_t t = -1;
     float lp = 0.f, loss = 0.f, c = 0.f;
@@ -443,7 +467,7 @@ __global__ __launch_bounds__(NT) void policy_row_kernel(Rows a, Policy pol, cons
         t = a.targets[m];
         // read before the barriers: the gradient may be written over it
         const float yt = t >= 0 && t < a.V ? load1(y + t) : __builtin_nanf("");
-        st = block_merge<NT>(scan_part<NT, H>(y, a.V, held), red);
+        st = block_merge<NT>(scan_part<NT, H, L, T>(y, a.V, held, more), red);
         if (threadIdx.x < 64) { // one wave: fp64 is slow
             const double lp64 = ((double)yt - (double)st.m) - log((double)st.s);
             lp = (float)lp64;
@@ -467,7 +491,7 @@ __global__ __launch_bounds__(NT) void policy_row_kernel(Rows a, Policy pol, cons
     }
     if (gscale)
         c *= *gscale;
-    grad_part<NT, H>(y, g, a.V, t, c, st, held);
+    grad_part<NT, H, L, T>(y, g, a.V, t, c, st, held, more);
 }
 
 // --- policy rows: logp, token loss and coefficient of every row -----------------
@@ -691,14 +715,14 @@ void run_grad(const Rows &a, const Stat *part, const float *coef, const Grad &g,
                            (uint16_t *)g.dy, g.ld, total);
 }
 
-template <int NT, int H, typename T>
+template <int NT, int H, int L, typename T>
 void run_policy_rows(const Rows &a, const Policy &pol, float *logp, float *token, const Grad &g, hipStream_t st)
 {
     if (g.type == ARCHEAD_F32)
-        hipLaunchKernelGGL((policy_row_kernel<NT, H, T, float>), dim3((unsigned)a.M), dim3(NT), 0, st, a, pol, g.scale,
+        hipLaunchKernelGGL((policy_row_kernel<NT, H, 0, T, float>), dim3((unsigned)a.M), dim3(NT), 0, st, a, pol, g.scale,
                            logp, token, (float *)g.dy, g.ld);
     else
-        hipLaunchKernelGGL((policy_row_kernel<NT, H, T, uint16_t>), dim3((unsigned)a.M), dim3(NT), 0, st, a, pol,
+        hipLaunchKernelGGL((policy_row_kernel<NT, H, L, T, uint16_t>), dim3((unsigned)a.M), dim3(NT), 0, st, a, pol,
                            g.scale, logp, token, (uint16_t *)g.dy, g.ld);
 }
 
@@ -706,24 +730,31 @@ void run_policy_rows(const Rows &a, const Policy &pol, float *logp, float *token
 // row fills (a vector past its end is a wasted load: V = 50021 in bf16 took
 // 128 us with 16 held of which 6 are filled, 102 us with none) and the
 // registers of 1024 threads allow.  2048 rows of 151936 fp32 logits with a
-// bf16 gradient: 400 us with eight held, 486 us with none.
+// bf16 gradient: 409 us with eight held, 486 us with none.  LDS holds four more
+// of fp32 logits where the gradient is in bf16 (395 us; 2048 x 128256: 325
+// against 343); with an fp32 gradient they cost more than they save (663 us
+// against 645), and bf16 logits gain nothing (274 against 275).
 template <typename T>
 void run_policy_whole(const Rows &a, const Policy &pol, float *logp, float *token, const Grad &g, hipStream_t st)
 {
     const int64_t narrow = (a.V + kNT * kVec - 1) / (kNT * kVec), wide = (a.V + kWide * kVec - 1) / (kWide * kVec);
     if (!g.dy || a.V < kHoldMin)
-        run_policy_rows<kNT, 0, T>(a, pol, logp, token, g, st);
+        run_policy_rows<kNT, 0, 0, T>(a, pol, logp, token, g, st);
     else if (narrow <= 4)
-        run_policy_rows<kNT, 4, T>(a, pol, logp, token, g, st);
+        run_policy_rows<kNT, 4, 0, T>(a, pol, logp, token, g, st);
     else if (wide < 4)
-        run_policy_rows<kWide, 2, T>(a, pol, logp, token, g, st);
+        run_policy_rows<kWide, 2, 0, T>(a, pol, logp, token, g, st);
     else if (wide < 8)
-        run_policy_rows<kWide, 4, T>(a, pol, logp, token, g, st);
-    else if constexpr (sizeof(T) == 2)
-        wide < 16 ? run_policy_rows<kWide, 8, T>(a, pol, logp, token, g, st)
-                  : run_policy_rows<kWide, 16, T>(a, pol, logp, token, g, st);
+        run_policy_rows<kWide, 4, 0, T>(a, pol, logp, token, g, st);
+    else if constexpr (sizeof(T) == 2) {
+        if (wide < 16)
+            run_policy_rows<kWide, 8, 0, T>(a, pol, logp, token, g, st);
+        else
+            run_policy_rows<kWide, 16, 0, T>(a, pol, logp, token, g, st);
+    } else if (wide < 12)
+        run_policy_rows<kWide, 8, 0, T>(a, pol, logp, token, g, st);
     else
-        run_policy_rows<kWide, 8, T>(a, pol, logp, token, g, st);
+        run_policy_rows<kWide, 8, 4, T>(a, pol, logp, token, g, st);
 }
 
 template <typename T>

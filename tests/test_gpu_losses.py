@@ -180,6 +180,44 @@ def test_policy_loss(M, V, dtype, pad, gtype, beta):
     assert torch.equal(again[2], dy) and torch.equal(again[0], got_loss)
 
 
+@pytest.mark.parametrize("V", [8200, 24575, 32776, 65529, 65545, 98297, 98312, 131077])
+@pytest.mark.parametrize("dtype,gtype", [("f32", "f32"), ("f32", "bf16"), ("bf16", "f32"), ("bf16", "bf16")])
+def test_policy_loss_long_rows(V, dtype, gtype):
+    """Enough rows for a workgroup each, which holds parts of its row: lengths
+    at and beyond what is held; most rows without weight, the others against
+    the oracle, out of place and in place."""
+    import torch
+    from packed_quantized_lm_amd import policy_loss
+    say(f"policy_loss long rows V={V} {dtype} grad={gtype}")
+    M, rows = 190, np.array([0, 1, 57, 128, 189])
+    _, y64, t, old, ref, adv, w, _ = policy_case(len(rows), V, dtype, 3, 7 + V, 0.05)
+    y = torch.full((M, V + 3), float("nan"), dtype=_dt(dtype), device="cuda")[:, :V]
+    y[torch.from_numpy(rows).cuda()] = torch.from_numpy(y64).to("cuda", _dt(dtype))
+    want, want_logp, grad, coef = losses.policy(y64, t, old, adv, w, ref, 0.05, 0.2, 0.28)
+
+    def spread(a, dtype="float32"):
+        full = np.zeros(M)
+        full[rows] = a
+        return dev(full, dtype)
+    args = (spread(t, "int32"), spread(old), spread(adv), spread(w), spread(ref))
+    loss, logp, dy = policy_loss(y, *args, beta=0.05, eps_low=0.2, eps_high=0.28, grad_dtype=_dt(gtype))
+    used = w != 0
+    dl = np.zeros(len(rows))
+    dl[used] = logp_tol(y64, t, np.nonzero(used)[0], V)
+    assert (np.abs(logp.double().cpu().numpy()[rows] - want_logp) <= dl).all()
+    rho, er = np.exp(want_logp - old) * used, np.exp(ref - want_logp) * used
+    dtok = np.abs(w) * ((np.abs(adv) * rho + 0.05 * (er + 1)) * (dl + 16 * U) + U * 1.6 * np.abs(ref - want_logp) * used)
+    dtok += np.abs(w) * (np.abs(adv) * rho + 0.05 * er) * 2 * U * np.abs(want_logp) * used
+    assert abs(float(loss) - want) <= dtok.sum() + U * abs(want)
+    check_grad(dy[torch.from_numpy(rows).cuda()], grad, t, coef, dtok, gtype)
+    rest = torch.ones(M, dtype=torch.bool, device="cuda")
+    rest[torch.from_numpy(rows).cuda()] = False
+    assert not dy[rest].any()
+    if dtype == gtype:
+        policy_loss(y, *args, beta=0.05, eps_low=0.2, eps_high=0.28, dlogits=y)
+        assert torch.equal(y, dy)
+
+
 def test_policy_gradient_against_differences():
     """The gradient against central differences of the kernel's own loss:
     truncation h^2 / 6 times a third derivative below 8 |c|, and two loss
