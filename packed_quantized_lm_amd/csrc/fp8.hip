@@ -99,7 +99,10 @@ __device__ __forceinline__ u32x2 codes8(const float v[8], float s)
     return o;
 }
 
-// one row's blocks: 16 lanes a block, 8 columns a lane
+// One row's blocks: 16 lanes a block, 8 columns a lane, so that a block's
+// largest magnitude takes four exchanges and a lane one load and one store
+// (2048 x 4096 bf16: 20 us with its exact quotients' arithmetic, which bounds
+// it; one row 5 us, a launch).
 template <typename T>
 __global__ __launch_bounds__(256) void quant_rows_kernel(const T *x, int64_t ldx, int64_t rows, int64_t cols,
                                                          uint8_t *q, int64_t ldq, float *s, int64_t lds)
@@ -184,7 +187,7 @@ __device__ __forceinline__ f16x8 halves(uint32_t lo, uint32_t hi)
 // cut off what lies 2^13 below it (measured: 2e-5 of the terms' magnitudes,
 // 1e-4 of a typical result), which would show in an fp32 result; a bf16
 // result, rounded at 2^-8, hides it, and there the tiles for many rows use
-// them (2048 x 151936 x 4096: 1.61 ms against 2.39 in fp16).
+// them (2048 x 151936 x 4096: 1.62 ms against 2.36 in fp16).
 __device__ __forceinline__ f32x4 block_product(i32x8 a, i32x8 b, f32x4 c)
 {
     for (int i = 0; i < 8; i += 2)
@@ -219,11 +222,12 @@ __device__ __forceinline__ i32x8 join(i32x4 a, i32x4 b)
 }
 
 // ---------------------------------------------------------------------------
-// Few rows (M <= 16): the weights are streamed once, which bounds it.  The
-// workgroups of 4 waves stay and take every gridDim-th block of 16 weight
-// rows; each wave takes a quarter of the row block's column blocks, and the
-// waves' sums meet in LDS.  Each wave keeps kDepth column blocks (2 KiB of
-// weights each) in flight, across the row blocks' ends.  The weights are the A
+// Few rows (M <= 16): the weights are streamed once, which bounds it (1 x 151936
+// x 4096: 105 us, 5.9 TB/s; a large copy runs at 4.9).  The workgroups of 4
+// waves stay and take every gridDim-th block of 16 weight rows; each wave takes
+// a quarter of the row block's column blocks, and the waves' sums meet in LDS.
+// Each wave keeps kDepth column blocks (2 KiB of weights each) in flight, across
+// the row blocks' ends; half or twice as many run alike.  The weights are the A
 // operand, so that a lane's four results are consecutive columns of one output
 // row.  Lane l takes bytes 16 (l / 16) .. +15 of both halves of a block's 128
 // columns: any order of the columns serves as long as both operands share it.
@@ -329,11 +333,14 @@ template <bool XL, typename O> __global__ __launch_bounds__(kSkinnyWaves * 64) v
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: tiles of BM output rows x BN columns, each wave [BM / 2 x 64].  A stage is one block of 128 columns of both operands, copied
-// straight into LDS as codes (16-byte pieces, a row's pieces exchanged by the
-// row's low bits so that the reads of eight neighbouring rows fall on
-// different banks) while the other buffer is worked on; the block's sums are
-// scaled into the accumulator in fp32.
+// Many rows: tiles of BM output rows x BN columns, each wave [BM / 2 x 64].  A
+// stage is one block of 128 columns of both operands, copied straight into LDS
+// as codes (16-byte pieces, a row's pieces exchanged by the row's low bits so
+// that the reads of eight neighbouring rows fall on different banks: no
+// conflicts counted) while the other buffer is worked on; the block's sums are
+// scaled into the accumulator in fp32.  2048 x 151936 x 4096: fp32 2.36 ms, 1080
+// TFLOP/s of the 1219 that a large bf16 library product reaches here, the matrix
+// cores 46 % busy beside the conversions; bf16 1.62 ms, 1577 TFLOP/s.
 // ---------------------------------------------------------------------------
 __device__ const u32x4 kNothing = {0u, 0u, 0u, 0u}; // what a piece past K is copied from
 
@@ -560,23 +567,22 @@ template <typename O> archead_status run_product(const ProdArgs &a, hipStream_t 
     else if (a.M <= 64)
         run_tile<64, 256, O>(a, st);
     else {
-        // Tiles by the rounds they take over kCu compute units, in units of a
-        // 128 x 256 tile: two of 128 x 128 run beside each other there (333 x
-        // 50021 x 2576, bf16: 119 us against 138; 1000 x 4096 x 4096, fp32: 53
-        // against 70), but move more per product (2048 x 151936 x 4096, fp32:
-        // 2.80 ms against 2.67); 256 x 256, bf16 only, is the most economical
-        // (1.95 ms against 2.14) and the coarsest.
-        auto rounds = [&](int64_t bm, int64_t bn) {
-            return double(((a.M + bm - 1) / bm * ((a.N + bn - 1) / bn) + kCu - 1) / kCu);
+        // 128 x 128, two of which run beside each other on a compute unit, or,
+        // for bf16 results, 256 x 256, which moves less per product (2048 x
+        // 151936 x 4096: 1.62 ms against 1.97) but fills a chip in coarser
+        // steps (333 x 50021 x 2576: 123 us against 104; 1000 x 4096 x 4096: 84
+        // against 34): by the rounds each takes, a round of the large ones
+        // being 1.64 times as long.  fp32 results run in fp16, whose 256 x 256
+        // tiles do not fit the registers (4.5 ms at 2048 x 151936 x 4096
+        // against 2.36).
+        auto rounds = [&](int64_t b, int64_t places) {
+            return double(((a.M + b - 1) / b * ((a.N + b - 1) / b) + places - 1) / places);
         };
-        const double small = 0.53 * rounds(128, 128), mid = rounds(128, 256), large = 1.75 * rounds(256, 256);
-        if (sizeof(O) == 2 && large < small && large < mid) {
+        if (sizeof(O) == 2 && 1.64 * rounds(256, kCu) < rounds(128, 2 * kCu)) {
             if constexpr (sizeof(O) == 2)
                 run_tile<256, 256, O>(a, st);
-        } else if (small < mid)
+        } else
             run_tile<128, 128, O>(a, st);
-        else
-            run_tile<128, 256, O>(a, st);
     }
     return launched("archead_fp8_matmul");
 }

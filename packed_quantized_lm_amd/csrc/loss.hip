@@ -16,8 +16,12 @@
 //   c = +-beta/P (sigma(h) - (1 - e)) w  (+ for the chosen answer).
 //
 // Everything is bound by the logits' bytes: one read for the statistics (a
-// running maximum and sum, fp32), one more read with a write for the
-// gradient.  Every sum has a fixed order: repeated calls agree bit for bit.
+// running maximum and sum, fp32; 2047 x 151936 fp32 205 us, 6.0 TB/s), one more
+// read with a write for the gradient.  Where a row's loss needs that row alone
+// (policy), a workgroup may keep much of it for the gradient; the preference
+// loss sums over answers first and reads twice (1800 x 151936 fp32, bf16
+// gradient: 174 + 10 + 291 us).  Every sum has a fixed order: repeated calls
+// agree bit for bit.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
