@@ -187,7 +187,7 @@ __device__ __forceinline__ f16x8 halves(uint32_t lo, uint32_t hi)
 // cut off what lies 2^13 below it (measured: 2e-5 of the terms' magnitudes,
 // 1e-4 of a typical result), which would show in an fp32 result; a bf16
 // result, rounded at 2^-8, hides it, and there the tiles for many rows use
-// them (2048 x 151936 x 4096: 1.62 ms against 2.36 in fp16).
+// them (2048 x 151936 x 4096: 1.62 ms against 2.40 in fp16).
 __device__ __forceinline__ f32x4 block_product(i32x8 a, i32x8 b, f32x4 c)
 {
     for (int i = 0; i < 8; i += 2)
@@ -338,7 +338,7 @@ template <bool XL, typename O> __global__ __launch_bounds__(kSkinnyWaves * 64) v
 // as codes (16-byte pieces, a row's pieces exchanged by the row's low bits so
 // that the reads of eight neighbouring rows fall on different banks: no
 // conflicts counted) while the other buffer is worked on; the block's sums are
-// scaled into the accumulator in fp32.  2048 x 151936 x 4096: fp32 2.36 ms, 1080
+// scaled into the accumulator in fp32.  2048 x 151936 x 4096: fp32 2.40 ms, 1062
 // TFLOP/s of the 1219 that a large bf16 library product reaches here, the matrix
 // cores 46 % busy beside the conversions; bf16 1.62 ms, 1577 TFLOP/s.
 // ---------------------------------------------------------------------------
@@ -347,13 +347,10 @@ __device__ const u32x4 kNothing = {0u, 0u, 0u, 0u}; // what a piece past K is co
 template <int BM, int BN> struct Tile {
     static constexpr int waves = BN / 32;                           // two along the rows, each 64 columns
     static constexpr int rows = BM + BN, codes = rows * kBlk / 4;
-    // The rows' scales lie behind the codes, but with BM = 64, where two
-    // workgroups share a compute unit's LDS only without them, in registers.
-    static constexpr bool reg = BM == 64;
-    static constexpr int words = codes + (reg ? 0 : BM);            // LDS of a stage
+    static constexpr int words = codes + BM;                        // LDS of a stage: the codes, the rows' scales
     static constexpr int copies = rows / 8 / waves;                 // 1 KiB copies per wave and stage
     static constexpr int mt = BM / 32, nt = 4;                      // 16 x 16 tiles per wave
-    static constexpr int wgs = words * 8 <= 80 * 1024 ? 2 : 1;      // workgroups a compute unit holds
+    static constexpr int wgs = 160 * 1024 / (words * 8);            // workgroups a compute unit holds
 };
 
 template <int BM, int BN, bool F8, typename O>
@@ -386,7 +383,6 @@ __global__ __launch_bounds__((BN * 2), (Tile<BM, BN>::wgs * BN / 128)) void prod
                                         : (uint32_t)min((int64_t)row - BM, a.N - 1 - n0) * (uint32_t)a.ldb) + col;
     }
     const uint32_t lds0 = lds_address(smem);
-    float sn[T::mt], sc[T::mt]; // T::reg: the next stage's row scales and this one's
     auto fill = [&](int at, int64_t b) { // at: the buffer's first word
         const int64_t k0 = b * kBlk;
         if (k0 + kBlk <= a.K) {
@@ -401,10 +397,7 @@ __global__ __launch_bounds__((BN * 2), (Tile<BM, BN>::wgs * BN / 128)) void prod
                 lds_dma16<false>(k0 + col < a.K ? p : (const uint8_t *)&kNothing, &smem[at + (T::waves * c + wv) * 256]);
             }
         }
-        if constexpr (T::reg)
-            for (int t = 0; t < T::mt; ++t)
-                sn[t] = a.sA[b * a.ldsa + min(m0 + wm + 16 * t + r, a.M - 1)];
-        else if (wv < BM / 64)
+        if (wv < BM / 64)
             lds_dma4(a.sA + b * a.ldsa + min(m0 + 64 * wv + lane, a.M - 1), &smem[at + T::codes + 64 * wv]);
     };
     const float *sw = a.sB + min((n0 + wn) / kBlk, (a.N - 1) / kBlk) * a.ldsb;
@@ -415,7 +408,7 @@ __global__ __launch_bounds__((BN * 2), (Tile<BM, BN>::wgs * BN / 128)) void prod
         return join(*(const i32x4 *)&smem[at + f0 + row * 32], *(const i32x4 *)&smem[at + f1 + row * 32]);
     };
     auto row_scale = [&](int at, int t) {
-        return T::reg ? sc[t] : __uint_as_float(smem[at + T::codes + wm + 16 * t + r]);
+        return __uint_as_float(smem[at + T::codes + wm + 16 * t + r]);
     };
     f32x4 acc[T::mt][4];
     for (int t = 0; t < T::mt; ++t)
@@ -516,9 +509,6 @@ __global__ __launch_bounds__((BN * 2), (Tile<BM, BN>::wgs * BN / 128)) void prod
         const float f = sw[b];
         wait_vm_all();
         __syncthreads(); // this stage is filled, and everyone is done with the other buffer
-        if constexpr (T::reg)
-            for (int t = 0; t < T::mt; ++t)
-                sc[t] = sn[t];
         if (b + 1 < nb)
             fill(T::words - cur, b + 1);
         work(cur, f);
@@ -564,8 +554,12 @@ template <typename O> archead_status run_product(const ProdArgs &a, hipStream_t 
 {
     if (a.M <= kSkinnyM)
         run_skinny<O>(a, st);
-    else if (a.M <= 64)
-        run_tile<64, 256, O>(a, st);
+    // 64 x 128, three of which run beside each other on a compute unit, for few
+    // rows (64 x 151936 x 4096, fp32: 164 us; two of 64 x 256: 189) and, in fp32,
+    // where 128 x 128 would leave compute units idle or alone with one (512 x 4096
+    // x 4096: 30 us against 43; 1000 x 4096 x 4096: 44 against 45).
+    else if (a.M <= 64 || (sizeof(O) == 4 && (a.M + 127) / 128 * ((a.N + 127) / 128) <= kCu))
+        run_tile<64, 128, O>(a, st);
     else {
         // 128 x 128, two of which run beside each other on a compute unit, or,
         // for bf16 results, 256 x 256, which moves less per product (2048 x
@@ -574,7 +568,7 @@ template <typename O> archead_status run_product(const ProdArgs &a, hipStream_t 
         // against 34): by the rounds each takes, a round of the large ones
         // being 1.64 times as long.  fp32 results run in fp16, whose 256 x 256
         // tiles do not fit the registers (4.5 ms at 2048 x 151936 x 4096
-        // against 2.36).
+        // against 2.40).
         auto rounds = [&](int64_t b, int64_t places) {
             return double(((a.M + b - 1) / b * ((a.N + b - 1) / b) + places - 1) / places);
         };

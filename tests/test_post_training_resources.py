@@ -46,7 +46,7 @@ def test_no_kernel_needs_scratch_memory(usage):
 
 @pytest.mark.parametrize("kernel,count,groups", [
     ("11tile_kernelILi32E", 1, 3), ("11tile_kernelILi64E", 1, 2), ("11tile_kernelILi256E", 1, 1),
-    ("product_tile_kernelILi64ELi256E", 2, 2), ("product_tile_kernelILi128ELi128E", 2, 2)])
+    ("product_tile_kernelILi64ELi128E", 2, 3), ("product_tile_kernelILi128ELi128E", 2, 2)])
 def test_workgroups_per_compute_unit(usage, kernel, count, groups):
     found = {n: u for n, u in usage.items() if kernel in n}
     assert len(found) == count, sorted(usage)
