@@ -51,6 +51,9 @@ def need_rows(t, name, dtypes, shape, device):
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
+    # the usual call, in one line; the rest says what is wrong with another
+    if device.type == "cuda" and t.device == device and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+        return max(shape[1], 1)
     if t.device.type != "cuda" or t.device != device:
         raise ValueError(f"{name} must live on {device}, not {t.device}")
     if t.dtype not in dtypes:
@@ -81,7 +84,7 @@ def _logit_args(logits, targets, **vectors):
     import torch
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError("logits must be an M x V tensor")
-    M, V = (int(n) for n in logits.shape)
+    M, V = logits.shape
     if V < 1:
         raise ValueError("logits need at least one column")
     code = _type_code(logits.dtype, "logits")
@@ -97,7 +100,7 @@ def _workspace(M, V, P, device):
     import torch
     n = ctypes.c_uint64()
     _check(load_library().archead_loss_workspace(M, V, P, ctypes.byref(n)), "archead_loss_workspace")
-    return torch.empty((n.value,), dtype=torch.uint8, device=device), n.value
+    return torch.empty(n.value, dtype=torch.uint8, device=device), n.value
 
 
 def _gradient(logits, M, V, grad_dtype, dlogits):
@@ -107,7 +110,7 @@ def _gradient(logits, M, V, grad_dtype, dlogits):
         return None, 0, 0
     if dlogits is None:
         code = _type_code(grad_dtype, "grad_dtype")
-        return torch.empty((M, V), dtype=grad_dtype, device=logits.device), code, V
+        return torch.empty(M, V, dtype=grad_dtype, device=logits.device), code, V
     if grad_dtype is not None and dlogits.dtype != grad_dtype:
         raise ValueError("dlogits and grad_dtype disagree")
     code = _type_code(dlogits.dtype, "dlogits")
@@ -122,8 +125,8 @@ def token_logp(logits, targets, stream=None):
     dev = logits.device
 
     def call(st):
-        logp = torch.empty((M,), dtype=torch.float32, device=dev)
-        lse = torch.empty((M,), dtype=torch.float32, device=dev)
+        logp = torch.empty(M, dtype=torch.float32, device=dev)
+        lse = torch.empty(M, dtype=torch.float32, device=dev)
         ws, n = _workspace(M, V, 0, dev)
         _check(load_library().archead_token_logp(M, V, ptr(logits), code, ld, ptr(targets), ptr(logp), ptr(lse),
                                                  ptr(ws), n, st), "archead_token_logp")
@@ -183,8 +186,8 @@ def preference_loss(logits, targets, weights, offsets, ref_logp=None, beta: floa
     def call(st):
         dy, gcode, ldg = _gradient(logits, M, V, grad_dtype, dlogits)
         loss = torch.empty((), dtype=torch.float32, device=dev)
-        margins = torch.empty((P,), dtype=torch.float32, device=dev)
-        logp = torch.empty((M,), dtype=torch.float32, device=dev)
+        margins = torch.empty(P, dtype=torch.float32, device=dev)
+        logp = torch.empty(M, dtype=torch.float32, device=dev)
         ws, n = _workspace(M, V, P, dev)
         _check(load_library().archead_preference_loss(
             M, V, ptr(logits), code, ld, ptr(targets), ptr(weights), P, ptr(offsets), ptr(ref_logp), float(beta),
