@@ -187,7 +187,7 @@ __device__ __forceinline__ f16x8 halves(uint32_t lo, uint32_t hi)
 // cut off what lies 2^13 below it (measured: 2e-5 of the terms' magnitudes,
 // 1e-4 of a typical result), which would show in an fp32 result; a bf16
 // result, rounded at 2^-8, hides it, and there the tiles for many rows use
-// them (2048 x 151936 x 4096: 1.62 ms against 2.40 in fp16).
+// them (2048 x 151936 x 4096: 1.62 ms against 2.14 in fp16).
 __device__ __forceinline__ f32x4 block_product(i32x8 a, i32x8 b, f32x4 c)
 {
     for (int i = 0; i < 8; i += 2)
@@ -338,9 +338,9 @@ template <bool XL, typename O> __global__ __launch_bounds__(kSkinnyWaves * 64) v
 // as codes (16-byte pieces, a row's pieces exchanged by the row's low bits so
 // that the reads of eight neighbouring rows fall on different banks: no
 // conflicts counted) while the other buffer is worked on; the block's sums are
-// scaled into the accumulator in fp32.  2048 x 151936 x 4096: fp32 2.40 ms, 1062
-// TFLOP/s of the 1219 that a large bf16 library product reaches here, the matrix
-// cores 46 % busy beside the conversions; bf16 1.62 ms, 1577 TFLOP/s.
+// scaled into the accumulator in fp32.  2048 x 151936 x 4096: fp32 2.14 ms, 1190
+// TFLOP/s of the 1219 that a large bf16 library product reaches here; bf16 1.62
+// ms, 1577 TFLOP/s.
 // ---------------------------------------------------------------------------
 __device__ const u32x4 kNothing = {0u, 0u, 0u, 0u}; // what a piece past K is copied from
 
@@ -465,15 +465,18 @@ __global__ __launch_bounds__((BN * 2), (Tile<BM, BN>::wgs * BN / 128)) void prod
                 if (hold_x)
                     sh[n] = row_scale(at, n) * f;
             }
-            f32x4 pp[2][nh];
+            // sums scaled while the next tile's are formed, but with 256 rows,
+            // where registers for one tile's sums are left alone
+            constexpr int depth = BM == 256 ? 1 : 2;
+            f32x4 pp[depth][nh];
             float s1 = 0.f;
             auto add = [&](int t, float st) {
                 for (int n = 0; n < nh; ++n)
                     for (int i = 0; i < 4; ++i) {
                         if constexpr (hold_x)
-                            acc[n][t][i] = __builtin_fmaf(pp[t & 1][n][i], sh[n], acc[n][t][i]);
+                            acc[n][t][i] = __builtin_fmaf(pp[t % depth][n][i], sh[n], acc[n][t][i]);
                         else
-                            acc[t][n][i] = __builtin_fmaf(pp[t & 1][n][i], st, acc[t][n][i]);
+                            acc[t][n][i] = __builtin_fmaf(pp[t % depth][n][i], st, acc[t][n][i]);
                     }
             };
             __builtin_amdgcn_sched_barrier(0);
@@ -486,7 +489,7 @@ __global__ __launch_bounds__((BN * 2), (Tile<BM, BN>::wgs * BN / 128)) void prod
                     if (!hold_x)
                         s = row_scale(at, t + 1) * f;
                 }
-                f32x4 (&p)[nh] = pp[t & 1];
+                f32x4 (&p)[nh] = pp[t % depth];
                 for (int n = 0; n < nh; ++n)
                     p[n] = f32x4{0.f, 0.f, 0.f, 0.f};
                 for (int h = 0; h < 4; ++h) {
@@ -495,12 +498,15 @@ __global__ __launch_bounds__((BN * 2), (Tile<BM, BN>::wgs * BN / 128)) void prod
                         p[n] = hold_x ? __builtin_amdgcn_mfma_f32_16x16x32_f16(y, held[n][h], p[n], 0, 0, 0)
                                       : __builtin_amdgcn_mfma_f32_16x16x32_f16(held[n][h], y, p[n], 0, 0, 0);
                 }
-                if (t > 0)
+                if (depth == 1)
+                    add(t, st);
+                else if (t > 0)
                     add(t - 1, s1);
                 s1 = st;
                 __builtin_amdgcn_sched_barrier(0);
             }
-            add(np - 1, s1);
+            if (depth == 2)
+                add(np - 1, s1);
         }
     };
     fill(0, 0);
@@ -561,21 +567,19 @@ template <typename O> archead_status run_product(const ProdArgs &a, hipStream_t 
     else if (a.M <= 64 || (sizeof(O) == 4 && (a.M + 127) / 128 * ((a.N + 127) / 128) <= kCu))
         run_tile<64, 128, O>(a, st);
     else {
-        // 128 x 128, two of which run beside each other on a compute unit, or,
-        // for bf16 results, 256 x 256, which moves less per product (2048 x
-        // 151936 x 4096: 1.62 ms against 1.97) but fills a chip in coarser
-        // steps (333 x 50021 x 2576: 123 us against 104; 1000 x 4096 x 4096: 84
-        // against 34): by the rounds each takes, a round of the large ones
-        // being 1.64 times as long.  fp32 results run in fp16, whose 256 x 256
-        // tiles do not fit the registers (4.5 ms at 2048 x 151936 x 4096
-        // against 2.40).
+        // 128 x 128, two of which run beside each other on a compute unit, or 256
+        // x 256, which move and convert less per product (2048 x 151936 x 4096:
+        // fp32 2.14 ms against 2.37, bf16 1.62 against 1.97) but fill a chip in
+        // coarser steps (333 x 50021 x 2576, bf16: 123 us against 104; 2048 x
+        // 50021 x 2576, fp32: 604 against 581): by the rounds each takes, a round
+        // of the large ones being 1.64 (bf16, in fp8) or 1.88 times (fp32, in
+        // fp16) as long.
         auto rounds = [&](int64_t b, int64_t places) {
             return double(((a.M + b - 1) / b * ((a.N + b - 1) / b) + places - 1) / places);
         };
-        if (sizeof(O) == 2 && 1.64 * rounds(256, kCu) < rounds(128, 2 * kCu)) {
-            if constexpr (sizeof(O) == 2)
-                run_tile<256, 256, O>(a, st);
-        } else
+        if ((sizeof(O) == 2 ? 1.64 : 1.88) * rounds(256, kCu) < rounds(128, 2 * kCu))
+            run_tile<256, 256, O>(a, st);
+        else
             run_tile<128, 128, O>(a, st);
     }
     return launched("archead_fp8_matmul");

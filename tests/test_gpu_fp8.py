@@ -109,7 +109,7 @@ def test_nan_and_infinity():
 SHAPES = [(1, 1, 16), (1, 37, 48), (2, 16, 128), (5, 129, 144), (16, 300, 256), (17, 40, 1040), (33, 1000, 400),
           (64, 257, 512), (65, 130, 272), (127, 515, 640), (128, 256, 256), (129, 257, 384), (200, 700, 1168),
           (300, 1100, 2064), (513, 300, 128), (1, 5000, 4096), (7, 3001, 2576), (16, 300, 4096),
-          (9, 200, 16400), (130, 4097, 1024), (600, 2500, 144)]
+          (9, 200, 16400), (130, 4097, 1024), (600, 2500, 144), (777, 6001, 400), (999, 16290, 272)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
