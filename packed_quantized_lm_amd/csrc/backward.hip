@@ -35,6 +35,7 @@
 #include "api_internal.hpp"
 #include "archead.h"
 #include "device.hpp"
+#include "lds_copy.hpp"
 
 namespace archead {
 namespace {

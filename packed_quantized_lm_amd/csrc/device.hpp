@@ -354,23 +354,6 @@ __device__ __forceinline__ void lds_dma16(const void *p, void *dst)
                      : "memory");
 }
 
-// The same from a uniform base (in scalar registers) and a 32-bit byte offset
-// per lane, with dst a byte address in LDS (uniform): no vector arithmetic.
-__device__ __forceinline__ void lds_dma16_from(const void *base, uint32_t offset, uint32_t dst)
-{
-    uint32_t m0;
-    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\t"
-                 "global_load_lds_dwordx4 %1, %2\n\ts_nop 0\n\ts_mov_b32 m0, %0"
-                 : "=&s"(m0)
-                 : "v"(offset), "s"(base), "s"(dst)
-                 : "memory");
-}
-
-// byte address in LDS of a __shared__ object
-__device__ __forceinline__ uint32_t lds_address(const void *p)
-{
-    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
-}
 
 // The same for one 4-byte piece per lane (LDS dst + 4 lane).
 __device__ __forceinline__ void lds_dma4(const void *p, void *dst)

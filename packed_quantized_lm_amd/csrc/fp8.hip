@@ -18,6 +18,7 @@
 #include "api_internal.hpp"
 #include "archead.h"
 #include "device.hpp"
+#include "lds_copy.hpp"
 
 namespace archead {
 namespace {
