@@ -533,28 +533,25 @@ __global__ __launch_bounds__(kNT) void pair_kernel(Rows a, const Stat *part, con
         if (i > 0)
             b[i] = max(b[i], b[i - 1]);
     }
-    double sum[2];
-    for (int i = 0; i < 2; ++i) {
-        double s = 0.;
-        for (int64_t m = b[i] + threadIdx.x; m < b[i + 1]; m += kNT) {
-            double lp = 0.;
-            if (row_counts(a, m)) {
-                lp = row_logp<T>(a, m, merge_slices(part + m * a.S, a.S));
-                s += (double)a.weights[m] * (lp - (double)(ref ? ref[m] : 0.f));
-            }
-            if (logp)
-                logp[m] = (float)lp;
+    // both answers in one pass, the rejected one's rows with a minus
+    double s = 0.;
+    for (int64_t m = b[0] + threadIdx.x; m < b[2]; m += kNT) {
+        double lp = 0.;
+        if (row_counts(a, m)) {
+            lp = row_logp<T>(a, m, merge_slices(part + m * a.S, a.S));
+            const double term = (double)a.weights[m] * (lp - (double)(ref ? ref[m] : 0.f));
+            s += m < b[1] ? term : -term;
         }
-        sum[i] = block_sum<kNT>(s, red);
+        if (logp)
+            logp[m] = (float)lp;
     }
-    const double h = (double)beta * (sum[0] - sum[1]), sm = smooth;
+    const double h = (double)beta * block_sum<kNT>(s, red), sm = smooth;
     const double e = exp(-fabs(h)), sp = log1p(e);             // log(1 + exp(-|h|))
     const double up = 1. / (1. + e), down = e / (1. + e);      // sigma(|h|), sigma(-|h|)
     // sigma(h) - (1 - smooth) = smooth sigma(h) - (1 - smooth) sigma(-h)
     const double slope = (double)beta / (double)P * (sm * (h >= 0. ? up : down) - (1. - sm) * (h >= 0. ? down : up));
-    for (int i = 0; i < 2; ++i)
-        for (int64_t m = b[i] + threadIdx.x; m < b[i + 1]; m += kNT)
-            coef[m] = row_counts(a, m) ? (float)((i ? -slope : slope) * a.weights[m]) : 0.f;
+    for (int64_t m = b[0] + threadIdx.x; m < b[2]; m += kNT)
+        coef[m] = row_counts(a, m) ? (float)((m < b[1] ? slope : -slope) * a.weights[m]) : 0.f;
     if (threadIdx.x == 0) {
         const double over = h != h ? h : fmax(h, 0.), under = h != h ? h : fmax(-h, 0.); // a NaN stays
         pair[p] = (float)((1. - sm) * (sp + under) + sm * (sp + over));
