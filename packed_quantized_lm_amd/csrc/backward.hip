@@ -729,13 +729,16 @@ double ranges_of(const TileKind &k, int64_t M, int64_t tiles, int64_t tile_cols,
     const int64_t places = kCu * k.places, most = std::max<int64_t>(1, nvc / kMinChunks);
     const double sums = double(M) * double(tiles * tile_cols) * 8 / kSumRate;
     double least = 1e300;
-    for (int64_t S = 1; S <= most && (S == 1 || S * t <= kMaxWg); ++S) {
-        const double cost = double((S * t + places - 1) / places) * (double((nvc + S - 1) / S) + 2.0) * k.us +
-                            double(S) * sums;
+    for (int64_t S = 1; S <= most && (S == 1 || S * t <= kMaxWg);) {
+        const int64_t chunks = (nvc + S - 1) / S;
+        const double cost = double((S * t + places - 1) / places) * (double(chunks) + 2.0) * k.us + double(S) * sums;
         if (cost < least * 0.995) {
             least = cost;
             *ranges = S;
         }
+        if (chunks == 1)
+            break;
+        S = (nvc + chunks - 2) / (chunks - 1); // the fewest ranges that shorten the longest
     }
     return least;
 }
