@@ -21,7 +21,7 @@
 // Few rows are bound by the codes' bytes, many by the matrix cores.  In us:
 //                    16 x 151936 x 4096     2048 x 151936 x 4096
 //   amax, convert         10                    239  (5.2 TB/s in one pass)
-//   tiles                 84 (4.7 TB/s)         340 + 2100 (1210 TFLOP/s in dX's,
+//   tiles                 84 (5.2 TB/s)         345 + 2160 (1180 TFLOP/s in dX's,
 //                                               matrix cores 65 % busy)
 //   sums, finish          15                     80
 #include <hip/hip_runtime.h>

@@ -350,7 +350,7 @@ template <int BM, int BN> struct Tile {
     static constexpr int rows = BM + BN, codes = rows * kBlk / 4;
     static constexpr int words = codes + BM;                        // LDS of a stage: the codes, the rows' scales
     static constexpr int copies = rows / 8 / waves;                 // 1 KiB copies per wave and stage
-    static constexpr int mt = BM / 32, nt = 4;                      // 16 x 16 tiles per wave
+    static constexpr int mt = BM / 32;                              // 16 x 16 tiles per wave: mt x 4
     static constexpr int wgs = 160 * 1024 / (words * 8);            // workgroups a compute unit holds
 };
 
