@@ -121,6 +121,21 @@ def test_empty_rows_and_bad_targets():
     assert logp.shape == (0,)
 
 
+@pytest.mark.parametrize("M,V", [(1, 8193), (37, 12289), (512, 9001), (513, 9001), (1, 32768), (2, 32769), (229, 33001),
+                                 (231, 33001), (256, 40003)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_token_logp_rows_and_slices(M, V, dtype):
+    """Row counts and lengths on both sides of where rows are cut into slices."""
+    from packed_quantized_lm_amd import token_logp
+    say(f"token_logp M={M} V={V} {dtype}")
+    _, logits, y64, t, want = make(M, V, 3 + M + V, dtype, 1)
+    logp, lse = token_logp(logits, dev(t, "int32"))
+    rows = np.arange(M)
+    tol = logp_tol(y64, t, rows, V)
+    assert (np.abs(logp.double().cpu().numpy() - want) <= tol).all()
+    assert (np.abs(lse.double().cpu().numpy() - (y64[rows, t] - want)) <= tol + 2 * U * np.abs(y64.max(1))).all()
+
+
 def policy_case(M, V, dtype, pad, seed, beta):
     rng, logits, y64, t, logp = make(M, V, seed, dtype, pad)
     step = rng.normal(0, 0.3, M)
