@@ -382,11 +382,12 @@ __device__ __forceinline__ f16x8 dequant4(uint32_t w, u32x4 s, uint32_t magic)
 // eight bytes likewise; off = -(1024 + the codes' offset)
 __device__ __forceinline__ f16x8 dequant8(uint32_t w0, uint32_t w1, u32x4 s, uint32_t magic, f16x2 off)
 {
-    // bytes 2 p, 2 p + 1 of a dword into the low bytes of its two halves
-    const f16x2 a = (as_h2(__builtin_amdgcn_perm(0u, w0, 0x0c010c00u) | magic) + off) * as_h2(s.x);
-    const f16x2 b = (as_h2(__builtin_amdgcn_perm(0u, w0, 0x0c030c02u) | magic) + off) * as_h2(s.y);
-    const f16x2 c = (as_h2(__builtin_amdgcn_perm(0u, w1, 0x0c010c00u) | magic) + off) * as_h2(s.z);
-    const f16x2 d = (as_h2(__builtin_amdgcn_perm(0u, w1, 0x0c030c02u) | magic) + off) * as_h2(s.w);
+    // bytes 2 p, 2 p + 1 of a dword into the low bytes of two halves, the high
+    // ones from magic (1024 in fp16)
+    const f16x2 a = (as_h2(__builtin_amdgcn_perm(magic, w0, 0x05010500u)) + off) * as_h2(s.x);
+    const f16x2 b = (as_h2(__builtin_amdgcn_perm(magic, w0, 0x05030502u)) + off) * as_h2(s.y);
+    const f16x2 c = (as_h2(__builtin_amdgcn_perm(magic, w1, 0x05010500u)) + off) * as_h2(s.z);
+    const f16x2 d = (as_h2(__builtin_amdgcn_perm(magic, w1, 0x05030502u)) + off) * as_h2(s.w);
     return f16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
