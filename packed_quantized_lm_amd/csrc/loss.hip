@@ -16,7 +16,7 @@
 //   c = +-beta/P (sigma(h) - (1 - e)) w  (+ for the chosen answer).
 //
 // Everything is bound by the logits' bytes: one read for the statistics (a
-// running maximum and sum, fp32; 2047 x 151936 fp32 205 us, 6.0 TB/s), one more
+// running maximum and sum; 2047 x 151936 fp32 205 us, 6.0 TB/s), one more
 // read with a write for the gradient.  Where a row's loss needs that row alone
 // (policy), a workgroup may keep much of it for the gradient; the preference
 // loss sums over answers first and reads twice (1800 x 151936 fp32, bf16
@@ -103,9 +103,12 @@ __device__ __forceinline__ float exp_neg(float x)
     return __builtin_amdgcn_exp2f(__builtin_fmaf(x, kLog2e, x * kLog2eLow));
 }
 
-// running maximum and sum of exp(y - m); m = -inf and s = 0 when empty
+// running maximum and sum of exp(y - m); m = -inf and s = 0 when empty.  The
+// sum is fp64 between vectors of eight: next to a term of 1, fp32 rounds off
+// what a token of probability near 1 has for its log probability.
 struct Stat {
-    float m, s;
+    double s;
+    float m;
 };
 
 // what exp is taken against: the maximum, or 0 while it is -inf (a row or
@@ -116,7 +119,7 @@ __device__ __forceinline__ float anchor(float m) { return m == -INFINITY ? 0.f :
 __device__ __forceinline__ Stat merge(Stat a, Stat b)
 {
     const float m = fmaxf(a.m, b.m), r = anchor(m);
-    return Stat{m, a.s * exp_neg(a.m - r) + b.s * exp_neg(b.m - r)};
+    return Stat{a.s * exp_neg(a.m - r) + b.s * exp_neg(b.m - r), m};
 }
 
 __device__ __forceinline__ void add8(Stat &st, const float v[kVec])
@@ -130,7 +133,7 @@ __device__ __forceinline__ void add8(Stat &st, const float v[kVec])
         e[i] = exp_neg(v[i] - r);
     // pairwise: a thread's chain of additions is an eighth as long
     const float add = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-    st = Stat{m, __builtin_fmaf(st.s, exp_neg(st.m - r), add)};
+    st = Stat{__builtin_fma(st.s, (double)exp_neg(st.m - r), (double)add), m};
 }
 
 // Statistics of y[0 .. n), one part per thread.  The thread's first H vectors
@@ -139,7 +142,7 @@ __device__ __forceinline__ void add8(Stat &st, const float v[kVec])
 template <int NT, int H, int L, typename T>
 __device__ __forceinline__ Stat scan_part(const T *y, int64_t n, Raw<T> (&held)[H > 0 ? H : 1], Raw<T> *more)
 {
-    Stat st{-INFINITY, 0.f};
+    Stat st{0., -INFINITY};
     const int64_t nv = n / kVec;
     int64_t q = threadIdx.x;
     if (H > 0 && nv > 0) {
@@ -188,7 +191,7 @@ __device__ __forceinline__ Stat scan_part(const T *y, int64_t n, Raw<T> (&held)[
     }
     const int64_t i = nv * kVec + threadIdx.x;
     if (i < n)
-        st = merge(st, Stat{load1(y + i), 1.f});
+        st = merge(st, Stat{1., load1(y + i)});
     return st;
 }
 
@@ -196,14 +199,18 @@ __device__ __forceinline__ Stat scan_part(const T *y, int64_t n, Raw<T> (&held)[
 template <int NT> __device__ __forceinline__ Stat block_merge(Stat st, Stat *red)
 {
     for (int off = 32; off >= 1; off >>= 1)
-        st = merge(st, Stat{__shfl_xor(st.m, off), __shfl_xor(st.s, off)});
+        st = merge(st, Stat{__shfl_xor(st.s, off), __shfl_xor(st.m, off)});
     if ((threadIdx.x & 63) == 0)
         red[threadIdx.x >> 6] = st;
     __syncthreads();
-    st = red[0];
+    float m = red[0].m;
     for (int w = 1; w < NT / 64; ++w)
-        st = merge(st, red[w]);
-    return st;
+        m = fmaxf(m, red[w].m);
+    const float r = anchor(m);
+    double s = 0.;
+    for (int w = 0; w < NT / 64; ++w)
+        s += red[w].s * exp_neg(red[w].m - r);
+    return Stat{s, m};
 }
 
 struct Rows {
@@ -239,14 +246,14 @@ template <typename T> __device__ __forceinline__ double row_logp(const Rows &a, 
     const int32_t t = a.targets[m];
     if (t < 0 || t >= a.V)
         return __builtin_nan("");
-    return ((double)load1(row_ptr<T>(a, m) + t) - (double)st.m) - log((double)st.s);
+    return ((double)load1(row_ptr<T>(a, m) + t) - (double)st.m) - log(st.s);
 }
-__device__ __forceinline__ float stat_lse(Stat st) { return (float)((double)st.m + log((double)st.s)); }
+__device__ __forceinline__ float stat_lse(Stat st) { return (float)((double)st.m + log(st.s)); }
 
 // the slices' parts of one row, eight loads in flight
 __device__ __forceinline__ Stat merge_slices(const Stat *part, int64_t S)
 {
-    Stat st{-INFINITY, 0.f};
+    Stat st{0., -INFINITY};
     for (int64_t i = 0; i < S; i += 8) {
         Stat p[8];
         for (int u = 0; u < 8; ++u)
@@ -255,10 +262,10 @@ __device__ __forceinline__ Stat merge_slices(const Stat *part, int64_t S)
         for (int u = 0; u < 8; ++u)
             m = fmaxf(m, p[u].m);
         const float r = anchor(m);
-        float s = st.s * exp_neg(st.m - r);
+        double s = st.s * exp_neg(st.m - r);
         for (int u = 0; u < 8; ++u)
-            s += i + u < S ? p[u].s * exp_neg(p[u].m - r) : 0.f;
-        st = Stat{m, s};
+            s += i + u < S ? p[u].s * exp_neg(p[u].m - r) : 0.;
+        st = Stat{s, m};
     }
     return st;
 }
@@ -355,7 +362,7 @@ template <int NT, int H, int L, typename T, typename G>
 __device__ __forceinline__ void grad_part(const T *y, G *g, int64_t n, int64_t t, float c, Stat st,
                                           const Raw<T> (&held)[H > 0 ? H : 1], const Raw<T> *more)
 {
-    const float r = anchor(st.m), k = -c / st.s;
+    const float r = anchor(st.m), k = -c / (float)st.s;
     auto put = [&](const Raw<T> &w, int64_t q) {
         float v[kVec];
         values(w, v);
@@ -460,7 +467,7 @@ __global__ __launch_bounds__(NT) void policy_row_kernel(Rows a, Policy pol, cons
     __shared__ Stat red[NT / 64];
     const int64_t m = blockIdx.x;
     __shared__ float coef;
-    Stat st{0.f, 1.f};
+    Stat st{1., 0.f};
     Raw<T> held[H > 0 ? H : 1];
     __shared__ Raw<T> more[L > 0 ? L * NT : 1];
     const T *y = row_ptr<T>(a, m);
@@ -473,7 +480,7 @@ __global__ __launch_bounds__(NT) void policy_row_kernel(Rows a, Policy pol, cons
         const float yt = t >= 0 && t < a.V ? load1(y + t) : __builtin_nanf("");
         st = block_merge<NT>(scan_part<NT, H, L, T>(y, a.V, held, more), red);
         if (threadIdx.x < 64) { // one wave: fp64 is slow
-            const double lp64 = ((double)yt - (double)st.m) - log((double)st.s);
+            const double lp64 = ((double)yt - (double)st.m) - log(st.s);
             lp = (float)lp64;
             loss = policy_token(pol, m, a.weights[m], lp64, &c);
         }

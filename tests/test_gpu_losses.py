@@ -136,6 +136,26 @@ def test_token_logp_rows_and_slices(M, V, dtype):
     assert (np.abs(lse.double().cpu().numpy() - (y64[rows, t] - want)) <= tol + 2 * U * np.abs(y64.max(1))).all()
 
 
+@pytest.mark.parametrize("V", [2, 3, 7])
+def test_token_logp_of_near_certain_tokens(V):
+    """Probabilities of 1 - 1e-3 and nearer: logp = -log(1 + rest) keeps the
+    relative precision of rest.  A term exp(-x), x < 13.5, is off by (2 x + 2) u
+    and by 2 u for each of six merges that may rescale it; logp's rounding adds
+    u: 42 u relative."""
+    from packed_quantized_lm_amd import token_logp
+    say(f"token_logp near certain V={V}")
+    rng = np.random.default_rng(V)
+    M = 300
+    y = rng.uniform(-3, 0, (M, V))
+    t = rng.integers(0, V, M)
+    y[np.arange(M), t] = rng.uniform(5.9, 8.5, M) + np.log(V)
+    y = y.astype(np.float32)
+    want = losses.token_logp(y.astype(np.float64), t)
+    assert (want < 0).all() and (want > -3e-3).all()
+    got = token_logp(dev(y), dev(t, "int32"))[0].double().cpu().numpy()
+    assert (np.abs(got - want) <= 42 * U * np.abs(want)).all(), (np.abs(got - want) / np.abs(want)).max() / U
+
+
 def policy_case(M, V, dtype, pad, seed, beta):
     rng, logits, y64, t, logp = make(M, V, seed, dtype, pad)
     step = rng.normal(0, 0.3, M)
