@@ -14,9 +14,11 @@ import numpy as np
 def _row_logp(row, target):
     if not 0 <= target < row.shape[0]:
         return np.nan
-    with np.errstate(invalid="ignore"):
+    with np.errstate(invalid="ignore", divide="ignore"):
         away = row - row.max()  # taken first: at the type's lowest values lse - y would lose everything
-        return away[target] - np.log(np.exp(away).sum())
+        top = int(away.argmax())
+        rest = np.exp(np.delete(away, top)).sum()  # next to the largest's 1 a sum would round off small terms
+        return away[target] - (np.log1p(rest) + away[top])  # away[top] is 0, or the row's NaN
 
 
 def token_logp(logits, targets):
