@@ -36,8 +36,9 @@ def _gradient(y, targets, coef):
             g[m] = np.nan
             continue
         e = np.exp(y[m] - y[m].max())
+        others = np.delete(e, int(targets[m])).sum()  # 1 - p of the target, however near p is to 1
         g[m] = -coef[m] * e / e.sum()
-        g[m, int(targets[m])] += coef[m]
+        g[m, int(targets[m])] = coef[m] * (others / e.sum())
     return g
 
 

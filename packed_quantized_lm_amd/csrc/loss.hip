@@ -277,15 +277,29 @@ __device__ __forceinline__ double log_z(double rest)
     return log(z) + (rest - (z - 1.)) * (double)__builtin_amdgcn_rcpf((float)fmax(z, 1.));
 }
 
-// Log probability of row m's target; NaN for a target outside [0, V).  A row's
-// few scalars are taken in fp64: log Z in fp32 alone is off by up to 5e-7, which
-// the losses' differences of log probabilities would keep.
-template <typename T> __device__ __forceinline__ double row_logp(const Rows &a, int64_t m, Stat st)
+// Log probability of a row's target and 1 - p, both NaN for a logit yt that is.  A
+// row's few scalars are taken in fp64: log Z in fp32 alone is off by up to 5e-7,
+// which the losses' differences of log probabilities would keep.  1 - p from
+// what is beside the target, (rest + 1 - exp(yt - m)) / Z: with p of fp32 the
+// difference would keep nothing for tokens of probability near 1.
+struct Token {
+    double logp;
+    float other;
+};
+__device__ __forceinline__ Token token_of(Stat st, float yt)
+{
+    const double beside = st.rest + (1. - (double)exp_neg(yt - anchor(st.m)));
+    return Token{((double)yt - (double)st.m) - log_z(st.rest), (float)beside / (float)(1. + st.rest)};
+}
+// row m's target's logit, NaN for a target outside [0, V)
+template <typename T> __device__ __forceinline__ float target_logit(const Rows &a, int64_t m)
 {
     const int32_t t = a.targets[m];
-    if (t < 0 || t >= a.V)
-        return __builtin_nan("");
-    return ((double)load1(row_ptr<T>(a, m) + t) - (double)st.m) - log_z(st.rest);
+    return t >= 0 && t < a.V ? load1(row_ptr<T>(a, m) + t) : __builtin_nanf("");
+}
+template <typename T> __device__ __forceinline__ Token row_token(const Rows &a, int64_t m, Stat st)
+{
+    return token_of(st, target_logit<T>(a, m));
 }
 __device__ __forceinline__ float stat_lse(Stat st) { return (float)((double)st.m + log_z(st.rest)); }
 
@@ -311,10 +325,16 @@ __device__ __forceinline__ Stat merge_slices(const Stat *part, int64_t S)
     return st;
 }
 
+// a row's derivative of the loss by its log probability, c, and the target's
+// gradient c (1 - p)
+struct Coef {
+    float c, own;
+};
+
 // --- statistics: workgroup (row, slice) -> part[row][slice]; with one slice
 // per row logp and lse (if not null) as well ---------------------------------------
 template <int NT, typename T>
-__global__ __launch_bounds__(NT) void stats_kernel(Rows a, Stat *part, float *logp, float *lse, float *coef)
+__global__ __launch_bounds__(NT) void stats_kernel(Rows a, Stat *part, float *logp, float *lse, Coef *coef)
 {
     __shared__ Stat red[NT / 64];
     const int64_t m = blockIdx.x / a.S, sl = blockIdx.x % a.S;
@@ -323,7 +343,7 @@ __global__ __launch_bounds__(NT) void stats_kernel(Rows a, Stat *part, float *lo
             if (logp)
                 logp[m] = 0.f;
             if (coef)
-                coef[m] = 0.f;
+                coef[m] = Coef{0.f, 0.f};
         }
         return;
     }
@@ -333,7 +353,7 @@ __global__ __launch_bounds__(NT) void stats_kernel(Rows a, Stat *part, float *lo
     if (threadIdx.x == 0) {
         part[blockIdx.x] = st;
         if (logp && a.S == 1)
-            logp[m] = (float)row_logp<T>(a, m, st);
+            logp[m] = (float)row_token<T>(a, m, st).logp;
         if (lse)
             lse[m] = stat_lse(st);
     }
@@ -347,7 +367,7 @@ __global__ __launch_bounds__(kNT) void logp_kernel(Rows a, const Stat *part, flo
         return;
     const Stat st = merge_slices(part + m * a.S, a.S);
     if (logp)
-        logp[m] = (float)row_logp<T>(a, m, st);
+        logp[m] = (float)row_token<T>(a, m, st).logp;
     if (lse)
         lse[m] = stat_lse(st);
 }
@@ -398,12 +418,12 @@ template <typename G> __device__ __forceinline__ void zero_part(G *g, int64_t n)
         store1(g + i, 0.f);
 }
 
-// g[i] = c (1[i = t] - exp(y[i] - m) / (1 + rest)) for i in [0, n); t relative to y
+// g[i] = -c exp(y[i] - m) / (1 + rest) for i in [0, n), own at i = t (relative to y)
 template <int NT, int H, int L, typename T, typename G>
-__device__ __forceinline__ void grad_part(const T *y, G *g, int64_t n, int64_t t, float c, Stat st,
+__device__ __forceinline__ void grad_part(const T *y, G *g, int64_t n, int64_t t, Coef c, Stat st,
                                           const Raw<T> (&held)[H > 0 ? H : 1], const Raw<T> *more)
 {
-    const float r = anchor(st.m), k = -c / (float)(1. + st.rest);
+    const float r = anchor(st.m), k = -c.c / (float)(1. + st.rest);
     auto put = [&](const Raw<T> &w, int64_t q) {
         float v[kVec];
         values(w, v);
@@ -411,7 +431,7 @@ __device__ __forceinline__ void grad_part(const T *y, G *g, int64_t n, int64_t t
             v[i] = k * exp_neg(v[i] - r);
         if (t >> 3 == q)
             for (int i = 0; i < kVec; ++i)
-                v[i] += (t & 7) == i ? c : 0.f;
+                v[i] = (t & 7) == i ? c.own : v[i];
         store8(g + q * kVec, v);
     };
     static_assert(kVec == 8, "t >> 3");
@@ -443,7 +463,7 @@ __device__ __forceinline__ void grad_part(const T *y, G *g, int64_t n, int64_t t
     const int64_t i = nv * kVec + threadIdx.x;
     if (i < n) {
         const float x = k * exp_neg(load1(y + i) - r);
-        store1(g + i, i == t ? x + c : x);
+        store1(g + i, i == t ? c.own : x);
     }
 }
 
@@ -452,7 +472,7 @@ __device__ __forceinline__ void grad_part(const T *y, G *g, int64_t n, int64_t t
 // gradient may be written over the logits.  The first workgroup also sums
 // the loss, which saves a launch.
 template <typename T, typename G>
-__global__ __launch_bounds__(kNT) void grad_kernel(Rows a, const Stat *part, const float *coef, const float *gscale,
+__global__ __launch_bounds__(kNT) void grad_kernel(Rows a, const Stat *part, const Coef *coef, const float *gscale,
                                                    G *dy, int64_t ldg, Sum total)
 {
     if (blockIdx.x == 0)
@@ -462,13 +482,13 @@ __global__ __launch_bounds__(kNT) void grad_kernel(Rows a, const Stat *part, con
     const int64_t b = gridDim.x - 1 - (int64_t)blockIdx.x, m = b / a.S, sl = b % a.S;
     const int64_t v0 = sl * a.slice, n = min(a.slice, a.V - v0);
     G *g = dy + m * ldg + v0;
-    float c = coef[m];
-    if (c == 0.f) { // a masked or clipped token: its logits are not read
+    Coef c = coef[m];
+    if (c.c == 0.f) { // a masked or clipped token: its logits are not read
         zero_part(g, n);
         return;
     }
     if (gscale)
-        c *= *gscale;
+        c = Coef{c.c * *gscale, c.own * *gscale};
     const Stat st = merge_slices(part + m * a.S, a.S);
     const Raw<T> none[1] = {};
     grad_part<kNT, 0, 0, T>(row_ptr<T>(a, m) + v0, g, n, (int64_t)a.targets[m] - v0, c, st, none, nullptr);
@@ -479,9 +499,10 @@ struct Policy {
     float eps_low, eps_high, beta;
 };
 
-// one token's loss and its derivative by logp
-__device__ __forceinline__ float policy_token(const Policy &p, int64_t m, float w, double logp, float *c)
+// one token's loss and its derivative
+__device__ __forceinline__ float policy_token(const Policy &p, int64_t m, float w, const Token &tok, Coef *c)
 {
+    const double logp = tok.logp;
     const double A = p.adv[m], rho = exp(logp - (double)p.old_logp[m]);
     const double cl = fmin(fmax(rho, 1. - (double)p.eps_low), 1. + (double)p.eps_high);
     double loss = -fmin(rho * A, cl * A);
@@ -493,7 +514,8 @@ __device__ __forceinline__ float policy_token(const Policy &p, int64_t m, float 
         loss += (double)p.beta * (e - gap);
         d -= (double)p.beta * e;
     }
-    *c = (float)(w * d);
+    c->c = (float)(w * d);
+    c->own = c->c * tok.other;
     return (float)(w * loss);
 }
 
@@ -507,23 +529,24 @@ __global__ __launch_bounds__(NT) void policy_row_kernel(Rows a, Policy pol, cons
 {
     __shared__ Stat red[NT / 64];
     const int64_t m = blockIdx.x;
-    __shared__ float coef;
+    __shared__ Coef coef;
     Stat st{0., 0.f};
     Raw<T> held[H > 0 ? H : 1];
     __shared__ Raw<T> more[L > 0 ? L * NT : 1];
     const T *y = row_ptr<T>(a, m);
     int64_t t = -1;
-    float lp = 0.f, loss = 0.f, c = 0.f;
+    float lp = 0.f, loss = 0.f;
+    Coef c{0.f, 0.f};
     const bool counts = row_counts(a, m);
     if (counts) {
         t = a.targets[m];
         // read before the barriers: the gradient may be written over it
-        const float yt = t >= 0 && t < a.V ? load1(y + t) : __builtin_nanf("");
+        const float yt = target_logit<T>(a, m);
         st = block_merge<NT>(scan_part<NT, H, L, T>(y, a.V, held, more), red);
         if (threadIdx.x < 64) { // one wave: fp64 is slow
-            const double lp64 = ((double)yt - (double)st.m) - log_z(st.rest);
-            lp = (float)lp64;
-            loss = policy_token(pol, m, a.weights[m], lp64, &c);
+            const Token tok = token_of(st, yt);
+            lp = (float)tok.logp;
+            loss = policy_token(pol, m, a.weights[m], tok, &c);
         }
     }
     if (threadIdx.x == 0) {
@@ -537,28 +560,29 @@ __global__ __launch_bounds__(NT) void policy_row_kernel(Rows a, Policy pol, cons
     if (!dy)
         return;
     G *g = dy + m * ldg;
-    if (c == 0.f) {
+    if (c.c == 0.f) {
         zero_part(g, a.V);
         return;
     }
     if (gscale)
-        c *= *gscale;
+        c = Coef{c.c * *gscale, c.own * *gscale};
     grad_part<NT, H, L, T>(y, g, a.V, t, c, st, held, more);
 }
 
 // --- policy rows: logp, token loss and coefficient of every row -----------------
 template <typename T>
 __global__ __launch_bounds__(kNT) void policy_rows_kernel(Rows a, const Stat *part, Policy pol, float *logp,
-                                                          float *token, float *coef)
+                                                          float *token, Coef *coef)
 {
     const int64_t m = (int64_t)blockIdx.x * kNT + threadIdx.x;
     if (m >= a.M)
         return;
-    float lp = 0.f, loss = 0.f, c = 0.f;
+    float lp = 0.f, loss = 0.f;
+    Coef c{0.f, 0.f};
     if (row_counts(a, m)) {
-        const double lp64 = row_logp<T>(a, m, merge_slices(part + m * a.S, a.S));
-        lp = (float)lp64;
-        loss = policy_token(pol, m, a.weights[m], lp64, &c);
+        const Token tok = row_token<T>(a, m, merge_slices(part + m * a.S, a.S));
+        lp = (float)tok.logp;
+        loss = policy_token(pol, m, a.weights[m], tok, &c);
     }
     token[m] = loss;
     coef[m] = c;
@@ -570,7 +594,7 @@ __global__ __launch_bounds__(kNT) void policy_rows_kernel(Rows a, const Stat *pa
 template <typename T>
 __global__ __launch_bounds__(kNT) void pair_kernel(Rows a, const Stat *part, const float *ref, int64_t P, float beta,
                                                    float smooth, float *logp, float *margins, float *pair,
-                                                   float *coef)
+                                                   Coef *coef)
 {
     __shared__ double red[kNT / 64];
     const int64_t p = blockIdx.x;
@@ -586,7 +610,9 @@ __global__ __launch_bounds__(kNT) void pair_kernel(Rows a, const Stat *part, con
     for (int64_t m = b[0] + threadIdx.x; m < b[2]; m += kNT) {
         double lp = 0.;
         if (row_counts(a, m)) {
-            lp = row_logp<T>(a, m, merge_slices(part + m * a.S, a.S));
+            const Token tok = row_token<T>(a, m, merge_slices(part + m * a.S, a.S));
+            lp = tok.logp;
+            coef[m].own = tok.other; // this thread's again below
             const double term = (double)a.weights[m] * (lp - (double)(ref ? ref[m] : 0.f));
             s += m < b[1] ? term : -term;
         }
@@ -598,8 +624,14 @@ __global__ __launch_bounds__(kNT) void pair_kernel(Rows a, const Stat *part, con
     const double up = 1. / (1. + e), down = e / (1. + e);      // sigma(|h|), sigma(-|h|)
     // sigma(h) - (1 - smooth) = smooth sigma(h) - (1 - smooth) sigma(-h)
     const double slope = (double)beta / (double)P * (sm * (h >= 0. ? up : down) - (1. - sm) * (h >= 0. ? down : up));
-    for (int64_t m = b[0] + threadIdx.x; m < b[2]; m += kNT)
-        coef[m] = row_counts(a, m) ? (float)((m < b[1] ? slope : -slope) * a.weights[m]) : 0.f;
+    for (int64_t m = b[0] + threadIdx.x; m < b[2]; m += kNT) {
+        if (row_counts(a, m)) {
+            const float c = (float)((m < b[1] ? slope : -slope) * a.weights[m]);
+            coef[m] = Coef{c, c * coef[m].own};
+        } else {
+            coef[m] = Coef{0.f, 0.f};
+        }
+    }
     if (threadIdx.x == 0) {
         const double over = h != h ? h : fmax(h, 0.), under = h != h ? h : fmax(-h, 0.); // a NaN stays
         pair[p] = (float)((1. - sm) * (sp + under) + sm * (sp + over));
@@ -658,7 +690,7 @@ LossWs loss_ws(int64_t M, int64_t V, int64_t P)
     };
     w.part = place(sizeof(Stat) * (size_t)(M * S));
     w.token = place(4 * (size_t)M);
-    w.coef = place(4 * (size_t)M);
+    w.coef = place(sizeof(Coef) * (size_t)M);
     w.pair = place(4 * (size_t)P);
     w.total = std::max<size_t>(off, 256);
     return w;
@@ -726,7 +758,7 @@ Rows make_rows(int64_t M, int64_t V, const void *logits, int64_t ld, const int32
 }
 
 template <typename T>
-void run_stats(const Rows &a, Stat *part, float *logp, float *lse, float *coef, hipStream_t st)
+void run_stats(const Rows &a, Stat *part, float *logp, float *lse, Coef *coef, hipStream_t st)
 {
     hipLaunchKernelGGL((stats_kernel<kNT, T>), dim3((unsigned)(a.M * a.S)), dim3(kNT), 0, st, a, part, logp, lse, coef);
 }
@@ -750,7 +782,7 @@ template <typename T> void run_logp(Rows a, Stat *part, float *logp, float *lse,
         a.S = 1;
         a.slice = a.V;
         hipLaunchKernelGGL((stats_kernel<kWide, T>), dim3((unsigned)a.M), dim3(kWide), 0, st, a, part, logp, lse,
-                           (float *)nullptr);
+                           (Coef *)nullptr);
         return;
     }
     const bool whole = a.S == 1;
@@ -773,7 +805,7 @@ struct Grad {
 };
 
 template <typename T>
-void run_grad(const Rows &a, const Stat *part, const float *coef, const Grad &g, const Sum &total, hipStream_t st)
+void run_grad(const Rows &a, const Stat *part, const Coef *coef, const Grad &g, const Sum &total, hipStream_t st)
 {
     const dim3 grid((unsigned)(a.M * a.S));
     if (g.type == ARCHEAD_F32)
@@ -831,7 +863,8 @@ void run_policy(const Rows &a, void *ws, const LossWs &L, const Policy &pol, flo
                 hipStream_t st)
 {
     Stat *part = (Stat *)((char *)ws + L.part);
-    float *token = (float *)((char *)ws + L.token), *coef = (float *)((char *)ws + L.coef);
+    float *token = (float *)((char *)ws + L.token);
+    Coef *coef = (Coef *)((char *)ws + L.coef);
     if (whole_rows(a.M, a.V)) {
         run_policy_whole<T>(a, pol, logp, token, g, st);
         run_sum(token, a.M, 1.0, loss, st);
@@ -851,7 +884,8 @@ void run_preference(const Rows &a, void *ws, const LossWs &L, const float *ref, 
                     float *loss, float *logp, float *margins, const Grad &g, hipStream_t st)
 {
     Stat *part = (Stat *)((char *)ws + L.part);
-    float *coef = (float *)((char *)ws + L.coef), *pair = (float *)((char *)ws + L.pair);
+    Coef *coef = (Coef *)((char *)ws + L.coef);
+    float *pair = (float *)((char *)ws + L.pair);
     if (a.M > 0)
         run_stats<T>(a, part, logp, nullptr, coef, st);
     hipLaunchKernelGGL(pair_kernel<T>, dim3((unsigned)P), dim3(kNT), 0, st, a, part, ref, P, beta, smoothing, logp,

@@ -100,6 +100,54 @@ def test_log_probabilities(M, V, kind, dtype):
         assert (off <= tol).all(), (name, (off / tol).max(), off.max() / U)
 
 
+@pytest.mark.parametrize("M,V,kind", CASES)
+@pytest.mark.parametrize("dtype,gtype", [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16")])
+def test_gradients_at_the_token(M, V, kind, dtype, gtype):
+    """c (1 - p) at the target relative to itself.  1 - p = rest / (1 + rest)
+    has rest's error and 4 u (its difference's, sum's and quotient's rounding);
+    c is taken in fp64 from logp, which is off by at most 2e-3 tol, and rounded,
+    as is the product: 3 u; the output's half step.  A scale of 2^12 is exact."""
+    import torch
+    from packed_quantized_lm_amd import policy_loss, preference_loss
+    say(f"gradient near certain M={M} V={V} {kind} {dtype} {gtype}")
+    logits, y, t, rest, tol = rows_of(M, V, kind, dtype)
+    rng = np.random.default_rng(V)
+    rows, used = np.arange(M), np.arange(M)[::max(1, M // 40)]  # the oracle looks at some rows
+    adv, w = rng.normal(0, 1, M), rng.uniform(0.5, 1.5, M) / M
+    logp = -np.log1p(rest)
+    ref = logp + rng.normal(0, 0.3, M)
+    adv, w, ref = (a.astype(np.float32) for a in (adv, w, ref))
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}[gtype]
+    half = {"f32": U, "bf16": 2.0 ** -8}[gtype]
+    ti, scale = dev(t, "int32"), torch.tensor(4096.0, device="cuda")
+    _, _, want, coef = losses.policy(y[used], t[used], np.zeros(len(used)), adv[used], w[used], ref[used], 0.04)
+    dy = policy_loss(logits, ti, dev(np.zeros(M)), dev(adv), dev(w), dev(ref), beta=0.04, grad_dtype=dt,
+                     grad_scale=scale)[2]
+    got = dy[torch.from_numpy(rows).cuda(), ti.long()].double().cpu().numpy() / 4096
+    own = want[np.arange(len(used)), t[used]]
+    assert np.allclose(own, coef * (rest / (1 + rest))[used], rtol=1e-12, atol=0)
+    # c = w (-A rho + beta (1 - exp(r))): logp's error moves both terms, which may nearly cancel
+    parts = w[used] * (np.abs(adv[used]) + 0.04 * (np.exp(ref[used] - logp[used]) + 1))
+    off = np.abs(got[used] - own) / np.abs(own)
+    allowed = tol[used] + (7 + 1) * U + half + 2 * parts / np.abs(coef) * np.abs(logp[used]) * tol[used]
+    assert (off <= allowed).all(), ((off / allowed).max(), off.max())
+    if dtype == gtype:  # over the logits
+        over = logits.clone()
+        policy_loss(over, ti, dev(np.zeros(M)), dev(adv), dev(w), dev(ref), beta=0.04, dlogits=over, grad_scale=scale)
+        assert torch.equal(over, dy)
+    offsets = np.array([0, M // 2, M])
+    s = (w.astype(np.float64) * (logp - ref))
+    margin = 0.3 * (s[:M // 2].sum() - s[M // 2:].sum())
+    slope = -0.3 / (1 + np.exp(margin)) * np.where(rows < M // 2, 1, -1) * w
+    dy = preference_loss(logits, ti, dev(w), dev(offsets, "int32"), dev(ref), beta=0.3, grad_dtype=dt)[3]
+    got = dy[torch.from_numpy(rows).cuda(), ti.long()].double().cpu().numpy()
+    own = slope * (rest / (1 + rest))
+    off = np.abs(got - own) / np.abs(own)
+    # the margin's error, of its rows' log probabilities, moves the slope by at most as much
+    allowed = tol + 8 * U + half + 0.3 * (w * np.abs(logp) * tol).sum()
+    assert (off <= allowed).all(), ((off / allowed).max(), off.max())
+
+
 @pytest.mark.parametrize("M,V", [(6, 1), (6, 9), (6, 64), (6, 4097), (6, 9001), (6, 50021), (240, 40003)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_nan_and_infinite_logits_reach_their_row(M, V, dtype):
