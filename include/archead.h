@@ -454,6 +454,9 @@ archead_status archead_token_logp(int64_t M, int64_t V, const void *logits, int 
  *   c_m    = weights_m ( -A_m rho_m [rho_m A_m <= clip(rho_m) A_m] + beta (1 - exp(r_m)) )
  * The weights carry the normalisation (1 / tokens for a mean over tokens).
  * A token whose clip is active and that has no KL term gets a zero row.
+ * A NaN among a token's inputs, or an infinite advantage at a ratio of 0, makes
+ * the loss and the token's row of the gradient NaN; an advantage of 0 gains
+ * nothing at any ratio.
  *
  * old_logp, advantages   DEVICE fp32 M.  ref_logp  DEVICE fp32 M, required
  * when beta > 0 and unused otherwise.  0 <= eps_low <= 1, eps_high >= 0,

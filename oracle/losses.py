@@ -54,10 +54,13 @@ def policy(logits, targets, old_logp, advantages, weights, ref_logp=None, beta=0
             continue
         lp = _row_logp(y[m], int(targets[m]))
         A = float(advantages[m])
-        rho = np.exp(lp - float(old_logp[m]))
+        with np.errstate(over="ignore", invalid="ignore"):
+            rho = np.exp(lp - float(old_logp[m]))
         kept = np.clip(rho, 1.0 - eps_low, 1.0 + eps_high)
-        value = -min(rho * A, kept * A) if rho == rho else np.nan
-        slope = -A * rho if rho * A <= kept * A else (0.0 if rho == rho else np.nan)
+        gain = float(rho) * A if A != 0.0 else 0.0  # no advantage, no gain: also at an infinite ratio
+        known = rho == rho and gain == gain  # min and the comparison drop a NaN
+        value = -min(gain, kept * A) if known else np.nan
+        slope = (-gain if gain <= kept * A else 0.0) if known else np.nan
         if beta:
             r = float(ref_logp[m]) - lp
             value += beta * (np.expm1(r) - r)

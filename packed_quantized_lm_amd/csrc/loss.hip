@@ -505,10 +505,11 @@ __device__ __forceinline__ float policy_token(const Policy &p, int64_t m, float 
     const double logp = tok.logp;
     const double A = p.adv[m], rho = exp(logp - (double)p.old_logp[m]);
     const double cl = fmin(fmax(rho, 1. - (double)p.eps_low), 1. + (double)p.eps_high);
-    double loss = -fmin(rho * A, cl * A);
-    double d = rho * A <= cl * A ? -A * rho : 0.;
-    if (!(rho == rho)) // fmin and fmax drop a NaN
-        loss = d = rho;
+    const double gain = A == 0. ? 0. : rho * A; // no advantage, no gain: also at an infinite ratio
+    double loss = -fmin(gain, cl * A);
+    double d = gain <= cl * A ? -gain : 0.;
+    if (rho != rho || gain != gain) // fmin, fmax and the comparison drop a NaN
+        loss = d = __builtin_nan("");
     if (p.beta != 0.f) { // without a KL term an infinite one is never formed
         const double gap = (double)p.ref_logp[m] - logp, e = expm1(gap);
         loss += (double)p.beta * (e - gap);

@@ -27,3 +27,22 @@ def test_near_certain_gradients():
         for m in range(2):
             assert g[m, t[m]] == pytest.approx(coef[m] * p, rel=2.0 ** -50, abs=0)
             assert g[m, 1 - t[m]] == pytest.approx(-coef[m] * p, rel=2.0 ** -50, abs=0)
+
+
+def test_an_unknown_advantage_is_not_a_zero_one():
+    """A NaN advantage (normalised by a zero deviation) or an infinite one at a
+    ratio of zero makes the loss and its row's gradient NaN; other rows keep
+    theirs.  No advantage is no gain, also where the old policy had the token
+    masked."""
+    y, t, w = np.zeros((4, 3)), np.array([0, 1, 2, 0]), np.array([0.5, 0.5, 0.5, 0.0])
+    y[3] = np.nan
+    old = np.full(4, -math.log(3))
+    for A, o in ((math.nan, old[0]), (math.inf, math.inf)):
+        old[0] = o
+        loss, _, g, coef = losses.policy(y, t, old, np.array([A, 1.0, -1.0, math.nan]), w)
+        assert math.isnan(loss) and math.isnan(coef[0]) and np.isnan(g[0]).all()
+        assert np.isfinite(g[1:]).all() and g[1:3].any(1).all() and not g[3].any()
+    old[0] = -math.inf
+    with np.errstate(over="ignore"):
+        loss, _, g, _ = losses.policy(y, t, old, np.array([0.0, 1.0, -1.0, 0.0]), w)
+    assert loss == pytest.approx(0.0) and not g[0].any()
