@@ -478,7 +478,10 @@ archead_status archead_policy_loss(int64_t M, int64_t V, const void *logits, int
  *   loss = 1/P sum_p [ -(1 - smoothing) log sigma(h_p) - smoothing log sigma(-h_p) ]
  *   dlogits[m, v] = c_m (1[v = target_m] - softmax(logits_m)[v]),
  *   c_m  = +-(beta / P) (sigma(h_p) - (1 - smoothing)) weights_m   (+ chosen, - rejected)
- * Answers may be empty (s = 0) and of any lengths.
+ * Answers may be empty (s = 0) and of any lengths.  An infinite margin (a masked
+ * token in one answer) is decided: h_p = inf adds nothing to the loss and the
+ * gradient unless smoothing > 0, h_p = -inf an infinite loss with the gradient
+ * of its limit.
  *
  * P          pairs, 1 <= P <= 2^20.
  * offsets    DEVICE int32 2P + 1, nondecreasing, within [0, M]; values that

@@ -86,7 +86,9 @@ def preference(logits, targets, weights, offsets, ref_logp=None, beta=0.1, smoot
                     total += float(weights[m]) * (logp[m] - (float(ref_logp[m]) if ref_logp is not None else 0.0))
             s.append(total)
         h[p] = beta * (s[0] - s[1])
-        loss += ((1 - smoothing) * np.logaddexp(0.0, -h[p]) + smoothing * np.logaddexp(0.0, h[p])) / P
+        loss += (1 - smoothing) * np.logaddexp(0.0, -h[p]) / P
+        if smoothing:  # else an infinite margin would make 0 times infinity of it
+            loss += smoothing * np.logaddexp(0.0, h[p]) / P
         slope = beta / P * (np.exp(-np.logaddexp(0.0, -h[p])) - (1 - smoothing))
         for i, sign in ((2 * p, 1.0), (2 * p + 1, -1.0)):
             for m in range(int(offsets[i]), int(offsets[i + 1])):

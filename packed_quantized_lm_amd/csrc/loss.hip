@@ -635,7 +635,8 @@ __global__ __launch_bounds__(kNT) void pair_kernel(Rows a, const Stat *part, con
     }
     if (threadIdx.x == 0) {
         const double over = h != h ? h : fmax(h, 0.), under = h != h ? h : fmax(-h, 0.); // a NaN stays
-        pair[p] = (float)((1. - sm) * (sp + under) + sm * (sp + over));
+        // without smoothing the second term's infinity at h = inf is never formed
+        pair[p] = (float)((1. - sm) * (sp + under) + (sm != 0. ? sm * (sp + over) : 0.));
         if (margins)
             margins[p] = (float)h;
     }

@@ -74,3 +74,45 @@ def test_unknown_advantages(M, V, beta):
     assert np.allclose(g[4], want[2][4], rtol=1e-4, atol=1e-12)
     rest = np.setdiff1d(np.arange(M), [0, 2, 3, 4])
     assert np.array_equal(g[rest], whole[2][rest]) and np.array_equal(logp[rest], whole[1][rest])
+
+
+@pytest.mark.parametrize("V", [5, 64, 4099, 50021])
+@pytest.mark.parametrize("smoothing", [0.0, 0.1])
+def test_infinite_margins(V, smoothing):
+    """Pairs with a masked token in the rejected answer (h = inf), in the chosen
+    one (h = -inf), in both (NaN) and in none."""
+    import torch
+    from packed_quantized_lm_amd import preference_loss
+    say(f"infinite margins V={V} smoothing={smoothing}")
+    rng = np.random.default_rng(V)
+    off = np.array([0, 2, 4, 6, 8, 10, 12, 14, 16])
+    y = rng.normal(0, 2, (16, V)).astype(np.float32)
+    t = rng.integers(0, V, 16)
+    for m in (2, 5, 9, 10):
+        y[m, t[m]] = -np.inf
+    y[0, (t[0] + 1) % V] = -np.inf  # and a mask beside a token
+    w = np.ones(16, np.float32)
+
+    def both(rows, offsets):
+        got = preference_loss(dev(y[rows]), dev(t[rows], "int32"), dev(w[rows]), dev(offsets, "int32"), beta=0.2,
+                              smoothing=smoothing, grad_dtype=torch.float32)
+        with np.errstate(invalid="ignore"):
+            want = losses.preference(y[rows], t[rows], w[rows], offsets, None, 0.2, smoothing)
+        return [x.double().cpu().numpy() for x in got], want
+    # fp32's exponentials and sums are within 1e-4 of anything here
+    for pair, margin in ((0, np.inf), (1, -np.inf), (2, np.nan), (3, None)):
+        rows = slice(4 * pair, 4 * pair + 4)
+        (loss, h, logp, g), (wl, wh, wp, wg, _) = both(rows, off[:3])
+        if margin is None:
+            assert np.isfinite(h).all()
+        else:
+            assert np.array_equal(h, [margin], equal_nan=True) and np.array_equal(wh, [margin], equal_nan=True)
+        assert np.allclose(loss, wl, rtol=1e-4, equal_nan=True), (loss, wl)
+        assert np.allclose(logp, wp, rtol=1e-4, atol=1e-4)
+        assert np.allclose(g, wg, rtol=1e-4, atol=1e-9, equal_nan=True)
+        if margin == np.inf and not smoothing:
+            assert loss == 0.0 and not g.any()
+    rows = np.r_[0:4, 12:16]
+    (loss, h, _, g), (wl, wh, _, wg, _) = both(rows, off[:5])
+    assert np.allclose(loss, wl, rtol=1e-4) and np.isfinite(loss) == (smoothing == 0.0)
+    assert np.allclose(g, wg, rtol=1e-4, atol=1e-9)

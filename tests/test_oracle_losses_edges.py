@@ -46,3 +46,18 @@ def test_an_unknown_advantage_is_not_a_zero_one():
     with np.errstate(over="ignore"):
         loss, _, g, _ = losses.policy(y, t, old, np.array([0.0, 1.0, -1.0, 0.0]), w)
     assert loss == pytest.approx(0.0) and not g[0].any()
+
+
+def test_infinite_margins_are_decided():
+    """A masked token in the rejected answer: -log sigma(inf) = 0 and no
+    gradient; in the chosen one an infinite loss and the limit's slope."""
+    y = np.zeros((4, 4))
+    y[1, 2] = y[2, 0] = -np.inf
+    t, w, off = np.array([1, 2, 0, 3]), np.ones(4), np.array([0, 1, 2, 3, 4])
+    loss, h, _, g, coef = losses.preference(y[:2], t[:2], w[:2], off[:3], beta=0.3)
+    assert h[0] == np.inf and loss == 0.0 and not g.any()
+    loss, h, _, g, coef = losses.preference(y, t, w, off, beta=0.3)
+    assert h[1] == -np.inf and loss == np.inf
+    assert coef[2] == pytest.approx(-0.15) and coef[3] == pytest.approx(0.15) and np.isfinite(g).all()
+    loss, h, _, g, coef = losses.preference(y[:2], t[:2], w[:2], off[:3], beta=0.3, smoothing=0.1)
+    assert loss == np.inf and coef[0] == pytest.approx(0.03)
