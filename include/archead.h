@@ -409,7 +409,8 @@ archead_status archead_backward(archead_t h, int64_t M, const void *dlogits, int
  *
  * Common to the three calls:
  * logits     DEVICE, aligned to one element; ld >= V.  M <= 2^20, V < 2^31.
- *            -inf logits (a vocabulary mask) have probability and gradient 0.
+ *            -inf logits (a vocabulary mask) have probability and, but for
+ *            the target's own, gradient 0 (NaN where c below is infinite).
  *            A row of -inf alone gives lse = -inf and logp = NaN; NaN or +inf
  *            logits make the row's results NaN.
  * targets    DEVICE int32 M.  A target outside [0, V) gives logp = NaN, and
@@ -456,7 +457,8 @@ archead_status archead_token_logp(int64_t M, int64_t V, const void *logits, int 
  * A token whose clip is active and that has no KL term gets a zero row.
  * A NaN among a token's inputs, or an infinite advantage at a ratio of 0, makes
  * the loss and the token's row of the gradient NaN; an advantage of 0 gains
- * nothing at any ratio.
+ * nothing at any ratio.  With beta > 0 a token that the policy masks (logp =
+ * -inf) and the reference does not has an infinite loss and c = -inf.
  *
  * old_logp, advantages   DEVICE fp32 M.  ref_logp  DEVICE fp32 M, required
  * when beta > 0 and unused otherwise.  0 <= eps_low <= 1, eps_high >= 0,

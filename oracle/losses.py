@@ -37,8 +37,9 @@ def _gradient(y, targets, coef):
             continue
         e = np.exp(y[m] - y[m].max())
         others = np.delete(e, int(targets[m])).sum()  # 1 - p of the target, however near p is to 1
-        g[m] = -coef[m] * e / e.sum()
-        g[m, int(targets[m])] = coef[m] * (others / e.sum())
+        with np.errstate(invalid="ignore"):  # an infinite coefficient at a probability of 0
+            g[m] = -coef[m] * e / e.sum()
+            g[m, int(targets[m])] = coef[m] * (others / e.sum())
     return g
 
 
@@ -63,7 +64,7 @@ def policy(logits, targets, old_logp, advantages, weights, ref_logp=None, beta=0
         slope = (-gain if gain <= kept * A else 0.0) if known else np.nan
         if beta:
             r = float(ref_logp[m]) - lp
-            value += beta * (np.expm1(r) - r)
+            value += beta * (np.expm1(r) - r if r != np.inf else r)  # exp(r) - r - 1 grows without end
             slope -= beta * np.expm1(r)
         loss += w * value
         logp[m], coef[m] = lp, w * slope

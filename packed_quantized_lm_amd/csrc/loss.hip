@@ -512,7 +512,7 @@ __device__ __forceinline__ float policy_token(const Policy &p, int64_t m, float 
         loss = d = __builtin_nan("");
     if (p.beta != 0.f) { // without a KL term an infinite one is never formed
         const double gap = (double)p.ref_logp[m] - logp, e = expm1(gap);
-        loss += (double)p.beta * (e - gap);
+        loss += (double)p.beta * (gap == INFINITY ? e : e - gap); // a masked token's: infinite, not inf - inf
         d -= (double)p.beta * e;
     }
     c->c = (float)(w * d);

@@ -116,3 +116,29 @@ def test_infinite_margins(V, smoothing):
     (loss, h, _, g), (wl, wh, _, wg, _) = both(rows, off[:5])
     assert np.allclose(loss, wl, rtol=1e-4) and np.isfinite(loss) == (smoothing == 0.0)
     assert np.allclose(g, wg, rtol=1e-4, atol=1e-9)
+
+
+@pytest.mark.parametrize("M,V", SIZES)
+def test_masked_tokens_under_a_kl_term(M, V):
+    """A token masked by the policy (an infinite KL term), by the reference (too,
+    with a finite gradient) and by both (unknown)."""
+    say(f"masked tokens M={M} V={V}")
+    for kind, expected in (("policy", np.inf), ("reference", np.inf), ("both", np.nan)):
+        y, t, old, ref, adv, w = batch(M, V)
+        whole = step(y, t, old, ref, adv, w, 0.1)
+        if kind != "reference":
+            y[0, t[0]] = -np.inf
+        if kind != "policy":
+            ref[0] = -np.inf
+        loss, logp, g = step(y, t, old, ref, adv, w, 0.1)
+        with np.errstate(invalid="ignore"):
+            want = losses.policy(y, t, old, adv, w, ref, 0.1)
+        assert np.array_equal(loss, expected, equal_nan=True) and np.array_equal(want[0], expected, equal_nan=True)
+        assert np.allclose(logp, want[1], rtol=1e-4, atol=1e-4)
+        if kind == "reference":
+            assert np.allclose(g[0], want[2][0], rtol=1e-4, atol=1e-12)
+        elif kind == "policy":
+            assert g[0, t[0]] == -np.inf and (np.delete(g[0], t[0]) == np.inf).all()
+        else:
+            assert np.isnan(g[0]).all()
+        assert np.array_equal(g[1:], whole[2][1:])

@@ -61,3 +61,15 @@ def test_infinite_margins_are_decided():
     assert coef[2] == pytest.approx(-0.15) and coef[3] == pytest.approx(0.15) and np.isfinite(g).all()
     loss, h, _, g, coef = losses.preference(y[:2], t[:2], w[:2], off[:3], beta=0.3, smoothing=0.1)
     assert loss == np.inf and coef[0] == pytest.approx(0.03)
+
+
+def test_a_masked_token_is_infinitely_far_from_its_reference():
+    y, t = np.zeros((2, 4)), np.array([1, 2])
+    y[0, 1] = -np.inf
+    old, ref = np.array([-1.4, -1.4]), np.array([-2.0, -1.4])
+    for A in (1.0, -1.0):
+        loss, lp, g, coef = losses.policy(y, t, old, np.array([A, 0.0]), np.ones(2), ref, beta=0.1)
+        assert lp[0] == -np.inf and loss == np.inf and coef[0] == -np.inf and np.isfinite(g[1]).all()
+    # the other way round the reference's mask costs as much, with a finite slope
+    loss, _, _, coef = losses.policy(np.zeros((1, 4)), t[:1], old[:1], np.ones(1), np.ones(1), np.array([-np.inf]), beta=0.1)
+    assert loss == np.inf and np.isfinite(coef[0])
