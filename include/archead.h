@@ -515,7 +515,7 @@ archead_status archead_preference_loss(int64_t M, int64_t V, const void *logits,
  * x    DEVICE rows x cols, fp32 or bf16 (type), row stride ldx elements,
  *      aligned to its element.  rows < 2^31; cols a multiple of 16 (the
  *      product reads rows in 16-byte pieces) up to 2^20; rows times blocks below
- *      2^28; else ARCHEAD_ESHAPE.
+ *      2^28, with block_rows = 1 at most 2^28 - 16; else ARCHEAD_ESHAPE.
  * q    DEVICE codes, rows x cols bytes, row stride ldq bytes; q and ldq
  *      multiples of 16.
  * s    DEVICE fp32.  block_rows = 1: s[b * lds + row] for block b of a row

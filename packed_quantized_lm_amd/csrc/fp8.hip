@@ -597,7 +597,6 @@ extern "C" archead_status archead_fp8_quantize(int64_t rows, int64_t cols, const
 {
     if (rows < 0)
         return api_fail(ARCHEAD_EINVAL, "rows < 0");
-    // a launch holds fewer than 2^32 threads, 16 a row block
     if (rows >= (int64_t(1) << 31) || cols < 16 || cols % 16 || cols > (int64_t(1) << 20) ||
         rows * ((cols + kBlk - 1) / kBlk) >= (int64_t(1) << 28))
         return api_fail(ARCHEAD_ESHAPE, "rows < 2^31, cols a multiple of 16 in [16, 2^20], fewer than 2^28 row blocks");
@@ -606,6 +605,9 @@ extern "C" archead_status archead_fp8_quantize(int64_t rows, int64_t cols, const
     if (block_rows != 1 && block_rows != kBlk)
         return api_fail(ARCHEAD_EINVAL, "block_rows must be 1 or 128");
     const int64_t nb = (cols + kBlk - 1) / kBlk;
+    // a launch holds fewer than 2^32 threads: 2^24 - 1 workgroups of 256, 16 row blocks each
+    if (block_rows == 1 && rows * nb > (int64_t(1) << 28) - 16)
+        return api_fail(ARCHEAD_ESHAPE, "with a scale per row at most 2^28 - 16 row blocks");
     if (ldx < cols || lds < (block_rows == 1 ? rows : nb))
         return api_fail(ARCHEAD_EINVAL, "a row stride is shorter than a row");
     if (rows == 0)
