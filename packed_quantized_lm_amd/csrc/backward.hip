@@ -762,22 +762,31 @@ Plan plan_of(const Cols &c, int64_t M, int64_t nvc)
     return best;
 }
 
-struct BwWs {
-    size_t g16, amax, unscale, low, thi, tlo, u, part, total;
-};
 constexpr int64_t kAmaxSlices = 64;
 
-// Fits every call of up to rows rows: with more than one range, ranges x
-// tiles x row tiles stays within kMaxWg, so the parts within kMaxWg tiles.
-BwWs bw_ws(const Shape &s, int64_t rows)
+} // namespace
+
+// byte offsets into the workspace
+struct BackwardWs {
+    size_t g16, amax, unscale, low, thi, tlo, u, part, total;
+};
+
+namespace {
+
+// Fits every call of up to rows rows: the ranges' sums by the plans of all of them
+// (151936 x 4096, k = 256, r = 64, 2048 rows: 623 MB for G, 264 MB for dX's sums,
+// 33 MB for T's and U's: 923 MB).
+BackwardWs backward_ws(const Shape &s, int64_t rows)
 {
     const Cols c = cols_of(s);
     const int64_t nvc = (s.V + kVC - 1) / kVC;
-    auto parts = [&](int64_t tiles) {
-        const int64_t one = rows * tiles * kJT, all = one * std::max<int64_t>(1, nvc / kMinChunks);
-        return std::max(one, std::min(all, kMaxWg * 256 * kJT));
-    };
-    BwWs w;
+    int64_t low = 0, part = 0;
+    for (int64_t M = 1; M <= rows; ++M) {
+        const Plan p = plan_of(c, M, nvc);
+        low = std::max(low, p.low * M * c.low_tiles() * kLT);
+        part = std::max(part, p.main * M * c.main_tiles() * kJT);
+    }
+    BackwardWs w;
     size_t off = 0;
     auto place = [&](size_t bytes) {
         const size_t o = off;
@@ -787,11 +796,11 @@ BwWs bw_ws(const Shape &s, int64_t rows)
     w.g16 = place(size_t(rows) * nvc * kVC * 2);
     w.amax = place(size_t(rows) * kAmaxSlices * 4);
     w.unscale = place(size_t(rows) * 4);
-    w.low = place(size_t(parts(c.low_tiles())) * 4);
+    w.low = place(size_t(low) * 4);
     w.thi = place(size_t(rows) * c.kst * kUnit * 2);
     w.tlo = place(size_t(rows) * c.kst * kUnit * 2);
     w.u = place(size_t(rows) * c.rst * kUnit * 4);
-    w.part = place(size_t(parts(c.main_tiles())) * 4);
+    w.part = place(size_t(part) * 4);
     w.total = off;
     return w;
 }
@@ -807,7 +816,8 @@ struct BackwardState {
     int32_t *ex;
     void *ws;
     size_t ws_bytes;
-    int64_t rows; // rows the workspace holds
+    BackwardWs at; // in the workspace
+    int64_t rows;  // rows it holds
 };
 
 void backward_release(BackwardState *b)
@@ -928,7 +938,7 @@ void backward_rows(const DevHead &h, const BackwardState &b, int64_t M, const vo
 {
     const Shape &s = h.s;
     const Cols c = cols_of(s);
-    const BwWs L = bw_ws(s, b.rows);
+    const BackwardWs &L = b.at;
     char *ws = (char *)b.ws;
     const int64_t nvc = (s.V + kVC - 1) / kVC;
     GArgs ga{};
@@ -1033,7 +1043,8 @@ extern "C" archead_status archead_reserve_backward(archead_t h, int64_t M_max, v
     if (!b)
         return api_fail(ARCHEAD_ENOMEM, "host allocation failed");
     void *ws = nullptr;
-    const size_t bytes = bw_ws(dev->s, rows).total;
+    const BackwardWs at = backward_ws(dev->s, rows);
+    const size_t bytes = at.total;
     s = device_alloc(&ws, bytes, "backward workspace");
     if (s == ARCHEAD_OK && !b->block)
         s = lay_out(*dev, b, st);
@@ -1050,6 +1061,7 @@ extern "C" archead_status archead_reserve_backward(archead_t h, int64_t M_max, v
         (void)hipFree(b->ws); // waits for the device
     b->ws = ws;
     b->ws_bytes = bytes;
+    b->at = at;
     b->rows = rows;
     *slot = b;
     return ARCHEAD_OK;

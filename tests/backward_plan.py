@@ -42,11 +42,14 @@ def _ranges_of(kind, M, tiles, tile_cols, nvc):
     return least, best
 
 
-def launches(V, d, k, r, M, dtype="bfloat16"):
-    """Of one part (M up to kChunkM rows): the set of kernel forms launched."""
-    nvc, main = _up(V, C["kVC"]), _up(d, C["kJT"])
-    units = _up(k, 32) + _up(r, 32)
-    low = _up(units * C["kUnit"], C["kLT"])
+def _tiles(V, d, k, r):
+    units = _up(k, C["kUnit"]) + _up(r, C["kUnit"])
+    return _up(V, C["kVC"]), _up(d, C["kJT"]), units, _up(units * C["kUnit"], C["kLT"])
+
+
+def _plan(V, d, k, r, M):
+    """Rows of a tile, ranges of the low-rank tiles and of dX's."""
+    nvc, main, _, low = _tiles(V, d, k, r)
     best, least = None, 1e300
     for kind in C["kTiles"]:
         if (kind[0] == 32) != (M <= 32):
@@ -55,7 +58,13 @@ def launches(V, d, k, r, M, dtype="bfloat16"):
         b, s_low = _ranges_of(kind, M, low, C["kLT"], nvc) if low else (0.0, 1)
         if a + b < least:
             least, best = a + b, (kind[0], s_low, s_main)
-    bm, s_low, s_main = best
+    return best
+
+
+def launches(V, d, k, r, M, dtype="bfloat16"):
+    """Of one part (M up to kChunkM rows): the set of kernel forms launched."""
+    _, main, units, low = _tiles(V, d, k, r)
+    bm, s_low, s_main = _plan(V, d, k, r, M)
     found = set()
     if low:
         found.add(f"low tiles {bm}, {'full' if low * C['kLT'] == units * C['kUnit'] else 'partly padding'}")
@@ -84,3 +93,18 @@ def of_call(V, d, k, r, M, reserved, dtype="bfloat16"):
     if M > part:
         found.add("parts of kChunkM" if part == C["kChunkM"] else "parts")
     return found
+
+
+def workspace_bytes(V, d, k, r, reserved):
+    """Of a head with room for reserved rows: G in fp16, a few numbers a row, T
+    sB in two parts and U, and the ranges' sums of the largest plan."""
+    rows = min(reserved, C["kChunkM"])
+    nvc, main, _, low = _tiles(V, d, k, r)
+    s_low = s_main = 0
+    for M in range(1, rows + 1):
+        _, a, b = _plan(V, d, k, r, M)
+        s_low, s_main = max(s_low, a * M * low * C["kLT"]), max(s_main, b * M * main * C["kJT"])
+    core, correction = _up(k, 32) * 32, _up(r, 32) * 32
+    parts = [rows * nvc * C["kVC"] * 2, rows * C["kAmaxSlices"] * 4, rows * 4, s_low * 4, rows * core * 2,
+             rows * core * 2, rows * correction * 4, s_main * 4]
+    return sum(_up(max(p, 16), 256) * 256 for p in parts)
