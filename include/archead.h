@@ -384,12 +384,15 @@ archead_status archead_reserve_backward(archead_t h, int64_t M_max, void *hip_st
  * M        0 <= M <= 2^20 rows (0 is a no-op that succeeds).
  * dlogits  DEVICE M x V, fp32 or bf16 (type), row stride ld >= V elements,
  *          aligned to its element.
- * dX       DEVICE bf16, M x d row-major, written in full.
+ * dX       DEVICE bf16, M x d row-major, written in full; must not overlap
+ *          dlogits.
  * Numerics: row m of G enters as fp16, scaled by a power of two that puts its
  * largest entry into [2^14, 2^15) (bf16 entries within 2^28 of it exactly, fp32
  * ones rounded to 11 bits); the residual's and the low-rank codes times their
- * scales are rounded once to fp16; sums are fp32; the low-rank factors T, U
- * enter their second product with 16 significant bits; dX is rounded once.
+ * scales are rounded once to fp16 (scales more than 2^25 below the largest sR,
+ * 2^24 below the largest sA or 2^21 below the largest sC lose bits, at most
+ * 2^-31 of the largest code times scale); sums are fp32; the low-rank factors T,
+ * U enter their second product with 16 significant bits; dX is rounded once.
  * A NaN or infinity in row m of G makes row m of dX NaN or infinite and no
  * other.
  * Enqueued on hip_stream, not waited for; nothing is allocated, so the call can
@@ -420,7 +423,8 @@ archead_status archead_backward(archead_t h, int64_t M, const void *dlogits, int
  * weights    DEVICE fp32 M.  A row of weight 0 carries no loss: its logits,
  *            target and other inputs are not used (they may hold anything),
  *            its logp is written as 0 and its gradient row as zeros.
- * logp       DEVICE fp32 M, or NULL.
+ * logp       DEVICE fp32 M, or NULL.  It and the target's gradient keep their
+ *            relative precision for tokens of probability near 1.
  * dlogits    DEVICE M x V with row stride ldg, grad_type (fp32 or bf16,
  *            rounded once), or NULL for the loss alone.  Every row is written
  *            in full, nothing beyond column V.  May be logits itself (same

@@ -20,10 +20,10 @@
 //   finish         dX's ranges + the products with B8 and D8, one rounding
 // Few rows are bound by the codes' bytes, many by the matrix cores.  In us:
 //                    16 x 151936 x 4096     2048 x 151936 x 4096
-//   amax, convert         10                    239  (5.2 TB/s in one pass)
-//   tiles                 84 (5.2 TB/s)         345 + 2160 (1180 TFLOP/s in dX's,
+//   amax, convert         10                    240  (6.1 TB/s fetched and written)
+//   tiles                 86 (5.1 TB/s)         322 + 1919 (1330 TFLOP/s in dX's,
 //                                               matrix cores 65 % busy)
-//   sums, finish          15                     80
+//   sums, finish          16                     73
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -999,8 +999,13 @@ void backward_rows(const DevHead &h, const BackwardState &b, int64_t M, const vo
     }
     const FinishArgs f{M, s.d, s.k, s.r, s.G(), s.g, p.main, c.main_tiles() * kJT, c, part, u, h.sd, thi, tlo,
                        b.b8t, b.d8t, dx};
-    // by measurement at d = 4096: four waves a tile 9 us against 14 at M = 16,
-    // 17 against 13 at M = 64; 16 x 16 a wave 41 us against 46 at M = 512
+    // Measured, us of whole calls, split / 16 x 16 / 64 x 64:
+    //   d      V       16 rows         64 rows         256 rows        512 rows        768 rows
+    //   4096   20011   34/38/116       48/47/134       97/92/122       158/154/162     208/203/203
+    //   1280   50257   36/49/312       47/48/288       88/84/175       134/130/175     182/184/207
+    //   640    30011   29/34/194       35/42/323       53/51/178       81/79/154       104/100/154
+    // The first border holds throughout; the second is that of d >= 4096, and for
+    // shorter rows of more than 512 gradients 16 x 16 would be ahead.
     const int64_t tiles = (M + 15) / 16 * (s.d / 16), waves = (M + 63) / 64 * (s.d / 64);
     if (tiles <= 512)
         hipLaunchKernelGGL((finish_kernel<1, 1, true>), dim3((unsigned)tiles), dim3(256), 0, st, f);

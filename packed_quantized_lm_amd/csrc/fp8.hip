@@ -102,8 +102,9 @@ __device__ __forceinline__ u32x2 codes8(const float v[8], float s)
 
 // One row's blocks: 16 lanes a block, 8 columns a lane, so that a block's
 // largest magnitude takes four exchanges and a lane one load and one store
-// (2048 x 4096 bf16: 20 us with its exact quotients' arithmetic, which bounds
-// it; one row 5 us, a launch).
+// (2048 x 4096 bf16: 16 us against 5 of its bytes, the vector units busy
+// throughout with the exact quotients: a division, its remainder and the last
+// bit of every element; one row 5 us, a launch).
 template <typename T>
 __global__ __launch_bounds__(256) void quant_rows_kernel(const T *x, int64_t ldx, int64_t rows, int64_t cols,
                                                          uint8_t *q, int64_t ldq, float *s, int64_t lds)
@@ -130,7 +131,10 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const T *x, int64_t ldx
         s[b * lds + row] = sc;
 }
 
-// 128 x 128 blocks, one per workgroup: two threads a row, 64 columns each
+// 128 x 128 blocks, one per workgroup: two threads a row, 64 columns each, read
+// once for the scale and again for the codes.  151936 x 4096 bf16, once per
+// head: 3.4 ms against 0.4 of its bytes, since a thread's 16-byte loads come to a
+// 128-byte line eight times in each pass, and 18 GB are fetched for 1.2.
 template <typename T>
 __global__ __launch_bounds__(256) void quant_tiles_kernel(const T *x, int64_t ldx, int64_t rows, int64_t cols,
                                                           uint8_t *q, int64_t ldq, float *s, int64_t lds)
@@ -188,7 +192,7 @@ __device__ __forceinline__ f16x8 halves(uint32_t lo, uint32_t hi)
 // cut off what lies 2^13 below it (measured: 2e-5 of the terms' magnitudes,
 // 1e-4 of a typical result), which would show in an fp32 result; a bf16
 // result, rounded at 2^-8, hides it, and there the tiles for many rows use
-// them (2048 x 151936 x 4096: 1.62 ms against 2.14 in fp16).
+// them (2048 x 151936 x 4096: 1.62 ms against 2.19 in fp16).
 __device__ __forceinline__ f32x4 block_product(i32x8 a, i32x8 b, f32x4 c)
 {
     for (int i = 0; i < 8; i += 2)
@@ -234,7 +238,7 @@ __device__ __forceinline__ i32x8 join(i32x4 a, i32x4 b)
 // columns: any order of the columns serves as long as both operands share it.
 // The hidden states' codes lie in LDS where they fit, M K <= 64 KiB: read
 // through the caches they pass at the weights' own rate (M = 16, N = 151936,
-// K = 4096: 163 us against 138).
+// K = 4096: 163 us against 141).
 // ---------------------------------------------------------------------------
 constexpr int kSkinnyM = 16, kSkinnyWaves = 4, kDepth = 4;
 constexpr int64_t kSkinnyX = 64 << 10;   // LDS for the hidden states' codes, two workgroups a compute unit
@@ -339,9 +343,10 @@ template <bool XL, typename O> __global__ __launch_bounds__(kSkinnyWaves * 64) v
 // as codes (16-byte pieces, a row's pieces exchanged by the row's low bits so
 // that the reads of eight neighbouring rows fall on different banks: no
 // conflicts counted) while the other buffer is worked on; the block's sums are
-// scaled into the accumulator in fp32.  2048 x 151936 x 4096: fp32 2.14 ms, 1190
+// scaled into the accumulator in fp32.  2048 x 151936 x 4096: fp32 2.19 ms, 1166
 // TFLOP/s of the 1219 that a large bf16 library product reaches here; bf16 1.62
-// ms, 1577 TFLOP/s.
+// ms, 1570 TFLOP/s of the 2940 of an fp8 one: matrix cores 35 % busy, all copies
+// of a stage waited for before each of its barriers.
 // ---------------------------------------------------------------------------
 __device__ const u32x4 kNothing = {0u, 0u, 0u, 0u}; // what a piece past K is copied from
 
@@ -562,17 +567,17 @@ template <typename O> archead_status run_product(const ProdArgs &a, hipStream_t 
     if (a.M <= kSkinnyM)
         run_skinny<O>(a, st);
     // 64 x 128, three of which run beside each other on a compute unit, for few
-    // rows (64 x 151936 x 4096, fp32: 164 us; two of 64 x 256: 189) and, in fp32,
+    // rows (64 x 151936 x 4096, fp32: 166 us; 128 x 128: 188) and, in fp32,
     // where 128 x 128 would leave compute units idle or alone with one (512 x 4096
-    // x 4096: 30 us against 43; 1000 x 4096 x 4096: 44 against 45).
+    // x 4096: 29 us against 42; 1000 x 4096 x 4096: 42 against 43).
     else if (a.M <= 64 || (sizeof(O) == 4 && (a.M + 127) / 128 * ((a.N + 127) / 128) <= kCu))
         run_tile<64, 128, O>(a, st);
     else {
         // 128 x 128, two of which run beside each other on a compute unit, or 256
         // x 256, which move and convert less per product (2048 x 151936 x 4096:
-        // fp32 2.14 ms against 2.37, bf16 1.62 against 1.97) but fill a chip in
-        // coarser steps (333 x 50021 x 2576, bf16: 123 us against 104; 2048 x
-        // 50021 x 2576, fp32: 604 against 581): by the rounds each takes, a round
+        // fp32 2.19 ms against 2.42, bf16 1.62 against 1.99) but fill a chip in
+        // coarser steps (333 x 50021 x 2576, bf16: 115 us against 90; 2048 x
+        // 50021 x 2576, fp32: 620 against 596): by the rounds each takes, a round
         // of the large ones being 1.64 (bf16, in fp8) or 1.88 times (fp32, in
         // fp16) as long.
         auto rounds = [&](int64_t b, int64_t places) {

@@ -6,7 +6,8 @@
 //   top = max_v y[v],  Z = sum_v exp(y[v] - top),  lse = top + log Z,
 //   logp = (y[t] - top) - log Z,  p[v] = exp(y[v] - top) / Z,
 // and both losses reach the logits through logp alone:
-//   dlogits[v] = c (1[v = t] - p[v]),   c = d loss / d logp[m].
+//   dlogits[v] = c (1[v = t] - p[v]),   c = d loss / d logp[m],
+// with 1 - p[t] taken from what is beside the target.
 // Policy:     rho = exp(logp - old), kl = exp(ref - logp) - (ref - logp) - 1,
 //   loss = sum_m w (-min(rho A, clip(rho, 1 - el, 1 + eh) A) + beta kl),
 //   c = w (-A rho [the unclipped branch] + beta (1 - exp(ref - logp))).
@@ -20,7 +21,7 @@
 // read with a write for the gradient.  Where a row's loss needs that row alone
 // (policy), a workgroup may keep much of it for the gradient; the preference
 // loss sums over answers first and reads twice (1800 x 151936 fp32, bf16
-// gradient: 174 + 10 + 291 us).  Every sum has a fixed order: repeated calls
+// gradient: 173 + 11 + 294 us).  Every sum has a fixed order: repeated calls
 // agree bit for bit.
 #include <hip/hip_runtime.h>
 
@@ -665,8 +666,16 @@ void choose_slices(int64_t M, int64_t V, int64_t *S, int64_t *slice)
 // Whether the policy loss runs as one workgroup per row (the logits read from
 // HBM once) rather than in slices (read twice).  A long row's workgroup fills
 // a compute unit, so the rows go in rounds of kCu, and a round that is mostly
-// empty costs more than the second read: at V = 151936 a round takes 50 us
-// and the slices 0.25 us a row + 8 us, which cross at 0.7 of a round filled.
+// empty can cost more than the second read; the rule asks for 0.7 of a round.
+// Measured, fp32 logits, bf16 gradient, us in slices against whole rows:
+//   rows               16       64      160      256      300      512
+//   V = 151936      17/27    33/28    55/36    70/50    79/72   134/94
+//   V = 50257       13/15    16/15    26/17    34/21    36/31    50/36
+//   V = 32000       12/12    12/12    19/13    25/13    27/22    37/26
+//   V = 12000        11/9    11/10    12/10    13/10    15/15    22/16
+// so whole rows are ahead from some 50 rows on, earlier than the rule takes
+// them.  Without a gradient the slices lead by up to 11 us at V = 151936 below
+// 200 rows (64 rows: 18/30) and the two are within 3 us elsewhere.
 bool whole_rows(int64_t M, int64_t V)
 {
     if (V <= 4 * kNT * kVec)
@@ -767,10 +776,10 @@ void run_stats(const Rows &a, Stat *part, float *logp, float *lse, Coef *coef, h
 
 // Whether the log probabilities take one workgroup of 1024 threads a row, and
 // one launch, rather than slices of rows and a second launch that merges them:
-// for rows of moderate length unless they are very many (16 x 8200 fp32: 4.9 us
-// against 5.8; 1500 x 16000: 22.8 against 20.3), for long ones where they fill
-// whole rounds of compute units (256 x 151936: fp32 27.7 us against 30.3, bf16
-// 16.9 against 21.9; one row: 12.3 against 7.5).
+// for rows of moderate length unless they are very many (16 x 8200 fp32: 5.9 us
+// against 7.1; 1500 x 16000: 23.8 against 21.8), for long ones where they fill
+// whole rounds of compute units (256 x 151936: fp32 27.7 us against 32.1, bf16
+// 18.6 against 25.0; one row: 14.2 against 9.2).
 bool whole_logp(int64_t M, int64_t V)
 {
     if (V <= 32768)
@@ -830,13 +839,13 @@ void run_policy_rows(const Rows &a, const Policy &pol, float *logp, float *token
 }
 
 // Threads and held vectors by the row's length: as many vectors held as the
-// row fills (a vector past its end is a wasted load: V = 50021 in bf16 took
-// 128 us with 16 held of which 6 are filled, 102 us with none) and the
-// registers of 1024 threads allow.  2048 rows of 151936 fp32 logits with a
-// bf16 gradient: 409 us with eight held, 486 us with none.  LDS holds four more
-// of fp32 logits where the gradient is in bf16 (395 us; 2048 x 128256: 325
-// against 343); with an fp32 gradient they cost more than they save (663 us
-// against 645), and bf16 logits gain nothing (274 against 275).
+// row fills (a vector past its end is a wasted load: 2048 rows of 50021 bf16
+// logits take 130 us with 16 held of which 6 are filled, 113 us with none) and
+// the registers of 1024 threads allow.  2048 rows of 151936 fp32 logits with a
+// bf16 gradient: 411 us with eight held, 508 us with none.  LDS holds four more
+// of fp32 logits where the gradient is in bf16 (393 us; 2048 x 128256: 318
+// against 343); with an fp32 gradient they cost more than they save (687 us
+// against 661).  bf16 logits do without them (274 us; with them 262).
 template <typename T>
 void run_policy_whole(const Rows &a, const Policy &pol, float *logp, float *token, const Grad &g, hipStream_t st)
 {

@@ -112,3 +112,33 @@ def test_rows_of_the_head_come_back(V, d, k, r, g, M, reserved):
     tol = (2.0 ** -11 + (k + r) * 2.0 ** -23 + 2.0 ** -16) * terms + 2.0 ** -8 * np.abs(want) + 2.0 ** -133
     err = np.abs(got - want)
     assert (err <= tol).all(), ((err / tol).max(), np.argwhere(err > tol)[:4])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["sR", "sA", "sC"])
+def test_scales_far_below_the_largest(kind):
+    """One scale near fp16's largest value beside ordinary and tiny ones: a code
+    times its scale keeps 11 bits, or 2^-31 of the largest code times scale."""
+    import torch
+    from packed_quantized_lm_amd import PackedHead
+    say(f"backward with one large {kind}")
+    V, d, k, r, g = 300, 256, 24, 16, 32
+    f = random_small_head(V, d, k, r, g, 1, seed=21)
+    rng = np.random.default_rng(3)
+    for n in ("sR", "sA", "sC"):
+        s = 2.0 ** rng.uniform(-20, -8, f[n].shape)
+        f[n] = s.astype(np.float16).view(np.uint16)
+    f[kind] = f[kind].copy()
+    f[kind].reshape(-1)[7] = np.array(60000, np.float16).view(np.uint16)
+    head = PackedHead(f)
+    head.reserve_backward(V)
+    got = head.backward(torch.eye(V, dtype=torch.bfloat16, device="cuda")).double().cpu().numpy()
+    head.close()
+    R, A, B, C, D = test_gpu_backward.magnitudes(f)
+    largest = {n: c * np.abs(test_gpu_backward.half(f[n])).max() for n, c in (("sR", 8), ("sA", 16), ("sC", 128))}
+    lost = 2.0 ** -31 * (largest["sR"] + largest["sA"] * B.sum(0) + largest["sC"] * D.sum(0))[None, :]
+    want = forward.dense_rows(f, np.arange(V))
+    tol = ((2.0 ** -11 + (k + r) * 2.0 ** -23 + 2.0 ** -16) * (R + A @ B + C @ D) + lost + 2.0 ** -8 * np.abs(want)
+           + 2.0 ** -133)
+    err = np.abs(got - want)
+    assert (err <= tol).all(), ((err / tol).max(), np.argwhere(err > tol)[:4])
