@@ -23,6 +23,14 @@ SHAPES = [(65537, 384, 40, 20, 96, 1500, 1500), (33001, 640, 100, 70, 32, 2047, 
           (1000, 384, 64, 64, 96, 700, 300), (500, 4224, 32, 96, 32, 31, 31), (257, 128, 64, 64, 128, 16, 16)]
 
 
+@pytest.fixture(autouse=True)
+def gpu(request):
+    if request.node.get_closest_marker("gpu"):
+        import torch
+        if not torch.cuda.is_available():
+            pytest.skip("no GPU")
+
+
 def test_the_shapes_reach_every_launch():
     """Of both lists of shapes together, by the rules in csrc/backward.hip: every
     kind of tile with full and padded low-rank tiles, one and several ranges,
