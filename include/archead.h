@@ -560,6 +560,66 @@ archead_status archead_fp8_matmul(int64_t M, int64_t N, int64_t K, const uint8_t
                                   void *out, int out_type, int64_t ldo, void *hip_stream);
 
 /*
+ * archead_rms_norm -- the root-mean-square norm in front of an output head (or a
+ * block of the model), with the residual's addition, and its results as the
+ * head takes them: in fp32 or bf16, and as archead_fp8_matmul's codes and scales.
+ *   h_j = x_j + residual_j, added in fp32 and rounded to the residual's type (h = x without one)
+ *   n_j = h_j / sqrt(mean_j h_j^2 + eps) * (weight_j + offset)
+ *   y   = n rounded once to its type; q, s as archead_fp8_quantize (block_rows = 1) of n
+ * offset is 0, or 1 for weights that are stored around zero.
+ *
+ * M         0 <= M < 2^22 rows (0 is a no-op that succeeds); 1 <= d <= 2^20.
+ * x         DEVICE M x d, fp32 or bf16 (x_type), row stride ldx elements.
+ * residual  DEVICE M x d (res_type), row stride ldr, or NULL; with it h, of the
+ *           same type (row stride ldh), written in full.
+ * weight    DEVICE d (weight_type).
+ * y         DEVICE M x d (y_type), row stride ldy, or NULL.
+ * q, s      DEVICE codes (row stride ldq bytes; q and ldq multiples of 16) and
+ *           scales s[b * lds + row], lds >= M, as archead_fp8_matmul reads them,
+ *           or both NULL; they need d to be a multiple of 16.  y or q is required.
+ * Strides lie in [d, 2^40].  h may be residual or x, and y may be x, with the same
+ * type and stride; other buffers must not overlap.  Buffers are aligned to their
+ * element.  eps is finite and not negative, offset finite.
+ * Numerics: squares are summed in fp64; n is fp32, with three roundings (1.5 x
+ * 2^-23 relative); rows whose root mean square passes 2^126 lose precision.  A NaN in
+ * row m makes its n NaN, an infinity 0 and NaN; no other row is touched by either.  A
+ * row of zeros with eps = 0 is 0 / 0.
+ * The current device must be the one the buffers and hip_stream belong to.
+ * Enqueued, not waited for; nothing is allocated (graph capture is fine); equal
+ * calls give equal bits.
+ */
+archead_status archead_rms_norm(int64_t M, int64_t d, const void *x, int x_type, int64_t ldx, const void *residual,
+                                int res_type, int64_t ldr, void *h, int64_t ldh, const void *weight, int weight_type,
+                                float eps, float offset, void *y, int y_type, int64_t ldy, uint8_t *q, int64_t ldq,
+                                float *s, int64_t lds, void *hip_stream);
+
+/*
+ * archead_rms_norm_backward -- the norm's gradients: with u = dy, r_m =
+ * 1 / sqrt(mean_j h_mj^2 + eps), g_j = u_j (weight_j + offset),
+ *   dh_j      = r (g_j - h_j r^2 mean_i g_i h_i) + dres_j
+ *   dweight_j = sum_m u_mj h_mj r_m
+ * h is archead_rms_norm's (x without a residual); dh is the gradient by x and by
+ * the residual alike, and dres what reaches h past the norm, through the residual
+ * stream (NULL for nothing).
+ *
+ * dy       DEVICE M x d (dy_type), row stride ldy.  h, dres, dh: DEVICE M x d of
+ *          h_type, row strides ldh, ldr, ldd.  dh may be dres (same stride), and
+ *          overlaps nothing else.
+ * dweight  DEVICE fp32 d, written (zeros for M = 0), or NULL.
+ * ws       DEVICE workspace of archead_rms_norm_workspace(M, d) bytes, 16-byte
+ *          aligned, contents irrelevant, the call's own until the stream has
+ *          passed it: calls, or captured graphs, that may overlap need one each.
+ * Sizes, alignment, streams and numerics as archead_rms_norm: the row's two sums
+ * are fp64, dh is fp32 rounded once, dweight's terms are added in fp32 over at most
+ * 64 rows and then in fp64, in a fixed order.
+ */
+archead_status archead_rms_norm_workspace(int64_t M, int64_t d, uint64_t *bytes);
+archead_status archead_rms_norm_backward(int64_t M, int64_t d, const void *dy, int dy_type, int64_t ldy, const void *h,
+                                         int h_type, int64_t ldh, const void *weight, int weight_type, float eps,
+                                         float offset, const void *dres, int64_t ldr, void *dh, int64_t ldd,
+                                         float *dweight, void *ws, uint64_t ws_bytes, void *hip_stream);
+
+/*
  * archead_packed_bytes -- eq 10 of the ARCHead paper: the sum over the
  * registered packed buffers of numel x element size (A5 counted at 5 bits,
  * R4 at 4 bits, int8 fields at 8, scales at 16; each buffer rounded up to a

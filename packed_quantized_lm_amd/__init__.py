@@ -12,6 +12,7 @@ e4m3 with a scale per block of 128, and their product); `synth` draws seeded syn
 from .binding import PackedHead, build_head, load_library, quantize, x_tensor_from_bits  # noqa: F401
 from .fp8 import Fp8Head, fp8_matmul, fp8_quantize  # noqa: F401
 from .losses import policy_loss, preference_loss, token_logp  # noqa: F401
+from .norm import rms_norm, rms_norm_backward  # noqa: F401
 
 __all__ = ["Fp8Head", "PackedHead", "build_head", "fp8_matmul", "fp8_quantize", "load_library", "policy_loss", "preference_loss", "quantize", "token_logp",
-           "x_tensor_from_bits"]
+           "rms_norm", "rms_norm_backward", "x_tensor_from_bits"]

@@ -53,6 +53,13 @@ SIGNATURES = {
                                             _VP]),
     "archead_fp8_matmul": (ctypes.c_int, [_I64] * 3 + [_VP, _I64, _VP, _I64, _VP, _I64, _VP, _I64, _VP, ctypes.c_int,
                                                        _I64, _VP]),
+    "archead_rms_norm": (ctypes.c_int, [_I64, _I64, _VP, ctypes.c_int, _I64, _VP, ctypes.c_int, _I64, _VP, _I64, _VP,
+                                        ctypes.c_int, ctypes.c_float, ctypes.c_float, _VP, ctypes.c_int, _I64, _VP,
+                                        _I64, _VP, _I64, _VP]),
+    "archead_rms_norm_workspace": (ctypes.c_int, [_I64, _I64, ctypes.POINTER(ctypes.c_uint64)]),
+    "archead_rms_norm_backward": (ctypes.c_int, [_I64, _I64, _VP, ctypes.c_int, _I64, _VP, ctypes.c_int, _I64, _VP,
+                                                 ctypes.c_int, ctypes.c_float, ctypes.c_float, _VP, _I64, _VP, _I64,
+                                                 _VP, _VP, ctypes.c_uint64, _VP]),
     "archead_reserve_backward": (ctypes.c_int, [_VP, _I64, _VP]),
     "archead_backward": (ctypes.c_int, [_VP, _I64, _VP, ctypes.c_int, _I64, _VP, _VP]),
     "archead_packed_bytes": (ctypes.c_int, [_VP, ctypes.POINTER(ctypes.c_uint64)]),

@@ -1,0 +1,111 @@
+// elements.hpp -- rows of fp32 or bf16 (uint16_t) elements as vectors of eight,
+// from any element boundary: a row's last vector may be partial, and rows of odd
+// length start anywhere.
+#pragma once
+
+#include "device.hpp"
+
+namespace archead {
+
+typedef float f32x4e __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint16_t u16x8e __attribute__((ext_vector_type(8), aligned(2)));
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2e;
+typedef __attribute__((ext_vector_type(2))) float f32x2e;
+
+// eight elements as they lie in memory
+template <typename T> struct Eight;
+template <> struct Eight<float> {
+    f32x4e a, b;
+};
+template <> struct Eight<uint16_t> {
+    u16x8e a;
+};
+
+__device__ __forceinline__ Eight<float> load_eight(const float *p) { return {*(const f32x4e *)p, *(const f32x4e *)(p + 4)}; }
+__device__ __forceinline__ Eight<uint16_t> load_eight(const uint16_t *p) { return {*(const u16x8e *)p}; }
+__device__ __forceinline__ float load_one(const float *p) { return *p; }
+__device__ __forceinline__ float load_one(const uint16_t *p) { return __uint_as_float((uint32_t)*p << 16); }
+
+__device__ __forceinline__ void widen(const Eight<float> &r, float v[8])
+{
+    for (int i = 0; i < 4; ++i) {
+        v[i] = r.a[i];
+        v[4 + i] = r.b[i];
+    }
+}
+__device__ __forceinline__ void widen(const Eight<uint16_t> &r, float v[8])
+{
+    for (int i = 0; i < 8; ++i)
+        v[i] = __uint_as_float((uint32_t)r.a[i] << 16);
+}
+
+// values as they lie in memory, rounded once to nearest even
+__device__ __forceinline__ void narrow(const float v[8], Eight<float> &o)
+{
+    for (int i = 0; i < 4; ++i) {
+        o.a[i] = v[i];
+        o.b[i] = v[4 + i];
+    }
+}
+__device__ __forceinline__ void narrow(const float v[8], Eight<uint16_t> &o)
+{
+    for (int i = 0; i < 8; i += 2) {
+        const uint32_t w = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2e{v[i], v[i + 1]}, bf16x2e));
+        o.a[i] = (uint16_t)w;
+        o.a[i + 1] = (uint16_t)(w >> 16);
+    }
+}
+__device__ __forceinline__ void store_eight(float *p, const Eight<float> &o)
+{
+    *(f32x4e *)p = o.a;
+    *(f32x4e *)(p + 4) = o.b;
+}
+__device__ __forceinline__ void store_eight(uint16_t *p, const Eight<uint16_t> &o) { *(u16x8e *)p = o.a; }
+// past the caches' working set: results that nothing reads before they are evicted
+__device__ __forceinline__ void stream_eight(float *p, const Eight<float> &o)
+{
+    __builtin_nontemporal_store(o.a, (f32x4e *)p);
+    __builtin_nontemporal_store(o.b, (f32x4e *)(p + 4));
+}
+__device__ __forceinline__ void stream_eight(uint16_t *p, const Eight<uint16_t> &o)
+{
+    __builtin_nontemporal_store(o.a, (u16x8e *)p);
+}
+__device__ __forceinline__ void store_one(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store_one(uint16_t *p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
+
+// Vector q of a row of d elements as it lies in memory; past the last whole
+// vector that one again (the load is not put under a branch, which would wait
+// for each in turn), which vector_values replaces.
+template <typename T> __device__ __forceinline__ Eight<T> load_vector(const T *row, int64_t q, int64_t d)
+{
+    if (d < 8) // no whole vector to read
+        return Eight<T>{};
+    return load_eight(row + 8 * min(q, d / 8 - 1));
+}
+// the values of vector q, given what load_vector read: zeros past the row's end
+template <typename T>
+__device__ __forceinline__ void vector_values(const T *row, int64_t q, int64_t d, const Eight<T> &r, float v[8])
+{
+    widen(r, v);
+    if (8 * q + 8 > d) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = 8 * q + i < d ? load_one(row + 8 * q + i) : 0.f;
+    }
+}
+template <typename T> __device__ __forceinline__ void store_vector(T *row, int64_t q, int64_t d, const float v[8])
+{
+    if (8 * q + 8 <= d) {
+        Eight<T> o;
+        narrow(v, o);
+        store_eight(row + 8 * q, o);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (8 * q + i < d)
+                store_one(row + 8 * q + i, v[i]);
+    }
+}
+
+} // namespace archead

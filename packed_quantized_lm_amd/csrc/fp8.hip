@@ -18,6 +18,7 @@
 #include "api_internal.hpp"
 #include "archead.h"
 #include "device.hpp"
+#include "e4m3.hpp"
 #include "lds_copy.hpp"
 
 namespace archead {
@@ -29,7 +30,6 @@ typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint16_t u16x8u __attribute__((ext_vector_type(8), aligned(2)));
 
 constexpr int kBlk = 128; // columns (and weight rows) that share a scale
-constexpr float kE4m3Max = 448.f;
 constexpr int64_t kMaxStride = int64_t(1) << 23; // of A and B: a tile's offsets fit 32 bits
 
 // ---------------------------------------------------------------------------
@@ -48,56 +48,6 @@ __device__ __forceinline__ void load8(const uint16_t *p, float v[8])
     const u16x8u a = *(const u16x8u *)p;
     for (int i = 0; i < 8; ++i)
         v[i] = __uint_as_float((uint32_t)a[i] << 16);
-}
-
-__device__ __forceinline__ float block_scale(float amax)
-{
-    return amax > 0.f ? fmaxf(amax * (1.f / kE4m3Max), 1.17549435e-38f) : 0.f;
-}
-
-// x / s with the last bit set where the quotient is not exact, so that the
-// rounding to e4m3 that follows never sees a tie that is not one: the
-// division's remainder x - q s is exact in one fma and says on which side of
-// q the quotient lies.
-__device__ __forceinline__ float sticky_quotient(float x, float s)
-{
-    float q, rem;
-    if (s < 7.9e-31f) { // 2^-100: the remainder could fall below fp32's range
-        const double d = (double)x / (double)s;
-        q = (float)d;
-        rem = (float)(d - (double)q);
-    } else {
-        q = x / s;
-        rem = __builtin_fmaf(-q, s, x);
-    }
-    uint32_t b = __float_as_uint(q);
-    if (rem != 0.f && (b & 1u) == 0u && fabsf(q) < 3.0e38f) {
-        const bool outward = (rem > 0.f) == (q > 0.f);
-        b = outward ? b + 1 : b - 1;
-    }
-    return q == 0.f ? q : __uint_as_float(b);
-}
-
-// eight codes in order
-__device__ __forceinline__ u32x2 codes8(const float v[8], float s)
-{
-    float q[8];
-    uint32_t nan = 0;
-    for (int i = 0; i < 8; ++i) {
-        const float t = s > 0.f ? sticky_quotient(v[i], s) : 0.f;
-        const bool is_nan = v[i] != v[i] || t != t;
-        nan |= (uint32_t)is_nan << i;
-        q[i] = is_nan ? 0.f : fminf(fmaxf(t, -kE4m3Max), kE4m3Max);
-    }
-    u32x2 o;
-    for (int h = 0; h < 2; ++h) {
-        int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * h], q[4 * h + 1], 0, false);
-        o[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[4 * h + 2], q[4 * h + 3], w, true);
-        for (int i = 0; i < 4; ++i)
-            if (nan >> (4 * h + i) & 1)
-                o[h] |= 0x7Fu << (8 * i);
-    }
-    return o;
 }
 
 // One row's blocks: 16 lanes a block, 8 columns a lane, so that a block's
@@ -126,7 +76,7 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const T *x, int64_t ldx
         m = fmaxf(m, __shfl_xor(m, off));
     const float sc = block_scale(m);
     if (in)
-        *(u32x2 *)(q + row * ldq + c) = codes8(v, sc);
+        *(u32x2 *)(q + row * ldq + c) = codes8_exact(v, sc);
     if ((threadIdx.x & 15) == 0)
         s[b * lds + row] = sc;
 }
@@ -160,7 +110,7 @@ __global__ __launch_bounds__(256) void quant_tiles_kernel(const T *x, int64_t ld
     for (int j = 0; j < 8; ++j)
         if (row < rows && c0 + 8 * j < cols) {
             load8(xr + c0 + 8 * j, v);
-            *(u32x2 *)(q + row * ldq + c0 + 8 * j) = codes8(v, sc);
+            *(u32x2 *)(q + row * ldq + c0 + 8 * j) = codes8_exact(v, sc);
         }
     if (threadIdx.x == 0)
         s[rb * lds + b] = sc;
