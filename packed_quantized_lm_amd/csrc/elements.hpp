@@ -74,27 +74,58 @@ __device__ __forceinline__ void stream_eight(uint16_t *p, const Eight<uint16_t> 
 __device__ __forceinline__ void store_one(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_one(uint16_t *p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
 
-// Vector q of a row of d elements as it lies in memory; past the last whole
-// vector that one again (the load is not put under a branch, which would wait
-// for each in turn), which vector_values replaces.
-template <typename T> __device__ __forceinline__ Eight<T> load_vector(const T *row, int64_t q, int64_t d)
+__device__ __forceinline__ void set_element(Eight<float> &r, int i, float e) { (i < 4 ? r.a : r.b)[i & 3] = e; }
+__device__ __forceinline__ void set_element(Eight<uint16_t> &r, int i, uint16_t e) { r.a[i] = e; }
+
+// What vector q of a row of d elements is made from: its eight elements, or the
+// row's last eight where it has fewer or lies past the end.  No load is under a
+// branch of a lane's own, so that all of a thread's stay in flight together.  Int is
+// int where rows are short enough (an offset of 32 bits from a uniform base).
+template <typename T, typename Int> __device__ __forceinline__ Eight<T> load_vector(const T *row, Int q, Int d)
 {
-    if (d < 8) // no whole vector to read
-        return Eight<T>{};
-    return load_eight(row + 8 * min(q, d / 8 - 1));
+    if (d >= 8)
+        return load_eight(row + min((Int)(8 * q), (Int)(d - 8)));
+    Eight<T> r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        // held in a vector register: of a uniform row the compiler makes scalar loads
+        // whose base and offset it splits into halves that need not be multiples of
+        // 4 (seen where one kernel reads both element types), and the hardware
+        // rounds each down
+        int at = (int)min((Int)i, (Int)(d - 1));
+        asm volatile("" : "+v"(at));
+        set_element(r, i, row[at]);
+    }
+    return r;
 }
-// the values of vector q, given what load_vector read: zeros past the row's end
-template <typename T>
-__device__ __forceinline__ void vector_values(const T *row, int64_t q, int64_t d, const Eight<T> &r, float v[8])
+// the values of vector q from what load_vector read, zeros past the row's end
+template <typename Int> __device__ __forceinline__ void keep_values(Int q, Int d, float v[8])
 {
-    widen(r, v);
-    if (8 * q + 8 > d) {
+    if (d < 8) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            v[i] = 8 * q + i < d ? load_one(row + 8 * q + i) : 0.f;
+            v[i] = 8 * q + i < d ? v[i] : 0.f;
+    } else {
+        const Int past = 8 * q - (d - 8); // elements read before the vector's first
+        if (d & 7) {
+#pragma unroll
+            for (int step = 4; step >= 1; step >>= 1)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[i] = past > 0 && (past & step) ? (i + step < 8 ? v[i + step] : 0.f) : v[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = past >= 8 ? 0.f : v[i];
     }
 }
-template <typename T> __device__ __forceinline__ void store_vector(T *row, int64_t q, int64_t d, const float v[8])
+template <typename T, typename Int>
+__device__ __forceinline__ void vector_values(Int q, Int d, const Eight<T> &r, float v[8])
+{
+    widen(r, v);
+    keep_values(q, d, v);
+}
+template <typename T, typename Int> __device__ __forceinline__ void store_vector(T *row, Int q, Int d, const float v[8])
 {
     if (8 * q + 8 <= d) {
         Eight<T> o;

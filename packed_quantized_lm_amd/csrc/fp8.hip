@@ -76,7 +76,7 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const T *x, int64_t ldx
         m = fmaxf(m, __shfl_xor(m, off));
     const float sc = block_scale(m);
     if (in)
-        *(u32x2 *)(q + row * ldq + c) = codes8_exact(v, sc);
+        *(u32x2 *)(q + row * ldq + c) = codes8(v, sc);
     if ((threadIdx.x & 15) == 0)
         s[b * lds + row] = sc;
 }
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(256) void quant_tiles_kernel(const T *x, int64_t ld
     for (int j = 0; j < 8; ++j)
         if (row < rows && c0 + 8 * j < cols) {
             load8(xr + c0 + 8 * j, v);
-            *(u32x2 *)(q + row * ldq + c0 + 8 * j) = codes8_exact(v, sc);
+            *(u32x2 *)(q + row * ldq + c0 + 8 * j) = codes8(v, sc);
         }
     if (threadIdx.x == 0)
         s[rb * lds + b] = sc;

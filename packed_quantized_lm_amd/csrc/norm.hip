@@ -81,7 +81,9 @@ __device__ __forceinline__ void team_sums(double &v, double &w, double (*red)[T 
 }
 
 struct NormArgs {
-    int64_t M, d, ldx, ldr, ldh, ldy, ldq, lds;
+    int64_t M;
+    int d;
+    int64_t ldx, ldr, ldh, ldy, ldq, lds;
     const void *x, *residual, *weight;
     void *h, *y;
     uint8_t *q;
@@ -91,18 +93,18 @@ struct NormArgs {
     int weight_type, y_type;
 };
 
-__device__ __forceinline__ void weights_of(const NormArgs &a, int64_t q, float w[8])
+__device__ __forceinline__ void weights_of(const NormArgs &a, int q, float w[8])
 {
     if (a.weight_type == ARCHEAD_F32)
-        vector_values((const float *)a.weight, q, a.d, load_vector((const float *)a.weight, q, a.d), w);
+        vector_values(q, a.d, load_vector((const float *)a.weight, q, a.d), w);
     else
-        vector_values((const uint16_t *)a.weight, q, a.d, load_vector((const uint16_t *)a.weight, q, a.d), w);
+        vector_values(q, a.d, load_vector((const uint16_t *)a.weight, q, a.d), w);
     for (int i = 0; i < 8; ++i)
         w[i] += a.offset;
 }
 
 // results of one vector n; sixteen neighbouring threads hold a block of columns
-__device__ __forceinline__ void put(const NormArgs &a, int64_t m, int64_t q, bool in, const float n[8])
+__device__ __forceinline__ void put(const NormArgs &a, int64_t m, int q, bool in, const float n[8])
 {
     if (a.y && in) {
         if (a.y_type == ARCHEAD_F32)
@@ -118,7 +120,7 @@ __device__ __forceinline__ void put(const NormArgs &a, int64_t m, int64_t q, boo
             top = fmaxf(top, __shfl_xor(top, off));
         const float sc = block_scale(top);
         if (in) {
-            *(u32x2 *)(a.q + m * a.ldq + 8 * q) = codes8_exact(n, sc);
+            *(u32x2 *)(a.q + m * a.ldq + 8 * q) = codes8(n, sc);
             if ((q & 15) == 0)
                 a.s[(q >> 4) * a.lds + m] = sc;
         }
@@ -140,7 +142,7 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void norm_kernel(NormArgs a)
         return;
     const XT *x = (const XT *)a.x + m * a.ldx;
     const RM *res = (const RM *)a.residual + m * a.ldr;
-    const int64_t nv = (a.d + 7) / 8;
+    const int nv = (a.d + 7) / 8;
     float v[H][8];
     {
         Eight<XT> xr[H];
@@ -153,11 +155,11 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void norm_kernel(NormArgs a)
         }
 #pragma unroll
         for (int j = 0; j < H; ++j) {
-            const int64_t q = t + j * T;
-            vector_values(x, q, a.d, xr[j], v[j]);
+            const int q = t + j * T;
+            vector_values(q, a.d, xr[j], v[j]);
             if constexpr (kRes) {
                 float o[8];
-                vector_values(res, q, a.d, rr[j], o);
+                vector_values(q, a.d, rr[j], o);
                 for (int i = 0; i < 8; ++i)
                     o[i] += v[j][i];
                 Eight<RM> sum;
@@ -178,7 +180,7 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void norm_kernel(NormArgs a)
     const float r = inverse_root(__builtin_fma(ss, a.inv_d, (double)a.eps));
 #pragma unroll
     for (int j = 0; j < H; ++j) {
-        const int64_t q = t + j * T;
+        const int q = t + j * T;
         if (j * T < nv) { // not uniform in a team only past the row's end
             float w[8], n[8];
             weights_of(a, q, w);
@@ -196,17 +198,18 @@ template <typename XT, typename RT> __global__ __launch_bounds__(kLongT) void no
     constexpr bool kRes = !std::is_same_v<RT, void>;
     using RM = std::conditional_t<kRes, RT, XT>;
     __shared__ double red[kLongT / 64];
-    const int64_t m = blockIdx.x, nv = (a.d + 7) / 8;
+    const int64_t m = blockIdx.x;
+    const int nv = (a.d + 7) / 8;
     const XT *x = (const XT *)a.x + m * a.ldx;
     const RM *res = (const RM *)a.residual + m * a.ldr;
     const RM *sum = kRes ? (const RM *)a.h + m * a.ldh : (const RM *)x;
     double ss = 0.;
-    for (int64_t q = threadIdx.x; q < nv; q += kLongT) {
+    for (int q = threadIdx.x; q < nv; q += kLongT) {
         float v[8];
-        vector_values(x, q, a.d, load_vector(x, q, a.d), v);
+        vector_values(q, a.d, load_vector(x, q, a.d), v);
         if constexpr (kRes) {
             float o[8];
-            vector_values(res, q, a.d, load_vector(res, q, a.d), o);
+            vector_values(q, a.d, load_vector(res, q, a.d), o);
             for (int i = 0; i < 8; ++i)
                 o[i] += v[i];
             Eight<RM> kept;
@@ -219,11 +222,11 @@ template <typename XT, typename RT> __global__ __launch_bounds__(kLongT) void no
     }
     ss = team_sum<kLongT>(ss, red);
     const float r = inverse_root(__builtin_fma(ss, a.inv_d, (double)a.eps));
-    for (int64_t q0 = 0; q0 < nv; q0 += kLongT) { // each thread reads back what it wrote
-        const int64_t q = q0 + threadIdx.x;
+    for (int q0 = 0; q0 < nv; q0 += kLongT) { // each thread reads back what it wrote
+        const int q = q0 + threadIdx.x;
         float v[8] = {}, w[8] = {};
         if (q < nv) {
-            vector_values(sum, q, a.d, load_vector(sum, q, a.d), v);
+            vector_values(q, a.d, load_vector(sum, q, a.d), v);
             weights_of(a, q, w);
         }
         for (int i = 0; i < 8; ++i)
@@ -261,7 +264,9 @@ template <typename XT, typename RT> void run_norm(const NormArgs &a, hipStream_t
 // backward
 // ---------------------------------------------------------------------------
 struct BackArgs {
-    int64_t M, d, ldu, ldh, ldr, ldd;
+    int64_t M;
+    int d;
+    int64_t ldu, ldh, ldr, ldd;
     const void *u, *h, *weight, *dres; // dres may be null
     void *dh;
     float *part; // [groups][d]
@@ -272,7 +277,7 @@ struct BackArgs {
     int64_t groups, slice; // long rows: rows a part sums
 };
 
-__device__ __forceinline__ void weights_of(const BackArgs &a, int64_t q, float w[8])
+__device__ __forceinline__ void weights_of(const BackArgs &a, int q, float w[8])
 {
     NormArgs n{};
     n.weight = a.weight;
@@ -282,49 +287,74 @@ __device__ __forceinline__ void weights_of(const BackArgs &a, int64_t q, float w
     weights_of(n, q, w);
 }
 
-// A workgroup's teams of T threads take every (groups x teams)-th row; weights and
-// dw's sums stay in registers, the teams' sums meet in LDS.
-template <int T, int H, typename UT, typename HT>
+// A workgroup's teams of T threads take every (groups x teams)-th row; dw's sums
+// stay in registers, and the weights where kHold (else they come from cache twice a
+// row); the teams' sums meet in LDS.
+template <int T, int H, bool kHold, bool kAhead, typename UT, typename HT>
 __global__ __launch_bounds__(T > 256 ? T : 256) void norm_back_kernel(BackArgs a)
 {
     constexpr int kWg = T > 256 ? T : 256, kTeams = kWg / T;
     __shared__ double red[2][2][T > 64 ? T / 64 : 1];
     __shared__ float meet[kTeams > 1 ? kTeams * T * H * 8 : 1];
     const int t = threadIdx.x % T, team = threadIdx.x / T;
-    const int64_t nv = (a.d + 7) / 8, step = a.groups * kTeams;
-    float w[H][8], dw[H][8];
+    const int nv = (a.d + 7) / 8;
+    const int64_t step = a.groups * kTeams;
+    float held[kHold ? H : 1][8], dw[H][8] = {};
+    if constexpr (kHold)
 #pragma unroll
-    for (int j = 0; j < H; ++j) {
-        weights_of(a, t + j * T, w[j]);
-        for (int i = 0; i < 8; ++i)
-            dw[j][i] = 0.f;
-    }
-    int turn = 0;
-    for (int64_t m = (int64_t)blockIdx.x * kTeams + team; m < a.M; m += step, turn ^= 1) {
+        for (int j = 0; j < H; ++j)
+            weights_of(a, t + j * T, held[j]);
+    auto weight = [&](int j, float w[8]) __attribute__((always_inline)) {
+        if constexpr (kHold) {
+            for (int i = 0; i < 8; ++i)
+                w[i] = held[j][i];
+        } else {
+            asm volatile("" : "+s"(a.weight)); // read here: not before the loop, into registers that are short
+            weights_of(a, t + j * T, w);
+        }
+    };
+    Eight<UT> ur[H];
+    Eight<HT> hr[H], rr[H];
+    auto fetch = [&](int64_t m) __attribute__((always_inline)) {
         const UT *u = (const UT *)a.u + m * a.ldu;
         const HT *h = (const HT *)a.h + m * a.ldh;
-        const HT *res = (const HT *)a.dres + m * a.ldr;
-        Eight<UT> ur[H];
-        Eight<HT> hr[H], rr[H];
 #pragma unroll
         for (int j = 0; j < H; ++j) {
             ur[j] = load_vector(u, t + j * T, a.d);
             hr[j] = load_vector(h, t + j * T, a.d);
         }
+    };
+    auto fetch_res = [&](int64_t m) __attribute__((always_inline)) {
         if (a.dres)
 #pragma unroll
             for (int j = 0; j < H; ++j)
-                rr[j] = load_vector(res, t + j * T, a.d);
+                rr[j] = load_vector((const HT *)a.dres + m * a.ldr, t + j * T, a.d);
+    };
+    int turn = 0;
+    int64_t m = (int64_t)blockIdx.x * kTeams + team;
+    if (kAhead && m < a.M)
+        fetch(m);
+    for (; m < a.M; m += step, turn ^= 1) {
+        if (!kAhead)
+            fetch(m);
+        fetch_res(m);
         float uv[H][8], hv[H][8];
         double ss = 0., c = 0.;
 #pragma unroll
         for (int j = 0; j < H; ++j) {
-            vector_values(u, t + j * T, a.d, ur[j], uv[j]);
-            vector_values(h, t + j * T, a.d, hr[j], hv[j]);
+            vector_values(t + j * T, a.d, ur[j], uv[j]);
+            vector_values(t + j * T, a.d, hr[j], hv[j]);
+        }
+        if (kAhead && m + step < a.M)
+            fetch(m + step); // the next row is on its way while this one is summed
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            float w[8];
+            weight(j, w);
             for (int i = 0; i < 8; ++i) {
                 const double hd = hv[j][i];
                 ss = __builtin_fma(hd, hd, ss);
-                c = __builtin_fma((double)(uv[j][i] * w[j][i]), hd, c);
+                c = __builtin_fma((double)(uv[j][i] * w[i]), hd, c);
             }
         }
         team_sums<T>(ss, c, red[turn]);
@@ -332,12 +362,13 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void norm_back_kernel(BackArgs a
         const float k = (float)((double)r * (double)r * (c * a.inv_d));
 #pragma unroll
         for (int j = 0; j < H; ++j) {
-            const int64_t q = t + j * T;
-            float o[8] = {};
+            const int q = t + j * T;
+            float o[8] = {}, w[8];
+            weight(j, w);
             if (a.dres)
-                vector_values(res, q, a.d, rr[j], o);
+                vector_values(q, a.d, rr[j], o);
             for (int i = 0; i < 8; ++i) {
-                o[i] = __builtin_fmaf(r, __builtin_fmaf(-hv[j][i], k, uv[j][i] * w[j][i]), o[i]);
+                o[i] = __builtin_fmaf(r, __builtin_fmaf(-hv[j][i], k, uv[j][i] * w[i]), o[i]);
                 dw[j][i] = __builtin_fmaf(uv[j][i], hv[j][i] * r, dw[j][i]);
             }
             if (q < nv)
@@ -351,7 +382,7 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void norm_back_kernel(BackArgs a
             for (int i = 0; i < 8; ++i)
                 meet[(team * T * H + j * T + t) * 8 + i] = dw[j][i];
         __syncthreads();
-        for (int64_t e = threadIdx.x; e < a.d; e += kWg) {
+        for (int e = threadIdx.x; e < a.d; e += kWg) {
             float s = 0.f;
             for (int k = 0; k < kTeams; ++k)
                 s += meet[k * T * H * 8 + e];
@@ -370,15 +401,16 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void norm_back_kernel(BackArgs a
 template <typename UT, typename HT> __global__ __launch_bounds__(kLongT) void norm_back_long_kernel(BackArgs a)
 {
     __shared__ double red[2][kLongT / 64];
-    const int64_t m = blockIdx.x, nv = (a.d + 7) / 8;
+    const int64_t m = blockIdx.x;
+    const int nv = (a.d + 7) / 8;
     const UT *u = (const UT *)a.u + m * a.ldu;
     const HT *h = (const HT *)a.h + m * a.ldh;
     const HT *res = (const HT *)a.dres + m * a.ldr;
     double ss = 0., c = 0.;
-    for (int64_t q = threadIdx.x; q < nv; q += kLongT) {
+    for (int q = threadIdx.x; q < nv; q += kLongT) {
         float uv[8], hv[8], w[8];
-        vector_values(u, q, a.d, load_vector(u, q, a.d), uv);
-        vector_values(h, q, a.d, load_vector(h, q, a.d), hv);
+        vector_values(q, a.d, load_vector(u, q, a.d), uv);
+        vector_values(q, a.d, load_vector(h, q, a.d), hv);
         weights_of(a, q, w);
         for (int i = 0; i < 8; ++i) {
             ss = __builtin_fma((double)hv[i], (double)hv[i], ss);
@@ -390,13 +422,13 @@ template <typename UT, typename HT> __global__ __launch_bounds__(kLongT) void no
     const float k = (float)((double)r * (double)r * (c * a.inv_d));
     if (threadIdx.x == 0)
         a.inv[m] = r;
-    for (int64_t q = threadIdx.x; q < nv; q += kLongT) {
+    for (int q = threadIdx.x; q < nv; q += kLongT) {
         float uv[8], hv[8], w[8], o[8] = {};
-        vector_values(u, q, a.d, load_vector(u, q, a.d), uv);
-        vector_values(h, q, a.d, load_vector(h, q, a.d), hv);
+        vector_values(q, a.d, load_vector(u, q, a.d), uv);
+        vector_values(q, a.d, load_vector(h, q, a.d), hv);
         weights_of(a, q, w);
         if (a.dres)
-            vector_values(res, q, a.d, load_vector(res, q, a.d), o);
+            vector_values(q, a.d, load_vector(res, q, a.d), o);
         for (int i = 0; i < 8; ++i)
             o[i] = __builtin_fmaf(r, __builtin_fmaf(-hv[i], k, uv[i] * w[i]), o[i]);
         store_vector((HT *)a.dh + m * a.ldd, q, a.d, o);
@@ -404,7 +436,8 @@ template <typename UT, typename HT> __global__ __launch_bounds__(kLongT) void no
 }
 template <typename UT, typename HT> __global__ __launch_bounds__(256) void weight_long_kernel(BackArgs a)
 {
-    const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x, nv = (a.d + 7) / 8, g = blockIdx.y;
+    const int q = (int)blockIdx.x * 256 + (int)threadIdx.x, nv = (a.d + 7) / 8;
+    const int64_t g = blockIdx.y;
     if (q >= nv)
         return;
     float dw[8] = {};
@@ -412,8 +445,8 @@ template <typename UT, typename HT> __global__ __launch_bounds__(256) void weigh
         float uv[8], hv[8];
         const UT *u = (const UT *)a.u + m * a.ldu;
         const HT *h = (const HT *)a.h + m * a.ldh;
-        vector_values(u, q, a.d, load_vector(u, q, a.d), uv);
-        vector_values(h, q, a.d, load_vector(h, q, a.d), hv);
+        vector_values(q, a.d, load_vector(u, q, a.d), uv);
+        vector_values(q, a.d, load_vector(h, q, a.d), hv);
         const float r = a.inv[m];
         for (int i = 0; i < 8; ++i)
             dw[i] = __builtin_fmaf(uv[i], hv[i] * r, dw[i]);
@@ -476,25 +509,25 @@ BackPlan plan_back(int64_t M, int64_t d)
     return p;
 }
 
-template <int T, int H, typename UT, typename HT> void launch_back(const BackArgs &a, hipStream_t st)
+template <int T, int H, bool kHold, bool kAhead, typename UT, typename HT> void launch_back(const BackArgs &a, hipStream_t st)
 {
-    hipLaunchKernelGGL((norm_back_kernel<T, H, UT, HT>), dim3((unsigned)a.groups), dim3(T > 256 ? T : 256), 0, st, a);
+    hipLaunchKernelGGL((norm_back_kernel<T, H, kHold, kAhead, UT, HT>), dim3((unsigned)a.groups), dim3(T > 256 ? T : 256), 0, st, a);
 }
 
 template <typename UT, typename HT> void run_back(const BackArgs &a, const BackPlan &p, float *dw, hipStream_t st)
 {
     if (p.T == 16)
-        launch_back<16, 1, UT, HT>(a, st);
+        launch_back<16, 1, true, true, UT, HT>(a, st);
     else if (p.T == 64)
-        launch_back<64, 1, UT, HT>(a, st);
+        launch_back<64, 1, true, true, UT, HT>(a, st);
     else if (p.T == 256 && p.H == 1)
-        launch_back<256, 1, UT, HT>(a, st);
+        launch_back<256, 1, true, true, UT, HT>(a, st);
     else if (p.T == 256 && p.H == 2)
-        launch_back<256, 2, UT, HT>(a, st);
+        launch_back<256, 2, true, true, UT, HT>(a, st);
     else if (p.T == 256)
-        launch_back<256, 4, UT, HT>(a, st);
+        launch_back<256, 4, false, false, UT, HT>(a, st);
     else if (p.T == 512)
-        launch_back<512, 4, UT, HT>(a, st);
+        launch_back<512, 4, false, false, UT, HT>(a, st);
     else {
         hipLaunchKernelGGL((norm_back_long_kernel<UT, HT>), dim3((unsigned)a.M), dim3(kLongT), 0, st, a);
         hipLaunchKernelGGL((weight_long_kernel<UT, HT>),
@@ -566,7 +599,7 @@ extern "C" archead_status archead_rms_norm(int64_t M, int64_t d, const void *x, 
         return api_fail(ARCHEAD_EINVAL, "in place, h needs the type and row stride of what it replaces");
     if (y && ((y == x && (y_type != x_type || ldy != ldx)) || y == h || y == residual))
         return api_fail(ARCHEAD_EINVAL, "y may be x, with its type and row stride, not h or residual");
-    const NormArgs a{M, d, ldx, ldr, ldh, ldy, ldq, lds, x, residual, weight, h, y, q, s, 1. / (double)d, eps, offset,
+    const NormArgs a{M, (int)d, ldx, ldr, ldh, ldy, ldq, lds, x, residual, weight, h, y, q, s, 1. / (double)d, eps, offset,
                      weight_type, y_type};
     hipStream_t stream = (hipStream_t)hip_stream;
     const bool xf = x_type == ARCHEAD_F32, rf = res_type == ARCHEAD_F32;
@@ -619,7 +652,7 @@ extern "C" archead_status archead_rms_norm_backward(int64_t M, int64_t d, const 
         return api_fail(ARCHEAD_EINVAL, "the workspace is smaller than archead_rms_norm_workspace asks for");
     if (M == 0 && !dweight)
         return ARCHEAD_OK;
-    const BackArgs a{M, d, ldy, ldh, ldr, ldd, dy, h, weight, dres, dh, (float *)ws, (float *)((char *)ws + p.inv),
+    const BackArgs a{M, (int)d, ldy, ldh, ldr, ldd, dy, h, weight, dres, dh, (float *)ws, (float *)((char *)ws + p.inv),
                      1. / (double)d, eps, offset, weight_type, p.groups, p.slice};
     hipStream_t stream = (hipStream_t)hip_stream;
     const bool uf = dy_type == ARCHEAD_F32, hf = h_type == ARCHEAD_F32;
