@@ -352,7 +352,8 @@ archead_status archead_quantize(const double *x, int64_t rows, int64_t cols, int
 /* Element types of the post-training entry points below. */
 typedef enum archead_type {
     ARCHEAD_F32 = 0,
-    ARCHEAD_BF16 = 1
+    ARCHEAD_BF16 = 1,
+    ARCHEAD_E4M3 = 2 /* 8-bit tables of archead_embed only */
 } archead_type;
 
 /*
@@ -618,6 +619,122 @@ archead_status archead_rms_norm_backward(int64_t M, int64_t d, const void *dy, i
                                          int h_type, int64_t ldh, const void *weight, int weight_type, float eps,
                                          float offset, const void *dres, int64_t ldr, void *dh, int64_t ldd,
                                          float *dweight, void *ws, uint64_t ws_bytes, void *hip_stream);
+
+/*
+ * archead_embed -- rows of an embedding table by token:
+ *   out[i, j] = scale * table[tokens[i], j], formed in fp32 and rounded once to out's type.
+ * The table may be an 8-bit head's own weights (a tied embedding): codes times
+ * their block's scale, as archead_fp8_quantize with block_rows = 128 leaves them.
+ * A token equal to pad gives a row of zeros (pad = -1 for none in the table);
+ * any other outside [0, V) a row of NaN; neither is an error.
+ *
+ * n        0 <= n <= 2^20 tokens (0 is a no-op that succeeds); 1 <= V < 2^31; 1 <= d <= 2^20.
+ * table    DEVICE V x d, ARCHEAD_F32, ARCHEAD_BF16 or ARCHEAD_E4M3 (table_type),
+ *          row stride ldt elements; 8-bit tables: d a multiple of 16, the table and
+ *          its stride of 16 bytes.
+ * scales   DEVICE fp32, scales[(token / 128) * lds + j / 128], lds >= ceil(d / 128),
+ *          for 8-bit tables; else unused.
+ * tokens   DEVICE int32 n.
+ * out      DEVICE n x d, fp32 or bf16 (out_type), row stride ldo.
+ * Strides lie in [row length, 2^40], scale is finite; streams as archead_rms_norm.
+ */
+archead_status archead_embed(int64_t n, int64_t V, int64_t d, const void *table, int table_type, int64_t ldt,
+                             const float *scales, int64_t lds, const int32_t *tokens, int32_t pad, float scale,
+                             void *out, int out_type, int64_t ldo, void *hip_stream);
+
+/*
+ * archead_embed_backward -- the table's gradient:
+ *   dtable[v, j] = scale * sum over i with tokens[i] = v of dout[i, j]
+ * Every row of the table is written, those of tokens that do not occur with
+ * zeros; or, with accumulate, the sums are added to the rows that do and no
+ * other is touched.  Tokens equal to pad or outside [0, V) add to no row; their
+ * rows of dout may hold anything.
+ *
+ * dout     DEVICE n x d, fp32 or bf16 (dout_type), row stride ldo.
+ * dtable   DEVICE V x d, fp32 or bf16 (grad_type), row stride ldt.
+ * ws       DEVICE workspace of archead_embed_workspace(n, V, d) bytes, 16-byte
+ *          aligned, contents irrelevant, the call's own until the stream has
+ *          passed it: calls, or captured graphs, that may overlap need one each.
+ * n ceil(d / 512) + V must lie below 2^26.  Other limits as archead_embed.
+ * Sums are fp32, their terms in the order of the tokens in groups of 32 (the error of
+ * n equal tokens grows with their logarithm), and rounded once with scale (and
+ * what they are added to); equal calls give equal bits.
+ * Enqueued, not waited for; nothing is allocated (graph capture is fine).
+ */
+archead_status archead_embed_workspace(int64_t n, int64_t V, int64_t d, uint64_t *bytes);
+archead_status archead_embed_backward(int64_t n, int64_t V, int64_t d, const void *dout, int dout_type, int64_t ldo,
+                                      const int32_t *tokens, int32_t pad, float scale, int accumulate, void *dtable,
+                                      int grad_type, int64_t ldt, void *ws, uint64_t ws_bytes, void *hip_stream);
+
+/*
+ * Logits as a request wants them, before a token is drawn: penalties for tokens
+ * that have occurred, biases and a grammar's mask.  For column v of row m,
+ *   y1 = y / repetition[m] for y > 0, y * repetition[m] otherwise, where v occurs in the history
+ *   y2 = (y1 - frequency[m] * count) - presence[m] where v occurs count > 0 times behind the prompt
+ *   y3 = y2 + the bias of v; a bias of -inf gives -inf whatever y2 is
+ *   y4 = -inf where the mask's bit v is clear, whatever y3 is
+ * each operation rounded to fp32 by itself.  Where a list does not name v, or is
+ * absent, its step is left out.
+ *
+ * Common to the two calls:
+ * logits     DEVICE M x V, fp32 or bf16 (type), row stride ld.  M <= 2^20, V < 2^31,
+ *            M ceil(V / 8192) < 2^24.
+ * history    DEVICE int32 M x L tokens, row stride ldh >= L, or NULL: row m's are its
+ *            first lengths[m] (DEVICE int32 M, or NULL for L), the first
+ *            prompt_lengths[m] of them (DEVICE int32 M, or NULL for 0) the prompt.
+ *            L <= 2^20; lengths outside [0, L] are taken as the nearest of the two, and
+ *            tokens outside [0, V) are not counted.
+ * repetition, frequency, presence   DEVICE fp32 M, or NULL for 1, 0 and 0.
+ * bias_ids, bias_values   DEVICE int32 and fp32 M x B, row stride ldb >= B, or 0 for
+ *            one list for all rows; or both NULL.  B <= 1023.  Ids outside [0, V) are
+ *            unused; of several entries with one id the last counts.
+ * mask       DEVICE R x ceil(V / 32) words, row stride ldm, or NULL: bit v % 32 of word v / 32
+ *            set lets v through.  Row m takes mask row mask_rows[m] (DEVICE int32 M),
+ *            none where that lies outside [0, R); or, with mask_rows NULL, row m
+ *            (R >= M).
+ * Strides lie below 2^40; buffers are aligned to their element.
+ * The current device must be the one the buffers and hip_stream belong to.
+ * Enqueued, not waited for; nothing is allocated, so the calls can be captured
+ * into a graph: replays read histories, lengths and masks as they are then.
+ */
+
+/* archead_adjust_logits -- y4 rounded once to the logits' type: out, DEVICE M x V, row
+ * stride ldo, every row written in full; it may be logits itself (same stride;
+ * columns that no rule names are then not written), otherwise it must not overlap them. */
+archead_status archead_adjust_logits(int64_t M, int64_t V, const void *logits, int type, int64_t ld,
+                                     const int32_t *history, int64_t L, int64_t ldh, const int32_t *lengths,
+                                     const int32_t *prompt_lengths, const float *repetition, const float *frequency,
+                                     const float *presence, const int32_t *bias_ids, const float *bias_values, int64_t B,
+                                     int64_t ldb, const uint32_t *mask, int64_t R, int64_t ldm, const int32_t *mask_rows,
+                                     void *out, int64_t ldo, void *hip_stream);
+
+/*
+ * archead_sample_logits -- the K largest of each row's y4 (in fp32, never written
+ * in full), in the order of archead_forward_topk, and one draw from them as
+ * archead_forward_sample's, with the weights exp((y4_j - y4_0) / temperature) in fp64.
+ *
+ * K             1 <= K <= min(16, V), else ARCHEAD_ESHAPE.
+ * temperature   finite and > 0, for all rows, unless temperatures (DEVICE fp32 M) is
+ *               given; rows whose own is not > 0 take their largest.
+ * u             DEVICE fp32 M in [0, 1), required with samples.
+ * values        DEVICE fp32 M x K, or NULL.  indices  DEVICE int32 M x K, or NULL.
+ * samples       DEVICE int32 M, or NULL; one of the three is required.  -1 for a row
+ *               with nothing left to draw (y4 all -inf) or a NaN.
+ * A NaN comes before all values in the order; -0 is +0.  +inf is drawn outright, the
+ * lowest index of several.
+ * ws            DEVICE workspace of archead_sample_workspace(M, V, K) bytes, 16-byte
+ *               aligned, contents irrelevant, the call's own until the stream has passed
+ *               it: calls, or captured graphs, that may overlap need one each.
+ */
+archead_status archead_sample_workspace(int64_t M, int64_t V, int32_t K, uint64_t *bytes);
+archead_status archead_sample_logits(int64_t M, int64_t V, const void *logits, int type, int64_t ld,
+                                     const int32_t *history, int64_t L, int64_t ldh, const int32_t *lengths,
+                                     const int32_t *prompt_lengths, const float *repetition, const float *frequency,
+                                     const float *presence, const int32_t *bias_ids, const float *bias_values, int64_t B,
+                                     int64_t ldb, const uint32_t *mask, int64_t R, int64_t ldm, const int32_t *mask_rows,
+                                     int32_t K, float temperature, const float *temperatures, const float *u,
+                                     float *values, int32_t *indices, int32_t *samples, void *ws, uint64_t ws_bytes,
+                                     void *hip_stream);
 
 /*
  * archead_packed_bytes -- eq 10 of the ARCHead paper: the sum over the

@@ -60,6 +60,18 @@ SIGNATURES = {
     "archead_rms_norm_backward": (ctypes.c_int, [_I64, _I64, _VP, ctypes.c_int, _I64, _VP, ctypes.c_int, _I64, _VP,
                                                  ctypes.c_int, ctypes.c_float, ctypes.c_float, _VP, _I64, _VP, _I64,
                                                  _VP, _VP, ctypes.c_uint64, _VP]),
+    "archead_embed": (ctypes.c_int, [_I64, _I64, _I64, _VP, ctypes.c_int, _I64, _VP, _I64, _VP, ctypes.c_int32,
+                                     ctypes.c_float, _VP, ctypes.c_int, _I64, _VP]),
+    "archead_embed_workspace": (ctypes.c_int, [_I64, _I64, _I64, ctypes.POINTER(ctypes.c_uint64)]),
+    "archead_embed_backward": (ctypes.c_int, [_I64, _I64, _I64, _VP, ctypes.c_int, _I64, _VP, ctypes.c_int32,
+                                              ctypes.c_float, ctypes.c_int, _VP, ctypes.c_int, _I64, _VP,
+                                              ctypes.c_uint64, _VP]),
+    "archead_adjust_logits": (ctypes.c_int, [_I64, _I64, _VP, ctypes.c_int, _I64, _VP, _I64, _I64] + [_VP] * 7 +
+                              [_I64, _I64, _VP, _I64, _I64, _VP, _VP, _I64, _VP]),
+    "archead_sample_workspace": (ctypes.c_int, [_I64, _I64, ctypes.c_int32, ctypes.POINTER(ctypes.c_uint64)]),
+    "archead_sample_logits": (ctypes.c_int, [_I64, _I64, _VP, ctypes.c_int, _I64, _VP, _I64, _I64] + [_VP] * 7 +
+                              [_I64, _I64, _VP, _I64, _I64, _VP, ctypes.c_int32, ctypes.c_float] + [_VP] * 6 +
+                              [ctypes.c_uint64, _VP]),
     "archead_reserve_backward": (ctypes.c_int, [_VP, _I64, _VP]),
     "archead_backward": (ctypes.c_int, [_VP, _I64, _VP, ctypes.c_int, _I64, _VP, _VP]),
     "archead_packed_bytes": (ctypes.c_int, [_VP, ctypes.POINTER(ctypes.c_uint64)]),

@@ -1,0 +1,662 @@
+// embed.hip -- rows of an embedding table by token, and the table's gradient.
+//
+//   out_i = scale * table[token_i]          (8-bit tables: code * its block's scale)
+//   dtable[v] = scale * sum over i with token_i = v of dout_i
+// Lookup: bound by the rows' bytes.  Gradient: bound by the table's, where all of it
+// is written, and then by dout's.  The tokens are sorted (stable, so that a row's
+// terms are always added in their order); what a row sums is then one run of the
+// sorted list.  Runs are of very different lengths (a few tokens hold much of a
+// text): each level of parts sums 32 neighbouring entries of the list where one
+// token holds them all, so that a run of any length ends in at most 62 entries of
+// each level.  Equal calls give equal bits.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <string>
+
+#include "api_internal.hpp"
+#include "archead.h"
+#include "elements.hpp"
+
+namespace archead {
+namespace {
+
+constexpr int kBlk = 128;                        // columns and rows that share a scale of an 8-bit table
+constexpr int64_t kMaxTokens = int64_t(1) << 20;
+constexpr int64_t kMaxWidth = int64_t(1) << 20;
+constexpr int64_t kMaxStride = int64_t(1) << 40;
+
+// ---------------------------------------------------------------------------
+// lookup
+// ---------------------------------------------------------------------------
+struct LookArgs {
+    int64_t n, V;
+    int d;
+    int64_t ldt, lds, ldo;
+    const void *table;
+    const float *scales;
+    const int32_t *tokens;
+    void *out;
+    float scale;
+    int32_t pad;
+};
+
+struct E4m3 {
+    uint8_t b;
+};
+template <typename T> struct Piece {
+    Eight<T> raw;
+    __device__ __forceinline__ void load(const LookArgs &a, int64_t row, int q)
+    {
+        raw = load_vector((const T *)a.table + row * a.ldt, q, a.d);
+    }
+    __device__ __forceinline__ void get(const LookArgs &a, int64_t row, int q, float v[8]) const
+    {
+        vector_values(q, a.d, raw, v);
+    }
+};
+template <> struct Piece<E4m3> { // d is a multiple of 16, rows 8-byte aligned
+    u32x2 raw;
+    float s;
+    __device__ __forceinline__ void load(const LookArgs &a, int64_t row, int q)
+    {
+        q = min(q, a.d / 8 - 1);
+        raw = *(const u32x2 *)((const uint8_t *)a.table + row * a.ldt + 8 * q);
+        s = a.scales[row / kBlk * a.lds + q / (kBlk / 8)];
+    }
+    __device__ __forceinline__ void get(const LookArgs &, int64_t, int, float v[8]) const
+    {
+        for (int i = 0; i < 2; ++i) {
+            const f32x2e lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)raw[i], false);
+            const f32x2e hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)raw[i], true);
+            v[4 * i] = lo[0] * s;
+            v[4 * i + 1] = lo[1] * s;
+            v[4 * i + 2] = hi[0] * s;
+            v[4 * i + 3] = hi[1] * s;
+        }
+    }
+};
+
+// T threads a token, U vectors of eight a thread; blockIdx.y walks a long row
+template <int T, int U, typename TT, typename OT> __global__ __launch_bounds__(256) void look_kernel(LookArgs a)
+{
+    const int64_t i = (int64_t)blockIdx.x * (256 / T) + threadIdx.x / T;
+    if (i >= a.n)
+        return;
+    const int nv = (a.d + 7) / 8, q0 = (int)blockIdx.y * (T * U) + (int)threadIdx.x % T;
+    const int32_t tok = a.tokens[i];
+    const bool held = tok >= 0 && tok < a.V && tok != a.pad;
+    const int64_t row = held ? tok : 0;
+    OT *out = (OT *)a.out + i * a.ldo;
+    Piece<TT> p[U];
+    if (held)
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            p[j].load(a, row, q0 + j * T);
+    const float none = tok == a.pad ? 0.f : __builtin_nanf("");
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+        const int q = q0 + j * T;
+        if (q >= nv)
+            break;
+        float v[8];
+        for (int e = 0; e < 8; ++e)
+            v[e] = none;
+        if (held) {
+            p[j].get(a, row, q, v);
+            for (int e = 0; e < 8; ++e)
+                v[e] *= a.scale;
+        }
+        store_vector(out, q, a.d, v);
+    }
+}
+
+template <int T, int U, typename TT, typename OT> void launch_look(const LookArgs &a, hipStream_t st)
+{
+    const int64_t nv = (a.d + 7) / 8;
+    hipLaunchKernelGGL((look_kernel<T, U, TT, OT>),
+                       dim3((unsigned)((a.n + 256 / T - 1) / (256 / T)), (unsigned)((nv + T * U - 1) / (T * U))),
+                       dim3(256), 0, st, a);
+}
+template <typename TT, typename OT> void run_look(const LookArgs &a, hipStream_t st)
+{
+    if (a.d <= 64)
+        launch_look<8, 1, TT, OT>(a, st);
+    else if (a.d <= 256 || a.n * (int64_t)a.d <= (int64_t(1) << 20))
+        launch_look<32, 1, TT, OT>(a, st);
+    else
+        launch_look<64, 4, TT, OT>(a, st);
+}
+template <typename TT> void run_look(const LookArgs &a, int out_type, hipStream_t st)
+{
+    if (out_type == ARCHEAD_F32)
+        run_look<TT, float>(a, st);
+    else
+        run_look<TT, uint16_t>(a, st);
+}
+
+// ---------------------------------------------------------------------------
+// sorting the tokens
+// ---------------------------------------------------------------------------
+struct Pair {
+    uint32_t key; // the token; the table's length for one that has no row
+    uint32_t at;  // its place among the tokens
+};
+
+__device__ __forceinline__ uint32_t key_of(int32_t tok, int64_t V, int32_t pad)
+{
+    return tok >= 0 && tok < V && tok != pad ? (uint32_t)tok : (uint32_t)V;
+}
+
+// Few tokens: each one's place is the number of tokens before it in (key, place)
+// order, counted outright: 64 tokens a workgroup, whose 16 waves take a part of
+// the list each.  n^2 / 39e12 comparisons and additions a second beside a launch's latency.
+__global__ __launch_bounds__(1024) void rank_kernel(const int32_t *tokens, int64_t n, int64_t V, int32_t pad,
+                                                    Pair *sorted, uint32_t *mark, int64_t words)
+{
+    __shared__ uint32_t meet[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t i = (int64_t)blockIdx.x * 64 + lane;
+    const uint32_t key = i < n ? key_of(tokens[i], V, pad) : 0xFFFFFFFFu;
+    const int64_t part = (n + 15) / 16, from = wave * part, to = min(from + part, n);
+    const int64_t first = (int64_t)blockIdx.x * 64;
+    uint32_t before = 0;
+    int64_t j = from;
+    for (const int64_t e = min(to, first); j < e; ++j) // all earlier ones: equal keys count
+        before += key_of(tokens[j], V, pad) <= key;
+    for (const int64_t e = min(to, first + 64); j < e; ++j) {
+        const uint32_t k = key_of(tokens[j], V, pad);
+        before += k < key || (k == key && j < i);
+    }
+    for (; j < to; ++j)
+        before += key_of(tokens[j], V, pad) < key;
+    meet[wave][lane] = before;
+    __syncthreads();
+    if (wave == 0 && i < n) {
+        for (int w = 1; w < 16; ++w)
+            before += meet[w][lane];
+        sorted[before] = Pair{key, (uint32_t)i};
+    }
+    // the rows' marks are cleared on the way
+    for (int64_t w = (int64_t)blockIdx.x * 1024 + threadIdx.x; w < words; w += (int64_t)gridDim.x * 1024)
+        mark[w] = 0;
+}
+
+// Many tokens: stable passes over kDigit bits of the key, tiles of kTile pairs.
+// Each workgroup counts its tile's digits, then every workgroup forms its own
+// places from all tiles' counts.
+constexpr int kDigit = 9, kDigits = 1 << kDigit, kTile = 2048, kSortT = 512, kPer = kTile / kSortT;
+
+struct SortArgs {
+    const int32_t *tokens; // first pass: the keys are theirs
+    const Pair *from;
+    Pair *to;
+    uint32_t *count; // [tiles][kDigits]
+    int64_t n, V;
+    int32_t pad;
+    int shift;
+    uint32_t *mark;
+    int64_t words;
+};
+__device__ __forceinline__ Pair sort_pair(const SortArgs &a, int64_t i)
+{
+    return a.from ? a.from[i] : Pair{key_of(a.tokens[i], a.V, a.pad), (uint32_t)i};
+}
+__device__ __forceinline__ int digit_of(const SortArgs &a, Pair p) { return (p.key >> a.shift) & (kDigits - 1); }
+
+__global__ __launch_bounds__(kSortT) void digit_count_kernel(SortArgs a)
+{
+    __shared__ uint32_t count[kDigits];
+    count[threadIdx.x] = 0;
+    __syncthreads();
+    for (int k = 0; k < kPer; ++k) {
+        const int64_t i = (int64_t)blockIdx.x * kTile + k * kSortT + threadIdx.x;
+        if (i < a.n)
+            atomicAdd(&count[digit_of(a, sort_pair(a, i))], 1u); // whole numbers: any order
+    }
+    __syncthreads();
+    a.count[(int64_t)blockIdx.x * kDigits + threadIdx.x] = count[threadIdx.x];
+    if (a.mark)
+        for (int64_t w = (int64_t)blockIdx.x * kSortT + threadIdx.x; w < a.words; w += (int64_t)gridDim.x * kSortT)
+            a.mark[w] = 0;
+}
+
+__global__ __launch_bounds__(kSortT) void digit_place_kernel(SortArgs a)
+{
+    constexpr int kWaves = kSortT / 64;
+    __shared__ uint32_t mine[kWaves][kDigits]; // a wave's counts, then where its next pair of a digit goes
+    __shared__ uint32_t sums[kWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, d = threadIdx.x; // one digit a thread
+    for (int w = 0; w < kWaves; ++w)
+        mine[w][d] = 0;
+    // all pairs of smaller digits, and the digit's in earlier tiles
+    uint32_t all = 0, earlier = 0;
+    for (int64_t t = 0; t < gridDim.x; ++t) {
+        const uint32_t c = a.count[t * kDigits + d];
+        all += c;
+        earlier += t < blockIdx.x ? c : 0;
+    }
+    uint32_t run = all;
+    for (int off = 1; off < 64; off <<= 1) {
+        const uint32_t o = __shfl_up(run, off);
+        run += lane >= off ? o : 0;
+    }
+    if (lane == 63)
+        sums[wave] = run;
+    __syncthreads();
+    uint32_t base = run - all + earlier;
+    for (int w = 0; w < wave; ++w)
+        base += sums[w];
+    // each wave takes kPer rounds of 64 consecutive pairs; a pair's rank in its
+    // wave is the count so far and the lanes before it with the same digit
+    Pair p[kPer];
+    uint32_t rank[kPer];
+    int dig[kPer];
+    for (int k = 0; k < kPer; ++k) {
+        const int64_t i = (int64_t)blockIdx.x * kTile + (wave * kPer + k) * 64 + lane;
+        const bool in = i < a.n;
+        p[k] = in ? sort_pair(a, i) : Pair{0, 0};
+        dig[k] = in ? digit_of(a, p[k]) : -1;
+        uint64_t same = __ballot(in);
+        for (int b = 0; b < kDigit; ++b) {
+            const uint64_t set = __ballot(dig[k] >> b & 1);
+            same &= dig[k] >> b & 1 ? set : ~set;
+        }
+        const uint32_t lower = (uint32_t)__popcll(same & ((uint64_t(1) << lane) - 1));
+        rank[k] = in ? mine[wave][dig[k]] + lower : 0;
+        __builtin_amdgcn_wave_barrier();
+        if (in && lower == 0)
+            mine[wave][dig[k]] += (uint32_t)__popcll(same);
+        __builtin_amdgcn_wave_barrier();
+    }
+    __syncthreads();
+    for (int w = 0; w < kWaves; ++w) {
+        const uint32_t c = mine[w][d];
+        mine[w][d] = base;
+        base += c;
+    }
+    __syncthreads();
+    for (int k = 0; k < kPer; ++k)
+        if (dig[k] >= 0)
+            a.to[mine[wave][dig[k]] + rank[k]] = p[k];
+}
+
+// ---------------------------------------------------------------------------
+// the rows' sums
+// ---------------------------------------------------------------------------
+constexpr int kGroup = 32;     // entries of the sorted list (or of a level) a part sums
+constexpr int kMaxLevels = 3;  // 32^3 tokens to a part of the last
+constexpr int kCols = 512;     // columns a wave takes: eight a lane
+
+struct GradArgs {
+    int64_t n, V;
+    int d;
+    int64_t ldo, ldt;
+    const void *dout;
+    const Pair *sorted;
+    uint32_t *mark;
+    float *part[kMaxLevels]; // [n / 32^(l+1)][d]
+    int levels;
+    void *dtable;
+    float scale;
+    int add;
+    int64_t tiles; // of kCols columns
+    int64_t heads; // waves of the sums, before those that clear rows
+};
+
+template <typename T> __device__ __forceinline__ void add_rows(const GradArgs &a, int64_t from, int64_t to, int q, float s[8])
+{
+    for (int64_t i = from; i < to; i += 4) { // four rows in flight; past the end the last again, not added
+        Eight<T> r[4];
+        const T *row[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            row[k] = (const T *)a.dout + (int64_t)a.sorted[min(i + k, to - 1)].at * a.ldo;
+            r[k] = load_vector(row[k], q, a.d);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i + k < to) {
+                float v[8];
+                vector_values(q, a.d, r[k], v);
+                for (int e = 0; e < 8; ++e)
+                    s[e] += v[e];
+            }
+    }
+}
+__device__ __forceinline__ void add_parts(const GradArgs &a, int level, int64_t from, int64_t to, int q, float s[8])
+{
+    for (int64_t i = from; i < to; i += 4) {
+        Eight<float> r[4];
+        const float *row[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            row[k] = a.part[level] + min(i + k, to - 1) * a.d;
+            r[k] = load_vector(row[k], q, a.d);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (i + k < to) {
+                float v[8];
+                vector_values(q, a.d, r[k], v);
+                for (int e = 0; e < 8; ++e)
+                    s[e] += v[e];
+            }
+    }
+}
+
+// a wave per part and kCols columns: parts whose entries are one token's
+template <typename T> __global__ __launch_bounds__(256) void part_kernel(GradArgs a, int level, int64_t parts)
+{
+    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), g = w / a.tiles;
+    if (level == 0) { // rows that occur, for the waves that clear the others
+        const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+        if (a.mark && i < a.n) {
+            const uint32_t k = a.sorted[i].key;
+            if (k < a.V && (i == 0 || a.sorted[i - 1].key != k))
+                atomicOr(&a.mark[k >> 5], 1u << (k & 31));
+        }
+    }
+    if (g >= parts)
+        return;
+    int64_t size = kGroup;
+    for (int l = 0; l < level; ++l)
+        size *= kGroup;
+    const uint32_t key = a.sorted[g * size].key;
+    if (key >= a.V || a.sorted[(g + 1) * size - 1].key != key)
+        return;
+    const int q = (int)(w % a.tiles) * (kCols / 8) + (int)(threadIdx.x & 63);
+    if (8 * q >= a.d)
+        return;
+    float s[8] = {};
+    if (level == 0)
+        add_rows<T>(a, g * kGroup, (g + 1) * kGroup, q, s);
+    else
+        add_parts(a, level - 1, g * kGroup, (g + 1) * kGroup, q, s);
+    store_vector(a.part[level] + g * a.d, q, a.d, s);
+}
+
+template <typename GT> __device__ __forceinline__ void put_row(const GradArgs &a, int64_t v, int q, const float s[8])
+{
+    GT *row = (GT *)a.dtable + v * a.ldt;
+    float o[8] = {};
+    if (a.add)
+        vector_values(q, a.d, load_vector(row, q, a.d), o);
+    for (int e = 0; e < 8; ++e)
+        o[e] = __builtin_fmaf(a.scale, s[e], o[e]);
+    store_vector(row, q, a.d, o);
+}
+
+// Waves first for the sums (one per entry of the sorted list that begins a run, and
+// kCols columns), then for clearing the rows that do not occur.
+template <typename T, typename GT> __global__ __launch_bounds__(256) void grad_kernel(GradArgs a)
+{
+    const int lane = threadIdx.x & 63;
+    int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (w >= a.heads) {
+        const int64_t v = w - a.heads;
+        // adding to rows there are no marks: these waves only fill the last workgroup
+        if (a.add || v >= a.V || (a.mark[v >> 5] >> (v & 31) & 1))
+            return;
+        const float none[8] = {};
+        for (int q = lane; 8 * q < a.d; q += 64)
+            store_vector((GT *)a.dtable + v * a.ldt, q, a.d, none);
+        return;
+    }
+    const int64_t i = w / a.tiles;
+    const int q = (int)(w % a.tiles) * (kCols / 8) + lane;
+    if (i >= a.n)
+        return;
+    const uint32_t key = a.sorted[i].key;
+    if (key >= a.V || (i > 0 && a.sorted[i - 1].key == key))
+        return;
+    // the run's end: 64 entries at a look, then by halves
+    int64_t end = a.n;
+    {
+        const int64_t look = i + 1 + lane;
+        const uint64_t other = __ballot(look >= a.n || a.sorted[min(look, a.n - 1)].key != key);
+        if (other)
+            end = i + 1 + __builtin_ctzll(other);
+        else {
+            int64_t lo = i + 65, hi = a.n; // entries below lo are the run's
+            while (lo < hi) {
+                const int64_t mid = (lo + hi) / 2;
+                if (a.sorted[mid].key == key)
+                    lo = mid + 1;
+                else
+                    hi = mid;
+            }
+            end = lo;
+        }
+    }
+    if (8 * q >= a.d)
+        return;
+    // entries up to the first whole part, parts up to the first whole part of the
+    // next level, and so on; then back down
+    float s[8] = {};
+    int64_t from = i, to = end;
+    int64_t tail_from[kMaxLevels + 1], tail_to[kMaxLevels + 1];
+    int top = 0;
+    for (int l = 0; l <= a.levels; ++l) {
+        const int64_t lo = (from + kGroup - 1) / kGroup, hi = to / kGroup;
+        top = l;
+        if (l == a.levels || lo >= hi) {
+            tail_from[l] = from;
+            tail_to[l] = to;
+            break;
+        }
+        if (l == 0)
+            add_rows<T>(a, from, lo * kGroup, q, s);
+        else
+            add_parts(a, l - 1, from, lo * kGroup, q, s);
+        tail_from[l] = hi * kGroup;
+        tail_to[l] = to;
+        from = lo;
+        to = hi;
+    }
+    for (int l = top; l >= 0; --l) {
+        if (l == 0)
+            add_rows<T>(a, tail_from[l], tail_to[l], q, s);
+        else
+            add_parts(a, l - 1, tail_from[l], tail_to[l], q, s);
+    }
+    put_row<GT>(a, key, q, s);
+}
+
+// where things lie in a gradient's workspace
+struct GradWs {
+    size_t sorted, other, count, mark, part[kMaxLevels], total;
+    int64_t parts[kMaxLevels], words, tiles;
+    int levels;
+};
+constexpr int64_t kRankMax = 16384; // tokens up to which places are counted outright
+
+size_t up16(size_t b) { return (b + 15) / 16 * 16; }
+GradWs grad_ws(int64_t n, int64_t V, int64_t d)
+{
+    GradWs w{};
+    w.tiles = (n + kTile - 1) / kTile;
+    w.words = (V + 31) / 32;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += up16(bytes);
+        return here;
+    };
+    w.sorted = take((size_t)n * sizeof(Pair));
+    if (n > kRankMax) {
+        w.other = take((size_t)n * sizeof(Pair));
+        w.count = take((size_t)w.tiles * kDigits * 4);
+    }
+    w.mark = take((size_t)w.words * 4);
+    for (int64_t m = n / kGroup; m > 0 && w.levels < kMaxLevels && (w.levels == 0 || m * kGroup > 64); m /= kGroup) {
+        w.parts[w.levels] = m;
+        w.part[w.levels++] = take((size_t)m * d * 4);
+    }
+    w.total = std::max<size_t>(16, at);
+    return w;
+}
+
+template <typename T> void run_parts(const GradArgs &a, const GradWs &w, hipStream_t st)
+{
+    for (int l = 0; l < w.levels; ++l) {
+        const int64_t waves = w.parts[l] * a.tiles, marks = l == 0 && a.mark ? (a.n + 255) / 256 : 0;
+        hipLaunchKernelGGL(part_kernel<T>, dim3((unsigned)std::max((waves + 3) / 4, marks)), dim3(256), 0, st, a, l,
+                           w.parts[l]);
+    }
+    if (w.levels == 0 && a.mark)
+        hipLaunchKernelGGL(part_kernel<T>, dim3(1), dim3(256), 0, st, a, 0, 0);
+}
+template <typename T> void run_grad(const GradArgs &a, const GradWs &w, int grad_type, hipStream_t st)
+{
+    run_parts<T>(a, w, st);
+    const int64_t waves = a.heads + (a.add ? 0 : a.V);
+    if (grad_type == ARCHEAD_F32)
+        hipLaunchKernelGGL((grad_kernel<T, float>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((grad_kernel<T, uint16_t>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, a);
+}
+
+bool bad_type(int t) { return t != ARCHEAD_F32 && t != ARCHEAD_BF16; }
+bool misaligned(const void *p, int t) { return (uintptr_t)p % (t == ARCHEAD_F32 ? 4 : 2) != 0; }
+
+archead_status launched(const char *what)
+{
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess)
+        return api_fail(ARCHEAD_EHIP, std::string(what) + ": " + hipGetErrorString(e));
+    return ARCHEAD_OK;
+}
+
+archead_status check_sizes(int64_t n, int64_t V, int64_t d)
+{
+    if (n < 0)
+        return api_fail(ARCHEAD_EINVAL, "n < 0");
+    if (n > kMaxTokens || V < 1 || V >= (int64_t(1) << 31) || d < 1 || d > kMaxWidth)
+        return api_fail(ARCHEAD_ESHAPE, "n <= 2^20, 1 <= V < 2^31 and 1 <= d <= 2^20");
+    return ARCHEAD_OK;
+}
+
+} // namespace
+} // namespace archead
+
+using namespace archead;
+
+extern "C" archead_status archead_embed(int64_t n, int64_t V, int64_t d, const void *table, int table_type, int64_t ldt,
+                                        const float *scales, int64_t lds, const int32_t *tokens, int32_t pad,
+                                        float scale, void *out, int out_type, int64_t ldo, void *hip_stream)
+{
+    archead_status st = check_sizes(n, V, d);
+    if (st != ARCHEAD_OK)
+        return st;
+    const bool f8 = table_type == ARCHEAD_E4M3;
+    if ((!f8 && bad_type(table_type)) || bad_type(out_type))
+        return api_fail(ARCHEAD_EINVAL, "table: ARCHEAD_F32, ARCHEAD_BF16 or ARCHEAD_E4M3; out: the former two");
+    if (f8 && d % 16 != 0)
+        return api_fail(ARCHEAD_ESHAPE, "an 8-bit table's d is a multiple of 16");
+    if (!std::isfinite(scale))
+        return api_fail(ARCHEAD_EINVAL, "scale must be finite");
+    if (ldt < d || ldt > kMaxStride || ldo < d || ldo > kMaxStride || (f8 && (lds < (d + kBlk - 1) / kBlk || lds > kMaxStride)))
+        return api_fail(ARCHEAD_EINVAL, "row strides must lie in [row length, 2^40]");
+    if (n == 0)
+        return ARCHEAD_OK;
+    if (!table || !tokens || !out || (f8 && !scales))
+        return api_fail(ARCHEAD_EINVAL, "table, tokens, out and an 8-bit table's scales are required");
+    if (f8 ? (uintptr_t)table % 16 || ldt % 16 || misaligned(scales, ARCHEAD_F32) : misaligned(table, table_type))
+        return api_fail(ARCHEAD_EINVAL, "table aligned to its element; 8-bit tables and their row strides to 16 bytes");
+    if (misaligned(out, out_type) || misaligned(tokens, ARCHEAD_F32))
+        return api_fail(ARCHEAD_EINVAL, "buffers must be aligned to their element");
+    const LookArgs a{n, V, (int)d, ldt, lds, ldo, table, scales, tokens, out, scale, pad};
+    hipStream_t stream = (hipStream_t)hip_stream;
+    if (f8)
+        run_look<E4m3>(a, out_type, stream);
+    else if (table_type == ARCHEAD_F32)
+        run_look<float>(a, out_type, stream);
+    else
+        run_look<uint16_t>(a, out_type, stream);
+    return launched("archead_embed");
+}
+
+extern "C" archead_status archead_embed_workspace(int64_t n, int64_t V, int64_t d, uint64_t *bytes)
+{
+    if (!bytes)
+        return api_fail(ARCHEAD_EINVAL, "bytes is NULL");
+    archead_status st = check_sizes(n, V, d);
+    if (st == ARCHEAD_OK)
+        *bytes = grad_ws(n, V, d).total;
+    return st;
+}
+
+extern "C" archead_status archead_embed_backward(int64_t n, int64_t V, int64_t d, const void *dout, int dout_type,
+                                                 int64_t ldo, const int32_t *tokens, int32_t pad, float scale,
+                                                 int accumulate, void *dtable, int grad_type, int64_t ldt, void *ws,
+                                                 uint64_t ws_bytes, void *hip_stream)
+{
+    archead_status st = check_sizes(n, V, d);
+    if (st != ARCHEAD_OK)
+        return st;
+    if (bad_type(dout_type) || bad_type(grad_type))
+        return api_fail(ARCHEAD_EINVAL, "types are ARCHEAD_F32 or ARCHEAD_BF16");
+    if (!std::isfinite(scale))
+        return api_fail(ARCHEAD_EINVAL, "scale must be finite");
+    if (ldo < d || ldo > kMaxStride || ldt < d || ldt > kMaxStride)
+        return api_fail(ARCHEAD_EINVAL, "row strides must lie in [d, 2^40]");
+    const GradWs w = grad_ws(n, V, d);
+    const int64_t tiles = (d + kCols - 1) / kCols;
+    // a launch holds fewer than 2^32 threads
+    if (n * tiles + V >= (int64_t(1) << 26))
+        return api_fail(ARCHEAD_ESHAPE, "n ceil(d / 512) + V must lie below 2^26");
+    if (!dtable || (n > 0 && (!dout || !tokens)))
+        return api_fail(ARCHEAD_EINVAL, "dout, tokens and dtable are required");
+    if (misaligned(dout, dout_type) || misaligned(dtable, grad_type) || misaligned(tokens, ARCHEAD_F32))
+        return api_fail(ARCHEAD_EINVAL, "buffers must be aligned to their element");
+    if (!ws || (uintptr_t)ws % 16)
+        return api_fail(ARCHEAD_EINVAL, "a 16-byte aligned workspace is required");
+    if (ws_bytes < w.total)
+        return api_fail(ARCHEAD_EINVAL, "the workspace is smaller than archead_embed_workspace asks for");
+    if (n == 0 && accumulate)
+        return ARCHEAD_OK;
+    char *base = (char *)ws;
+    hipStream_t stream = (hipStream_t)hip_stream;
+    GradArgs a{};
+    a.n = n;
+    a.V = V;
+    a.d = (int)d;
+    a.ldo = ldo;
+    a.ldt = ldt;
+    a.dout = dout;
+    a.sorted = (const Pair *)(base + w.sorted);
+    a.mark = accumulate ? nullptr : (uint32_t *)(base + w.mark);
+    for (int l = 0; l < w.levels; ++l)
+        a.part[l] = (float *)(base + w.part[l]);
+    a.levels = w.levels;
+    a.dtable = dtable;
+    a.scale = scale;
+    a.add = accumulate != 0;
+    a.tiles = tiles;
+    a.heads = n * tiles;
+    if (n <= kRankMax) {
+        hipLaunchKernelGGL(rank_kernel, dim3((unsigned)std::max<int64_t>(1, (n + 63) / 64)), dim3(1024), 0, stream, tokens, n,
+                           V, pad, (Pair *)(base + w.sorted), a.mark, a.mark ? w.words : 0);
+    } else {
+        int bits = 1;
+        while (bits < 32 && V >> bits)
+            ++bits;
+        const int passes = (bits + kDigit - 1) / kDigit;
+        SortArgs s{tokens, nullptr, nullptr, (uint32_t *)(base + w.count), n, V, pad, 0, a.mark, w.words};
+        for (int p = 0; p < passes; ++p) {
+            s.to = (Pair *)(base + ((passes - 1 - p) % 2 ? w.other : w.sorted));
+            s.shift = p * kDigit;
+            hipLaunchKernelGGL(digit_count_kernel, dim3((unsigned)w.tiles), dim3(kSortT), 0, stream, s);
+            hipLaunchKernelGGL(digit_place_kernel, dim3((unsigned)w.tiles), dim3(kSortT), 0, stream, s);
+            s.from = s.to;
+            s.mark = nullptr;
+        }
+    }
+    if (dout_type == ARCHEAD_F32)
+        run_grad<float>(a, w, grad_type, stream);
+    else
+        run_grad<uint16_t>(a, w, grad_type, stream);
+    return launched("archead_embed_backward");
+}

@@ -107,3 +107,13 @@ class Fp8Head:
         q, s = fp8_quantize(X, 1, stream=stream)
         y = fp8_matmul(q, s, self.weight, self.scales, out_dtype=out_dtype, out=out, stream=stream)
         return y
+
+    def forward_codes(self, codes, scales, out_dtype=None, out=None, stream=None):
+        """forward of hidden states that are already codes and scales (rms_norm's with want_codes)."""
+        return fp8_matmul(codes, scales, self.weight, self.scales, out_dtype=out_dtype, out=out, stream=stream)
+
+    def embed(self, tokens, scale: float = 1.0, pad: int = -1, out_dtype=None, out=None, stream=None):
+        """The head's rows as a tied embedding: scale * weight[tokens], n x d (bfloat16 by default)."""
+        from .embedding import embed
+        return embed(self.weight, tokens, scale=scale, pad=pad, out_dtype=out_dtype, out=out, scales=self.scales,
+                     stream=stream)
