@@ -656,9 +656,9 @@ archead_status archead_embed(int64_t n, int64_t V, int64_t d, const void *table,
  *          aligned, contents irrelevant, the call's own until the stream has
  *          passed it: calls, or captured graphs, that may overlap need one each.
  * n ceil(d / 512) + V must lie below 2^26.  Other limits as archead_embed.
- * Sums are fp32, their terms in the order of the tokens in groups of 32 (the error of
- * n equal tokens grows with their logarithm), and rounded once with scale (and
- * what they are added to); equal calls give equal bits.
+ * Sums are fp32, of groups of 32 terms in the order of the tokens and of such sums (a
+ * term passes through 400 additions at most), and rounded once with scale (and what
+ * they are added to); equal calls give equal bits.
  * Enqueued, not waited for; nothing is allocated (graph capture is fine).
  */
 archead_status archead_embed_workspace(int64_t n, int64_t V, int64_t d, uint64_t *bytes);
@@ -692,11 +692,16 @@ archead_status archead_embed_backward(int64_t n, int64_t V, int64_t d, const voi
  *            set lets v through.  Row m takes mask row mask_rows[m] (DEVICE int32 M),
  *            none where that lies outside [0, R); or, with mask_rows NULL, row m
  *            (R >= M).
+ * ws         DEVICE workspace of archead_rules_workspace(M, V, L, K) bytes (K = 0 for
+ *            archead_adjust_logits, L = 0 without a history), 16-byte aligned, contents
+ *            irrelevant, the call's own until the stream has passed it: calls, or
+ *            captured graphs, that may overlap need one each.  May be NULL for 0 bytes.
  * Strides lie below 2^40; buffers are aligned to their element.
  * The current device must be the one the buffers and hip_stream belong to.
  * Enqueued, not waited for; nothing is allocated, so the calls can be captured
  * into a graph: replays read histories, lengths and masks as they are then.
  */
+archead_status archead_rules_workspace(int64_t M, int64_t V, int64_t L, int32_t K, uint64_t *bytes);
 
 /* archead_adjust_logits -- y4 rounded once to the logits' type: out, DEVICE M x V, row
  * stride ldo, every row written in full; it may be logits itself (same stride;
@@ -706,7 +711,7 @@ archead_status archead_adjust_logits(int64_t M, int64_t V, const void *logits, i
                                      const int32_t *prompt_lengths, const float *repetition, const float *frequency,
                                      const float *presence, const int32_t *bias_ids, const float *bias_values, int64_t B,
                                      int64_t ldb, const uint32_t *mask, int64_t R, int64_t ldm, const int32_t *mask_rows,
-                                     void *out, int64_t ldo, void *hip_stream);
+                                     void *out, int64_t ldo, void *ws, uint64_t ws_bytes, void *hip_stream);
 
 /*
  * archead_sample_logits -- the K largest of each row's y4 (in fp32, never written
@@ -722,11 +727,7 @@ archead_status archead_adjust_logits(int64_t M, int64_t V, const void *logits, i
  *               with nothing left to draw (y4 all -inf) or a NaN.
  * A NaN comes before all values in the order; -0 is +0.  +inf is drawn outright, the
  * lowest index of several.
- * ws            DEVICE workspace of archead_sample_workspace(M, V, K) bytes, 16-byte
- *               aligned, contents irrelevant, the call's own until the stream has passed
- *               it: calls, or captured graphs, that may overlap need one each.
  */
-archead_status archead_sample_workspace(int64_t M, int64_t V, int32_t K, uint64_t *bytes);
 archead_status archead_sample_logits(int64_t M, int64_t V, const void *logits, int type, int64_t ld,
                                      const int32_t *history, int64_t L, int64_t ldh, const int32_t *lengths,
                                      const int32_t *prompt_lengths, const float *repetition, const float *frequency,

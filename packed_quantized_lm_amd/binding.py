@@ -67,8 +67,8 @@ SIGNATURES = {
                                               ctypes.c_float, ctypes.c_int, _VP, ctypes.c_int, _I64, _VP,
                                               ctypes.c_uint64, _VP]),
     "archead_adjust_logits": (ctypes.c_int, [_I64, _I64, _VP, ctypes.c_int, _I64, _VP, _I64, _I64] + [_VP] * 7 +
-                              [_I64, _I64, _VP, _I64, _I64, _VP, _VP, _I64, _VP]),
-    "archead_sample_workspace": (ctypes.c_int, [_I64, _I64, ctypes.c_int32, ctypes.POINTER(ctypes.c_uint64)]),
+                              [_I64, _I64, _VP, _I64, _I64, _VP, _VP, _I64, _VP, ctypes.c_uint64, _VP]),
+    "archead_rules_workspace": (ctypes.c_int, [_I64, _I64, _I64, ctypes.c_int32, ctypes.POINTER(ctypes.c_uint64)]),
     "archead_sample_logits": (ctypes.c_int, [_I64, _I64, _VP, ctypes.c_int, _I64, _VP, _I64, _I64] + [_VP] * 7 +
                               [_I64, _I64, _VP, _I64, _I64, _VP, ctypes.c_int32, ctypes.c_float] + [_VP] * 6 +
                               [ctypes.c_uint64, _VP]),

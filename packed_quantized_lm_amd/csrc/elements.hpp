@@ -81,9 +81,10 @@ __device__ __forceinline__ void set_element(Eight<uint16_t> &r, int i, uint16_t 
 // row's last eight where it has fewer or lies past the end.  No load is under a
 // branch of a lane's own, so that all of a thread's stay in flight together.  Int is
 // int where rows are short enough (an offset of 32 bits from a uniform base).
-template <typename T, typename Int> __device__ __forceinline__ Eight<T> load_vector(const T *row, Int q, Int d)
+template <bool kShort = true, typename T, typename Int>
+__device__ __forceinline__ Eight<T> load_vector(const T *row, Int q, Int d)
 {
-    if (d >= 8)
+    if (!kShort || d >= 8) // kShort: rows may be shorter than a vector
         return load_eight(row + min((Int)(8 * q), (Int)(d - 8)));
     Eight<T> r;
 #pragma unroll

@@ -150,36 +150,53 @@ __device__ __forceinline__ uint32_t key_of(int32_t tok, int64_t V, int32_t pad)
 }
 
 // Few tokens: each one's place is the number of tokens before it in (key, place)
-// order, counted outright: 64 tokens a workgroup, whose 16 waves take a part of
-// the list each.  n^2 / 39e12 comparisons and additions a second beside a launch's latency.
-__global__ __launch_bounds__(1024) void rank_kernel(const int32_t *tokens, int64_t n, int64_t V, int32_t pad,
-                                                    Pair *sorted, uint32_t *mark, int64_t words)
+// order, counted outright: n^2 / 64 comparisons of a wave.  A workgroup places kRank
+// tokens; its waves hold 64 kHold tokens of the list at a time in their lanes, and
+// compare them with one of the kRank after the other (in a scalar register): one vector
+// instruction for 64 pairs, the counting is scalar.
+constexpr int kRank = 32, kHold = 8, kRankT = 1024;
+__global__ __launch_bounds__(kRankT) void rank_kernel(const int32_t *tokens, int64_t n64, int64_t V, int32_t pad,
+                                                      Pair *sorted, uint32_t *mark, int64_t words)
 {
-    __shared__ uint32_t meet[16][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t i = (int64_t)blockIdx.x * 64 + lane;
-    const uint32_t key = i < n ? key_of(tokens[i], V, pad) : 0xFFFFFFFFu;
-    const int64_t part = (n + 15) / 16, from = wave * part, to = min(from + part, n);
-    const int64_t first = (int64_t)blockIdx.x * 64;
-    uint32_t before = 0;
-    int64_t j = from;
-    for (const int64_t e = min(to, first); j < e; ++j) // all earlier ones: equal keys count
-        before += key_of(tokens[j], V, pad) <= key;
-    for (const int64_t e = min(to, first + 64); j < e; ++j) {
-        const uint32_t k = key_of(tokens[j], V, pad);
-        before += k < key || (k == key && j < i);
+    __shared__ uint32_t meet[kRankT / 64][kRank];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = (int)n64;
+    const int first = (int)blockIdx.x * kRank, i = first + (lane & (kRank - 1));
+    const int own = i < n ? (int)key_of(tokens[i], V, pad) : 0; // keys fit 31 bits
+    uint32_t before = 0; // lane k's: of token first + k
+    for (int j0 = wave * 64 * kHold; j0 < n; j0 += kRankT * kHold) {
+        int key[kHold];
+#pragma unroll
+        for (int h = 0; h < kHold; ++h) { // tokens before the workgroup's own count also where keys are equal
+            const int j = j0 + 64 * h + lane;
+            const int k = (int)key_of(tokens[min(j, n - 1)], V, pad) - (j < first ? 1 : 0);
+            key[h] = j < n ? k : 0x7FFFFFFF;
+        }
+#pragma unroll 4
+        for (int k = 0; k < kRank; ++k) {
+            const int one = __builtin_amdgcn_readlane(own, k);
+            uint32_t c = 0;
+#pragma unroll
+            for (int h = 0; h < kHold; ++h)
+                c += __builtin_popcountll(__ballot(key[h] < one));
+            before = lane == k ? before + c : before;
+        }
     }
-    for (; j < to; ++j)
-        before += key_of(tokens[j], V, pad) < key;
-    meet[wave][lane] = before;
+    if (lane < kRank)
+        meet[wave][lane] = before;
     __syncthreads();
-    if (wave == 0 && i < n) {
-        for (int w = 1; w < 16; ++w)
-            before += meet[w][lane];
-        sorted[before] = Pair{key, (uint32_t)i};
+    if (wave == 0) {
+        uint32_t place = 0, ties = 0; // and equal ones before it among the own
+        for (int w = 0; w < kRankT / 64; ++w)
+            place += meet[w][lane & (kRank - 1)];
+        for (int k = 0; k < kRank; ++k) {
+            const int one = __builtin_amdgcn_readlane(own, k);
+            ties += one == own && k < lane;
+        }
+        if (lane < kRank && i < n)
+            sorted[place + ties] = Pair{(uint32_t)own, (uint32_t)i};
     }
     // the rows' marks are cleared on the way
-    for (int64_t w = (int64_t)blockIdx.x * 1024 + threadIdx.x; w < words; w += (int64_t)gridDim.x * 1024)
+    for (int64_t w = (int64_t)blockIdx.x * kRankT + threadIdx.x; w < words; w += (int64_t)gridDim.x * kRankT)
         mark[w] = 0;
 }
 
@@ -305,51 +322,44 @@ struct GradArgs {
     int64_t heads; // waves of the sums, before those that clear rows
 };
 
-template <typename T> __device__ __forceinline__ void add_rows(const GradArgs &a, int64_t from, int64_t to, int q, float s[8])
+// the sum of rows row(from) .. row(to - 1) at vector q onto s, kFly rows in flight;
+// past the end the last again, not added
+template <bool kShort, typename T, typename Row>
+__device__ __forceinline__ void add_rows(Row row, int64_t from, int64_t to, int q, int d, float s[8])
 {
-    for (int64_t i = from; i < to; i += 4) { // four rows in flight; past the end the last again, not added
-        Eight<T> r[4];
-        const T *row[4];
+    constexpr int kFly = sizeof(T) == 2 ? 8 : 6;
+    for (int64_t i = from; i < to; i += kFly) {
+        Eight<T> r[kFly];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            row[k] = (const T *)a.dout + (int64_t)a.sorted[min(i + k, to - 1)].at * a.ldo;
-            r[k] = load_vector(row[k], q, a.d);
-        }
+        for (int k = 0; k < kFly; ++k)
+            r[k] = load_vector<kShort>(row(min(i + k, to - 1)), q, d);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < kFly; ++k)
             if (i + k < to) {
                 float v[8];
-                vector_values(q, a.d, r[k], v);
+                vector_values(q, d, r[k], v);
                 for (int e = 0; e < 8; ++e)
                     s[e] += v[e];
             }
     }
 }
-__device__ __forceinline__ void add_parts(const GradArgs &a, int level, int64_t from, int64_t to, int q, float s[8])
+// entries [from, to) of the sorted list (level 0), or of the parts of a level below
+template <bool kShort, typename T>
+__device__ __forceinline__ void add_entries(const GradArgs &a, int level, int64_t from, int64_t to, int q, float s[8])
 {
-    for (int64_t i = from; i < to; i += 4) {
-        Eight<float> r[4];
-        const float *row[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            row[k] = a.part[level] + min(i + k, to - 1) * a.d;
-            r[k] = load_vector(row[k], q, a.d);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (i + k < to) {
-                float v[8];
-                vector_values(q, a.d, r[k], v);
-                for (int e = 0; e < 8; ++e)
-                    s[e] += v[e];
-            }
-    }
+    if (level == 0)
+        add_rows<kShort, T>([&](int64_t i) { return (const T *)a.dout + (int64_t)a.sorted[i].at * a.ldo; }, from, to, q, a.d, s);
+    else
+        add_rows<kShort, float>([&](int64_t i) { return a.part[level - 1] + i * a.d; }, from, to, q, a.d, s);
 }
 
-// a wave per part and kCols columns: parts whose entries are one token's
-template <typename T> __global__ __launch_bounds__(256) void part_kernel(GradArgs a, int level, int64_t parts)
+// A workgroup per part and kCols columns, for parts whose entries are one token's: its
+// four waves sum a quarter each, all of it in flight, and meet in LDS.
+template <bool kShort, typename T> __global__ __launch_bounds__(256) void part_kernel(GradArgs a, int level, int64_t parts)
 {
-    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), g = w / a.tiles;
+    __shared__ float meet[4][64][9]; // nine: neighbouring lanes in different banks
+    const int64_t g = blockIdx.x / a.tiles;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     if (level == 0) { // rows that occur, for the waves that clear the others
         const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
         if (a.mark && i < a.n) {
@@ -365,24 +375,28 @@ template <typename T> __global__ __launch_bounds__(256) void part_kernel(GradArg
         size *= kGroup;
     const uint32_t key = a.sorted[g * size].key;
     if (key >= a.V || a.sorted[(g + 1) * size - 1].key != key)
-        return;
-    const int q = (int)(w % a.tiles) * (kCols / 8) + (int)(threadIdx.x & 63);
-    if (8 * q >= a.d)
-        return;
+        return; // the whole workgroup
+    const int q = (int)(blockIdx.x % a.tiles) * (kCols / 8) + lane;
+    const int64_t from = g * kGroup + wave * (kGroup / 4);
     float s[8] = {};
-    if (level == 0)
-        add_rows<T>(a, g * kGroup, (g + 1) * kGroup, q, s);
-    else
-        add_parts(a, level - 1, g * kGroup, (g + 1) * kGroup, q, s);
-    store_vector(a.part[level] + g * a.d, q, a.d, s);
+    if (8 * q < a.d)
+        add_entries<kShort, T>(a, level, from, from + kGroup / 4, q, s);
+    for (int e = 0; e < 8; ++e)
+        meet[wave][lane][e] = s[e];
+    __syncthreads();
+    if (wave == 0 && 8 * q < a.d) {
+        for (int e = 0; e < 8; ++e)
+            s[e] = (meet[0][lane][e] + meet[1][lane][e]) + (meet[2][lane][e] + meet[3][lane][e]);
+        store_vector(a.part[level] + g * a.d, q, a.d, s);
+    }
 }
 
-template <typename GT> __device__ __forceinline__ void put_row(const GradArgs &a, int64_t v, int q, const float s[8])
+template <bool kShort, typename GT> __device__ __forceinline__ void put_row(const GradArgs &a, int64_t v, int q, const float s[8])
 {
     GT *row = (GT *)a.dtable + v * a.ldt;
     float o[8] = {};
     if (a.add)
-        vector_values(q, a.d, load_vector(row, q, a.d), o);
+        vector_values(q, a.d, load_vector<kShort>(row, q, a.d), o);
     for (int e = 0; e < 8; ++e)
         o[e] = __builtin_fmaf(a.scale, s[e], o[e]);
     store_vector(row, q, a.d, o);
@@ -390,10 +404,10 @@ template <typename GT> __device__ __forceinline__ void put_row(const GradArgs &a
 
 // Waves first for the sums (one per entry of the sorted list that begins a run, and
 // kCols columns), then for clearing the rows that do not occur.
-template <typename T, typename GT> __global__ __launch_bounds__(256) void grad_kernel(GradArgs a)
+template <bool kShort, typename T, typename GT> __global__ __launch_bounds__(256) void grad_kernel(GradArgs a)
 {
     const int lane = threadIdx.x & 63;
-    int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (w >= a.heads) {
         const int64_t v = w - a.heads;
         // adding to rows there are no marks: these waves only fill the last workgroup
@@ -446,22 +460,15 @@ template <typename T, typename GT> __global__ __launch_bounds__(256) void grad_k
             tail_to[l] = to;
             break;
         }
-        if (l == 0)
-            add_rows<T>(a, from, lo * kGroup, q, s);
-        else
-            add_parts(a, l - 1, from, lo * kGroup, q, s);
+        add_entries<kShort, T>(a, l, from, lo * kGroup, q, s);
         tail_from[l] = hi * kGroup;
         tail_to[l] = to;
         from = lo;
         to = hi;
     }
-    for (int l = top; l >= 0; --l) {
-        if (l == 0)
-            add_rows<T>(a, tail_from[l], tail_to[l], q, s);
-        else
-            add_parts(a, l - 1, tail_from[l], tail_to[l], q, s);
-    }
-    put_row<GT>(a, key, q, s);
+    for (int l = top; l >= 0; --l)
+        add_entries<kShort, T>(a, l, tail_from[l], tail_to[l], q, s);
+    put_row<kShort, GT>(a, key, q, s);
 }
 
 // where things lie in a gradient's workspace
@@ -470,6 +477,7 @@ struct GradWs {
     int64_t parts[kMaxLevels], words, tiles;
     int levels;
 };
+constexpr int64_t kFewParts = 256;  // of a level, that a run sums without another
 constexpr int64_t kRankMax = 16384; // tokens up to which places are counted outright
 
 size_t up16(size_t b) { return (b + 15) / 16 * 16; }
@@ -490,7 +498,7 @@ GradWs grad_ws(int64_t n, int64_t V, int64_t d)
         w.count = take((size_t)w.tiles * kDigits * 4);
     }
     w.mark = take((size_t)w.words * 4);
-    for (int64_t m = n / kGroup; m > 0 && w.levels < kMaxLevels && (w.levels == 0 || m * kGroup > 64); m /= kGroup) {
+    for (int64_t m = n / kGroup; m > 0 && w.levels < kMaxLevels && (w.levels == 0 || m * kGroup > kFewParts); m /= kGroup) {
         w.parts[w.levels] = m;
         w.part[w.levels++] = take((size_t)m * d * 4);
     }
@@ -498,24 +506,24 @@ GradWs grad_ws(int64_t n, int64_t V, int64_t d)
     return w;
 }
 
-template <typename T> void run_parts(const GradArgs &a, const GradWs &w, hipStream_t st)
+template <bool kShort, typename T> void run_grad(const GradArgs &a, const GradWs &w, int grad_type, hipStream_t st)
 {
     for (int l = 0; l < w.levels; ++l) {
-        const int64_t waves = w.parts[l] * a.tiles, marks = l == 0 && a.mark ? (a.n + 255) / 256 : 0;
-        hipLaunchKernelGGL(part_kernel<T>, dim3((unsigned)std::max((waves + 3) / 4, marks)), dim3(256), 0, st, a, l,
+        const int64_t groups = w.parts[l] * a.tiles, marks = l == 0 && a.mark ? (a.n + 255) / 256 : 0;
+        hipLaunchKernelGGL((part_kernel<kShort, T>), dim3((unsigned)std::max(groups, marks)), dim3(256), 0, st, a, l,
                            w.parts[l]);
     }
-    if (w.levels == 0 && a.mark)
-        hipLaunchKernelGGL(part_kernel<T>, dim3(1), dim3(256), 0, st, a, 0, 0);
+    if (w.levels == 0 && a.mark) // the marks alone
+        hipLaunchKernelGGL((part_kernel<kShort, T>), dim3(1), dim3(256), 0, st, a, 0, 0);
+    const int64_t waves = a.heads + (a.add ? 0 : a.V);
+    if (grad_type == ARCHEAD_F32)
+        hipLaunchKernelGGL((grad_kernel<kShort, T, float>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((grad_kernel<kShort, T, uint16_t>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, a);
 }
 template <typename T> void run_grad(const GradArgs &a, const GradWs &w, int grad_type, hipStream_t st)
 {
-    run_parts<T>(a, w, st);
-    const int64_t waves = a.heads + (a.add ? 0 : a.V);
-    if (grad_type == ARCHEAD_F32)
-        hipLaunchKernelGGL((grad_kernel<T, float>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, a);
-    else
-        hipLaunchKernelGGL((grad_kernel<T, uint16_t>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, a);
+    a.d < 8 ? run_grad<true, T>(a, w, grad_type, st) : run_grad<false, T>(a, w, grad_type, st);
 }
 
 bool bad_type(int t) { return t != ARCHEAD_F32 && t != ARCHEAD_BF16; }
@@ -637,7 +645,7 @@ extern "C" archead_status archead_embed_backward(int64_t n, int64_t V, int64_t d
     a.tiles = tiles;
     a.heads = n * tiles;
     if (n <= kRankMax) {
-        hipLaunchKernelGGL(rank_kernel, dim3((unsigned)std::max<int64_t>(1, (n + 63) / 64)), dim3(1024), 0, stream, tokens, n,
+        hipLaunchKernelGGL(rank_kernel, dim3((unsigned)std::max<int64_t>(1, (n + kRank - 1) / kRank)), dim3(kRankT), 0, stream, tokens, n,
                            V, pad, (Pair *)(base + w.sorted), a.mark, a.mark ? w.words : 0);
     } else {
         int bits = 1;

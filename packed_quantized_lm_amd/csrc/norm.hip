@@ -457,13 +457,21 @@ template <typename UT, typename HT> __global__ __launch_bounds__(256) void weigh
 // dw = the sum of the workgroups' parts: 32 columns a workgroup, 32 threads a column
 __global__ __launch_bounds__(1024) void weight_sum_kernel(const float *part, int64_t groups, int64_t d, float *dw)
 {
+    constexpr int kFly = 16;
     __shared__ double meet[32][33];
     const int col = threadIdx.x & 31, row = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + col;
     double s = 0.;
     if (c < d)
-        for (int64_t g = row; g < groups; g += 32)
-            s += (double)part[g * d + c];
+        for (int64_t g0 = row; g0 < groups; g0 += 32 * kFly) { // loads in flight together, past the end not added
+            float v[kFly];
+#pragma unroll
+            for (int k = 0; k < kFly; ++k)
+                v[k] = part[min(g0 + 32 * k, groups - 1) * d + c];
+#pragma unroll
+            for (int k = 0; k < kFly; ++k)
+                s += g0 + 32 * k < groups ? (double)v[k] : 0.;
+        }
     meet[row][col] = s;
     __syncthreads();
     if (row == 0 && c < d) {
@@ -479,7 +487,7 @@ struct BackPlan {
     int64_t groups, slice;
     size_t inv, total; // byte offsets in the workspace
 };
-constexpr int64_t kGroups = 1024; // workgroups that share the rows
+constexpr int64_t kGroups = 512;  // workgroups that share the rows
 constexpr int64_t kPartRows = 64; // rows whose terms of dw are added in fp32
 
 BackPlan plan_back(int64_t M, int64_t d)

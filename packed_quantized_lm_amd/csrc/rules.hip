@@ -31,6 +31,8 @@
 namespace archead {
 namespace {
 
+typedef int32_t i32x4u __attribute__((ext_vector_type(4), aligned(4)));
+
 constexpr int kNT = 256;
 constexpr int64_t kMaxRows = int64_t(1) << 20;
 constexpr int64_t kMaxHistory = int64_t(1) << 20;
@@ -52,8 +54,11 @@ struct RuleArgs {
     const uint32_t *mask;
     const int32_t *mask_rows;
     int K;
-    uint64_t *part; // [M][S][K] keys, 0 = none
+    uint64_t *part;       // [M][S][K] keys, 0 = none
+    uint16_t *routed;     // [M][L]: the history by slices (column within one, kRoutedPrompt), or null
+    uint32_t *ends;       // [M][S]: where each slice's tokens end
 };
+constexpr uint32_t kRoutedPrompt = 1u << 15;
 
 struct Row {
     float rho, beta, alpha;
@@ -87,153 +92,347 @@ __device__ __forceinline__ float value_of(uint64_t key)
     return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
 
-__device__ __forceinline__ uint64_t shfl_xor_key(uint64_t k, int off)
+// A bound that K of the wave's 64 values reach and no more, or, where values are
+// equal, the K-th largest of them (0 counts as none): by bits from the top, one
+// comparison a bit and scalar arithmetic, where sorting would take 21 exchanges
+// through LDS.
+__device__ __forceinline__ uint32_t wave_kth(uint32_t v, int K)
 {
-    return (uint64_t)(uint32_t)__shfl_xor((int)(k >> 32), off) << 32 | (uint32_t)__shfl_xor((int)(uint32_t)k, off);
+    uint32_t t = 0;
+#pragma unroll 1
+    for (uint32_t bit = 1u << 31; bit; bit >>= 1) {
+        const int reach = __builtin_popcountll(__ballot(v >= (t | bit)));
+        t = reach >= K ? t | bit : t;
+        if (reach == K)
+            break;
+    }
+    return t;
 }
 
-// the wave's keys in descending order over its lanes
-__device__ __forceinline__ uint64_t wave_sort(uint64_t k)
+// The K largest of a workgroup's keys, in order, written by best(rank, key).  A key
+// is order << 32 | place, 0 for none; key(thread, e), e < E, reads them from LDS, and
+// top is the largest order of the thread's own.  At most K lanes of a wave reach its
+// bound, so that a few lanes' keys are left to look through, by all threads.
+template <int NT, int E, typename Key, typename Best>
+__device__ __forceinline__ void block_top(int K, uint32_t top, Key key, Best best)
 {
-    const int lane = threadIdx.x & 63;
-    for (int size = 2; size <= 64; size <<= 1)
-        for (int off = size >> 1; off >= 1; off >>= 1) {
-            const uint64_t o = shfl_xor_key(k, off);
-            const bool keep_max = ((lane & off) == 0) == ((lane & size) == 0);
-            k = (k > o) == keep_max ? k : o;
-        }
-    return k;
-}
-
-// The K largest of the workgroup's keys (key(e), e < E, of each thread; 0 for
-// none), in order, written by best(rank, key); list holds 64 E keys.
-template <int E, typename Key, typename Best>
-__device__ __forceinline__ void block_top(int K, Key key, Best best, uint64_t *list)
-{
-    __shared__ uint64_t bounds[kNT / 64];
-    __shared__ uint32_t n_list;
-    uint64_t top = 0;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        top = umax64(top, key(e));
-    const uint64_t sorted = wave_sort(top);
-    if ((int)(threadIdx.x & 63) == K - 1)
-        bounds[threadIdx.x >> 6] = sorted;
-    if (threadIdx.x == 0)
-        n_list = 0;
-    __syncthreads(); // also: what list overlays has been read
-    const uint64_t bound = umax64(umax64(bounds[0], bounds[1]), umax64(bounds[2], bounds[3]));
-    if (top >= bound)
-#pragma unroll
+    constexpr int kList = 256; // at least NT / 64 K; more only where one lane holds many of the slice's largest
+    __shared__ uint64_t bounds[NT / 64];
+    __shared__ uint64_t list[kList];
+    __shared__ uint32_t n_list, n_lanes;
+    __shared__ uint32_t ranks[64];
+    __shared__ uint16_t lanes[NT];
+    const int tid = threadIdx.x;
+    auto first = [&](uint32_t t) { // the largest place of the thread's keys of order t
+        uint32_t place = 0;
+#pragma unroll 1
         for (int e = 0; e < E; ++e) {
-            const uint64_t k = key(e);
-            if (k >= bound && k != 0)
-                list[atomicAdd(&n_list, 1u)] = k; // in any order: keys are distinct and ranked below
+            const uint64_t k = key(tid, e);
+            place = (uint32_t)(k >> 32) == t ? max(place, (uint32_t)k) : place;
         }
+        return place;
+    };
+    const uint32_t t = wave_kth(top, K);
+    uint32_t low = 0;
+    if (t != 0 && __builtin_popcountll(__ballot(top >= t)) > K) // several lanes at the bound's value: by place
+        low = wave_kth(top == t ? first(t) : 0, K - __builtin_popcountll(__ballot(top > t)));
+    if ((tid & 63) == 0)
+        bounds[tid >> 6] = (uint64_t)t << 32 | low;
+    if (tid < 64)
+        ranks[tid] = 0;
+    if (tid == 0)
+        n_list = n_lanes = 0;
+    __syncthreads();
+    uint64_t bound = bounds[0];
+#pragma unroll
+    for (int w = 1; w < NT / 64; ++w)
+        bound = umax64(bound, bounds[w]);
+    const uint32_t least = (uint32_t)(bound >> 32);
+    if (top != 0 && top >= least && (top > least || (uint32_t)bound == 0 || first(least) >= (uint32_t)bound))
+        lanes[atomicAdd(&n_lanes, 1u)] = (uint16_t)tid;
+    __syncthreads();
+#pragma unroll 1
+    for (int i = tid; i < (int)n_lanes * E; i += NT) {
+        const uint64_t k = key(lanes[i / E], i % E);
+        if (k >= bound && k != 0) {
+            const uint32_t to = atomicAdd(&n_list, 1u); // in any order: keys are distinct and ranked below
+            if (to < kList)
+                list[to] = k;
+        }
+    }
     __syncthreads();
     const int n = (int)n_list;
-    for (int c = threadIdx.x; c < n; c += kNT) {
-        const uint64_t k = list[c];
+    if (n <= 64) { // a key's rank, counted by a thread of each wave
+        const int c = tid & 63, part = tid >> 6;
+        const uint64_t k = c < n ? list[c] : 0;
+        uint32_t rank = 0;
+        for (int j = part; j < n; j += NT / 64)
+            rank += list[j] > k;
+        if (c < n && rank)
+            atomicAdd(&ranks[c], rank);
+        __syncthreads();
+        if (part == 0 && c < n && ranks[c] < (uint32_t)K)
+            best((int)ranks[c], k);
+    } else if (n <= kList) {
+        const uint64_t k = tid < n ? list[tid] : 0;
         int rank = 0;
         for (int j = 0; j < n; ++j)
             rank += list[j] > k;
-        if (rank < K)
+        if (tid < n && rank < K)
             best(rank, k);
+    } else { // the largest below the last, K times
+        uint64_t last = ~(uint64_t)0;
+#pragma unroll 1
+        for (int rank = 0; rank < K; ++rank) {
+            uint64_t most = 0;
+#pragma unroll 1
+            for (int i = tid; i < (int)n_lanes * E; i += NT) {
+                const uint64_t k = key(lanes[i / E], i % E);
+                most = k < last ? umax64(most, k) : most;
+            }
+            for (int off = 32; off >= 1; off >>= 1)
+                most = umax64(most, shfl_xor_u64(most, off));
+            __syncthreads(); // bounds have been read
+            if ((tid & 63) == 0)
+                bounds[tid >> 6] = most;
+            __syncthreads();
+            last = bounds[0];
+            for (int w = 1; w < NT / 64; ++w)
+                last = umax64(last, bounds[w]);
+            if (tid == 0)
+                best(rank, last);
+        }
     }
-    for (int c = n + (int)threadIdx.x; c < K; c += kNT)
-        best(c, (uint64_t)0);
+    if (tid >= n && tid < K)
+        best(tid, (uint64_t)0);
 }
 
-// E columns a thread, in vectors of eight
-template <int E, typename T, bool kWrite, bool kSelect> __global__ __launch_bounds__(kNT) void rules_kernel(RuleArgs a)
-{
-    constexpr int kCols = kNT * E, kVecs = E / 8;
-    __shared__ alignas(16) uint32_t word[kCols];
-    const int64_t m = blockIdx.x / a.S, sl = blockIdx.x % a.S, base = sl * kCols, q0 = base / 8 + threadIdx.x;
-    const int cols = (int)min((int64_t)kCols, a.V - base);
-    const T *y = (const T *)a.y + m * a.ld;
-    Row r{a.repetition ? a.repetition[m] : 1.f, a.frequency ? a.frequency[m] : 0.f, a.presence ? a.presence[m] : 0.f,
-          a.bias_values ? a.bias_values + m * a.ldb : nullptr, nullptr};
-    if (a.mask) {
-        const int64_t at = a.mask_rows ? a.mask_rows[m] : m;
-        r.mask = at >= 0 && at < a.R ? a.mask + at * a.ldm : nullptr;
-    }
+// a column that rules name, once its logit is adjusted: its bits + 1, never 0
+__device__ __forceinline__ uint32_t settled(float x) { return (x != x ? 0x7FC00000u : __float_as_uint(x)) + 1u; }
+
+// One slice of a row, and what is on its way into registers for it: the first of
+// the row's history, then the logits and the mask's words, so that the history's
+// arrival does not wait for theirs.
+constexpr int kAhead = 4; // loads of four tokens in flight
+template <int NT, int E, typename T> struct Slice {
+    static constexpr int kCols = NT * E, kVecs = E / 8;
+    int64_t m, sl, base;
+    int cols, n, prompt; // columns; tokens of the history and of its prompt
+    uint32_t from, to;   // or the slice's own of a routed one
+    Row r;
+    const int32_t *h;
+    i32x4u tok[kAhead];
     Eight<T> raw[kVecs];
     uint32_t bits[kVecs];
+
+    // tokens [i0, i0 + 16 NT) of the history's first `most`, four a thread and load;
+    // their last four where there are fewer
+    __device__ __forceinline__ void tokens(int i0, int most)
+    {
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-        raw[j] = load_vector(y, q0 + j * kNT, a.V);
-        bits[j] = r.mask ? r.mask[min((q0 + j * kNT) >> 2, (a.V - 1) >> 5)] : 0xFFFFFFFFu;
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + (k * NT + (int)threadIdx.x) * 4;
+            tok[k] = most >= 4 ? *(const i32x4u *)(h + min(i, most - 4))
+                               : i32x4u{h[0], h[min(1, most - 1)], h[most - 1], -1};
+        }
     }
+    static __device__ __forceinline__ int same(int v) { return __builtin_amdgcn_readfirstlane(v); }
+    static __device__ __forceinline__ float same(float v) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v))); }
+    __device__ __forceinline__ void fetch(const RuleArgs &a, uint32_t at)
+    {
+        m = at / (uint32_t)a.S;
+        sl = at % (uint32_t)a.S;
+        base = sl * kCols;
+        cols = (int)min((int64_t)kCols, a.V - base);
+        const T *y = (const T *)a.y + m * a.ld;
+        const float rho = a.repetition ? a.repetition[m] : 1.f, beta = a.frequency ? a.frequency[m] : 0.f;
+        const float alpha = a.presence ? a.presence[m] : 0.f;
+        const int row = a.mask_rows ? a.mask_rows[m] : (int)m, len = a.lengths ? a.lengths[m] : (int)a.L;
+        const int head = a.prompts ? a.prompts[m] : 0;
+        n = 0;
+        if (a.routed) {
+            const uint32_t *e = a.ends + m * a.S + sl;
+            to = e[0];
+            from = sl ? e[-1] : 0;
+        } else if (a.history) {
+            h = a.history + m * a.ldh;
+            if (a.L > 0)
+                tokens(0, (int)a.L);
+        }
+        const int64_t q0 = base / 8 + threadIdx.x;
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j)
+            raw[j] = load_vector<E == 8>(y, q0 + j * NT, a.V);
+        if (a.history && !a.routed) {
+            n = max(0, min(same(len), (int)a.L));
+            prompt = same(head);
+        }
+        r = Row{same(rho), same(beta), same(alpha), a.bias_values ? a.bias_values + m * a.ldb : nullptr,
+                nullptr};
+        if (a.mask) {
+            const int64_t at_row = same(row);
+            r.mask = at_row >= 0 && at_row < a.R ? a.mask + at_row * a.ldm : nullptr;
+        }
+        if (r.mask)
+#pragma unroll
+            for (int j = 0; j < kVecs; ++j)
+                bits[j] = r.mask[min((q0 + j * NT) >> 2, (a.V - 1) >> 5)];
+    }
+};
+
+// E columns a thread, in vectors of eight
+template <int NT, int E, typename T, bool kSelect> __global__ __launch_bounds__(NT) void rules_kernel(RuleArgs a)
+{
+    constexpr int kCols = NT * E, kVecs = E / 8;
+    // Columns that rules name are listed as they are found and adjusted by a thread
+    // each: in place, every vector with such a column among its wave's 512 would pay
+    // for eight divisions.  A slice with more of them than the list holds does.
+    constexpr int kListed = kCols / 8;
+    __shared__ alignas(16) uint32_t word[kCols];
+    __shared__ uint16_t listed[kListed];
+    __shared__ uint32_t n_listed;
     const bool lists = a.history || a.bias_ids;
+    Slice<NT, E, T> s;
+    s.fetch(a, blockIdx.x);
+    const int64_t m = s.m, sl = s.sl, base = s.base, q0 = base / 8 + threadIdx.x;
+    const int cols = s.cols;
+    const T *y = (const T *)a.y + m * a.ld;
     if (lists) {
-        for (int c = threadIdx.x * 4; c < kCols; c += kNT * 4)
+        for (int c = threadIdx.x * 4; c < kCols; c += NT * 4)
             *(u32x4 *)&word[c] = u32x4{0, 0, 0, 0};
+        if (threadIdx.x == 0)
+            n_listed = 0;
         __syncthreads();
         if (a.bias_ids) {
             const int32_t *ids = a.bias_ids + m * a.ldb;
-            for (int64_t j = threadIdx.x; j < a.B; j += kNT) {
-                const int64_t c = (int64_t)ids[j] - base;
-                if (c >= 0 && c < cols)
-                    atomicMax(&word[c], (uint32_t)(j + 1) << kBiasAt); // the last entry of an id
+            for (int j = threadIdx.x; j < (int)a.B; j += NT) {
+                const uint32_t c = (uint32_t)ids[j] - (uint32_t)base;
+                if (c < (uint32_t)cols && atomicMax(&word[c], (uint32_t)(j + 1) << kBiasAt) == 0) {
+                    const uint32_t i = atomicAdd(&n_listed, 1u); // the first to name the column
+                    if (i < (uint32_t)kListed)
+                        listed[i] = (uint16_t)c;
+                }
             }
             __syncthreads();
         }
-        if (a.history) {
-            const int32_t *h = a.history + m * a.ldh;
-            const int64_t len = a.lengths ? max((int64_t)0, min((int64_t)a.lengths[m], a.L)) : a.L;
-            const int64_t prompt = a.prompts ? (int64_t)a.prompts[m] : 0;
-            for (int64_t i = threadIdx.x; i < len; i += kNT) {
-                const int64_t c = (int64_t)h[i] - base;
-                if (c >= 0 && c < cols) {
-                    if (i < prompt)
-                        atomicOr(&word[c], kPrompt);
-                    else
-                        atomicAdd(&word[c], 1u);
+        if (a.routed) {
+            const uint16_t *mine = a.routed + m * a.L;
+            for (uint32_t i = s.from + threadIdx.x; i < s.to; i += NT) {
+                const uint32_t t = mine[i], c = t & (kRoutedPrompt - 1);
+                if ((t & kRoutedPrompt ? atomicOr(&word[c], kPrompt) : atomicAdd(&word[c], 1u)) == 0) {
+                    const uint32_t at = atomicAdd(&n_listed, 1u);
+                    if (at < (uint32_t)kListed)
+                        listed[at] = (uint16_t)c;
+                }
+            }
+        }
+        for (int i0 = 0; i0 < s.n; i0 += NT * 4 * kAhead) {
+            if (i0 > 0)
+                s.tokens(i0, (int)a.L);
+            if (i0 + NT * 4 * kAhead > s.n) { // every token once
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const int i = i0 + (k * NT + (int)threadIdx.x) * 4, first = max(0, min(i, (int)a.L - 4));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s.tok[k][e] = first + e >= i && first + e < s.n ? s.tok[k][e] : -1;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = max(0, min(i0 + (k * NT + (int)threadIdx.x) * 4, (int)a.L - 4));
+                uint32_t before[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t c = (uint32_t)s.tok[k][e] - (uint32_t)base; // negative tokens stay above cols
+                    before[e] = 1;
+                    if (c < (uint32_t)cols)
+                        before[e] = i + e < s.prompt ? atomicOr(&word[c], kPrompt) : atomicAdd(&word[c], 1u);
+                }
+                uint32_t fresh = 0; // columns this thread is the first to name
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    fresh += before[e] == 0;
+                if (fresh) {
+                    uint32_t to = atomicAdd(&n_listed, fresh);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (before[e] == 0) {
+                            if (to < (uint32_t)kListed)
+                                listed[to] = (uint16_t)((uint32_t)s.tok[k][e] - (uint32_t)base);
+                            ++to;
+                        }
                 }
             }
         }
         __syncthreads();
+        if (n_listed <= (uint32_t)kListed) {
+            for (int i = threadIdx.x; i < (int)n_listed; i += NT) {
+                const int c = listed[i];
+                word[c] = settled(adjust(s.r, load_one(y + base + c), word[c]));
+            }
+            __syncthreads();
+        }
     }
-    uint32_t ord[kSelect ? E : 1];
+    const bool crowded = lists && n_listed > (uint32_t)kListed;
+    float most = -INFINITY; // NaN if any is
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-        const int64_t q = q0 + j * kNT;
+        const int64_t q = q0 + j * NT;
+        uint32_t *mine = &word[8 * (j * NT + threadIdx.x)];
         float v[8];
-        vector_values(q, a.V, raw[j], v);
+        widen(s.raw[j], v);
+        if (cols < kCols) // the row's last slice
+            keep_values(q, a.V, v);
         bool changed = false;
         if (lists) {
-            const u32x4 lo = *(const u32x4 *)&word[8 * (j * kNT + threadIdx.x)];
-            const u32x4 hi = *(const u32x4 *)&word[8 * (j * kNT + threadIdx.x) + 4];
-            if ((lo.x | lo.y | lo.z | lo.w | hi.x | hi.y | hi.z | hi.w) != 0) {
-                changed = true;
+            const u32x4 lo = *(const u32x4 *)mine, hi = *(const u32x4 *)(mine + 4);
+            changed = (lo.x | lo.y | lo.z | lo.w | hi.x | hi.y | hi.z | hi.w) != 0;
+            if (crowded) {
+                if (changed)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        v[i] = adjust(s.r, v[i], lo[i]);
+                        v[4 + i] = adjust(s.r, v[4 + i], hi[i]);
+                    }
+            } else
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    v[i] = adjust(r, v[i], lo[i]);
-                    v[4 + i] = adjust(r, v[4 + i], hi[i]);
+                    v[i] = lo[i] ? __uint_as_float(lo[i] - 1u) : v[i];
+                    v[4 + i] = hi[i] ? __uint_as_float(hi[i] - 1u) : v[4 + i];
                 }
+        }
+        if (s.r.mask) {
+            const uint32_t byte = s.bits[j] >> (8 * (q & 3));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t let = (uint32_t)__builtin_amdgcn_sbfe((int)byte, i, 1); // all ones or none
+                v[i] = __uint_as_float((__float_as_uint(v[i]) & let) | (0xFF800000u & ~let));
             }
         }
-        const uint32_t byte = bits[j] >> (8 * (q & 3)) & 0xFFu;
+        if constexpr (kSelect) {
+            if (cols < kCols)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = byte >> i & 1 ? v[i] : -INFINITY;
-        if (kWrite && 8 * q < a.V && (changed || r.mask || a.out != a.y))
-            store_vector((T *)a.out + m * a.ldo, q, a.V, v);
-        if constexpr (kSelect)
+                for (int i = 0; i < 8; ++i)
+                    v[i] = 8 * q + i < a.V ? v[i] : -INFINITY; // and no key
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                ord[8 * j + i] = 8 * q + i < a.V ? order_of(v[i]) : 0;
+                most = __builtin_elementwise_maximum(most, v[i]);
+            *(f32x4 *)mine = f32x4{v[0], v[1], v[2], v[3]}; // the adjusted logits in the words' place
+            *(f32x4 *)(mine + 4) = f32x4{v[4], v[5], v[6], v[7]};
+        } else if (8 * q < a.V && (changed || s.r.mask || a.out != a.y))
+            store_vector((T *)a.out + m * a.ldo, q, a.V, v);
     }
     if constexpr (kSelect) {
         uint64_t *part = a.part + (m * a.S + sl) * a.K;
-        block_top<E>(
-            a.K,
-            [&](int e) {
-                const uint32_t c = (uint32_t)(base + 8 * ((e >> 3) * kNT + threadIdx.x) + (e & 7));
-                return ord[e] ? (uint64_t)ord[e] << 32 | (0xFFFFFFFFu - c) : 0;
+        block_top<NT, E>(
+            a.K, 8 * (int)threadIdx.x < cols ? order_of(most) : 0u,
+            [&](int thread, int e) {
+                const int c = 8 * ((e >> 3) * NT + thread) + (e & 7);
+                return c < cols ? (uint64_t)order_of(__uint_as_float(word[c])) << 32 | ~((uint32_t)base + (uint32_t)c)
+                                : 0;
             },
-            [&](int rank, uint64_t k) { part[rank] = k; }, (uint64_t *)word);
+            [&](int rank, uint64_t k) { part[rank] = k; });
     }
 }
 
@@ -252,20 +451,28 @@ struct DrawArgs {
 constexpr int kPer = 8;
 __global__ __launch_bounds__(kNT) void draw_kernel(DrawArgs a)
 {
-    __shared__ uint64_t list[64 * (kPer + 1)];
+    __shared__ uint64_t keys[kPer + 1][kNT];
     __shared__ uint64_t win[kTopKMax];
     const int64_t m = blockIdx.x;
     const uint64_t *part = a.part + m * a.n;
     for (int64_t at = 0; at < a.n; at += kNT * kPer) {
         uint64_t k[kPer + 1];
+        k[0] = at > 0 && (int)threadIdx.x < a.K ? win[threadIdx.x] : 0; // the best so far
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
             const int64_t i = at + e * kNT + threadIdx.x;
-            k[e] = part[min(i, a.n - 1)];
-            k[e] = i < a.n ? k[e] : 0;
+            k[1 + e] = part[min(i, a.n - 1)];
+            k[1 + e] = i < a.n ? k[1 + e] : 0;
         }
-        k[kPer] = at > 0 && (int)threadIdx.x < a.K ? win[threadIdx.x] : 0; // the best so far
-        block_top<kPer + 1>(a.K, [&](int e) { return k[e]; }, [&](int rank, uint64_t key) { win[rank] = key; }, list);
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e <= kPer; ++e) {
+            top = max(top, (uint32_t)(k[e] >> 32));
+            keys[e][threadIdx.x] = k[e];
+        }
+        block_top<kNT, kPer + 1>(
+            a.K, top, [&](int thread, int e) { return keys[e][thread]; },
+            [&](int rank, uint64_t key) { win[rank] = key; });
         __syncthreads();
     }
     if (threadIdx.x >= 64)
@@ -301,11 +508,58 @@ __global__ __launch_bounds__(kNT) void draw_kernel(DrawArgs a)
         a.samples[m] = none ? -1 : drawn;
 }
 
-// columns a thread: the more, the fewer slices read a row's lists; fewer where
+// Long histories of many rows are first sorted by the slices they fall into: a slice's
+// workgroup then takes its own tokens in place of the whole list.  One row a
+// workgroup; the order within a slice is any, since its tokens are counted.
+constexpr int kRouteT = 1024;
+constexpr int64_t kRouteSlices = 1024;
+constexpr int64_t kRouteRows = 128, kRouteMin = 32768;
+__global__ __launch_bounds__(kRouteT) void route_kernel(RuleArgs a, int shift)
+{
+    __shared__ uint32_t count[kRouteSlices], wave_sums[kRouteT / 64];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int64_t m = blockIdx.x;
+    const int32_t *h = a.history + m * a.ldh;
+    const int n = a.lengths ? max(0, min(a.lengths[m], (int)a.L)) : (int)a.L, prompt = a.prompts ? a.prompts[m] : 0;
+    count[tid] = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (int i = tid; i < n; i += kRouteT) {
+        const uint32_t t = (uint32_t)h[i];
+        if (t < (uint32_t)a.V) // negative tokens are above it
+            atomicAdd(&count[t >> shift], 1u);
+    }
+    __syncthreads();
+    const uint32_t mine = count[tid];
+    uint32_t run = mine;
+    for (int off = 1; off < 64; off <<= 1) {
+        const uint32_t o = __shfl_up(run, off);
+        run += lane >= off ? o : 0;
+    }
+    if (lane == 63)
+        wave_sums[tid >> 6] = run;
+    __syncthreads();
+    for (int w = 0; w < tid >> 6; ++w)
+        run += wave_sums[w];
+    count[tid] = run - mine; // where the slice's next token goes
+    if (tid < a.S)
+        a.ends[m * a.S + tid] = run;
+    __syncthreads();
+    uint16_t *to = a.routed + m * a.L;
+#pragma unroll 4
+    for (int i = tid; i < n; i += kRouteT) {
+        const uint32_t t = (uint32_t)h[i];
+        if (t < (uint32_t)a.V)
+            to[atomicAdd(&count[t >> shift], 1u)] =
+                (uint16_t)((t & ((1u << shift) - 1)) | (i < prompt ? kRoutedPrompt : 0));
+    }
+}
+
+// columns a thread: the more, the fewer slices go through a row's lists; fewer where
 // that leaves compute units without a workgroup
 int columns_of(int64_t M, int64_t V)
 {
-    for (int e : {32, 16})
+    for (const int e : {32, 16})
         if (M * ((V + kNT * e - 1) / (kNT * e)) >= 1024)
             return e;
     return 8;
@@ -316,20 +570,56 @@ int64_t slices_of(int64_t M, int64_t V)
     return (V + c - 1) / c;
 }
 
+// where things lie in a workspace: the draw's keys, the routed history
+struct RuleWs {
+    int64_t S;
+    bool route;
+    size_t ends, routed, total;
+};
+RuleWs rule_ws(int64_t M, int64_t V, int64_t L, int K)
+{
+    RuleWs w{};
+    w.S = slices_of(M, V);
+    w.ends = (size_t)M * w.S * K * 8;
+    w.total = w.ends;
+    // a launch of a workgroup a row against every slice's own pass over the row's list: 256
+    // rows of 151936 with 2048 tokens 61 us routed, 64 not; 1024 tokens 59, 60; 8192
+    // 76, 91; 16 rows with 32768 tokens 53, 46
+    w.route = M >= kRouteRows && w.S <= kRouteSlices && w.S * L >= kRouteMin;
+    if (w.route) {
+        w.routed = w.ends + (size_t)M * w.S * 4;
+        w.total = w.routed + (size_t)M * L * 2;
+    }
+    return w;
+}
+constexpr int kShift[3] = {11, 12, 13}; // of a slice's columns
+
 template <int E, typename T> void launch_rules(const RuleArgs &a, hipStream_t st)
 {
     const dim3 grid((unsigned)(a.M * a.S));
     if (a.part)
-        hipLaunchKernelGGL((rules_kernel<E, T, false, true>), grid, dim3(kNT), 0, st, a);
+        hipLaunchKernelGGL((rules_kernel<kNT, E, T, true>), grid, dim3(kNT), 0, st, a);
     else
-        hipLaunchKernelGGL((rules_kernel<E, T, true, false>), grid, dim3(kNT), 0, st, a);
+        hipLaunchKernelGGL((rules_kernel<kNT, E, T, false>), grid, dim3(kNT), 0, st, a);
 }
 template <typename T> void run_rules(const RuleArgs &a, hipStream_t st)
 {
-    switch (columns_of(a.M, a.V)) {
+    const int e = columns_of(a.M, a.V);
+    if (a.routed)
+        hipLaunchKernelGGL(route_kernel, dim3((unsigned)a.M), dim3(kRouteT), 0, st, a, kShift[e / 16]);
+    switch (e) {
     case 32: return launch_rules<32, T>(a, st);
     case 16: return launch_rules<16, T>(a, st);
     default: return launch_rules<8, T>(a, st);
+    }
+}
+// the slices and the workspace's parts
+void lay_out(RuleArgs &a, const RuleWs &w, void *ws)
+{
+    a.S = w.S;
+    if (w.route && a.history) {
+        a.ends = (uint32_t *)((char *)ws + w.ends);
+        a.routed = (uint16_t *)((char *)ws + w.routed);
     }
 }
 
@@ -368,6 +658,15 @@ archead_status check_rules(const RuleArgs &a, int type)
                           (const void *)a.mask_rows})
         if (misaligned(p, 4))
             return api_fail(ARCHEAD_EINVAL, "buffers must be aligned to their element");
+    return ARCHEAD_OK;
+}
+
+archead_status check_ws(const RuleWs &w, const void *ws, uint64_t bytes)
+{
+    if (w.total && (!ws || misaligned(ws, 16)))
+        return api_fail(ARCHEAD_EINVAL, "a 16-byte aligned workspace is required");
+    if (bytes < w.total)
+        return api_fail(ARCHEAD_EINVAL, "the workspace is smaller than archead_rules_workspace asks for");
     return ARCHEAD_OK;
 }
 
@@ -419,7 +718,7 @@ extern "C" archead_status archead_adjust_logits(int64_t M, int64_t V, const void
                                                 const float *frequency, const float *presence, const int32_t *bias_ids,
                                                 const float *bias_values, int64_t B, int64_t ldb, const uint32_t *mask,
                                                 int64_t R, int64_t ldm, const int32_t *mask_rows, void *out, int64_t ldo,
-                                                void *hip_stream)
+                                                void *ws, uint64_t ws_bytes, void *hip_stream)
 {
     RuleArgs a = rule_args(M, V, logits, ld, history, L, ldh, lengths, prompt_lengths, repetition, frequency, presence,
                            bias_ids, bias_values, B, ldb, mask, R, ldm, mask_rows);
@@ -434,11 +733,13 @@ extern "C" archead_status archead_adjust_logits(int64_t M, int64_t V, const void
         return api_fail(ARCHEAD_EINVAL, "in place, out needs the logits' row stride");
     if (misaligned(out, type == ARCHEAD_F32 ? 4 : 2))
         return api_fail(ARCHEAD_EINVAL, "out must be aligned to its element");
-    if (M == 0)
-        return ARCHEAD_OK;
+    const RuleWs w = rule_ws(M, V, L, 0);
+    s = check_ws(w, ws, ws_bytes);
+    if (s != ARCHEAD_OK || M == 0)
+        return s;
     a.out = out;
     a.ldo = ldo;
-    a.S = slices_of(M, V);
+    lay_out(a, w, ws);
     if (type == ARCHEAD_F32)
         run_rules<float>(a, (hipStream_t)hip_stream);
     else
@@ -446,15 +747,15 @@ extern "C" archead_status archead_adjust_logits(int64_t M, int64_t V, const void
     return launched("archead_adjust_logits");
 }
 
-extern "C" archead_status archead_sample_workspace(int64_t M, int64_t V, int32_t K, uint64_t *bytes)
+extern "C" archead_status archead_rules_workspace(int64_t M, int64_t V, int64_t L, int32_t K, uint64_t *bytes)
 {
     if (!bytes)
         return api_fail(ARCHEAD_EINVAL, "bytes is NULL");
-    if (M < 0)
-        return api_fail(ARCHEAD_EINVAL, "M < 0");
-    if (M > kMaxRows || V < 1 || V >= (int64_t(1) << 31) || K < 1 || K > kTopKMax || K > V)
-        return api_fail(ARCHEAD_ESHAPE, "M <= 2^20, 1 <= V < 2^31 and 1 <= K <= min(16, V)");
-    *bytes = std::max<uint64_t>(16, (uint64_t)M * slices_of(M, V) * K * 8);
+    if (M < 0 || L < 0)
+        return api_fail(ARCHEAD_EINVAL, "M < 0 or L < 0");
+    if (M > kMaxRows || V < 1 || V >= (int64_t(1) << 31) || L > kMaxHistory || K < 0 || K > kTopKMax || K > V)
+        return api_fail(ARCHEAD_ESHAPE, "M, L <= 2^20, 1 <= V < 2^31 and 0 <= K <= min(16, V)");
+    *bytes = rule_ws(M, V, L, K).total;
     return ARCHEAD_OK;
 }
 
@@ -485,15 +786,13 @@ extern "C" archead_status archead_sample_logits(int64_t M, int64_t V, const void
                           (const void *)samples})
         if (misaligned(p, 4))
             return api_fail(ARCHEAD_EINVAL, "buffers must be aligned to their element");
-    if (!ws || misaligned(ws, 16))
-        return api_fail(ARCHEAD_EINVAL, "a 16-byte aligned workspace is required");
-    a.S = slices_of(M, V);
-    if (ws_bytes < (uint64_t)M * a.S * K * 8)
-        return api_fail(ARCHEAD_EINVAL, "the workspace is smaller than archead_sample_workspace asks for");
-    if (M == 0)
-        return ARCHEAD_OK;
+    const RuleWs w = rule_ws(M, V, L, K);
+    s = check_ws(w, ws, ws_bytes);
+    if (s != ARCHEAD_OK || M == 0)
+        return s;
     a.K = K;
     a.part = (uint64_t *)ws;
+    lay_out(a, w, ws);
     hipStream_t st = (hipStream_t)hip_stream;
     if (type == ARCHEAD_F32)
         run_rules<float>(a, st);

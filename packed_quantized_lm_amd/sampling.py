@@ -18,7 +18,7 @@ def _rows_of(t, name, dtype, M, n, dev):
 
 def _rules(logits, history, lengths, prompt_lengths, repetition, frequency, presence, bias_ids, bias_values, mask,
            mask_rows):
-    """Checks everything the two calls share; (M, V, type, the C arguments from logits to mask_rows)."""
+    """Checks everything the two calls share; (M, V, L, the C arguments from logits to mask_rows)."""
     import torch
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or logits.shape[1] < 1:
         raise ValueError("logits must be an M x V tensor")
@@ -66,9 +66,17 @@ def _rules(logits, history, lengths, prompt_lengths, repetition, frequency, pres
         raise ValueError("mask_rows belong to a mask")
     if L == 0:
         history = lengths = prompt_lengths = None
-    return M, V, code, (M, V, ptr(logits), code, ld, ptr(history), L, ldh, ptr(lengths), ptr(prompt_lengths),
+    return M, V, L, (M, V, ptr(logits), code, ld, ptr(history), L, ldh, ptr(lengths), ptr(prompt_lengths),
                         ptr(repetition), ptr(frequency), ptr(presence), ptr(bias_ids), ptr(bias_values), B, ldb,
                         ptr(mask), R, ldm, ptr(mask_rows))
+
+
+def _workspace(M, V, L, K, dev):
+    """The calls' workspace and its size; none where nothing is needed."""
+    import torch
+    n = ctypes.c_uint64()
+    _check(load_library().archead_rules_workspace(M, V, L, K, ctypes.byref(n)), "archead_rules_workspace")
+    return (torch.empty(n.value, dtype=torch.uint8, device=dev) if n.value else None), n.value
 
 
 def adjust_logits(logits, history=None, lengths=None, prompt_lengths=None, repetition=None, frequency=None,
@@ -83,13 +91,14 @@ def adjust_logits(logits, history=None, lengths=None, prompt_lengths=None, repet
     - mask, int32 R x ceil(V / 32) bits of the tokens a grammar allows, row
       mask_rows[m] (int32 M; -1 for none) or row m: all others become -inf."""
     import torch
-    M, V, code, args = _rules(logits, history, lengths, prompt_lengths, repetition, frequency, presence, bias_ids,
+    M, V, L, args = _rules(logits, history, lengths, prompt_lengths, repetition, frequency, presence, bias_ids,
                               bias_values, mask, mask_rows)
     ldo = V if out is None else need_rows(out, "out", (logits.dtype,), (M, V), logits.device)
 
     def call(st):
         y = torch.empty((M, V), dtype=logits.dtype, device=logits.device) if out is None else out
-        _check(load_library().archead_adjust_logits(*args, ptr(y), ldo, st), "archead_adjust_logits")
+        ws, n = _workspace(M, V, L, 0, logits.device)
+        _check(load_library().archead_adjust_logits(*args, ptr(y), ldo, ptr(ws), n, st), "archead_adjust_logits")
         return y
     return on_stream(logits.device, stream, call)
 
@@ -102,7 +111,7 @@ def sample_logits(logits, K: int, u=None, temperature=1.0, history=None, lengths
     in [0, 1)) a draw from them at the temperature (a number, or fp32 M; rows whose
     own is not positive take their largest).  A row whose rules leave nothing draws -1."""
     import torch
-    M, V, code, args = _rules(logits, history, lengths, prompt_lengths, repetition, frequency, presence, bias_ids,
+    M, V, L, args = _rules(logits, history, lengths, prompt_lengths, repetition, frequency, presence, bias_ids,
                               bias_values, mask, mask_rows)
     dev, K = logits.device, int(K)
     if not 1 <= K <= min(16, V):
@@ -117,14 +126,11 @@ def sample_logits(logits, K: int, u=None, temperature=1.0, history=None, lengths
         tau = float(temperature)
 
     def call(st):
-        lib = load_library()
         values = torch.empty((M, K), dtype=torch.float32, device=dev)
         indices = torch.empty((M, K), dtype=torch.int32, device=dev)
         samples = None if u is None else torch.empty(M, dtype=torch.int32, device=dev)
-        n = ctypes.c_uint64()
-        _check(lib.archead_sample_workspace(M, V, K, ctypes.byref(n)), "archead_sample_workspace")
-        ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
-        _check(lib.archead_sample_logits(*args, K, tau, ptr(taus), ptr(u), ptr(values), ptr(indices), ptr(samples),
-                                         ptr(ws), n.value, st), "archead_sample_logits")
+        ws, n = _workspace(M, V, L, K, dev)
+        _check(load_library().archead_sample_logits(*args, K, tau, ptr(taus), ptr(u), ptr(values), ptr(indices),
+                                                    ptr(samples), ptr(ws), n, st), "archead_sample_logits")
         return values, indices, samples
     return on_stream(dev, stream, call)

@@ -96,7 +96,8 @@ def _same(got, want, what):
 
 
 SHAPES = [(1, 1, 1, 1), (2, 7, 5, 3), (3, 8, 40, 8), (1, 33, 9, 2), (5, 1000, 300, 40), (2, 2048, 64, 5), (3, 2049, 2000, 20),
-          (1, 50021, 700, 1023), (2, 16390, 5000, 64), (130, 40000, 50, 7), (600, 9000, 33, 3), (1030, 300, 20, 5)]
+          (1, 50021, 700, 1023), (2, 16390, 5000, 64), (130, 40000, 50, 7), (600, 9000, 33, 3), (1030, 300, 20, 5),
+          (130, 40000, 8000, 7), (300, 30000, 9000, 4), (130, 20000, 4000, 9)]  # the last three: histories sorted by slices first
 
 
 @pytest.mark.parametrize("type", ["f32", "bf16"])
@@ -134,21 +135,21 @@ def test_each_rule_alone_and_every_k(pq, rules_of):
 
 @pytest.mark.parametrize("V", [5000, 300000])
 def test_ties_sorted_and_equal_rows(pq, V):
-    """Orders that are hard on a bound: all equal, few values, rising, falling, one workgroup's or one thread's best."""
+    """Orders that are hard on a bound: all equal, few values, rising, falling, one workgroup's, one thread's or fifteen threads' best."""
     rng = np.random.default_rng(V)
     y = np.stack([np.zeros(V), np.full(V, -INF), rng.integers(0, 3, V), np.arange(V), -np.arange(V),
                   np.where(np.arange(V) // 8 % 256 == 7, 5.0, 0.0), np.where(np.arange(V) < V - 9, -INF, 1.0),
-                  rng.permutation(V)]).astype(np.float32)
+                  rng.permutation(V), np.where(np.arange(V) // 8 % 256 < 15, rng.permutation(V), -1)]).astype(np.float32)
     y[0, 3] = -0.0
-    for M in (1, 8, 512):
-        rows = np.arange(M) % 8
+    for M in (1, 9, 512):
+        rows = np.arange(M) % 9
         t = _cuda(y)[_cuda(rows)].contiguous()
         values, ids, samples = pq.sample_logits(t, 16, u=_cuda(np.full(M, 0.999, dtype=np.float32)), temperature=0.7)
-        for m in range(min(M, 16)):
+        for m in range(min(M, 18)):
             v, i = rules.top(y[rows[m]], 16)
             assert np.array_equal(ids[m].cpu().numpy(), i), (M, m)
             assert np.array_equal(values[m].cpu().numpy(), v)
-            if m in (1, 9):
+            if m in (1, 10):
                 assert int(samples[m]) == -1
 
 

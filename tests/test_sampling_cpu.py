@@ -28,7 +28,8 @@ def _common(over):
 
 
 def _adjust(lib, over):
-    return lib.archead_adjust_logits(*_common(over), over.get("out", C), over.get("ldo", 40), None)
+    return lib.archead_adjust_logits(*_common(over), over.get("out", C), over.get("ldo", 40), over.get("ws", B),
+                                     over.get("n", 1 << 40), None)
 
 
 def _sample(lib, over):
@@ -52,7 +53,9 @@ BAD = [
 
 @pytest.mark.parametrize("over,status", BAD + [
     (dict(out=None), binding.EINVAL), (dict(out=ODD), binding.EINVAL), (dict(ldo=39), binding.EINVAL),
-    (dict(out=B, ldo=41), binding.EINVAL)])
+    (dict(out=B, ldo=41), binding.EINVAL),
+    (dict(M=1 << 10, V=1 << 14, ld=1 << 14, ldm=512, R=1 << 10, L=8192, ldh=8192, ldo=1 << 14, n=1 << 20), binding.EINVAL),
+    (dict(M=1 << 10, V=1 << 14, ld=1 << 14, ldm=512, R=1 << 10, L=8192, ldh=8192, ldo=1 << 14, ws=None), binding.EINVAL)])
 def test_adjust_refusals(lib, over, status):
     assert _adjust(lib, over) == status
     assert lib.archead_last_error().decode()
@@ -76,13 +79,16 @@ def test_no_rows_is_no_work(lib):
 
 def test_workspace_sizes(lib):
     n = ctypes.c_uint64()
-    assert lib.archead_sample_workspace(1, 1, 1, ctypes.byref(n)) == binding.OK and n.value >= 16
-    for M, V, K in ((1, 151936, 16), (256, 151936, 16), (1 << 20, 17, 1), (1, (1 << 31) - 1, 16)):
-        assert lib.archead_sample_workspace(M, V, K, ctypes.byref(n)) == binding.OK
-        assert M * K * 8 <= n.value <= M * K * 8 * (-(-V // 2048))
-    for M, V, K, status in ((-1, 8, 1, binding.EINVAL), (1, 0, 1, binding.ESHAPE), (1, 8, 9, binding.ESHAPE)):
-        assert lib.archead_sample_workspace(M, V, K, ctypes.byref(n)) == status
-    assert lib.archead_sample_workspace(1, 1, 1, None) == binding.EINVAL
+    assert lib.archead_rules_workspace(1, 151936, 300, 0, ctypes.byref(n)) == binding.OK and n.value == 0
+    for M, V, L, K in ((1, 1, 0, 1), (1, 151936, 0, 16), (256, 151936, 8192, 16), (256, 151936, 8192, 0),
+                       (1 << 20, 17, 1 << 20, 1), (1, (1 << 31) - 1, 1 << 20, 16)):
+        assert lib.archead_rules_workspace(M, V, L, K, ctypes.byref(n)) == binding.OK
+        assert M * K * 8 <= n.value <= M * (K * 8 + 4) * -(-V // 2048) + 2 * M * L
+    for M, V, L, K, status in ((-1, 8, 0, 1, binding.EINVAL), (1, 8, -1, 1, binding.EINVAL), (1, 0, 0, 1, binding.ESHAPE),
+                               (1, 8, 0, 9, binding.ESHAPE), (1, 80, 0, 17, binding.ESHAPE), (1, 8, 0, -1, binding.ESHAPE),
+                               (1, 8, (1 << 20) + 1, 0, binding.ESHAPE)):
+        assert lib.archead_rules_workspace(M, V, L, K, ctypes.byref(n)) == status
+    assert lib.archead_rules_workspace(1, 1, 0, 1, None) == binding.EINVAL
 
 
 def test_python_refuses_host_tensors_and_wrong_arguments():
