@@ -677,8 +677,8 @@ archead_status archead_embed_backward(int64_t n, int64_t V, int64_t d, const voi
  * absent, its step is left out.
  *
  * Common to the two calls:
- * logits     DEVICE M x V, fp32 or bf16 (type), row stride ld.  M <= 2^20, V < 2^31,
- *            M ceil(V / 8192) < 2^24.
+ * logits     DEVICE M x V, fp32 or bf16 (type), row stride ld.  M <= 2^20, V <= 2^30,
+ *            M ceil(V / 4096) < 2^24.
  * history    DEVICE int32 M x L tokens, row stride ldh >= L, or NULL: row m's are its
  *            first lengths[m] (DEVICE int32 M, or NULL for L), the first
  *            prompt_lengths[m] of them (DEVICE int32 M, or NULL for 0) the prompt.

@@ -35,6 +35,7 @@ typedef int32_t i32x4u __attribute__((ext_vector_type(4), aligned(4)));
 
 constexpr int kNT = 256;
 constexpr int64_t kMaxRows = int64_t(1) << 20;
+constexpr int64_t kMaxColumns = int64_t(1) << 30; // offsets within a row fit 32 bits
 constexpr int64_t kMaxHistory = int64_t(1) << 20;
 constexpr int64_t kMaxBias = 1023;
 constexpr int64_t kMaxStride = int64_t(1) << 40;
@@ -44,7 +45,9 @@ constexpr uint32_t kCount = (1u << 21) - 1, kPrompt = 1u << 21;
 constexpr int kBiasAt = 22;
 
 struct RuleArgs {
-    int64_t M, V, ld, ldo, L, ldh, B, ldb, R, ldm, S;
+    int64_t M;
+    int V, L, B; // columns, tokens and biases of a row
+    int64_t ld, ldo, ldh, ldb, R, ldm, S;
     const void *y;
     void *out;
     const int32_t *history, *lengths, *prompts;
@@ -216,8 +219,8 @@ __device__ __forceinline__ uint32_t settled(float x) { return (x != x ? 0x7FC000
 constexpr int kAhead = 4; // loads of four tokens in flight
 template <int NT, int E, typename T> struct Slice {
     static constexpr int kCols = NT * E, kVecs = E / 8;
-    int64_t m, sl, base;
-    int cols, n, prompt; // columns; tokens of the history and of its prompt
+    int64_t m;
+    int sl, base, cols, n, prompt; // columns; tokens of the history and of its prompt
     uint32_t from, to;   // or the slice's own of a routed one
     Row r;
     const int32_t *h;
@@ -241,13 +244,13 @@ template <int NT, int E, typename T> struct Slice {
     __device__ __forceinline__ void fetch(const RuleArgs &a, uint32_t at)
     {
         m = at / (uint32_t)a.S;
-        sl = at % (uint32_t)a.S;
+        sl = (int)(at % (uint32_t)a.S);
         base = sl * kCols;
-        cols = (int)min((int64_t)kCols, a.V - base);
+        cols = min(kCols, a.V - base);
         const T *y = (const T *)a.y + m * a.ld;
         const float rho = a.repetition ? a.repetition[m] : 1.f, beta = a.frequency ? a.frequency[m] : 0.f;
         const float alpha = a.presence ? a.presence[m] : 0.f;
-        const int row = a.mask_rows ? a.mask_rows[m] : (int)m, len = a.lengths ? a.lengths[m] : (int)a.L;
+        const int row = a.mask_rows ? a.mask_rows[m] : (int)m, len = a.lengths ? a.lengths[m] : a.L;
         const int head = a.prompts ? a.prompts[m] : 0;
         n = 0;
         if (a.routed) {
@@ -257,14 +260,14 @@ template <int NT, int E, typename T> struct Slice {
         } else if (a.history) {
             h = a.history + m * a.ldh;
             if (a.L > 0)
-                tokens(0, (int)a.L);
+                tokens(0, a.L);
         }
-        const int64_t q0 = base / 8 + threadIdx.x;
+        const int q0 = base / 8 + (int)threadIdx.x;
 #pragma unroll
         for (int j = 0; j < kVecs; ++j)
             raw[j] = load_vector<E == 8>(y, q0 + j * NT, a.V);
         if (a.history && !a.routed) {
-            n = max(0, min(same(len), (int)a.L));
+            n = max(0, min(same(len), a.L));
             prompt = same(head);
         }
         r = Row{same(rho), same(beta), same(alpha), a.bias_values ? a.bias_values + m * a.ldb : nullptr,
@@ -294,8 +297,8 @@ template <int NT, int E, typename T, bool kSelect> __global__ __launch_bounds__(
     const bool lists = a.history || a.bias_ids;
     Slice<NT, E, T> s;
     s.fetch(a, blockIdx.x);
-    const int64_t m = s.m, sl = s.sl, base = s.base, q0 = base / 8 + threadIdx.x;
-    const int cols = s.cols;
+    const int64_t m = s.m;
+    const int sl = s.sl, base = s.base, q0 = base / 8 + (int)threadIdx.x, cols = s.cols;
     const T *y = (const T *)a.y + m * a.ld;
     if (lists) {
         for (int c = threadIdx.x * 4; c < kCols; c += NT * 4)
@@ -305,7 +308,7 @@ template <int NT, int E, typename T, bool kSelect> __global__ __launch_bounds__(
         __syncthreads();
         if (a.bias_ids) {
             const int32_t *ids = a.bias_ids + m * a.ldb;
-            for (int j = threadIdx.x; j < (int)a.B; j += NT) {
+            for (int j = threadIdx.x; j < a.B; j += NT) {
                 const uint32_t c = (uint32_t)ids[j] - (uint32_t)base;
                 if (c < (uint32_t)cols && atomicMax(&word[c], (uint32_t)(j + 1) << kBiasAt) == 0) {
                     const uint32_t i = atomicAdd(&n_listed, 1u); // the first to name the column
@@ -328,11 +331,11 @@ template <int NT, int E, typename T, bool kSelect> __global__ __launch_bounds__(
         }
         for (int i0 = 0; i0 < s.n; i0 += NT * 4 * kAhead) {
             if (i0 > 0)
-                s.tokens(i0, (int)a.L);
+                s.tokens(i0, a.L);
             if (i0 + NT * 4 * kAhead > s.n) { // every token once
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k) {
-                    const int i = i0 + (k * NT + (int)threadIdx.x) * 4, first = max(0, min(i, (int)a.L - 4));
+                    const int i = i0 + (k * NT + (int)threadIdx.x) * 4, first = max(0, min(i, a.L - 4));
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         s.tok[k][e] = first + e >= i && first + e < s.n ? s.tok[k][e] : -1;
@@ -340,7 +343,7 @@ template <int NT, int E, typename T, bool kSelect> __global__ __launch_bounds__(
             }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                const int i = max(0, min(i0 + (k * NT + (int)threadIdx.x) * 4, (int)a.L - 4));
+                const int i = max(0, min(i0 + (k * NT + (int)threadIdx.x) * 4, a.L - 4));
                 uint32_t before[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -378,7 +381,7 @@ template <int NT, int E, typename T, bool kSelect> __global__ __launch_bounds__(
     float most = -INFINITY; // NaN if any is
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-        const int64_t q = q0 + j * NT;
+        const int q = q0 + j * NT;
         uint32_t *mine = &word[8 * (j * NT + threadIdx.x)];
         float v[8];
         widen(s.raw[j], v);
@@ -513,14 +516,14 @@ __global__ __launch_bounds__(kNT) void draw_kernel(DrawArgs a)
 // workgroup; the order within a slice is any, since its tokens are counted.
 constexpr int kRouteT = 1024;
 constexpr int64_t kRouteSlices = 1024;
-constexpr int64_t kRouteRows = 128, kRouteMin = 32768;
+constexpr int64_t kRouteRows = 128, kRouteMin = 65536;
 __global__ __launch_bounds__(kRouteT) void route_kernel(RuleArgs a, int shift)
 {
     __shared__ uint32_t count[kRouteSlices], wave_sums[kRouteT / 64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int64_t m = blockIdx.x;
     const int32_t *h = a.history + m * a.ldh;
-    const int n = a.lengths ? max(0, min(a.lengths[m], (int)a.L)) : (int)a.L, prompt = a.prompts ? a.prompts[m] : 0;
+    const int n = a.lengths ? max(0, min(a.lengths[m], a.L)) : a.L, prompt = a.prompts ? a.prompts[m] : 0;
     count[tid] = 0;
     __syncthreads();
 #pragma unroll 4
@@ -556,14 +559,9 @@ __global__ __launch_bounds__(kRouteT) void route_kernel(RuleArgs a, int shift)
 }
 
 // columns a thread: the more, the fewer slices go through a row's lists; fewer where
-// that leaves compute units without a workgroup
-int columns_of(int64_t M, int64_t V)
-{
-    for (const int e : {32, 16})
-        if (M * ((V + kNT * e - 1) / (kNT * e)) >= 1024)
-            return e;
-    return 8;
-}
+// that leaves compute units without a workgroup (twice as many, in half as many
+// workgroups a compute unit, run alike)
+int columns_of(int64_t M, int64_t V) { return M * ((V + kNT * 16 - 1) / (kNT * 16)) >= 1024 ? 16 : 8; }
 int64_t slices_of(int64_t M, int64_t V)
 {
     const int64_t c = (int64_t)kNT * columns_of(M, V);
@@ -592,7 +590,6 @@ RuleWs rule_ws(int64_t M, int64_t V, int64_t L, int K)
     }
     return w;
 }
-constexpr int kShift[3] = {11, 12, 13}; // of a slice's columns
 
 template <int E, typename T> void launch_rules(const RuleArgs &a, hipStream_t st)
 {
@@ -606,12 +603,8 @@ template <typename T> void run_rules(const RuleArgs &a, hipStream_t st)
 {
     const int e = columns_of(a.M, a.V);
     if (a.routed)
-        hipLaunchKernelGGL(route_kernel, dim3((unsigned)a.M), dim3(kRouteT), 0, st, a, kShift[e / 16]);
-    switch (e) {
-    case 32: return launch_rules<32, T>(a, st);
-    case 16: return launch_rules<16, T>(a, st);
-    default: return launch_rules<8, T>(a, st);
-    }
+        hipLaunchKernelGGL(route_kernel, dim3((unsigned)a.M), dim3(kRouteT), 0, st, a, e == 16 ? 12 : 11);
+    e == 16 ? launch_rules<16, T>(a, st) : launch_rules<8, T>(a, st);
 }
 // the slices and the workspace's parts
 void lay_out(RuleArgs &a, const RuleWs &w, void *ws)
@@ -625,20 +618,20 @@ void lay_out(RuleArgs &a, const RuleWs &w, void *ws)
 
 bool misaligned(const void *p, size_t to) { return (uintptr_t)p % to != 0; }
 
-archead_status check_rules(const RuleArgs &a, int type)
+archead_status check_rules(const RuleArgs &a, int64_t V, int64_t L, int64_t B, int type)
 {
     if (a.M < 0)
         return api_fail(ARCHEAD_EINVAL, "M < 0");
-    if (a.M > kMaxRows || a.V < 1 || a.V >= (int64_t(1) << 31) || a.L > kMaxHistory || a.B > kMaxBias)
-        return api_fail(ARCHEAD_ESHAPE, "M <= 2^20, 1 <= V < 2^31, histories up to 2^20 tokens, up to 1023 biases a row");
+    if (a.M > kMaxRows || V < 1 || V > kMaxColumns || L > kMaxHistory || B > kMaxBias)
+        return api_fail(ARCHEAD_ESHAPE, "M <= 2^20, 1 <= V <= 2^30, histories up to 2^20 tokens, up to 1023 biases a row");
     // a launch holds fewer than 2^32 threads
-    if (a.M * ((a.V + kNT * 32 - 1) / (kNT * 32)) >= (int64_t(1) << 24))
-        return api_fail(ARCHEAD_ESHAPE, "M ceil(V / 8192) must lie below 2^24");
+    if (a.M * slices_of(a.M, V) >= (int64_t(1) << 24))
+        return api_fail(ARCHEAD_ESHAPE, "M ceil(V / 4096) must lie below 2^24");
     if (type != ARCHEAD_F32 && type != ARCHEAD_BF16)
         return api_fail(ARCHEAD_EINVAL, "logits must be ARCHEAD_F32 or ARCHEAD_BF16");
     if (a.ld < a.V || a.ld > kMaxStride)
         return api_fail(ARCHEAD_EINVAL, "the row stride must lie in [V, 2^40]");
-    if (a.L < 0 || a.B < 0 || a.R < 0)
+    if (L < 0 || B < 0 || a.R < 0)
         return api_fail(ARCHEAD_EINVAL, "a list's length is negative");
     if (a.history ? a.ldh < a.L || a.ldh > kMaxStride : a.lengths || a.prompts)
         return api_fail(ARCHEAD_EINVAL, "a history has a row stride in [its length, 2^40]; lengths belong to one");
@@ -685,11 +678,11 @@ RuleArgs rule_args(int64_t M, int64_t V, const void *logits, int64_t ld, const i
 {
     RuleArgs a{};
     a.M = M;
-    a.V = V;
+    a.V = (int)V;
     a.y = logits;
     a.ld = ld;
     a.history = history;
-    a.L = L;
+    a.L = (int)L;
     a.ldh = ldh;
     a.lengths = lengths;
     a.prompts = prompts;
@@ -698,7 +691,7 @@ RuleArgs rule_args(int64_t M, int64_t V, const void *logits, int64_t ld, const i
     a.presence = presence;
     a.bias_ids = bias_ids;
     a.bias_values = bias_values;
-    a.B = B;
+    a.B = (int)B;
     a.ldb = ldb;
     a.mask = mask;
     a.R = R;
@@ -722,7 +715,7 @@ extern "C" archead_status archead_adjust_logits(int64_t M, int64_t V, const void
 {
     RuleArgs a = rule_args(M, V, logits, ld, history, L, ldh, lengths, prompt_lengths, repetition, frequency, presence,
                            bias_ids, bias_values, B, ldb, mask, R, ldm, mask_rows);
-    archead_status s = check_rules(a, type);
+    archead_status s = check_rules(a, V, L, B, type);
     if (s != ARCHEAD_OK)
         return s;
     if (ldo < V || ldo > kMaxStride)
@@ -753,8 +746,8 @@ extern "C" archead_status archead_rules_workspace(int64_t M, int64_t V, int64_t 
         return api_fail(ARCHEAD_EINVAL, "bytes is NULL");
     if (M < 0 || L < 0)
         return api_fail(ARCHEAD_EINVAL, "M < 0 or L < 0");
-    if (M > kMaxRows || V < 1 || V >= (int64_t(1) << 31) || L > kMaxHistory || K < 0 || K > kTopKMax || K > V)
-        return api_fail(ARCHEAD_ESHAPE, "M, L <= 2^20, 1 <= V < 2^31 and 0 <= K <= min(16, V)");
+    if (M > kMaxRows || V < 1 || V > kMaxColumns || L > kMaxHistory || K < 0 || K > kTopKMax || K > V)
+        return api_fail(ARCHEAD_ESHAPE, "M, L <= 2^20, 1 <= V <= 2^30 and 0 <= K <= min(16, V)");
     *bytes = rule_ws(M, V, L, K).total;
     return ARCHEAD_OK;
 }
@@ -771,7 +764,7 @@ extern "C" archead_status archead_sample_logits(int64_t M, int64_t V, const void
 {
     RuleArgs a = rule_args(M, V, logits, ld, history, L, ldh, lengths, prompt_lengths, repetition, frequency, presence,
                            bias_ids, bias_values, B, ldb, mask, R, ldm, mask_rows);
-    archead_status s = check_rules(a, type);
+    archead_status s = check_rules(a, V, L, B, type);
     if (s != ARCHEAD_OK)
         return s;
     if (K < 1 || K > kTopKMax || K > V)

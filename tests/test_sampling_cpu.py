@@ -40,7 +40,7 @@ def _sample(lib, over):
 
 BAD = [
     (dict(M=-1), binding.EINVAL), (dict(M=(1 << 20) + 1), binding.ESHAPE), (dict(V=0), binding.ESHAPE),
-    (dict(V=1 << 31, ld=1 << 31, ldm=1 << 26), binding.ESHAPE), (dict(L=(1 << 20) + 1, ldh=1 << 21), binding.ESHAPE),
+    (dict(V=(1 << 30) + 1, ld=1 << 31, ldm=1 << 26), binding.ESHAPE), (dict(L=(1 << 20) + 1, ldh=1 << 21), binding.ESHAPE),
     (dict(nb=1024, ldb=1024), binding.ESHAPE), (dict(M=1 << 18, V=1 << 20, ld=1 << 20, ldm=1 << 15, R=1 << 18), binding.ESHAPE),
     (dict(type=2), binding.EINVAL), (dict(ld=39), binding.EINVAL), (dict(ld=(1 << 40) + 1), binding.EINVAL),
     (dict(L=-1), binding.EINVAL), (dict(nb=-1), binding.EINVAL), (dict(R=-1), binding.EINVAL),
@@ -54,8 +54,8 @@ BAD = [
 @pytest.mark.parametrize("over,status", BAD + [
     (dict(out=None), binding.EINVAL), (dict(out=ODD), binding.EINVAL), (dict(ldo=39), binding.EINVAL),
     (dict(out=B, ldo=41), binding.EINVAL),
-    (dict(M=1 << 10, V=1 << 14, ld=1 << 14, ldm=512, R=1 << 10, L=8192, ldh=8192, ldo=1 << 14, n=1 << 20), binding.EINVAL),
-    (dict(M=1 << 10, V=1 << 14, ld=1 << 14, ldm=512, R=1 << 10, L=8192, ldh=8192, ldo=1 << 14, ws=None), binding.EINVAL)])
+    (dict(M=1 << 10, V=1 << 14, ld=1 << 14, ldm=512, R=1 << 10, L=1 << 15, ldh=1 << 15, ldo=1 << 14, n=1 << 20), binding.EINVAL),
+    (dict(M=1 << 10, V=1 << 14, ld=1 << 14, ldm=512, R=1 << 10, L=1 << 15, ldh=1 << 15, ldo=1 << 14, ws=None), binding.EINVAL)])
 def test_adjust_refusals(lib, over, status):
     assert _adjust(lib, over) == status
     assert lib.archead_last_error().decode()
@@ -81,12 +81,12 @@ def test_workspace_sizes(lib):
     n = ctypes.c_uint64()
     assert lib.archead_rules_workspace(1, 151936, 300, 0, ctypes.byref(n)) == binding.OK and n.value == 0
     for M, V, L, K in ((1, 1, 0, 1), (1, 151936, 0, 16), (256, 151936, 8192, 16), (256, 151936, 8192, 0),
-                       (1 << 20, 17, 1 << 20, 1), (1, (1 << 31) - 1, 1 << 20, 16)):
+                       (1 << 20, 17, 1 << 20, 1), (1, 1 << 30, 1 << 20, 16)):
         assert lib.archead_rules_workspace(M, V, L, K, ctypes.byref(n)) == binding.OK
         assert M * K * 8 <= n.value <= M * (K * 8 + 4) * -(-V // 2048) + 2 * M * L
     for M, V, L, K, status in ((-1, 8, 0, 1, binding.EINVAL), (1, 8, -1, 1, binding.EINVAL), (1, 0, 0, 1, binding.ESHAPE),
                                (1, 8, 0, 9, binding.ESHAPE), (1, 80, 0, 17, binding.ESHAPE), (1, 8, 0, -1, binding.ESHAPE),
-                               (1, 8, (1 << 20) + 1, 0, binding.ESHAPE)):
+                               (1, 8, (1 << 20) + 1, 0, binding.ESHAPE), (1, (1 << 30) + 1, 0, 1, binding.ESHAPE)):
         assert lib.archead_rules_workspace(M, V, L, K, ctypes.byref(n)) == status
     assert lib.archead_rules_workspace(1, 1, 0, 1, None) == binding.EINVAL
 
