@@ -154,7 +154,7 @@ __device__ __forceinline__ uint32_t key_of(int32_t tok, int64_t V, int32_t pad)
 // tokens; its waves hold 64 kHold tokens of the list at a time in their lanes, and
 // compare them with one of the kRank after the other (in a scalar register): one vector
 // instruction for 64 pairs, the counting is scalar.
-constexpr int kRank = 32, kHold = 8, kRankT = 1024;
+constexpr int kRank = 32, kHold = 4, kRankT = 1024;
 __global__ __launch_bounds__(kRankT) void rank_kernel(const int32_t *tokens, int64_t n64, int64_t V, int32_t pad,
                                                       Pair *sorted, uint32_t *mark, int64_t words)
 {
@@ -343,13 +343,21 @@ __device__ __forceinline__ void add_rows(Row row, int64_t from, int64_t to, int 
             }
     }
 }
-// entries [from, to) of the sorted list (level 0), or of the parts of a level below
+// Entries [from, to) of the sorted list (level 0), or of the parts of a level below.
+// All 64 lanes come along, whatever their columns: they hold the entries' places.
 template <bool kShort, typename T>
 __device__ __forceinline__ void add_entries(const GradArgs &a, int level, int64_t from, int64_t to, int q, float s[8])
 {
-    if (level == 0)
-        add_rows<kShort, T>([&](int64_t i) { return (const T *)a.dout + (int64_t)a.sorted[i].at * a.ldo; }, from, to, q, a.d, s);
-    else
+    if (level == 0) {
+        for (int64_t b = from; b < to; b += 64) {
+            const uint32_t at = a.sorted[min(b + (int64_t)(threadIdx.x & 63), to - 1)].at;
+            add_rows<kShort, T>(
+                [&](int64_t i) {
+                    return (const T *)a.dout + (int64_t)(uint32_t)__builtin_amdgcn_readlane(at, (int)i) * a.ldo;
+                },
+                0, min(to - b, (int64_t)64), q, a.d, s);
+        }
+    } else
         add_rows<kShort, float>([&](int64_t i) { return a.part[level - 1] + i * a.d; }, from, to, q, a.d, s);
 }
 
@@ -379,8 +387,7 @@ template <bool kShort, typename T> __global__ __launch_bounds__(256) void part_k
     const int q = (int)(blockIdx.x % a.tiles) * (kCols / 8) + lane;
     const int64_t from = g * kGroup + wave * (kGroup / 4);
     float s[8] = {};
-    if (8 * q < a.d)
-        add_entries<kShort, T>(a, level, from, from + kGroup / 4, q, s);
+    add_entries<kShort, T>(a, level, from, from + kGroup / 4, q, s);
     for (int e = 0; e < 8; ++e)
         meet[wave][lane][e] = s[e];
     __syncthreads();
@@ -444,8 +451,6 @@ template <bool kShort, typename T, typename GT> __global__ __launch_bounds__(256
             end = lo;
         }
     }
-    if (8 * q >= a.d)
-        return;
     // entries up to the first whole part, parts up to the first whole part of the
     // next level, and so on; then back down
     float s[8] = {};
@@ -468,7 +473,124 @@ template <bool kShort, typename T, typename GT> __global__ __launch_bounds__(256
     }
     for (int l = top; l >= 0; --l)
         add_entries<kShort, T>(a, l, tail_from[l], tail_to[l], q, s);
-    put_row<kShort, GT>(a, key, q, s);
+    if (8 * q < a.d)
+        put_row<kShort, GT>(a, key, q, s);
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens and a small table: one launch.  A workgroup takes R rows of the table
+// (and kCols columns), goes through all tokens for those of its rows, in order, and
+// sums each row by a wave, or, where it has many terms, by all of them.
+// ---------------------------------------------------------------------------
+constexpr int kScanT = 512, kScanWaves = kScanT / 64, kScanMax = 1024, kScanRows = 64, kScanLong = 32;
+constexpr int kAtBits = 10; // of a token's place
+
+// the terms of row r among entries [from, to) of the list of matches, added in order
+template <bool kShort, typename T>
+__device__ __forceinline__ void add_matches(const GradArgs &a, const uint32_t *match, int from, int to, uint32_t r, int q,
+                                            float s[8])
+{
+    constexpr int kFly = 8;
+    const int lane = threadIdx.x & 63;
+    for (int b = from; b < to; b += 64) {
+        const uint32_t e = b + lane < to ? match[b + lane] : ~0u;
+        uint64_t bits = __ballot(e >> kAtBits == r);
+        while (bits) { // uniform
+            const int n = min(__builtin_popcountll(bits), kFly);
+            Eight<T> v[kFly];
+            int at = 0;
+#pragma unroll
+            for (int k = 0; k < kFly; ++k) { // past the last the last again, not added
+                if (k < n) {
+                    at = (int)(__builtin_amdgcn_readlane(e, __builtin_ctzll(bits)) & ((1u << kAtBits) - 1));
+                    bits &= bits - 1;
+                }
+                v[k] = load_vector<kShort>((const T *)a.dout + (int64_t)at * a.ldo, q, a.d);
+            }
+#pragma unroll
+            for (int k = 0; k < kFly; ++k)
+                if (k < n) {
+                    float f[8];
+                    vector_values(q, a.d, v[k], f);
+                    for (int i = 0; i < 8; ++i)
+                        s[i] += f[i];
+                }
+        }
+    }
+}
+
+template <bool kShort, typename T, typename GT>
+__global__ __launch_bounds__(kScanT) void scan_grad_kernel(GradArgs a, const int32_t *tokens, int32_t pad, int rows)
+{
+    __shared__ uint32_t match[kScanMax];
+    __shared__ float meet[kScanWaves][64 * 8];
+    __shared__ uint32_t count[kScanRows], found[kScanWaves];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = (int)a.n;
+    const int64_t v0 = (int64_t)blockIdx.x * rows;
+    const uint32_t here = (uint32_t)min((int64_t)rows, a.V - v0);
+    const int q = (int)blockIdx.y * (kCols / 8) + lane;
+    if (threadIdx.x < kScanRows)
+        count[threadIdx.x] = 0;
+    // the tokens of a wave's part of the list, and where its matches go
+    constexpr int kRounds = kScanMax / kScanT;
+    const int part = (n + kScanT - 1) / kScanT * 64, first = wave * part;
+    uint32_t row[kRounds];
+    uint32_t mine = 0;
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+        const int i = first + 64 * k + lane;
+        const bool in = 64 * k < part && i < n;
+        const int32_t t = in ? tokens[i] : -1;
+        row[k] = t >= 0 && t != pad ? (uint32_t)t - (uint32_t)v0 : ~0u; // tokens of other rows wrap past `here`
+        mine += __builtin_popcountll(__ballot(row[k] < here));
+    }
+    if (lane == 0)
+        found[wave] = mine;
+    __syncthreads();
+    int to = 0, total = 0;
+    for (int w = 0; w < kScanWaves; ++w) {
+        to += w < wave ? (int)found[w] : 0;
+        total += (int)found[w];
+    }
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+        const bool in = row[k] < here;
+        const uint64_t all = __ballot(in);
+        if (in) {
+            match[to + __builtin_popcountll(all & ((uint64_t(1) << lane) - 1))] =
+                row[k] << kAtBits | (uint32_t)(first + 64 * k + lane);
+            atomicAdd(&count[row[k]], 1u);
+        }
+        to += __builtin_popcountll(all);
+    }
+    __syncthreads();
+    for (uint32_t r = wave; r < here; r += kScanWaves) { // a wave a row
+        const uint32_t c = count[r];
+        if (c > kScanLong || (c == 0 && a.add)) // the same for the wave: all lanes look for matches
+            continue;
+        float s[8] = {};
+        if (c)
+            add_matches<kShort, T>(a, match, 0, total, r, q, s);
+        if (8 * q < a.d)
+            put_row<kShort, GT>(a, v0 + r, q, s);
+    }
+    for (uint32_t r = 0; r < here; ++r) { // all waves a row
+        if (count[r] <= kScanLong)
+            continue;
+        const int share = (total + kScanWaves - 1) / kScanWaves;
+        float s[8] = {};
+        add_matches<kShort, T>(a, match, min(wave * share, total), min((wave + 1) * share, total), r, q, s);
+        *(f32x4 *)&meet[wave][8 * lane] = f32x4{s[0], s[1], s[2], s[3]};
+        *(f32x4 *)&meet[wave][8 * lane + 4] = f32x4{s[4], s[5], s[6], s[7]};
+        __syncthreads();
+        if (wave == 0 && 8 * q < a.d) {
+            for (int w = 1; w < kScanWaves; ++w)
+                for (int i = 0; i < 8; ++i)
+                    s[i] += meet[w][8 * lane + i];
+            put_row<kShort, GT>(a, v0 + r, q, s);
+        }
+        __syncthreads();
+    }
 }
 
 // where things lie in a gradient's workspace
@@ -520,6 +642,31 @@ template <bool kShort, typename T> void run_grad(const GradArgs &a, const GradWs
         hipLaunchKernelGGL((grad_kernel<kShort, T, float>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, a);
     else
         hipLaunchKernelGGL((grad_kernel<kShort, T, uint16_t>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, a);
+}
+// Whether the gradient is taken in one launch: few tokens, and a table small enough that
+// the workgroups' passes over the tokens cost less than sorting them (64 tokens into
+// 2048 x 256: 6.5 us against 14; 1000 into 32000 x 512: 22, 26; 1000 into 32000 x 2048:
+// 67, 38; 4099 into 2048 x 257: 39, 35).
+bool scans(int64_t n, int64_t V, int64_t d)
+{
+    return n <= kScanMax && V * ((d + kCols - 1) / kCols) <= (1 << 15);
+}
+template <bool kShort, typename T>
+void run_scan(const GradArgs &a, const int32_t *tokens, int32_t pad, int grad_type, hipStream_t st)
+{
+    int rows = 1; // a workgroup's: as many as leave 512 workgroups
+    while (rows < kScanRows && a.V * a.tiles >= 1024 * rows)
+        rows *= 2;
+    const dim3 grid((unsigned)((a.V + rows - 1) / rows), (unsigned)a.tiles);
+    if (grad_type == ARCHEAD_F32)
+        hipLaunchKernelGGL((scan_grad_kernel<kShort, T, float>), grid, dim3(kScanT), 0, st, a, tokens, pad, rows);
+    else
+        hipLaunchKernelGGL((scan_grad_kernel<kShort, T, uint16_t>), grid, dim3(kScanT), 0, st, a, tokens, pad, rows);
+}
+template <typename T>
+void run_scan(const GradArgs &a, const int32_t *tokens, int32_t pad, int grad_type, hipStream_t st)
+{
+    a.d < 8 ? run_scan<true, T>(a, tokens, pad, grad_type, st) : run_scan<false, T>(a, tokens, pad, grad_type, st);
 }
 template <typename T> void run_grad(const GradArgs &a, const GradWs &w, int grad_type, hipStream_t st)
 {
@@ -644,6 +791,11 @@ extern "C" archead_status archead_embed_backward(int64_t n, int64_t V, int64_t d
     a.add = accumulate != 0;
     a.tiles = tiles;
     a.heads = n * tiles;
+    if (scans(n, V, d)) {
+        dout_type == ARCHEAD_F32 ? run_scan<float>(a, tokens, pad, grad_type, stream)
+                                 : run_scan<uint16_t>(a, tokens, pad, grad_type, stream);
+        return launched("archead_embed_backward");
+    }
     if (n <= kRankMax) {
         hipLaunchKernelGGL(rank_kernel, dim3((unsigned)std::max<int64_t>(1, (n + kRank - 1) / kRank)), dim3(kRankT), 0, stream, tokens, n,
                            V, pad, (Pair *)(base + w.sorted), a.mark, a.mark ? w.words : 0);

@@ -6,6 +6,7 @@ calls can be captured into a graph."""
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from .binding import _check, _need, load_library
 from .fp8 import _blocks
@@ -14,12 +15,19 @@ from .losses import _need_vector, _type_code, need_rows, on_stream, ptr
 E4M3 = 2
 
 
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(n, V, d):
+    need = ctypes.c_uint64()
+    _check(load_library().archead_embed_workspace(n, V, d, ctypes.byref(need)), "archead_embed_workspace")
+    return need.value
+
+
 def _tokens(tokens, dev):
     import torch
     if not isinstance(tokens, torch.Tensor) or tokens.dim() != 1:
         raise ValueError("tokens must be a vector")
     _need_vector(tokens, "tokens", torch.int32, tokens.shape[0], dev)
-    return int(tokens.shape[0])
+    return tokens.shape[0]
 
 
 def embed(table, tokens, scale: float = 1.0, pad: int = -1, out_dtype=None, out=None, scales=None, stream=None):
@@ -31,7 +39,7 @@ def embed(table, tokens, scale: float = 1.0, pad: int = -1, out_dtype=None, out=
     import torch
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("table must be a V x d tensor")
-    (V, d), dev = (int(x) for x in table.shape), table.device
+    (V, d), dev = table.shape, table.device
     f8 = table.dtype == torch.float8_e4m3fn
     code = E4M3 if f8 else _type_code(table.dtype, "table")
     ldt = need_rows(table, "table", (table.dtype,), (V, d), dev)
@@ -51,9 +59,9 @@ def embed(table, tokens, scale: float = 1.0, pad: int = -1, out_dtype=None, out=
         oc, ldo = _type_code(out_dtype, "out_dtype"), d
 
     def call(st):
-        y = torch.empty((n, d), dtype=out_dtype, device=dev) if out is None else out
-        _check(load_library().archead_embed(n, V, d, ptr(table), code, ldt, ptr(scales), _blocks(d), ptr(tokens), pad,
-                                            scale, ptr(y), oc, ldo, st), "archead_embed")
+        y = table.new_empty((n, d), dtype=out_dtype) if out is None else out
+        _check(load_library().archead_embed(n, V, d, table.data_ptr(), code, ldt, ptr(scales), _blocks(d),
+                                            tokens.data_ptr(), pad, scale, y.data_ptr(), oc, ldo, st), "archead_embed")
         return y
     return on_stream(dev, stream, call)
 
@@ -68,7 +76,7 @@ def embed_backward(dout, tokens, V: int, scale: float = 1.0, pad: int = -1, grad
     import torch
     if not isinstance(dout, torch.Tensor) or dout.dim() != 2:
         raise ValueError("dout must be an n x d tensor")
-    (n, d), dev, V = (int(x) for x in dout.shape), dout.device, int(V)
+    (n, d), dev, V = dout.shape, dout.device, int(V)
     code = _type_code(dout.dtype, "dout")
     ldo = need_rows(dout, "dout", (dout.dtype,), (n, d), dev)
     if _tokens(tokens, dev) != n:
@@ -84,12 +92,11 @@ def embed_backward(dout, tokens, V: int, scale: float = 1.0, pad: int = -1, grad
         gc, ldt = _type_code(grad_dtype, "grad_dtype"), d
 
     def call(st):
-        lib = load_library()
-        g = torch.empty((V, d), dtype=grad_dtype, device=dev) if dtable is None else dtable
-        need = ctypes.c_uint64()
-        _check(lib.archead_embed_workspace(n, V, d, ctypes.byref(need)), "archead_embed_workspace")
-        ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
-        _check(lib.archead_embed_backward(n, V, d, ptr(dout), code, ldo, ptr(tokens), pad, scale, int(accumulate),
-                                          ptr(g), gc, ldt, ptr(ws), need.value, st), "archead_embed_backward")
+        g = dout.new_empty((V, d), dtype=grad_dtype) if dtable is None else dtable
+        need = _workspace_bytes(n, V, d)
+        ws = dout.new_empty(need, dtype=torch.uint8)
+        _check(load_library().archead_embed_backward(
+            n, V, d, dout.data_ptr(), code, ldo, tokens.data_ptr(), pad, scale, int(accumulate), g.data_ptr(), gc, ldt,
+            ws.data_ptr(), need, st), "archead_embed_backward")
         return g
     return on_stream(dev, stream, call)

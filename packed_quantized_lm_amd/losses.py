@@ -40,7 +40,7 @@ def on_stream(device, stream, call):
     # entering torch's device and stream contexts costs 10 us, more than the
     # smallest calls, and a Stream object 2 us: both are skipped where they
     # would change nothing
-    if stream is None and device.index == torch.cuda.current_device():
+    if stream is None and device.index is not None and device.index == torch._C._cuda_getDevice():
         return call(torch._C._cuda_getCurrentRawStream(device.index))
     with _entered(device, stream) as st:
         return call(st)
@@ -51,8 +51,9 @@ def need_rows(t, name, dtypes, shape, device):
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    # the usual call, in one line; the rest says what is wrong with another
-    if device.type == "cuda" and t.device == device and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+    # the usual call, in one line; the rest says what is wrong with another (a host
+    # tensor's device number is -1, a host device's None)
+    if t.get_device() == device.index and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
         return max(shape[1], 1)
     if t.device.type != "cuda" or t.device != device:
         raise ValueError(f"{name} must live on {device}, not {t.device}")
@@ -75,7 +76,8 @@ def ptr(t):
 
 def _need_vector(t, name, dtype, n, device):
     # what a sound call costs is this one line; _need says what is wrong with another
-    if not (hasattr(t, "dtype") and t.dtype == dtype and t.shape == (n,) and t.device == device and t.is_contiguous()):
+    if not (hasattr(t, "get_device") and t.dtype == dtype and t.shape == (n,) and t.get_device() == device.index
+            and t.is_contiguous()):
         _need(t, name, (dtype,), (n,), device)
 
 

@@ -6,6 +6,7 @@ the call's stream, so the calls can be captured into a graph."""
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from .binding import _check, _need, load_library
 from .fp8 import _blocks
@@ -16,13 +17,32 @@ def _matrix(t, name):
     import torch
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be an M x d tensor")
-    return int(t.shape[0]), int(t.shape[1]), t.device
+    M, d = t.shape
+    return M, d, t.device
 
 
 def _weight(weight, d, dev):
     import torch
-    _need(weight, "weight", (torch.float32, torch.bfloat16), (d,), dev)
+    if not (isinstance(weight, torch.Tensor) and weight.get_device() == dev.index and weight.shape == (d,)
+            and weight.is_contiguous()):
+        _need(weight, "weight", (torch.float32, torch.bfloat16), (d,), dev)
     return _type_code(weight.dtype, "weight")
+
+
+def _like(t, shape, dtype):
+    """A contiguous tensor of this shape and type on t's device."""
+    import torch
+    # the cheapest of torch's allocations, where it is the same one
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return torch.empty_like(t)
+    return t.new_empty(shape, dtype=dtype)
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(M, d):
+    n = ctypes.c_uint64()
+    _check(load_library().archead_rms_norm_workspace(M, d, ctypes.byref(n)), "archead_rms_norm_workspace")
+    return n.value
 
 
 def rms_norm(x, weight, residual=None, eps: float = 1e-6, offset: float = 0.0, want_y: bool = True, out_dtype=None,
@@ -60,26 +80,19 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, offset: float = 0.0, w
         raise ValueError("codes need d to be a multiple of 16")
 
     def call(st):
-        y = torch.empty((M, d), dtype=yt, device=dev) if want_y else None
-        h = h_out
-        stride = ldh
+        y = _like(x, (M, d), yt) if want_y else None
+        h, stride = h_out, ldh
         if residual is not None and h is None:
-            h, stride = torch.empty((M, d), dtype=residual.dtype, device=dev), d
+            h, stride = _like(residual, (M, d), residual.dtype), d
         q = s = None
         if want_codes:
-            q = torch.empty((M, d), dtype=torch.float8_e4m3fn, device=dev)
-            s = torch.empty((_blocks(d), M), dtype=torch.float32, device=dev)
-        _check(load_library().archead_rms_norm(
-            M, d, ptr(x), xc, ldx, ptr(residual), rc, ldr, ptr(h), stride, ptr(weight), wc, eps, offset, ptr(y), yc, d,
-            ptr(q), d, ptr(s), M, st), "archead_rms_norm")
+            q = x.new_empty((M, d), dtype=torch.float8_e4m3fn)
+            s = x.new_empty((_blocks(d), M), dtype=torch.float32)
+        if M:  # empty tensors have no addresses to pass on
+            _check(load_library().archead_rms_norm(
+                M, d, x.data_ptr(), xc, ldx, ptr(residual), rc, ldr, ptr(h), stride, weight.data_ptr(), wc, eps, offset,
+                ptr(y), yc, d, ptr(q), d, ptr(s), M, st), "archead_rms_norm")
         return y, h, q, s
-    if M == 0:  # empty tensors have no addresses to pass on
-        return on_stream(dev, stream, lambda st: (
-            torch.empty((0, d), dtype=yt, device=dev) if want_y else None,
-            None if residual is None else torch.empty((0, d), dtype=residual.dtype, device=dev) if h_out is None
-            else h_out,
-            torch.empty((0, d), dtype=torch.float8_e4m3fn, device=dev) if want_codes else None,
-            torch.empty((_blocks(d), 0), dtype=torch.float32, device=dev) if want_codes else None))
     return on_stream(dev, stream, call)
 
 
@@ -103,14 +116,12 @@ def rms_norm_backward(dy, h, weight, dres=None, eps: float = 1e-6, offset: float
     ldd = d if dh_out is None else need_rows(dh_out, "dh_out", (h.dtype,), (M, d), dev)
 
     def call(st):
-        lib = load_library()
-        dh = torch.empty((M, d), dtype=h.dtype, device=dev) if dh_out is None else dh_out
-        dw = torch.empty(d, dtype=torch.float32, device=dev) if want_dweight else None
-        n = ctypes.c_uint64()
-        _check(lib.archead_rms_norm_workspace(M, d, ctypes.byref(n)), "archead_rms_norm_workspace")
-        ws = torch.empty(n.value, dtype=torch.uint8, device=dev)
-        _check(lib.archead_rms_norm_backward(
-            M, d, ptr(dy), uc, ldu, ptr(h), hc, ldh, ptr(weight), wc, eps, offset, ptr(dres), ldr, ptr(dh), ldd,
-            ptr(dw), ptr(ws), n.value, st), "archead_rms_norm_backward")
+        dh = _like(h, (M, d), h.dtype) if dh_out is None else dh_out
+        dw = h.new_empty(d, dtype=torch.float32) if want_dweight else None
+        n = _workspace_bytes(M, d)
+        ws = h.new_empty(n, dtype=torch.uint8)
+        _check(load_library().archead_rms_norm_backward(
+            M, d, dy.data_ptr(), uc, ldu, h.data_ptr(), hc, ldh, weight.data_ptr(), wc, eps, offset, ptr(dres), ldr,
+            dh.data_ptr(), ldd, ptr(dw), ws.data_ptr(), n, st), "archead_rms_norm_backward")
         return dh, dw
     return on_stream(dev, stream, call)

@@ -6,6 +6,7 @@ calls can be captured into a graph."""
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from .binding import _check, _need, load_library
 from .losses import _need_vector, _type_code, need_rows, on_stream, ptr
@@ -22,7 +23,7 @@ def _rules(logits, history, lengths, prompt_lengths, repetition, frequency, pres
     import torch
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or logits.shape[1] < 1:
         raise ValueError("logits must be an M x V tensor")
-    (M, V), dev = (int(n) for n in logits.shape), logits.device
+    (M, V), dev = logits.shape, logits.device
     code = _type_code(logits.dtype, "logits")
     ld = need_rows(logits, "logits", (logits.dtype,), (M, V), dev)
     for name, t, dtype in (("lengths", lengths, torch.int32), ("prompt_lengths", prompt_lengths, torch.int32),
@@ -71,12 +72,18 @@ def _rules(logits, history, lengths, prompt_lengths, repetition, frequency, pres
                         ptr(mask), R, ldm, ptr(mask_rows))
 
 
-def _workspace(M, V, L, K, dev):
-    """The calls' workspace and its size; none where nothing is needed."""
-    import torch
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(M, V, L, K):
     n = ctypes.c_uint64()
     _check(load_library().archead_rules_workspace(M, V, L, K, ctypes.byref(n)), "archead_rules_workspace")
-    return (torch.empty(n.value, dtype=torch.uint8, device=dev) if n.value else None), n.value
+    return n.value
+
+
+def _workspace(logits, L, K):
+    """The calls' workspace and its size; none where nothing is needed."""
+    import torch
+    n = _workspace_bytes(*logits.shape, L, K)
+    return (logits.new_empty(n, dtype=torch.uint8) if n else None), n
 
 
 def adjust_logits(logits, history=None, lengths=None, prompt_lengths=None, repetition=None, frequency=None,
@@ -96,8 +103,8 @@ def adjust_logits(logits, history=None, lengths=None, prompt_lengths=None, repet
     ldo = V if out is None else need_rows(out, "out", (logits.dtype,), (M, V), logits.device)
 
     def call(st):
-        y = torch.empty((M, V), dtype=logits.dtype, device=logits.device) if out is None else out
-        ws, n = _workspace(M, V, L, 0, logits.device)
+        y = logits.new_empty((M, V)) if out is None else out
+        ws, n = _workspace(logits, L, 0)
         _check(load_library().archead_adjust_logits(*args, ptr(y), ldo, ptr(ws), n, st), "archead_adjust_logits")
         return y
     return on_stream(logits.device, stream, call)
@@ -126,10 +133,10 @@ def sample_logits(logits, K: int, u=None, temperature=1.0, history=None, lengths
         tau = float(temperature)
 
     def call(st):
-        values = torch.empty((M, K), dtype=torch.float32, device=dev)
-        indices = torch.empty((M, K), dtype=torch.int32, device=dev)
-        samples = None if u is None else torch.empty(M, dtype=torch.int32, device=dev)
-        ws, n = _workspace(M, V, L, K, dev)
+        values = logits.new_empty((M, K), dtype=torch.float32)
+        indices = logits.new_empty((M, K), dtype=torch.int32)
+        samples = None if u is None else logits.new_empty(M, dtype=torch.int32)
+        ws, n = _workspace(logits, L, K)
         _check(load_library().archead_sample_logits(*args, K, tau, ptr(taus), ptr(u), ptr(values), ptr(indices),
                                                     ptr(samples), ptr(ws), n, st), "archead_sample_logits")
         return values, indices, samples
