@@ -436,8 +436,8 @@ template <typename UT, typename HT> __global__ __launch_bounds__(kLongT) void no
 }
 template <typename UT, typename HT> __global__ __launch_bounds__(256) void weight_long_kernel(BackArgs a)
 {
-    const int q = (int)blockIdx.x * 256 + (int)threadIdx.x, nv = (a.d + 7) / 8;
-    const int64_t g = blockIdx.y;
+    const int q = (int)blockIdx.y * 256 + (int)threadIdx.x, nv = (a.d + 7) / 8;
+    const int64_t g = blockIdx.x;
     if (q >= nv)
         return;
     float dw[8] = {};
@@ -539,7 +539,7 @@ template <typename UT, typename HT> void run_back(const BackArgs &a, const BackP
     else {
         hipLaunchKernelGGL((norm_back_long_kernel<UT, HT>), dim3((unsigned)a.M), dim3(kLongT), 0, st, a);
         hipLaunchKernelGGL((weight_long_kernel<UT, HT>),
-                           dim3((unsigned)(((a.d + 7) / 8 + 255) / 256), (unsigned)a.groups), dim3(256), 0, st, a);
+                           dim3((unsigned)a.groups, (unsigned)(((a.d + 7) / 8 + 255) / 256)), dim3(256), 0, st, a);
     }
     if (dw)
         hipLaunchKernelGGL(weight_sum_kernel, dim3((unsigned)((a.d + 31) / 32)), dim3(1024), 0, st, a.part, a.groups,

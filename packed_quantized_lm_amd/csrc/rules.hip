@@ -560,8 +560,9 @@ __global__ __launch_bounds__(kRouteT) void route_kernel(RuleArgs a, int shift)
 
 // columns a thread: the more, the fewer slices go through a row's lists; fewer where
 // that leaves compute units without a workgroup (twice as many, in half as many
-// workgroups a compute unit, run alike)
-int columns_of(int64_t M, int64_t V) { return M * ((V + kNT * 16 - 1) / (kNT * 16)) >= 1024 ? 16 : 8; }
+// workgroups a compute unit, run alike), and for rows shorter than a vector, which only
+// that form reads element by element
+int columns_of(int64_t M, int64_t V) { return V >= 8 && M * ((V + kNT * 16 - 1) / (kNT * 16)) >= 1024 ? 16 : 8; }
 int64_t slices_of(int64_t M, int64_t V)
 {
     const int64_t c = (int64_t)kNT * columns_of(M, V);

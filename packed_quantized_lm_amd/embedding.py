@@ -30,6 +30,12 @@ def _tokens(tokens, dev):
     return tokens.shape[0]
 
 
+def _pad(pad):
+    if not -2 ** 31 <= pad < 2 ** 31:
+        raise ValueError("pad must be a 32-bit number")
+    return int(pad)
+
+
 def embed(table, tokens, scale: float = 1.0, pad: int = -1, out_dtype=None, out=None, scales=None, stream=None):
     """scale * table[tokens], n x d in out_dtype (the table's type by default,
     bfloat16 for 8-bit tables) or written to out (its rows may be strided).
@@ -43,7 +49,7 @@ def embed(table, tokens, scale: float = 1.0, pad: int = -1, out_dtype=None, out=
     f8 = table.dtype == torch.float8_e4m3fn
     code = E4M3 if f8 else _type_code(table.dtype, "table")
     ldt = need_rows(table, "table", (table.dtype,), (V, d), dev)
-    n = _tokens(tokens, dev)
+    n, pad = _tokens(tokens, dev), _pad(pad)
     if f8:
         if scales is None:
             raise ValueError("an 8-bit table needs its scales")
@@ -81,6 +87,7 @@ def embed_backward(dout, tokens, V: int, scale: float = 1.0, pad: int = -1, grad
     ldo = need_rows(dout, "dout", (dout.dtype,), (n, d), dev)
     if _tokens(tokens, dev) != n:
         raise ValueError("dout needs a row for every token")
+    pad = _pad(pad)
     if dtable is not None:
         if grad_dtype is not None and grad_dtype != dtable.dtype:
             raise ValueError("dtable and grad_dtype disagree")

@@ -76,3 +76,7 @@ def test_python_refuses_host_tensors_and_wrong_arguments():
         pq.embed(t.half(), tok)
     with pytest.raises(ValueError):
         pq.embed_backward(t, tok, 4)
+    from packed_quantized_lm_amd import embedding
+    for pad in (2 ** 31, -2 ** 31 - 1):
+        with pytest.raises(ValueError):
+            embedding._pad(pad)

@@ -96,7 +96,7 @@ def _same(got, want, what):
 
 
 SHAPES = [(1, 1, 1, 1), (2, 7, 5, 3), (3, 8, 40, 8), (1, 33, 9, 2), (5, 1000, 300, 40), (2, 2048, 64, 5), (3, 2049, 2000, 20),
-          (1, 50021, 700, 1023), (2, 16390, 5000, 64), (130, 40000, 50, 7), (600, 9000, 33, 3), (1030, 300, 20, 5),
+          (1, 50021, 700, 1023), (2, 16390, 5000, 64), (130, 40000, 50, 7), (600, 9000, 33, 3), (1030, 300, 20, 5), (1100, 3, 2, 2), (1100, 9, 5, 2),
           (130, 40000, 8000, 7), (300, 30000, 9000, 4), (130, 20000, 4000, 9)]  # the last three: histories sorted by slices first
 
 
