@@ -144,6 +144,28 @@ struct Pair {
     uint32_t at;  // its place among the tokens
 };
 
+// The table is cleared, where it is written whole, by workgroups of the first launch
+// that come after its own `after` ones: all of it, while the tokens are sorted; what
+// occurs is written over it (8192 tokens into 151936 x 4096 bf16: clearing alone 190 us,
+// 6.5 TB/s, beside 15 of sorting).  Rows as 16-bit words.
+struct Clear {
+    uint32_t after;
+    int64_t rows, ld;
+    int words;
+    uint16_t *table; // null: nothing to clear
+};
+__device__ __forceinline__ void clear_rows(const Clear &c)
+{
+    const int64_t v = (int64_t)(blockIdx.x - c.after) * (blockDim.x / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (v >= c.rows)
+        return;
+    const float none[8] = {};
+    for (int q = threadIdx.x & 63; 8 * q < c.words; q += 64)
+        store_vector(c.table + v * c.ld, q, c.words, none);
+}
+// workgroups of `threads` that clear it
+int64_t clear_groups(const Clear &c, int threads) { return c.table ? (c.rows + threads / 64 - 1) / (threads / 64) : 0; }
+
 __device__ __forceinline__ uint32_t key_of(int32_t tok, int64_t V, int32_t pad)
 {
     return tok >= 0 && tok < V && tok != pad ? (uint32_t)tok : (uint32_t)V;
@@ -156,9 +178,13 @@ __device__ __forceinline__ uint32_t key_of(int32_t tok, int64_t V, int32_t pad)
 // instruction for 64 pairs, the counting is scalar.
 constexpr int kRank = 32, kHold = 4, kRankT = 1024;
 __global__ __launch_bounds__(kRankT) void rank_kernel(const int32_t *tokens, int64_t n64, int64_t V, int32_t pad,
-                                                      Pair *sorted, uint32_t *mark, int64_t words)
+                                                      Pair *sorted, Clear c)
 {
     __shared__ uint32_t meet[kRankT / 64][kRank];
+    if (blockIdx.x >= c.after) {
+        clear_rows(c);
+        return;
+    }
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n = (int)n64;
     const int first = (int)blockIdx.x * kRank, i = first + (lane & (kRank - 1));
     const int own = i < n ? (int)key_of(tokens[i], V, pad) : 0; // keys fit 31 bits
@@ -195,9 +221,6 @@ __global__ __launch_bounds__(kRankT) void rank_kernel(const int32_t *tokens, int
         if (lane < kRank && i < n)
             sorted[place + ties] = Pair{(uint32_t)own, (uint32_t)i};
     }
-    // the rows' marks are cleared on the way
-    for (int64_t w = (int64_t)blockIdx.x * kRankT + threadIdx.x; w < words; w += (int64_t)gridDim.x * kRankT)
-        mark[w] = 0;
 }
 
 // Many tokens: stable passes over kDigit bits of the key, tiles of kTile pairs.
@@ -213,8 +236,7 @@ struct SortArgs {
     int64_t n, V;
     int32_t pad;
     int shift;
-    uint32_t *mark;
-    int64_t words;
+    Clear c;
 };
 __device__ __forceinline__ Pair sort_pair(const SortArgs &a, int64_t i)
 {
@@ -225,6 +247,10 @@ __device__ __forceinline__ int digit_of(const SortArgs &a, Pair p) { return (p.k
 __global__ __launch_bounds__(kSortT) void digit_count_kernel(SortArgs a)
 {
     __shared__ uint32_t count[kDigits];
+    if (blockIdx.x >= a.c.after) {
+        clear_rows(a.c);
+        return;
+    }
     count[threadIdx.x] = 0;
     __syncthreads();
     for (int k = 0; k < kPer; ++k) {
@@ -234,9 +260,6 @@ __global__ __launch_bounds__(kSortT) void digit_count_kernel(SortArgs a)
     }
     __syncthreads();
     a.count[(int64_t)blockIdx.x * kDigits + threadIdx.x] = count[threadIdx.x];
-    if (a.mark)
-        for (int64_t w = (int64_t)blockIdx.x * kSortT + threadIdx.x; w < a.words; w += (int64_t)gridDim.x * kSortT)
-            a.mark[w] = 0;
 }
 
 __global__ __launch_bounds__(kSortT) void digit_place_kernel(SortArgs a)
@@ -312,14 +335,12 @@ struct GradArgs {
     int64_t ldo, ldt;
     const void *dout;
     const Pair *sorted;
-    uint32_t *mark;
     float *part[kMaxLevels]; // [n / 32^(l+1)][d]
     int levels;
     void *dtable;
     float scale;
     int add;
     int64_t tiles; // of kCols columns
-    int64_t heads; // waves of the sums, before those that clear rows
 };
 
 // the sum of rows row(from) .. row(to - 1) at vector q onto s, kFly rows in flight;
@@ -368,14 +389,6 @@ template <bool kShort, typename T> __global__ __launch_bounds__(256) void part_k
     __shared__ float meet[4][64][9]; // nine: neighbouring lanes in different banks
     const int64_t g = blockIdx.x / a.tiles;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    if (level == 0) { // rows that occur, for the waves that clear the others
-        const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-        if (a.mark && i < a.n) {
-            const uint32_t k = a.sorted[i].key;
-            if (k < a.V && (i == 0 || a.sorted[i - 1].key != k))
-                atomicOr(&a.mark[k >> 5], 1u << (k & 31));
-        }
-    }
     if (g >= parts)
         return;
     int64_t size = kGroup;
@@ -409,51 +422,46 @@ template <bool kShort, typename GT> __device__ __forceinline__ void put_row(cons
     store_vector(row, q, a.d, o);
 }
 
-// Waves first for the sums (one per entry of the sorted list that begins a run, and
-// kCols columns), then for clearing the rows that do not occur.
+// A wave per entry of the sorted list that begins a run, and kCols columns.
 template <bool kShort, typename T, typename GT> __global__ __launch_bounds__(256) void grad_kernel(GradArgs a)
 {
     const int lane = threadIdx.x & 63;
     const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (w >= a.heads) {
-        const int64_t v = w - a.heads;
-        // adding to rows there are no marks: these waves only fill the last workgroup
-        if (a.add || v >= a.V || (a.mark[v >> 5] >> (v & 31) & 1))
-            return;
-        const float none[8] = {};
-        for (int q = lane; 8 * q < a.d; q += 64)
-            store_vector((GT *)a.dtable + v * a.ldt, q, a.d, none);
-        return;
-    }
     const int64_t i = w / a.tiles;
     const int q = (int)(w % a.tiles) * (kCols / 8) + lane;
     if (i >= a.n)
         return;
-    const uint32_t key = a.sorted[i].key;
-    if (key >= a.V || (i > 0 && a.sorted[i - 1].key == key))
+    // lane l holds entry i - 1 + l: the one before, the run's first and what follows
+    const Pair p = a.sorted[max((int64_t)0, min(i - 1 + lane, a.n - 1))];
+    const uint32_t key = __builtin_amdgcn_readlane(p.key, 1);
+    if (key >= a.V || (i > 0 && __builtin_amdgcn_readlane(p.key, 0) == key))
         return;
-    // the run's end: 64 entries at a look, then by halves
+    // the run's end: within the lanes', or by halves
     int64_t end = a.n;
-    {
-        const int64_t look = i + 1 + lane;
-        const uint64_t other = __ballot(look >= a.n || a.sorted[min(look, a.n - 1)].key != key);
-        if (other)
-            end = i + 1 + __builtin_ctzll(other);
-        else {
-            int64_t lo = i + 65, hi = a.n; // entries below lo are the run's
-            while (lo < hi) {
-                const int64_t mid = (lo + hi) / 2;
-                if (a.sorted[mid].key == key)
-                    lo = mid + 1;
-                else
-                    hi = mid;
-            }
-            end = lo;
+    const uint64_t other = __ballot(lane >= 2 && (i - 1 + lane >= a.n || p.key != key));
+    if (other)
+        end = i - 1 + __builtin_ctzll(other);
+    else {
+        int64_t lo = i + 63, hi = a.n; // entries below lo are the run's
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) / 2;
+            if (a.sorted[mid].key == key)
+                lo = mid + 1;
+            else
+                hi = mid;
         }
+        end = lo;
     }
     // entries up to the first whole part, parts up to the first whole part of the
     // next level, and so on; then back down
     float s[8] = {};
+    auto add_held = [&](int64_t first, int64_t last) __attribute__((always_inline)) { // at most 62 entries from i on
+        add_rows<kShort, T>(
+            [&](int64_t e) {
+                return (const T *)a.dout + (int64_t)(uint32_t)__builtin_amdgcn_readlane(p.at, (int)(e - i) + 1) * a.ldo;
+            },
+            first, last, q, a.d, s);
+    };
     int64_t from = i, to = end;
     int64_t tail_from[kMaxLevels + 1], tail_to[kMaxLevels + 1];
     int top = 0;
@@ -465,14 +473,21 @@ template <bool kShort, typename T, typename GT> __global__ __launch_bounds__(256
             tail_to[l] = to;
             break;
         }
-        add_entries<kShort, T>(a, l, from, lo * kGroup, q, s);
+        if (l == 0)
+            add_held(from, lo * kGroup);
+        else
+            add_entries<kShort, T>(a, l, from, lo * kGroup, q, s);
         tail_from[l] = hi * kGroup;
         tail_to[l] = to;
         from = lo;
         to = hi;
     }
-    for (int l = top; l >= 0; --l)
-        add_entries<kShort, T>(a, l, tail_from[l], tail_to[l], q, s);
+    for (int l = top; l >= 0; --l) {
+        if (l == 0 && top == 0) // no whole part: all of a run of 62 at most
+            add_held(tail_from[0], tail_to[0]);
+        else
+            add_entries<kShort, T>(a, l, tail_from[l], tail_to[l], q, s);
+    }
     if (8 * q < a.d)
         put_row<kShort, GT>(a, key, q, s);
 }
@@ -595,8 +610,8 @@ __global__ __launch_bounds__(kScanT) void scan_grad_kernel(GradArgs a, const int
 
 // where things lie in a gradient's workspace
 struct GradWs {
-    size_t sorted, other, count, mark, part[kMaxLevels], total;
-    int64_t parts[kMaxLevels], words, tiles;
+    size_t sorted, other, count, part[kMaxLevels], total;
+    int64_t parts[kMaxLevels], tiles;
     int levels;
 };
 constexpr int64_t kFewParts = 256;  // of a level, that a run sums without another
@@ -607,7 +622,6 @@ GradWs grad_ws(int64_t n, int64_t V, int64_t d)
 {
     GradWs w{};
     w.tiles = (n + kTile - 1) / kTile;
-    w.words = (V + 31) / 32;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -619,7 +633,6 @@ GradWs grad_ws(int64_t n, int64_t V, int64_t d)
         w.other = take((size_t)n * sizeof(Pair));
         w.count = take((size_t)w.tiles * kDigits * 4);
     }
-    w.mark = take((size_t)w.words * 4);
     for (int64_t m = n / kGroup; m > 0 && w.levels < kMaxLevels && (w.levels == 0 || m * kGroup > kFewParts); m /= kGroup) {
         w.parts[w.levels] = m;
         w.part[w.levels++] = take((size_t)m * d * 4);
@@ -630,14 +643,12 @@ GradWs grad_ws(int64_t n, int64_t V, int64_t d)
 
 template <bool kShort, typename T> void run_grad(const GradArgs &a, const GradWs &w, int grad_type, hipStream_t st)
 {
-    for (int l = 0; l < w.levels; ++l) {
-        const int64_t groups = w.parts[l] * a.tiles, marks = l == 0 && a.mark ? (a.n + 255) / 256 : 0;
-        hipLaunchKernelGGL((part_kernel<kShort, T>), dim3((unsigned)std::max(groups, marks)), dim3(256), 0, st, a, l,
+    for (int l = 0; l < w.levels; ++l)
+        hipLaunchKernelGGL((part_kernel<kShort, T>), dim3((unsigned)(w.parts[l] * a.tiles)), dim3(256), 0, st, a, l,
                            w.parts[l]);
-    }
-    if (w.levels == 0 && a.mark) // the marks alone
-        hipLaunchKernelGGL((part_kernel<kShort, T>), dim3(1), dim3(256), 0, st, a, 0, 0);
-    const int64_t waves = a.heads + (a.add ? 0 : a.V);
+    const int64_t waves = a.n * a.tiles;
+    if (waves == 0)
+        return;
     if (grad_type == ARCHEAD_F32)
         hipLaunchKernelGGL((grad_kernel<kShort, T, float>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, a);
     else
@@ -760,8 +771,8 @@ extern "C" archead_status archead_embed_backward(int64_t n, int64_t V, int64_t d
     const GradWs w = grad_ws(n, V, d);
     const int64_t tiles = (d + kCols - 1) / kCols;
     // a launch holds fewer than 2^32 threads
-    if (n * tiles + V >= (int64_t(1) << 26))
-        return api_fail(ARCHEAD_ESHAPE, "n ceil(d / 512) + V must lie below 2^26");
+    if (n * tiles >= (int64_t(1) << 26) || V >= (int64_t(1) << 26) - (int64_t(1) << 24))
+        return api_fail(ARCHEAD_ESHAPE, "n ceil(d / 512) must lie below 2^26, V below 2^26 - 2^24");
     if (!dtable || (n > 0 && (!dout || !tokens)))
         return api_fail(ARCHEAD_EINVAL, "dout, tokens and dtable are required");
     if (misaligned(dout, dout_type) || misaligned(dtable, grad_type) || misaligned(tokens, ARCHEAD_F32))
@@ -782,7 +793,6 @@ extern "C" archead_status archead_embed_backward(int64_t n, int64_t V, int64_t d
     a.ldt = ldt;
     a.dout = dout;
     a.sorted = (const Pair *)(base + w.sorted);
-    a.mark = accumulate ? nullptr : (uint32_t *)(base + w.mark);
     for (int l = 0; l < w.levels; ++l)
         a.part[l] = (float *)(base + w.part[l]);
     a.levels = w.levels;
@@ -790,28 +800,32 @@ extern "C" archead_status archead_embed_backward(int64_t n, int64_t V, int64_t d
     a.scale = scale;
     a.add = accumulate != 0;
     a.tiles = tiles;
-    a.heads = n * tiles;
     if (scans(n, V, d)) {
         dout_type == ARCHEAD_F32 ? run_scan<float>(a, tokens, pad, grad_type, stream)
                                  : run_scan<uint16_t>(a, tokens, pad, grad_type, stream);
         return launched("archead_embed_backward");
     }
+    const int words = grad_type == ARCHEAD_F32 ? 2 : 1;
+    Clear c{0, V, ldt * words, (int)d * words, accumulate ? nullptr : (uint16_t *)dtable};
     if (n <= kRankMax) {
-        hipLaunchKernelGGL(rank_kernel, dim3((unsigned)std::max<int64_t>(1, (n + kRank - 1) / kRank)), dim3(kRankT), 0, stream, tokens, n,
-                           V, pad, (Pair *)(base + w.sorted), a.mark, a.mark ? w.words : 0);
+        c.after = (uint32_t)((n + kRank - 1) / kRank);
+        const int64_t groups = c.after + clear_groups(c, kRankT);
+        hipLaunchKernelGGL(rank_kernel, dim3((unsigned)groups), dim3(kRankT), 0, stream, tokens, n, V, pad,
+                           (Pair *)(base + w.sorted), c);
     } else {
         int bits = 1;
         while (bits < 32 && V >> bits)
             ++bits;
         const int passes = (bits + kDigit - 1) / kDigit;
-        SortArgs s{tokens, nullptr, nullptr, (uint32_t *)(base + w.count), n, V, pad, 0, a.mark, w.words};
+        c.after = (uint32_t)w.tiles;
+        SortArgs s{tokens, nullptr, nullptr, (uint32_t *)(base + w.count), n, V, pad, 0, c};
         for (int p = 0; p < passes; ++p) {
             s.to = (Pair *)(base + ((passes - 1 - p) % 2 ? w.other : w.sorted));
             s.shift = p * kDigit;
-            hipLaunchKernelGGL(digit_count_kernel, dim3((unsigned)w.tiles), dim3(kSortT), 0, stream, s);
+            const int64_t groups = w.tiles + (p == 0 ? clear_groups(c, kSortT) : 0);
+            hipLaunchKernelGGL(digit_count_kernel, dim3((unsigned)groups), dim3(kSortT), 0, stream, s);
             hipLaunchKernelGGL(digit_place_kernel, dim3((unsigned)w.tiles), dim3(kSortT), 0, stream, s);
             s.from = s.to;
-            s.mark = nullptr;
         }
     }
     if (dout_type == ARCHEAD_F32)
