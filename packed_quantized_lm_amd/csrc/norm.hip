@@ -9,8 +9,11 @@
 //   g_j = u_j (w_j + offset),  c = mean_j g_j h_j,
 //   dh_j = r (g_j - h_j r^2 c) + dres_j,   dw_j = sum_m u_mj h_mj r_m.
 // Both are bound by their rows' bytes: a row is read once and stays in registers
-// between its sums and its results.  A row's sums are fp64 (its squares pass
-// fp32's range from 2^64 on), dw's parts fp32 over at most 64 rows, then fp64.
+// between its sums and its results (8192 x 4096 bf16 with the residual: codes out 50
+// us, 4.7 TB/s, backward 51 + 5 of dw's last sum, 5.0 TB/s; a large copy runs at
+// 4.9).  One row is a launch and the loads' and the sum's latency: 3.7 us.
+// A row's sums are fp64 (its squares pass fp32's range from 2^64 on), dw's parts fp32
+// over at most 64 rows a team, then fp64.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -242,6 +245,15 @@ template <int T, int H, typename XT, typename RT> void launch_norm(const NormArg
                        a);
 }
 
+// Threads a row: enough for its vectors to stay in registers, and few where that
+// leaves lanes idle or waves waiting for each other (bf16 with a residual, in us: 128
+// wide, 65535 rows, 16 threads 13, 64 31; 512 wide, 65535, 64 threads 49, 256 109;
+// 2048 wide, 16384, 256 threads 48.6, 64 50.6; 8192 wide, 4096, 256 threads 51, 1024
+// 60; 2571 wide, 8192, 256 threads 45.6, 512 52).  With a row to a compute unit or
+// fewer the loads' latency is what counts, and one vector a thread is fastest (one row of
+// 4096 3.7 against 4.2, 256 rows 4.4, 4.9; one of 8192 4.2, 5.5, 256 rows 6.0, 7.4; 1024
+// rows of 8192 16.6, 14.1).
+constexpr int64_t kFewRows = 256;
 template <typename XT, typename RT> void run_norm(const NormArgs &a, hipStream_t st)
 {
     if (a.d <= 128)
@@ -250,8 +262,12 @@ template <typename XT, typename RT> void run_norm(const NormArgs &a, hipStream_t
         launch_norm<64, 1, XT, RT>(a, st);
     else if (a.d <= 2048)
         launch_norm<256, 1, XT, RT>(a, st);
+    else if (a.d <= 4096 && a.M <= kFewRows)
+        launch_norm<512, 1, XT, RT>(a, st);
     else if (a.d <= 4096)
         launch_norm<256, 2, XT, RT>(a, st);
+    else if (a.d <= 8192 && a.M <= kFewRows)
+        launch_norm<1024, 1, XT, RT>(a, st);
     else if (a.d <= 8192)
         launch_norm<256, 4, XT, RT>(a, st);
     else if (a.d <= 16384)
@@ -287,10 +303,12 @@ __device__ __forceinline__ void weights_of(const BackArgs &a, int q, float w[8])
     weights_of(n, q, w);
 }
 
-// A workgroup's teams of T threads take every (groups x teams)-th row; dw's sums
-// stay in registers, and the weights where kHold (else they come from cache twice a
-// row); the teams' sums meet in LDS.
-template <int T, int H, bool kHold, bool kAhead, typename UT, typename HT>
+// A workgroup's teams of T threads take every (groups x teams)-th row; the weights
+// and dw's sums stay in registers (8192 x 4096: 55 us, weights from cache twice a row 79).
+// kAhead: the next row is on its way while one is summed, where registers allow that (two
+// vectors a thread: 8192 x 4096 55 us against 57; four: 8192 x 2048 104 against 59).  The
+// teams' sums meet in LDS.
+template <int T, int H, bool kAhead, typename UT, typename HT>
 __global__ __launch_bounds__(T > 256 ? T : 256) void norm_back_kernel(BackArgs a)
 {
     constexpr int kWg = T > 256 ? T : 256, kTeams = kWg / T;
@@ -299,20 +317,10 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void norm_back_kernel(BackArgs a
     const int t = threadIdx.x % T, team = threadIdx.x / T;
     const int nv = (a.d + 7) / 8;
     const int64_t step = a.groups * kTeams;
-    float held[kHold ? H : 1][8], dw[H][8] = {};
-    if constexpr (kHold)
+    float w[H][8], dw[H][8] = {};
 #pragma unroll
-        for (int j = 0; j < H; ++j)
-            weights_of(a, t + j * T, held[j]);
-    auto weight = [&](int j, float w[8]) __attribute__((always_inline)) {
-        if constexpr (kHold) {
-            for (int i = 0; i < 8; ++i)
-                w[i] = held[j][i];
-        } else {
-            asm volatile("" : "+s"(a.weight)); // read here: not before the loop, into registers that are short
-            weights_of(a, t + j * T, w);
-        }
-    };
+    for (int j = 0; j < H; ++j)
+        weights_of(a, t + j * T, w[j]);
     Eight<UT> ur[H];
     Eight<HT> hr[H], rr[H];
     auto fetch = [&](int64_t m) __attribute__((always_inline)) {
@@ -349,12 +357,10 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void norm_back_kernel(BackArgs a
             fetch(m + step); // the next row is on its way while this one is summed
 #pragma unroll
         for (int j = 0; j < H; ++j) {
-            float w[8];
-            weight(j, w);
             for (int i = 0; i < 8; ++i) {
                 const double hd = hv[j][i];
                 ss = __builtin_fma(hd, hd, ss);
-                c = __builtin_fma((double)(uv[j][i] * w[i]), hd, c);
+                c = __builtin_fma((double)(uv[j][i] * w[j][i]), hd, c);
             }
         }
         team_sums<T>(ss, c, red[turn]);
@@ -363,12 +369,11 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void norm_back_kernel(BackArgs a
 #pragma unroll
         for (int j = 0; j < H; ++j) {
             const int q = t + j * T;
-            float o[8] = {}, w[8];
-            weight(j, w);
+            float o[8] = {};
             if (a.dres)
                 vector_values(q, a.d, rr[j], o);
             for (int i = 0; i < 8; ++i) {
-                o[i] = __builtin_fmaf(r, __builtin_fmaf(-hv[j][i], k, uv[j][i] * w[i]), o[i]);
+                o[i] = __builtin_fmaf(r, __builtin_fmaf(-hv[j][i], k, uv[j][i] * w[j][i]), o[i]);
                 dw[j][i] = __builtin_fmaf(uv[j][i], hv[j][i] * r, dw[j][i]);
             }
             if (q < nv)
@@ -487,22 +492,33 @@ struct BackPlan {
     int64_t groups, slice;
     size_t inv, total; // byte offsets in the workspace
 };
-constexpr int64_t kGroups = 512;  // workgroups that share the rows
+// workgroups that share the rows: more leave dw's last sum more parts, fewer leave
+// compute units waiting (256, 512, 1024: 8192 x 4096 80, 55, 66 us; 777 x 2571 fp32 18,
+// 16, 19; 16384 x 2048 -, 59, 64)
+constexpr int64_t kGroups = 512;
 constexpr int64_t kPartRows = 64; // rows whose terms of dw are added in fp32
 
+// Threads a row and vectors a thread.  Narrow rows stay within a wave, whose sums wait
+// for no other (bf16, 2^25 elements, in us: 512 wide, 16 threads of four vectors 58, 64 of
+// one 75; 1024 wide, 64 of two 55, 256 of one 112; 2048 wide, 64 of four 59, 256 of one
+// 65); wide ones take as many threads as hold them in two vectors each (8192 wide, 512 60,
+// 256 of four 64), up to where 1024 have too few registers (16384 wide, 512 of four 82,
+// 1024 of two 232).
 BackPlan plan_back(int64_t M, int64_t d)
 {
     BackPlan p{};
     if (d <= 128)
         p = {16, 1};
     else if (d <= 512)
-        p = {64, 1};
+        p = {16, 4};
+    else if (d <= 1024)
+        p = {64, 2};
     else if (d <= 2048)
-        p = {256, 1};
+        p = {64, 4};
     else if (d <= 4096)
         p = {256, 2};
     else if (d <= 8192)
-        p = {256, 4};
+        p = {512, 2};
     else if (d <= 16384)
         p = {512, 4};
     if (p.T) {
@@ -517,25 +533,27 @@ BackPlan plan_back(int64_t M, int64_t d)
     return p;
 }
 
-template <int T, int H, bool kHold, bool kAhead, typename UT, typename HT> void launch_back(const BackArgs &a, hipStream_t st)
+template <int T, int H, bool kAhead, typename UT, typename HT> void launch_back(const BackArgs &a, hipStream_t st)
 {
-    hipLaunchKernelGGL((norm_back_kernel<T, H, kHold, kAhead, UT, HT>), dim3((unsigned)a.groups), dim3(T > 256 ? T : 256), 0, st, a);
+    hipLaunchKernelGGL((norm_back_kernel<T, H, kAhead, UT, HT>), dim3((unsigned)a.groups), dim3(T > 256 ? T : 256), 0, st, a);
 }
 
 template <typename UT, typename HT> void run_back(const BackArgs &a, const BackPlan &p, float *dw, hipStream_t st)
 {
-    if (p.T == 16)
-        launch_back<16, 1, true, true, UT, HT>(a, st);
+    if (p.T == 16 && p.H == 1)
+        launch_back<16, 1, true, UT, HT>(a, st);
+    else if (p.T == 16)
+        launch_back<16, 4, false, UT, HT>(a, st);
+    else if (p.T == 64 && p.H == 2)
+        launch_back<64, 2, false, UT, HT>(a, st);
     else if (p.T == 64)
-        launch_back<64, 1, true, true, UT, HT>(a, st);
-    else if (p.T == 256 && p.H == 1)
-        launch_back<256, 1, true, true, UT, HT>(a, st);
-    else if (p.T == 256 && p.H == 2)
-        launch_back<256, 2, true, true, UT, HT>(a, st);
+        launch_back<64, 4, false, UT, HT>(a, st);
     else if (p.T == 256)
-        launch_back<256, 4, false, false, UT, HT>(a, st);
+        launch_back<256, 2, true, UT, HT>(a, st);
+    else if (p.T == 512 && p.H == 2)
+        launch_back<512, 2, true, UT, HT>(a, st);
     else if (p.T == 512)
-        launch_back<512, 4, false, false, UT, HT>(a, st);
+        launch_back<512, 4, false, UT, HT>(a, st);
     else {
         hipLaunchKernelGGL((norm_back_long_kernel<UT, HT>), dim3((unsigned)a.M), dim3(kLongT), 0, st, a);
         hipLaunchKernelGGL((weight_long_kernel<UT, HT>),

@@ -108,7 +108,7 @@ def test_gradient(pq, dt, gt):
             _check(pq, n, V, d, dt, gt, tok, 0.75, f"{name} {n} {V} {d}")
 
 
-@pytest.mark.parametrize("n", [16384, 16385, 40000, 70001])
+@pytest.mark.parametrize("n", [8192, 8193, 16384, 16385, 40000, 70001])
 def test_gradient_of_many_tokens(pq, n):
     for V in (2, 300, 70000):
         for name, tok in _lists(np.random.default_rng(n + V), n, V):

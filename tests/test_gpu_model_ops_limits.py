@@ -133,7 +133,7 @@ def test_a_vocabulary_of_many_slices(pq, plenty):
     assert float(out[0, V - 1]) == -np.inf and float(out[0, V - 2]) == 7.0 and float(out[0, 5]) == 4.0
 
 
-@pytest.mark.parametrize("d", [128, 129, 512, 513, 2048, 2049, 4096, 4097, 8192, 8193, 16384, 16385])
+@pytest.mark.parametrize("d", [128, 129, 512, 513, 1024, 1025, 2048, 2049, 4096, 4097, 8192, 8193, 16384, 16385])
 def test_widths_next_to_the_forms_borders(pq, d):
     rng = np.random.default_rng(d)
     h, u = (rng.normal(0, 2, (5, d)).astype(np.float32) for _ in range(2))
@@ -145,6 +145,24 @@ def test_widths_next_to_the_forms_borders(pq, d):
     want, want_dw, size = norm.backward(u.astype(np.float64), h.astype(np.float64), w, 1e-6, 0.0)
     assert np.all(np.abs(_np(dh) - want) <= 1.01 * (8 * U32 * size + U32 * np.abs(want)))
     assert np.all(np.abs(_np(dw) - want_dw) <= 1.01 * 84 * U32 * np.sum(np.abs(u * h) / norm.rms(h.astype(np.float64), 1e-6), axis=0))
+
+
+@pytest.mark.parametrize("M,d", [(256, 2560), (257, 2560), (257, 4096), (256, 4104), (257, 4104), (257, 8192)])
+def test_row_counts_next_to_the_forms_borders(pq, M, d):
+    """Few wide rows take more threads each than many."""
+    import torch
+    rng = np.random.default_rng(M + d)
+    x, res = (rng.normal(0, 2, (M, d)).astype(np.float32) for _ in range(2))
+    w = rng.normal(1, 0.2, d).astype(np.float32)
+    codes = d % 16 == 0
+    y, h, q, s = pq.rms_norm(_cuda(x), _cuda(w), residual=_cuda(res), out_dtype=torch.float32, want_codes=codes)
+    want_h = norm.add(x.astype(np.float64), res.astype(np.float64), False)
+    assert np.array_equal(_np(h), want_h)
+    n = norm.forward(want_h, w, 1e-6, 0.0)
+    assert np.all(np.abs(_np(y) - n) <= 1.01 * 4.04 * U32 * np.abs(n) + 2.0 ** -126)
+    if codes:
+        q2, s2 = pq.fp8_quantize(y)
+        assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2)
 
 
 @pytest.mark.parametrize("n,V,d", [(1024, 32768, 24), (1025, 32768, 24), (1024, 32769, 24), (1024, 16384, 513),
