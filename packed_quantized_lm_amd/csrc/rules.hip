@@ -14,9 +14,12 @@
 // biases are gathered into one word of LDS a column, so that no count is kept
 // in memory between calls and a long history costs its own length only (each
 // slice reads the row's list, from cache).  The K largest of a slice are found
-// among the few that reach a bound: the K-th largest of a wave's 64 lane maxima is
-// reached by K of the wave's columns at least, so no column of the slice below the
-// best of the four waves' bounds is among the slice's K largest.
+// among the few that reach a bound that sixteen of its columns reach.
+// 256 x 151936 fp32 with grammars: 1024 tokens of history, adjusted logits out 61 us,
+// 5.1 TB/s, a copy's rate; 8192 tokens and 64 biases, a draw 67 us: routing the
+// histories 10, this kernel 53 (2.9 TB/s: of it 37 without any rule, each slice a chain
+// of waits with eight workgroups a compute unit to hide them), the draw 7.  One row
+// 12 us, of it two launches' work and waits.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -57,7 +60,7 @@ struct RuleArgs {
     const uint32_t *mask;
     const int32_t *mask_rows;
     int K;
-    uint64_t *part;       // [M][S][K] keys, 0 = none
+    uint64_t *part;       // [M][K][S] keys, 0 = none
     uint16_t *routed;     // [M][L]: the history by slices (column within one, kRoutedPrompt), or null
     uint32_t *ends;       // [M][S]: where each slice's tokens end
 };
@@ -112,58 +115,113 @@ __device__ __forceinline__ uint32_t wave_kth(uint32_t v, int K)
     return t;
 }
 
+// the largest, and the smallest, of the values of lanes that are equal in their last
+// four bits, and of a row of sixteen
+__device__ __forceinline__ uint32_t max_of_rows(uint32_t v)
+{
+    const auto half = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = max((uint32_t)half[0], (uint32_t)half[1]);
+    const auto row = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return max((uint32_t)row[0], (uint32_t)row[1]);
+}
+template <int kCtrl> __device__ __forceinline__ uint32_t min_moved(uint32_t v)
+{
+    return min(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kCtrl, 0xF, 0xF, false));
+}
+__device__ __forceinline__ uint32_t min_of_row(uint32_t v)
+{
+    v = min_moved<kDppQuadXor1>(v);
+    v = min_moved<kDppQuadXor2>(v);
+    v = min_moved<kDppHalfMirror>(v);
+    return min_moved<kDppRowMirror>(v);
+}
+
 // The K largest of a workgroup's keys, in order, written by best(rank, key).  A key
 // is order << 32 | place, 0 for none; key(thread, e), e < E, reads them from LDS, and
-// top is the largest order of the thread's own.  At most K lanes of a wave reach its
-// bound, so that a few lanes' keys are left to look through, by all threads.
+// top is the largest order of the thread's own.  The keys are in sixteen groups (threads
+// equal in their last four bits), so sixteen of them, at least K, reach the least of
+// the groups' largest, and few others do (of 4096 random ones some 45); the lanes whose
+// largest does are looked through by all threads (256 x 151936 without rules 46 us, by
+// the waves' bounds alone 53).  Where many do (equal values, a group without any), by a
+// bound of a wave's own: at most K of its lanes reach that.
 template <int NT, int E, typename Key, typename Best>
 __device__ __forceinline__ void block_top(int K, uint32_t top, Key key, Best best)
 {
-    constexpr int kList = 256; // at least NT / 64 K; more only where one lane holds many of the slice's largest
+    // at least NT / 64 K, which a wave's own bounds leave (more only where one lane holds
+    // many of the slice's largest), and no more than leaves rules_kernel's eight
+    // workgroups a compute unit their LDS (seven: 256 x 151936 with rules 77 us, eight 73)
+    constexpr int kList = 192;
+    constexpr int kGroups = 16, kFewLanes = NT / 2;
+    static_assert(kGroups >= kTopKMax);
+    __shared__ uint32_t tops[NT / 64][kGroups];
     __shared__ uint64_t bounds[NT / 64];
     __shared__ uint64_t list[kList];
     __shared__ uint32_t n_list, n_lanes;
     __shared__ uint32_t ranks[64];
     __shared__ uint16_t lanes[NT];
     const int tid = threadIdx.x;
-    auto first = [&](uint32_t t) { // the largest place of the thread's keys of order t
-        uint32_t place = 0;
-#pragma unroll 1
-        for (int e = 0; e < E; ++e) {
-            const uint64_t k = key(tid, e);
-            place = (uint32_t)(k >> 32) == t ? max(place, (uint32_t)k) : place;
-        }
-        return place;
-    };
-    const uint32_t t = wave_kth(top, K);
-    uint32_t low = 0;
-    if (t != 0 && __builtin_popcountll(__ballot(top >= t)) > K) // several lanes at the bound's value: by place
-        low = wave_kth(top == t ? first(t) : 0, K - __builtin_popcountll(__ballot(top > t)));
-    if ((tid & 63) == 0)
-        bounds[tid >> 6] = (uint64_t)t << 32 | low;
+    const uint32_t largest = max_of_rows(top);
+    if ((tid & 63) < kGroups)
+        tops[tid >> 6][tid & 63] = largest;
     if (tid < 64)
         ranks[tid] = 0;
     if (tid == 0)
         n_list = n_lanes = 0;
     __syncthreads();
-    uint64_t bound = bounds[0];
+    uint32_t least = tops[0][tid & (kGroups - 1)];
 #pragma unroll
     for (int w = 1; w < NT / 64; ++w)
-        bound = umax64(bound, bounds[w]);
-    const uint32_t least = (uint32_t)(bound >> 32);
-    if (top != 0 && top >= least && (top > least || (uint32_t)bound == 0 || first(least) >= (uint32_t)bound))
+        least = max(least, tops[w][tid & (kGroups - 1)]);
+    least = __builtin_amdgcn_readfirstlane(min_of_row(least));
+    uint64_t bound = (uint64_t)least << 32;
+    if (top != 0 && top >= least)
         lanes[atomicAdd(&n_lanes, 1u)] = (uint16_t)tid;
     __syncthreads();
+    auto gather = [&]() __attribute__((always_inline)) {
 #pragma unroll 1
-    for (int i = tid; i < (int)n_lanes * E; i += NT) {
-        const uint64_t k = key(lanes[i / E], i % E);
-        if (k >= bound && k != 0) {
-            const uint32_t to = atomicAdd(&n_list, 1u); // in any order: keys are distinct and ranked below
-            if (to < kList)
-                list[to] = k;
+        for (int i = tid; i < (int)n_lanes * E; i += NT) {
+            const uint64_t k = key(lanes[i / E], i % E);
+            if (k >= bound && k != 0) {
+                const uint32_t to = atomicAdd(&n_list, 1u); // in any order: keys are distinct and ranked below
+                if (to < kList)
+                    list[to] = k;
+            }
         }
+        __syncthreads();
+    };
+    const bool few = n_lanes <= (uint32_t)kFewLanes; // of all threads
+    if (few)
+        gather();
+    if (!few || n_list > (uint32_t)kList) {
+        auto first = [&](uint32_t t) { // the largest place of the thread's keys of order t
+            uint32_t place = 0;
+#pragma unroll 1
+            for (int e = 0; e < E; ++e) {
+                const uint64_t k = key(tid, e);
+                place = (uint32_t)(k >> 32) == t ? max(place, (uint32_t)k) : place;
+            }
+            return place;
+        };
+        const uint32_t t = wave_kth(top, K);
+        uint32_t low = 0;
+        if (t != 0 && __builtin_popcountll(__ballot(top >= t)) > K) // several lanes at the bound's value: by place
+            low = wave_kth(top == t ? first(t) : 0, K - __builtin_popcountll(__ballot(top > t)));
+        if ((tid & 63) == 0)
+            bounds[tid >> 6] = (uint64_t)t << 32 | low;
+        __syncthreads(); // the counts have been read
+        if (tid == 0)
+            n_list = n_lanes = 0;
+        __syncthreads();
+        bound = bounds[0];
+#pragma unroll
+        for (int w = 1; w < NT / 64; ++w)
+            bound = umax64(bound, bounds[w]);
+        least = (uint32_t)(bound >> 32);
+        if (top != 0 && top >= least && (top > least || (uint32_t)bound == 0 || first(least) >= (uint32_t)bound))
+            lanes[atomicAdd(&n_lanes, 1u)] = (uint16_t)tid;
+        __syncthreads();
+        gather();
     }
-    __syncthreads();
     const int n = (int)n_list;
     if (n <= 64) { // a key's rank, counted by a thread of each wave
         const int c = tid & 63, part = tid >> 6;
@@ -225,6 +283,7 @@ template <int NT, int E, typename T> struct Slice {
     Row r;
     const int32_t *h;
     i32x4u tok[kAhead];
+    int routed, bias; // the first of a routed history's words and of the row's bias columns
     Eight<T> raw[kVecs];
     uint32_t bits[kVecs];
 
@@ -262,10 +321,14 @@ template <int NT, int E, typename T> struct Slice {
             if (a.L > 0)
                 tokens(0, a.L);
         }
+        if (a.bias_ids && a.B > 0)
+            bias = a.bias_ids[m * a.ldb + min((int)threadIdx.x, a.B - 1)];
         const int q0 = base / 8 + (int)threadIdx.x;
 #pragma unroll
         for (int j = 0; j < kVecs; ++j)
             raw[j] = load_vector<E == 8>(y, q0 + j * NT, a.V);
+        if (a.routed && to > from)
+            routed = a.routed[m * a.L + min(from + threadIdx.x, to - 1)];
         if (a.history && !a.routed) {
             n = max(0, min(same(len), a.L));
             prompt = same(head);
@@ -309,7 +372,7 @@ template <int NT, int E, typename T, bool kSelect> __global__ __launch_bounds__(
         if (a.bias_ids) {
             const int32_t *ids = a.bias_ids + m * a.ldb;
             for (int j = threadIdx.x; j < a.B; j += NT) {
-                const uint32_t c = (uint32_t)ids[j] - (uint32_t)base;
+                const uint32_t c = (uint32_t)(j < NT ? s.bias : ids[j]) - (uint32_t)base;
                 if (c < (uint32_t)cols && atomicMax(&word[c], (uint32_t)(j + 1) << kBiasAt) == 0) {
                     const uint32_t i = atomicAdd(&n_listed, 1u); // the first to name the column
                     if (i < (uint32_t)kListed)
@@ -321,7 +384,7 @@ template <int NT, int E, typename T, bool kSelect> __global__ __launch_bounds__(
         if (a.routed) {
             const uint16_t *mine = a.routed + m * a.L;
             for (uint32_t i = s.from + threadIdx.x; i < s.to; i += NT) {
-                const uint32_t t = mine[i], c = t & (kRoutedPrompt - 1);
+                const uint32_t t = i - s.from < NT ? s.routed : mine[i], c = t & (kRoutedPrompt - 1);
                 if ((t & kRoutedPrompt ? atomicOr(&word[c], kPrompt) : atomicAdd(&word[c], 1u)) == 0) {
                     const uint32_t at = atomicAdd(&n_listed, 1u);
                     if (at < (uint32_t)kListed)
@@ -427,7 +490,7 @@ template <int NT, int E, typename T, bool kSelect> __global__ __launch_bounds__(
             store_vector((T *)a.out + m * a.ldo, q, a.V, v);
     }
     if constexpr (kSelect) {
-        uint64_t *part = a.part + (m * a.S + sl) * a.K;
+        uint64_t *part = a.part + m * a.S * a.K + sl; // the slices' best first: draw_kernel's groups have each a few
         block_top<NT, E>(
             a.K, 8 * (int)threadIdx.x < cols ? order_of(most) : 0u,
             [&](int thread, int e) {
@@ -435,7 +498,7 @@ template <int NT, int E, typename T, bool kSelect> __global__ __launch_bounds__(
                 return c < cols ? (uint64_t)order_of(__uint_as_float(word[c])) << 32 | ~((uint32_t)base + (uint32_t)c)
                                 : 0;
             },
-            [&](int rank, uint64_t k) { part[rank] = k; });
+            [&](int rank, uint64_t k) { part[rank * a.S] = k; });
     }
 }
 
@@ -524,13 +587,24 @@ __global__ __launch_bounds__(kRouteT) void route_kernel(RuleArgs a, int shift)
     const int64_t m = blockIdx.x;
     const int32_t *h = a.history + m * a.ldh;
     const int n = a.lengths ? max(0, min(a.lengths[m], a.L)) : a.L, prompt = a.prompts ? a.prompts[m] : 0;
+    constexpr int kHeld = 8; // a thread's tokens in flight, and kept for the second pass where these are all
+    uint32_t t[kHeld];
+    auto load = [&](int i0) __attribute__((always_inline)) { // past the end none, negative ones above V
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k)
+            t[k] = (uint32_t)h[min(i0 + k * kRouteT + tid, n - 1)];
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k)
+            t[k] = i0 + k * kRouteT + tid < n ? t[k] : ~0u;
+    };
     count[tid] = 0;
     __syncthreads();
-#pragma unroll 4
-    for (int i = tid; i < n; i += kRouteT) {
-        const uint32_t t = (uint32_t)h[i];
-        if (t < (uint32_t)a.V) // negative tokens are above it
-            atomicAdd(&count[t >> shift], 1u);
+    for (int i0 = 0; i0 < n; i0 += kHeld * kRouteT) {
+        load(i0);
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k)
+            if (t[k] < (uint32_t)a.V)
+                atomicAdd(&count[t[k] >> shift], 1u);
     }
     __syncthreads();
     const uint32_t mine = count[tid];
@@ -549,19 +623,22 @@ __global__ __launch_bounds__(kRouteT) void route_kernel(RuleArgs a, int shift)
         a.ends[m * a.S + tid] = run;
     __syncthreads();
     uint16_t *to = a.routed + m * a.L;
-#pragma unroll 4
-    for (int i = tid; i < n; i += kRouteT) {
-        const uint32_t t = (uint32_t)h[i];
-        if (t < (uint32_t)a.V)
-            to[atomicAdd(&count[t >> shift], 1u)] =
-                (uint16_t)((t & ((1u << shift) - 1)) | (i < prompt ? kRoutedPrompt : 0));
+    for (int i0 = 0; i0 < n; i0 += kHeld * kRouteT) {
+        if (n > kHeld * kRouteT)
+            load(i0);
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k)
+            if (t[k] < (uint32_t)a.V)
+                to[atomicAdd(&count[t[k] >> shift], 1u)] =
+                    (uint16_t)((t[k] & ((1u << shift) - 1)) | (i0 + k * kRouteT + tid < prompt ? kRoutedPrompt : 0));
     }
 }
 
 // columns a thread: the more, the fewer slices go through a row's lists; fewer where
-// that leaves compute units without a workgroup (twice as many, in half as many
-// workgroups a compute unit, run alike), and for rows shorter than a vector, which only
-// that form reads element by element
+// that leaves compute units without a workgroup (rows of 151936 with 1024 tokens, a
+// draw, in us: 16 columns, 8 columns: one row 15.0, 14.4; 16 rows 22.5, 21.3; 32 rows
+// 26.1, 26.9; 128 rows 41, 49), and for rows shorter than a vector, which only that form
+// reads element by element
 int columns_of(int64_t M, int64_t V) { return V >= 8 && M * ((V + kNT * 16 - 1) / (kNT * 16)) >= 1024 ? 16 : 8; }
 int64_t slices_of(int64_t M, int64_t V)
 {
