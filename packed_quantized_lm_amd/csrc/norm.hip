@@ -317,10 +317,29 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void norm_back_kernel(BackArgs a
     const int t = threadIdx.x % T, team = threadIdx.x / T;
     const int nv = (a.d + 7) / 8;
     const int64_t step = a.groups * kTeams;
-    float w[H][8], dw[H][8] = {};
+    constexpr bool kShared = T >= 512 && H == 4; // a thread's weights in LDS: 256 registers do not hold them too
+    __shared__ f32x4 own[kShared ? H * 2 * T : 1];
+    float held[kShared ? 1 : H][8], dw[H][8] = {};
 #pragma unroll
-    for (int j = 0; j < H; ++j)
-        weights_of(a, t + j * T, w[j]);
+    for (int j = 0; j < H; ++j) {
+        float *w = held[kShared ? 0 : j];
+        weights_of(a, t + j * T, w);
+        if constexpr (kShared) { // read by this thread alone
+            own[2 * j * T + t] = f32x4{w[0], w[1], w[2], w[3]};
+            own[(2 * j + 1) * T + t] = f32x4{w[4], w[5], w[6], w[7]};
+        }
+    }
+    auto weight = [&](int j, float w[8]) __attribute__((always_inline)) {
+        if constexpr (kShared) {
+            const f32x4 lo = own[2 * j * T + t], hi = own[(2 * j + 1) * T + t];
+            for (int i = 0; i < 4; ++i) {
+                w[i] = lo[i];
+                w[4 + i] = hi[i];
+            }
+        } else
+            for (int i = 0; i < 8; ++i)
+                w[i] = held[j][i];
+    };
     Eight<UT> ur[H];
     Eight<HT> hr[H], rr[H];
     auto fetch = [&](int64_t m) __attribute__((always_inline)) {
@@ -357,10 +376,12 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void norm_back_kernel(BackArgs a
             fetch(m + step); // the next row is on its way while this one is summed
 #pragma unroll
         for (int j = 0; j < H; ++j) {
+            float w[8];
+            weight(j, w);
             for (int i = 0; i < 8; ++i) {
                 const double hd = hv[j][i];
                 ss = __builtin_fma(hd, hd, ss);
-                c = __builtin_fma((double)(uv[j][i] * w[j][i]), hd, c);
+                c = __builtin_fma((double)(uv[j][i] * w[i]), hd, c);
             }
         }
         team_sums<T>(ss, c, red[turn]);
@@ -369,11 +390,12 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void norm_back_kernel(BackArgs a
 #pragma unroll
         for (int j = 0; j < H; ++j) {
             const int q = t + j * T;
-            float o[8] = {};
+            float o[8] = {}, w[8];
+            weight(j, w);
             if (a.dres)
                 vector_values(q, a.d, rr[j], o);
             for (int i = 0; i < 8; ++i) {
-                o[i] = __builtin_fmaf(r, __builtin_fmaf(-hv[j][i], k, uv[j][i] * w[j][i]), o[i]);
+                o[i] = __builtin_fmaf(r, __builtin_fmaf(-hv[j][i], k, uv[j][i] * w[i]), o[i]);
                 dw[j][i] = __builtin_fmaf(uv[j][i], hv[j][i] * r, dw[j][i]);
             }
             if (q < nv)
