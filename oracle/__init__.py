@@ -32,6 +32,10 @@ softmax  log-normaliser lse = log sum_v exp(logits) and cross-entropy
 losses   token log probabilities, the clipped policy loss with a KL term and
          the preference loss over logits, with the logits' gradients
 fp8      matrices in e4m3 with a scale per block of 128, and their product
+norm     the root-mean-square norm with the residual's addition, and its gradients
+embedding
+         rows of a table by token, and the table's gradient
+rules    penalties, biases and grammar masks on logits
 
 Parity pins (what each function is checked against, in tests/):
   quant   -- closed-form bounds |x - s q| <= s/2, ranges, idempotence, and
@@ -51,6 +55,10 @@ Parity pins (what each function is checked against, in tests/):
              (equal logits, no margin), the cross-entropy above
   fp8     -- every e4m3 code against torch's, ties and ends, the nearest code by
              exact fractions, products of small integers
+  norm    -- closed forms, differences of the forward, scale invariance, bf16
+             rounding against torch's
+  embedding -- the one-hot products and differences
+  rules   -- worked examples, neutral rules, select's top-k and draw, mask words
   packer  -- correction: Eckart-Young-Mirsky tail energy, brute force over
              random and grid rank-r candidates, the eigenvector route, the
              p = 1/2 identity with eq 1, the isotropic (C = I) reduction;

@@ -60,8 +60,9 @@ __device__ __forceinline__ u32x2 codes8_exact(const float v[8], float s)
 
 // The same at a fifth of the work: the quotient by the scale's reciprocal is within
 // 2^-22 of the exact one, so where it converts alike 2^-21 below and above itself,
-// that is the code.  The others (one vector in some 2^14), NaN (its code is
-// 0x7f without a sign) and the ends of the scales' range go the exact way.
+// that is the code.  The others (one vector of fp32 values in some 2^14; more of bf16
+// ones, whose quotients are true ties at times), NaN (its code is 0x7f without a sign)
+// and the ends of the scales' range go the exact way.
 __device__ __forceinline__ u32x2 codes8(const float v[8], float s)
 {
     const float r = __builtin_amdgcn_rcpf(s);

@@ -52,9 +52,10 @@ __device__ __forceinline__ void load8(const uint16_t *p, float v[8])
 
 // One row's blocks: 16 lanes a block, 8 columns a lane, so that a block's
 // largest magnitude takes four exchanges and a lane one load and one store
-// (2048 x 4096 bf16: 16 us against 5 of its bytes, the vector units busy
-// throughout with the exact quotients: a division, its remainder and the last
-// bit of every element; one row 5 us, a launch).
+// (2048 x 4096 bf16: 17 us against 5 of its bytes, the vector units busy
+// throughout: finding a thread's row divides 64-bit numbers, and the quotients of
+// bf16 values are true ties often enough for some third of the waves to take the
+// exact way; one row 5 us, a launch).
 template <typename T>
 __global__ __launch_bounds__(256) void quant_rows_kernel(const T *x, int64_t ldx, int64_t rows, int64_t cols,
                                                          uint8_t *q, int64_t ldq, float *s, int64_t lds)
