@@ -635,7 +635,7 @@ archead_status archead_rms_norm_backward(int64_t M, int64_t d, const void *dy, i
  * scales   DEVICE fp32, scales[(token / 128) * lds + j / 128], lds >= ceil(d / 128),
  *          for 8-bit tables; else unused.
  * tokens   DEVICE int32 n.
- * out      DEVICE n x d, fp32 or bf16 (out_type), row stride ldo.
+ * out      DEVICE n x d, fp32 or bf16 (out_type), row stride ldo; overlaps nothing else.
  * Strides lie in [row length, 2^40], scale is finite; streams as archead_rms_norm.
  */
 archead_status archead_embed(int64_t n, int64_t V, int64_t d, const void *table, int table_type, int64_t ldt,
@@ -651,7 +651,7 @@ archead_status archead_embed(int64_t n, int64_t V, int64_t d, const void *table,
  * rows of dout may hold anything.
  *
  * dout     DEVICE n x d, fp32 or bf16 (dout_type), row stride ldo.
- * dtable   DEVICE V x d, fp32 or bf16 (grad_type), row stride ldt.
+ * dtable   DEVICE V x d, fp32 or bf16 (grad_type), row stride ldt; overlaps nothing else.
  * ws       DEVICE workspace of archead_embed_workspace(n, V, d) bytes, 16-byte
  *          aligned, contents irrelevant, the call's own until the stream has
  *          passed it: calls, or captured graphs, that may overlap need one each.

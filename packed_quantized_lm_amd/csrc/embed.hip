@@ -750,6 +750,8 @@ extern "C" archead_status archead_embed(int64_t n, int64_t V, int64_t d, const v
         return api_fail(ARCHEAD_EINVAL, "table aligned to its element; 8-bit tables and their row strides to 16 bytes");
     if (misaligned(out, out_type) || misaligned(tokens, ARCHEAD_F32))
         return api_fail(ARCHEAD_EINVAL, "buffers must be aligned to their element");
+    if (out == table || out == tokens)
+        return api_fail(ARCHEAD_EINVAL, "out overlaps what is read");
     const LookArgs a{n, V, (int)d, ldt, lds, ldo, table, scales, tokens, out, scale, pad};
     hipStream_t stream = (hipStream_t)hip_stream;
     if (f8)
@@ -794,6 +796,8 @@ extern "C" archead_status archead_embed_backward(int64_t n, int64_t V, int64_t d
         return api_fail(ARCHEAD_EINVAL, "dout, tokens and dtable are required");
     if (misaligned(dout, dout_type) || misaligned(dtable, grad_type) || misaligned(tokens, ARCHEAD_F32))
         return api_fail(ARCHEAD_EINVAL, "buffers must be aligned to their element");
+    if (dtable == dout || dtable == tokens)
+        return api_fail(ARCHEAD_EINVAL, "dtable overlaps what is read");
     if (!ws || (uintptr_t)ws % 16)
         return api_fail(ARCHEAD_EINVAL, "a 16-byte aligned workspace is required");
     if (ws_bytes < w.total)

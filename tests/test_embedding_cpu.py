@@ -29,7 +29,7 @@ def _look(lib, n=2, V=8, d=16, table=B, tt=1, ldt=16, scales=B, lds=1, tok=B, pa
     (dict(tt=2, lds=0), binding.EINVAL), (dict(table=None), binding.EINVAL), (dict(tok=None), binding.EINVAL),
     (dict(out=None), binding.EINVAL), (dict(tt=2, scales=None), binding.EINVAL), (dict(table=ODD), binding.EINVAL),
     (dict(tt=2, table=ctypes.c_void_p(4104)), binding.EINVAL), (dict(tt=2, ldt=24), binding.EINVAL),
-    (dict(out=ODD), binding.EINVAL), (dict(tok=ctypes.c_void_p(4098)), binding.EINVAL)])
+    (dict(out=B), binding.EINVAL), (dict(table=C), binding.EINVAL), (dict(out=ODD), binding.EINVAL), (dict(tok=ctypes.c_void_p(4098)), binding.EINVAL)])
 def test_lookup_refusals(lib, over, status):
     assert _look(lib, **over) == status
     assert lib.archead_last_error().decode()
@@ -47,7 +47,7 @@ def _grad(lib, n=2, V=8, d=16, dout=B, dt=1, ldo=16, tok=B, pad=-1, scale=1.0, a
     (dict(ldo=15), binding.EINVAL), (dict(ldt=15), binding.EINVAL), (dict(dout=None), binding.EINVAL),
     (dict(tok=None), binding.EINVAL), (dict(dtable=None), binding.EINVAL), (dict(dtable=ODD), binding.EINVAL),
     (dict(dout=ODD), binding.EINVAL), (dict(ws=None), binding.EINVAL), (dict(ws=ctypes.c_void_p(4104)), binding.EINVAL),
-    (dict(size=15), binding.EINVAL)])
+    (dict(size=15), binding.EINVAL), (dict(dtable=B), binding.EINVAL), (dict(dout=C), binding.EINVAL)])
 def test_gradient_refusals(lib, over, status):
     assert _grad(lib, **over) == status
     assert lib.archead_last_error().decode()

@@ -153,6 +153,31 @@ def test_ties_sorted_and_equal_rows(pq, V):
                 assert int(samples[m]) == -1
 
 
+@pytest.mark.parametrize("M,V", [(1, 2048), (1, 5000), (1030, 4096), (300, 20000)])
+def test_rows_whose_largest_lie_together(pq, M, V):
+    """Few threads hold more of the largest than the list of candidates: a sixteenth of the columns without a
+    large value, one wave's sixteen threads rising, and one thread's columns among them."""
+    rng = np.random.default_rng(V)
+    c = np.arange(V)
+    lane, order = c // 8 % 16, rng.permutation(V) / V
+    thread = c // 8 % 256
+    y = np.stack([np.where(lane == 0, -3.0, np.where(lane < 8, 1 + order, -10 - order)),
+                  np.where(lane == 5, -INF, order),
+                  np.where(thread < 16, thread + 0.001 * (c // 2048 * 8 + c % 8), -1.0 - order),
+                  np.where(thread < 32, 100 - thread + 0.001 * (c % 8), -1.0),
+                  np.where(thread % 64 < 16, 7.0, order), np.where(lane < 15, 2.0, -INF)]).astype(np.float32)
+    rows = np.arange(M) % len(y)
+    for K in (1, 5, 16):
+        values, ids, _ = pq.sample_logits(_cuda(y)[_cuda(rows)].contiguous(), K)
+        for m in range(min(M, 12)):
+            v, i = rules.top(y[rows[m]], K)
+            assert np.array_equal(ids[m].cpu().numpy(), i), (K, m)
+            assert np.array_equal(values[m].cpu().numpy(), v)
+    for r in range(len(y)) if M == 1 else ():  # each row alone
+        values, ids, _ = pq.sample_logits(_cuda(y[r:r + 1]), 16)
+        assert np.array_equal(ids[0].cpu().numpy(), rules.top(y[r], 16)[1]), r
+
+
 def test_numbers_that_are_not_numbers(pq):
     V = 700
     y = np.random.default_rng(0).normal(0, 1, (6, V)).astype(np.float32)
