@@ -612,7 +612,7 @@ archead_status archead_rms_norm(int64_t M, int64_t d, const void *x, int x_type,
  *          passed it: calls, or captured graphs, that may overlap need one each.
  * Sizes, alignment, streams and numerics as archead_rms_norm: the row's two sums
  * are fp64, dh is fp32 rounded once, dweight's terms are added in fp32 over at most
- * 64 rows and then in fp64, in a fixed order.
+ * 64 rows, those sums in fp32 over at most 16 and then in fp64, in a fixed order.
  */
 archead_status archead_rms_norm_workspace(int64_t M, int64_t d, uint64_t *bytes);
 archead_status archead_rms_norm_backward(int64_t M, int64_t d, const void *dy, int dy_type, int64_t ldy, const void *h,

@@ -370,12 +370,16 @@ __device__ __forceinline__ void add_some(Row row, int64_t i, int64_t left, int q
                 s[e] += v[e];
         }
 }
-// the sum of rows row(from) .. row(to - 1) onto s; most runs are one row
-template <bool kShort, typename T, typename Row>
+// The sum of rows row(from) .. row(to - 1) onto s; most runs are one row.  kDeep: eight
+// of a long run in flight in place of four.
+template <bool kShort, bool kDeep, typename T, typename Row>
 __device__ __forceinline__ void add_rows(Row row, int64_t from, int64_t to, int q, int d, float s[8])
 {
-    constexpr int kFly = 4; // eight: more registers, fewer waves (8192 x 4096 into 151936: 264 us against 256)
+    constexpr int kFly = 4;
     int64_t i = from;
+    if (kDeep)
+        for (; to - i >= 8; i += 8)
+            add_some<8, kShort, T>(row, i, 8, q, d, s);
     for (; to - i > 2; i += kFly)
         add_some<kFly, kShort, T>(row, i, to - i, q, d, s);
     for (; i < to; ++i)
@@ -383,20 +387,20 @@ __device__ __forceinline__ void add_rows(Row row, int64_t from, int64_t to, int 
 }
 // Entries [from, to) of the sorted list (level 0), or of the parts of a level below.
 // All 64 lanes come along, whatever their columns: they hold the entries' places.
-template <bool kShort, typename T>
+template <bool kShort, bool kDeep, typename T>
 __device__ __forceinline__ void add_entries(const GradArgs &a, int level, int64_t from, int64_t to, int q, float s[8])
 {
     if (level == 0) {
         for (int64_t b = from; b < to; b += 64) {
             const uint32_t at = a.sorted[min(b + (int64_t)(threadIdx.x & 63), to - 1)].at;
-            add_rows<kShort, T>(
+            add_rows<kShort, kDeep, T>(
                 [&](int64_t i) {
                     return (const T *)a.dout + (int64_t)(uint32_t)__builtin_amdgcn_readlane(at, (int)i) * a.ldo;
                 },
                 0, min(to - b, (int64_t)64), q, a.d, s);
         }
     } else
-        add_rows<kShort, float>([&](int64_t i) { return a.part[level - 1] + i * a.d; }, from, to, q, a.d, s);
+        add_rows<kShort, kDeep, float>([&](int64_t i) { return a.part[level - 1] + i * a.d; }, from, to, q, a.d, s);
 }
 
 // A workgroup per part and kCols columns, for parts whose entries are one token's: its
@@ -417,7 +421,7 @@ template <bool kShort, typename T> __global__ __launch_bounds__(256) void part_k
     const int q = (int)(blockIdx.x % a.tiles) * (kCols / 8) + lane;
     const int64_t from = g * kGroup + wave * (kGroup / 4);
     float s[8] = {};
-    add_entries<kShort, T>(a, level, from, from + kGroup / 4, q, s);
+    add_entries<kShort, true, T>(a, level, from, from + kGroup / 4, q, s);
     for (int e = 0; e < 8; ++e)
         meet[wave][lane][e] = s[e];
     __syncthreads();
@@ -440,7 +444,7 @@ template <bool kShort, typename GT> __device__ __forceinline__ void put_row(cons
 }
 
 // A wave per entry of the sorted list that begins a run, and kCols columns.
-template <bool kShort, typename T, typename GT> __global__ __launch_bounds__(256) void grad_kernel(GradArgs a)
+template <bool kShort, bool kDeep, typename T, typename GT> __global__ __launch_bounds__(256) void grad_kernel(GradArgs a)
 {
     const int lane = threadIdx.x & 63;
     const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -473,7 +477,7 @@ template <bool kShort, typename T, typename GT> __global__ __launch_bounds__(256
     // next level, and so on; then back down
     float s[8] = {};
     auto add_held = [&](int64_t first, int64_t last) __attribute__((always_inline)) { // at most 62 entries from i on
-        add_rows<kShort, T>(
+        add_rows<kShort, kDeep, T>(
             [&](int64_t e) {
                 return (const T *)a.dout + (int64_t)(uint32_t)__builtin_amdgcn_readlane(p.at, (int)(e - i) + 1) * a.ldo;
             },
@@ -493,7 +497,7 @@ template <bool kShort, typename T, typename GT> __global__ __launch_bounds__(256
         if (l == 0)
             add_held(from, lo * kGroup);
         else
-            add_entries<kShort, T>(a, l, from, lo * kGroup, q, s);
+            add_entries<kShort, kDeep, T>(a, l, from, lo * kGroup, q, s);
         tail_from[l] = hi * kGroup;
         tail_to[l] = to;
         from = lo;
@@ -503,7 +507,7 @@ template <bool kShort, typename T, typename GT> __global__ __launch_bounds__(256
         if (l == 0 && top == 0) // no whole part: all of a run of 62 at most
             add_held(tail_from[0], tail_to[0]);
         else
-            add_entries<kShort, T>(a, l, tail_from[l], tail_to[l], q, s);
+            add_entries<kShort, kDeep, T>(a, l, tail_from[l], tail_to[l], q, s);
     }
     if (8 * q < a.d)
         put_row<kShort, GT>(a, key, q, s);
@@ -658,6 +662,19 @@ GradWs grad_ws(int64_t n, int64_t V, int64_t d)
     return w;
 }
 
+template <bool kShort, bool kDeep, typename T> void run_heads(const GradArgs &a, int grad_type, hipStream_t st)
+{
+    const dim3 grid((unsigned)((a.n * a.tiles + 3) / 4));
+    if (grad_type == ARCHEAD_F32)
+        hipLaunchKernelGGL((grad_kernel<kShort, kDeep, T, float>), grid, dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((grad_kernel<kShort, kDeep, T, uint16_t>), grid, dim3(256), 0, st, a);
+}
+// waves of the last launch up to which the longest run's chain of waits counts, not how
+// many waves the registers leave (a whole gradient, deep, not, in us: 4099 x 257 fp32 26.0,
+// 28.0; 4096 x 2048 bf16 40.7, 44.0; 8192 x 1000 fp32 61, 66; 8192 x 4096 bf16 265, 260;
+// 65536 x 2048 bf16 182, 167)
+constexpr int64_t kDeepWaves = 16384;
 template <bool kShort, typename T> void run_grad(const GradArgs &a, const GradWs &w, int grad_type, hipStream_t st)
 {
     for (int l = 0; l < w.levels; ++l)
@@ -666,10 +683,7 @@ template <bool kShort, typename T> void run_grad(const GradArgs &a, const GradWs
     const int64_t waves = a.n * a.tiles;
     if (waves == 0)
         return;
-    if (grad_type == ARCHEAD_F32)
-        hipLaunchKernelGGL((grad_kernel<kShort, T, float>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, a);
-    else
-        hipLaunchKernelGGL((grad_kernel<kShort, T, uint16_t>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, a);
+    waves <= kDeepWaves ? run_heads<kShort, true, T>(a, grad_type, st) : run_heads<kShort, false, T>(a, grad_type, st);
 }
 // Whether the gradient is taken in one launch: few tokens, and a table small enough that
 // the workgroups' passes over the tokens cost less than sorting them (64 tokens into

@@ -166,7 +166,7 @@ def test_row_counts_next_to_the_forms_borders(pq, M, d):
 
 
 @pytest.mark.parametrize("n,V,d", [(1024, 32768, 24), (1025, 32768, 24), (1024, 32769, 24), (1024, 16384, 513),
-                                   (1024, 16385, 513), (8223, 40, 8), (8224, 40, 8)])
+                                   (1024, 16385, 513), (8223, 40, 8), (8224, 40, 8), (4096, 400, 2048), (4097, 400, 2048)])
 def test_token_counts_next_to_the_forms_borders(pq, n, V, d):
     rng = np.random.default_rng(n + V)
     tok = np.where(rng.random(n) < 0.4, V - 1, rng.integers(0, V, n)).astype(np.int32)
