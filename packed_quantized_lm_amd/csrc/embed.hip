@@ -688,7 +688,7 @@ template <bool kShort, typename T> void run_grad(const GradArgs &a, const GradWs
 // Whether the gradient is taken in one launch: few tokens, and a table small enough that
 // the workgroups' passes over the tokens cost less than sorting them (64 tokens into
 // 2048 x 256: 6.5 us against 14; 1000 into 32000 x 512: 22, 26; 1000 into 32000 x 2048:
-// 67, 38; 4099 into 2048 x 257: 39, 28).
+// 67, 38; 4099 into 2048 x 257: 39, 26).
 bool scans(int64_t n, int64_t V, int64_t d)
 {
     return n <= kScanMax && V * ((d + kCols - 1) / kCols) <= (1 << 15);
