@@ -720,7 +720,8 @@ archead_status archead_adjust_logits(int64_t M, int64_t V, const void *logits, i
  *
  * K             1 <= K <= min(16, V), else ARCHEAD_ESHAPE.
  * temperature   finite and > 0, for all rows, unless temperatures (DEVICE fp32 M) is
- *               given; rows whose own is not > 0 take their largest.
+ *               given; rows whose own is not > 0 take their largest, at +inf all of
+ *               the K weigh the same.  A y4 of -inf weighs nothing at any temperature.
  * u             DEVICE fp32 M in [0, 1), required with samples.
  * values        DEVICE fp32 M x K, or NULL.  indices  DEVICE int32 M x K, or NULL.
  * samples       DEVICE int32 M, or NULL; one of the three is required.  -1 for a row

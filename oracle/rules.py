@@ -47,7 +47,8 @@ def draw(values, indices, u, temperature) -> int:
         return -1
     if v[0] == np.inf or not temperature > 0:
         return int(indices[0])
-    w = np.exp((v - v[0]) / np.float64(temperature))
+    with np.errstate(invalid="ignore"):
+        w = np.where(v > -np.inf, np.exp((v - v[0]) / np.float64(temperature)), 0.0)
     run = np.cumsum(w)
     over = np.nonzero(run > np.float64(u) * run[-1])[0]
     return int(indices[over[0] if len(over) else np.nonzero(w > 0)[0][-1]])

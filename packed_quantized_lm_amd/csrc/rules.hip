@@ -558,7 +558,7 @@ __global__ __launch_bounds__(kNT) void draw_kernel(DrawArgs a)
     const float tau = a.temperatures ? a.temperatures[m] : a.temperature;
     const bool none = !(v0 > -INFINITY), first = v0 == INFINITY || !(tau > 0.f);
     double w = 0.;
-    if (j < a.K && !none && !first)
+    if (j < a.K && !none && !first && v > -INFINITY) // -inf / inf, at an infinite temperature, is no number
         w = exp(((double)v - (double)v0) / (double)tau);
     double run = w; // sums of the weights so far, in a fixed order
     for (int off = 1; off < 16; off <<= 1) {

@@ -116,7 +116,8 @@ def sample_logits(logits, K: int, u=None, temperature=1.0, history=None, lengths
     """(values fp32 M x K, indices int32 M x K, samples int32 M or None): the K <= 16
     largest of the logits under adjust_logits' rules, in order, and with u (fp32 M,
     in [0, 1)) a draw from them at the temperature (a number, or fp32 M; rows whose
-    own is not positive take their largest).  A row whose rules leave nothing draws -1."""
+    own is not positive take their largest, at inf all that are left weigh the same).  A
+    row whose rules leave nothing draws -1."""
     import torch
     M, V, L, args = _rules(logits, history, lengths, prompt_lengths, repetition, frequency, presence, bias_ids,
                               bias_values, mask, mask_rows)
