@@ -582,7 +582,7 @@ archead_status archead_fp8_matmul(int64_t M, int64_t N, int64_t K, const uint8_t
  * type and stride; other buffers must not overlap.  Buffers are aligned to their
  * element.  eps is finite and not negative, offset finite.
  * Numerics: squares are summed in fp64; n is fp32, with three roundings (1.5 x
- * 2^-23 relative); rows whose root mean square passes 2^126 lose precision.  A NaN in
+ * 2^-23 relative), for rows of any finite size, with eps = 0 too.  A NaN in
  * row m makes its n NaN, an infinity 0 and NaN; no other row is touched by either.  A
  * row of zeros with eps = 0 is 0 / 0.
  * The current device must be the one the buffers and hip_stream belong to.
@@ -610,9 +610,10 @@ archead_status archead_rms_norm(int64_t M, int64_t d, const void *x, int x_type,
  * ws       DEVICE workspace of archead_rms_norm_workspace(M, d) bytes, 16-byte
  *          aligned, contents irrelevant, the call's own until the stream has
  *          passed it: calls, or captured graphs, that may overlap need one each.
- * Sizes, alignment, streams and numerics as archead_rms_norm: the row's two sums
- * are fp64, dh is fp32 rounded once, dweight's terms are added in fp32 over at most
- * 64 rows, those sums in fp32 over at most 16 and then in fp64, in a fixed order.
+ * Sizes, alignment, streams and numerics as archead_rms_norm: g_j is fp32 (one below
+ * 2^-126 is rounded to a multiple of 2^-149), the row's two sums are fp64, dh is fp32
+ * rounded once, dweight's terms are added in fp32 over at most 64 rows, those sums in
+ * fp32 over at most 16 and then in fp64, in a fixed order.
  */
 archead_status archead_rms_norm_workspace(int64_t M, int64_t d, uint64_t *bytes);
 archead_status archead_rms_norm_backward(int64_t M, int64_t d, const void *dy, int dy_type, int64_t ldy, const void *h,

@@ -50,13 +50,13 @@ template <int T> __device__ __forceinline__ double team_sum(double v, double *re
     return v;
 }
 
-// 1 / sqrt(v): the instruction's estimate and one step of Newton's, in fp64
-__device__ __forceinline__ float inverse_root(double v)
+// 1 / sqrt(v): the instruction's estimate and one step of Newton's.  Rows at the ends of
+// fp32's range have one, from 2^-128 to 2^149, that fp32 does not hold.
+__device__ __forceinline__ double inverse_root(double v)
 {
-    double r = __builtin_amdgcn_rsq(v);
+    const double r = __builtin_amdgcn_rsq(v);
     const double better = r * __builtin_fma(-0.5 * v * r, r, 1.5);
-    r = v > 0. && v < INFINITY ? better : r; // 0 and infinity have theirs; NaN stays NaN
-    return (float)r;
+    return v > 0. && v < INFINITY ? better : r; // 0 and infinity have theirs; NaN stays NaN
 }
 
 // the same of two sums at once, one wait: red holds two sets, taken in turn, so
@@ -96,14 +96,30 @@ struct NormArgs {
     int weight_type, y_type;
 };
 
-__device__ __forceinline__ void weights_of(const NormArgs &a, int q, float w[8])
+// (weight + offset) times, a power of two
+__device__ __forceinline__ void weights_of(const NormArgs &a, int q, float times, float w[8])
 {
     if (a.weight_type == ARCHEAD_F32)
         vector_values(q, a.d, load_vector((const float *)a.weight, q, a.d), w);
     else
         vector_values(q, a.d, load_vector((const uint16_t *)a.weight, q, a.d), w);
     for (int i = 0; i < 8; ++i)
-        w[i] += a.offset;
+        w[i] = __builtin_fmaf(w[i], times, a.offset * times);
+}
+
+// r as by * times: times, a power of two, goes to the weights, where it costs nothing, and
+// by stays far enough inside fp32's range for its full precision
+struct Root {
+    float by, times;
+};
+__device__ __forceinline__ Root split(double r)
+{
+    Root s{(float)r, 1.f};
+    if (__builtin_expect(s.by > 0x1p125f || s.by < 0x1p-125f, 0)) {
+        s.times = s.by > 1.f ? 0x1p24f : 0x1p-4f;
+        s.by = (float)(r / (double)s.times);
+    }
+    return s;
 }
 
 // results of one vector n; sixteen neighbouring threads hold a block of columns
@@ -180,15 +196,15 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void norm_kernel(NormArgs a)
             for (int i = 0; i < 8; ++i)
                 ss = __builtin_fma((double)v[j][i], (double)v[j][i], ss);
     ss = team_sum<T>(ss, red);
-    const float r = inverse_root(__builtin_fma(ss, a.inv_d, (double)a.eps));
+    const Root r = split(inverse_root(__builtin_fma(ss, a.inv_d, (double)a.eps)));
 #pragma unroll
     for (int j = 0; j < H; ++j) {
         const int q = t + j * T;
         if (j * T < nv) { // not uniform in a team only past the row's end
             float w[8], n[8];
-            weights_of(a, q, w);
+            weights_of(a, q, r.times, w);
             for (int i = 0; i < 8; ++i)
-                n[i] = q < nv ? v[j][i] * r * w[i] : 0.f;
+                n[i] = q < nv ? v[j][i] * r.by * w[i] : 0.f;
             put(a, m, q, q < nv, n);
         }
     }
@@ -224,16 +240,16 @@ template <typename XT, typename RT> __global__ __launch_bounds__(kLongT) void no
             ss = __builtin_fma((double)v[i], (double)v[i], ss);
     }
     ss = team_sum<kLongT>(ss, red);
-    const float r = inverse_root(__builtin_fma(ss, a.inv_d, (double)a.eps));
+    const Root r = split(inverse_root(__builtin_fma(ss, a.inv_d, (double)a.eps)));
     for (int q0 = 0; q0 < nv; q0 += kLongT) { // each thread reads back what it wrote
         const int q = q0 + threadIdx.x;
         float v[8] = {}, w[8] = {};
         if (q < nv) {
             vector_values(q, a.d, load_vector(sum, q, a.d), v);
-            weights_of(a, q, w);
+            weights_of(a, q, r.times, w);
         }
         for (int i = 0; i < 8; ++i)
-            v[i] = q < nv ? v[i] * r * w[i] : 0.f;
+            v[i] = q < nv ? v[i] * r.by * w[i] : 0.f;
         put(a, m, q, q < nv, v);
     }
 }
@@ -286,7 +302,7 @@ struct BackArgs {
     const void *u, *h, *weight, *dres; // dres may be null
     void *dh;
     float *part; // [groups][d]
-    float *inv;  // [M], the long rows' r
+    float4 *inv; // [M], the long rows' us, hs and rw
     double inv_d;
     float eps, offset;
     int weight_type;
@@ -300,7 +316,35 @@ __device__ __forceinline__ void weights_of(const BackArgs &a, int q, float w[8])
     n.weight_type = a.weight_type;
     n.d = a.d;
     n.offset = a.offset;
-    weights_of(n, q, w);
+    weights_of(n, q, 1.f, w);
+}
+
+// a vector's share of a row's sums of h^2 and g h
+__device__ __forceinline__ void add_sums(const float u[8], const float h[8], const float w[8], double &ss, double &c)
+{
+    for (int i = 0; i < 8; ++i) {
+        const double hd = h[i];
+        ss = __builtin_fma(hd, hd, ss);
+        c = __builtin_fma((double)(u[i] * w[i]), hd, c);
+    }
+}
+
+// Rows near the ends of fp32's range have an r, or an r^2 c beside it, that fp32 does not
+// hold.  Their u and h are multiplied by powers of two, us and hs, first, and
+//   dh = r / us (g us - (h hs) (r^2 c us / hs)),   dw's term = (u us) (h hs) (r / us / hs).
+// All others' are taken as they are.
+struct FarRow {
+    float us, hs, r, rw, k;
+};
+template <int T> __device__ __forceinline__ bool is_far(float r) // the same for a wave that shares a row
+{
+    const bool far = r < 0x1p-60f || r > 0x1p60f;
+    return T < 64 ? far : __ballot(far) != 0;
+}
+__device__ __forceinline__ FarRow far_row(double r, double c)
+{
+    const double us = r > 1. ? 0x1p24 : 0x1p-4, hs = r > 1. ? 0x1p64 : 0x1p-64;
+    return {(float)us, (float)hs, (float)(r / us), (float)(r / us / hs), (float)(r * r * c * (us / hs))};
 }
 
 // A workgroup's teams of T threads take every (groups x teams)-th row; the weights
@@ -378,15 +422,21 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void norm_back_kernel(BackArgs a
         for (int j = 0; j < H; ++j) {
             float w[8];
             weight(j, w);
-            for (int i = 0; i < 8; ++i) {
-                const double hd = hv[j][i];
-                ss = __builtin_fma(hd, hd, ss);
-                c = __builtin_fma((double)(uv[j][i] * w[i]), hd, c);
-            }
+            add_sums(uv[j], hv[j], w, ss, c);
         }
         team_sums<T>(ss, c, red[turn]);
-        const float r = inverse_root(__builtin_fma(ss, a.inv_d, (double)a.eps));
-        const float k = (float)((double)r * (double)r * (c * a.inv_d));
+        const double root = inverse_root(__builtin_fma(ss, a.inv_d, (double)a.eps));
+        float r = (float)root, rw = r, k = (float)((double)r * (double)r * (c * a.inv_d));
+        if (__builtin_expect(is_far<T>(r), 0)) {
+            const FarRow f = far_row(root, c * a.inv_d);
+            r = f.r, rw = f.rw, k = f.k;
+#pragma unroll
+            for (int j = 0; j < H; ++j)
+                for (int i = 0; i < 8; ++i) {
+                    uv[j][i] *= f.us;
+                    hv[j][i] *= f.hs;
+                }
+        }
 #pragma unroll
         for (int j = 0; j < H; ++j) {
             const int q = t + j * T;
@@ -396,7 +446,7 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void norm_back_kernel(BackArgs a
                 vector_values(q, a.d, rr[j], o);
             for (int i = 0; i < 8; ++i) {
                 o[i] = __builtin_fmaf(r, __builtin_fmaf(-hv[j][i], k, uv[j][i] * w[i]), o[i]);
-                dw[j][i] = __builtin_fmaf(uv[j][i], hv[j][i] * r, dw[j][i]);
+                dw[j][i] = __builtin_fmaf(uv[j][i], hv[j][i] * rw, dw[j][i]);
             }
             if (q < nv)
                 store_vector((HT *)a.dh + m * a.ldd, q, a.d, o);
@@ -445,10 +495,13 @@ template <typename UT, typename HT> __global__ __launch_bounds__(kLongT) void no
         }
     }
     team_sums<kLongT>(ss, c, red);
-    const float r = inverse_root(__builtin_fma(ss, a.inv_d, (double)a.eps));
-    const float k = (float)((double)r * (double)r * (c * a.inv_d));
+    const double root = inverse_root(__builtin_fma(ss, a.inv_d, (double)a.eps));
+    const float r0 = (float)root;
+    FarRow f{1.f, 1.f, r0, r0, (float)((double)r0 * (double)r0 * (c * a.inv_d))};
+    if (is_far<kLongT>(r0))
+        f = far_row(root, c * a.inv_d);
     if (threadIdx.x == 0)
-        a.inv[m] = r;
+        a.inv[m] = make_float4(f.us, f.hs, f.rw, 0.f);
     for (int q = threadIdx.x; q < nv; q += kLongT) {
         float uv[8], hv[8], w[8], o[8] = {};
         vector_values(q, a.d, load_vector(u, q, a.d), uv);
@@ -457,7 +510,7 @@ template <typename UT, typename HT> __global__ __launch_bounds__(kLongT) void no
         if (a.dres)
             vector_values(q, a.d, load_vector(res, q, a.d), o);
         for (int i = 0; i < 8; ++i)
-            o[i] = __builtin_fmaf(r, __builtin_fmaf(-hv[i], k, uv[i] * w[i]), o[i]);
+            o[i] = __builtin_fmaf(f.r, __builtin_fmaf(-(hv[i] * f.hs), f.k, uv[i] * f.us * w[i]), o[i]);
         store_vector((HT *)a.dh + m * a.ldd, q, a.d, o);
     }
 }
@@ -474,9 +527,9 @@ template <typename UT, typename HT> __global__ __launch_bounds__(256) void weigh
         const HT *h = (const HT *)a.h + m * a.ldh;
         vector_values(q, a.d, load_vector(u, q, a.d), uv);
         vector_values(q, a.d, load_vector(h, q, a.d), hv);
-        const float r = a.inv[m];
+        const float4 r = a.inv[m];
         for (int i = 0; i < 8; ++i)
-            dw[i] = __builtin_fmaf(uv[i], hv[i] * r, dw[i]);
+            dw[i] = __builtin_fmaf(uv[i] * r.x, hv[i] * r.y * r.z, dw[i]);
     }
     store_vector(a.part + g * a.d, q, a.d, dw);
 }
@@ -551,7 +604,7 @@ BackPlan plan_back(int64_t M, int64_t d)
         p.groups = (M + kPartRows - 1) / kPartRows;
     }
     p.inv = (size_t)((p.groups * d * 4 + 15) / 16 * 16);
-    p.total = std::max<size_t>(16, p.inv + (p.T ? 0 : (size_t)M * 4));
+    p.total = std::max<size_t>(16, p.inv + (p.T ? 0 : (size_t)M * sizeof(float4)));
     return p;
 }
 
@@ -700,7 +753,7 @@ extern "C" archead_status archead_rms_norm_backward(int64_t M, int64_t d, const 
         return api_fail(ARCHEAD_EINVAL, "the workspace is smaller than archead_rms_norm_workspace asks for");
     if (M == 0 && !dweight)
         return ARCHEAD_OK;
-    const BackArgs a{M, (int)d, ldy, ldh, ldr, ldd, dy, h, weight, dres, dh, (float *)ws, (float *)((char *)ws + p.inv),
+    const BackArgs a{M, (int)d, ldy, ldh, ldr, ldd, dy, h, weight, dres, dh, (float *)ws, (float4 *)((char *)ws + p.inv),
                      1. / (double)d, eps, offset, weight_type, p.groups, p.slice};
     hipStream_t stream = (hipStream_t)hip_stream;
     const bool uf = dy_type == ARCHEAD_F32, hf = h_type == ARCHEAD_F32;
