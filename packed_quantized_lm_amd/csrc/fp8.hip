@@ -50,13 +50,21 @@ __device__ __forceinline__ void load8(const uint16_t *p, float v[8])
         v[i] = __uint_as_float((uint32_t)a[i] << 16);
 }
 
+// Whether codes are taken the exact way at once.  The quotients of bf16 values are true
+// ties often enough for some third of the waves to need it, and where a launch is short
+// enough for the longest wave's time to count, the quick way before it is time lost (bf16,
+// exact at once, quick first, in us: 1 row of 4096 4.3, 5.6; 512 rows 7.2, 7.6; 2048 16.6,
+// 16.7; 4096 28.5, 27.4; 8192 50.0, 46.8; 128 x 4096 by 128 x 128 blocks 23, 36; 1024 x
+// 4096 25, 33; 4096 x 4096 66.6, 62.5).  fp32 values have few such ties (1 row 4.3, 2.4;
+// 8192 rows 54.7, 27.3).
+constexpr int64_t kExactRows = 4096, kExactTiles = 512; // workgroups
+
 // One row's blocks: 16 lanes a block, 8 columns a lane, so that a block's
 // largest magnitude takes four exchanges and a lane one load and one store
-// (2048 x 4096 bf16: 17 us against 5 of its bytes, the vector units busy
-// throughout: finding a thread's row divides 64-bit numbers, and the quotients of
-// bf16 values are true ties often enough for some third of the waves to take the
-// exact way; one row 5 us, a launch).
-template <typename T>
+// (2048 x 4096 bf16: 16.6 us against 5 of its bytes, the vector units busy
+// throughout: finding a thread's row divides 64-bit numbers, and exact quotients are
+// a division, its remainder and the last bit of every element; one row 4.3 us, a launch).
+template <typename T, bool kExact>
 __global__ __launch_bounds__(256) void quant_rows_kernel(const T *x, int64_t ldx, int64_t rows, int64_t cols,
                                                          uint8_t *q, int64_t ldq, float *s, int64_t lds)
 {
@@ -77,7 +85,7 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const T *x, int64_t ldx
         m = fmaxf(m, __shfl_xor(m, off));
     const float sc = block_scale(m);
     if (in)
-        *(u32x2 *)(q + row * ldq + c) = codes8(v, sc);
+        *(u32x2 *)(q + row * ldq + c) = kExact ? codes8_exact(v, sc) : codes8(v, sc);
     if ((threadIdx.x & 15) == 0)
         s[b * lds + row] = sc;
 }
@@ -86,7 +94,7 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const T *x, int64_t ldx
 // once for the scale and again for the codes.  151936 x 4096 bf16, once per
 // head: 3.4 ms against 0.4 of its bytes, since a thread's 16-byte loads come to a
 // 128-byte line eight times in each pass, and 18 GB are fetched for 1.2.
-template <typename T>
+template <typename T, bool kExact>
 __global__ __launch_bounds__(256) void quant_tiles_kernel(const T *x, int64_t ldx, int64_t rows, int64_t cols,
                                                           uint8_t *q, int64_t ldq, float *s, int64_t lds)
 {
@@ -111,7 +119,7 @@ __global__ __launch_bounds__(256) void quant_tiles_kernel(const T *x, int64_t ld
     for (int j = 0; j < 8; ++j)
         if (row < rows && c0 + 8 * j < cols) {
             load8(xr + c0 + 8 * j, v);
-            *(u32x2 *)(q + row * ldq + c0 + 8 * j) = codes8(v, sc);
+            *(u32x2 *)(q + row * ldq + c0 + 8 * j) = kExact ? codes8_exact(v, sc) : codes8(v, sc);
         }
     if (threadIdx.x == 0)
         s[rb * lds + b] = sc;
@@ -573,23 +581,24 @@ extern "C" archead_status archead_fp8_quantize(int64_t rows, int64_t cols, const
     if ((uintptr_t)x % (type == ARCHEAD_F32 ? 4 : 2) || bad_rows(q, ldq, cols))
         return api_fail(ARCHEAD_EINVAL, "x aligned to its element; q and its row stride to 16 bytes");
     hipStream_t st = (hipStream_t)hip_stream;
-    if (block_rows == 1) {
-        const dim3 grid((unsigned)((rows * nb + 15) / 16));
-        if (type == ARCHEAD_F32)
-            hipLaunchKernelGGL(quant_rows_kernel<float>, grid, dim3(256), 0, st, (const float *)x, ldx, rows, cols, q,
-                               ldq, s, lds);
-        else
-            hipLaunchKernelGGL(quant_rows_kernel<uint16_t>, grid, dim3(256), 0, st, (const uint16_t *)x, ldx, rows,
-                               cols, q, ldq, s, lds);
-    } else {
-        const dim3 grid((unsigned)((rows + kBlk - 1) / kBlk * nb));
-        if (type == ARCHEAD_F32)
-            hipLaunchKernelGGL(quant_tiles_kernel<float>, grid, dim3(256), 0, st, (const float *)x, ldx, rows, cols, q,
-                               ldq, s, lds);
-        else
-            hipLaunchKernelGGL(quant_tiles_kernel<uint16_t>, grid, dim3(256), 0, st, (const uint16_t *)x, ldx, rows,
-                               cols, q, ldq, s, lds);
-    }
+    const bool by_rows = block_rows == 1;
+    const int64_t groups = by_rows ? (rows * nb + 15) / 16 : (rows + kBlk - 1) / kBlk * nb;
+    const bool exact = type == ARCHEAD_BF16 && groups <= (by_rows ? kExactRows : kExactTiles);
+    const dim3 grid((unsigned)groups);
+    const float *x4 = (const float *)x;
+    const uint16_t *x2 = (const uint16_t *)x;
+    if (by_rows && type == ARCHEAD_F32)
+        hipLaunchKernelGGL((quant_rows_kernel<float, false>), grid, dim3(256), 0, st, x4, ldx, rows, cols, q, ldq, s, lds);
+    else if (by_rows && exact)
+        hipLaunchKernelGGL((quant_rows_kernel<uint16_t, true>), grid, dim3(256), 0, st, x2, ldx, rows, cols, q, ldq, s, lds);
+    else if (by_rows)
+        hipLaunchKernelGGL((quant_rows_kernel<uint16_t, false>), grid, dim3(256), 0, st, x2, ldx, rows, cols, q, ldq, s, lds);
+    else if (type == ARCHEAD_F32)
+        hipLaunchKernelGGL((quant_tiles_kernel<float, false>), grid, dim3(256), 0, st, x4, ldx, rows, cols, q, ldq, s, lds);
+    else if (exact)
+        hipLaunchKernelGGL((quant_tiles_kernel<uint16_t, true>), grid, dim3(256), 0, st, x2, ldx, rows, cols, q, ldq, s, lds);
+    else
+        hipLaunchKernelGGL((quant_tiles_kernel<uint16_t, false>), grid, dim3(256), 0, st, x2, ldx, rows, cols, q, ldq, s, lds);
     return launched("archead_fp8_quantize");
 }
 
