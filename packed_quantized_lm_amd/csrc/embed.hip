@@ -654,7 +654,8 @@ GradWs grad_ws(int64_t n, int64_t V, int64_t d)
         w.other = take((size_t)n * sizeof(Pair));
         w.count = take((size_t)w.tiles * kDigits * 4);
     }
-    for (int64_t m = n / kGroup; m > 0 && w.levels < kMaxLevels && (w.levels == 0 || m * kGroup > kFewParts); m /= kGroup) {
+    for (int64_t m = n / kGroup; m > 0 && w.levels < kMaxLevels && (w.levels == 0 || w.parts[w.levels - 1] > kFewParts);
+         m /= kGroup) {
         w.parts[w.levels] = m;
         w.part[w.levels++] = take((size_t)m * d * 4);
     }
