@@ -656,7 +656,7 @@ archead_status archead_embed(int64_t n, int64_t V, int64_t d, const void *table,
  * ws       DEVICE workspace of archead_embed_workspace(n, V, d) bytes, 16-byte
  *          aligned, contents irrelevant, the call's own until the stream has
  *          passed it: calls, or captured graphs, that may overlap need one each.
- * n ceil(d / 512) must lie below 2^26, V below 2^26 - 2^24.  Other limits as archead_embed.
+ * n ceil(d / 512) must be 2^26 - 4 at most, V below 2^26 - 2^24.  Other limits as archead_embed.
  * Sums are fp32, of groups of 32 terms in the order of the tokens and of such sums (a
  * term passes through 400 additions at most), and rounded once with scale (and what
  * they are added to); equal calls give equal bits.

@@ -805,8 +805,8 @@ extern "C" archead_status archead_embed_backward(int64_t n, int64_t V, int64_t d
     const GradWs w = grad_ws(n, V, d);
     const int64_t tiles = (d + kCols - 1) / kCols;
     // a launch holds fewer than 2^32 threads
-    if (n * tiles >= (int64_t(1) << 26) || V >= (int64_t(1) << 26) - (int64_t(1) << 24))
-        return api_fail(ARCHEAD_ESHAPE, "n ceil(d / 512) must lie below 2^26, V below 2^26 - 2^24");
+    if (n * tiles > (int64_t(1) << 26) - 4 || V >= (int64_t(1) << 26) - (int64_t(1) << 24))
+        return api_fail(ARCHEAD_ESHAPE, "n ceil(d / 512) must be 2^26 - 4 at most, V below 2^26 - 2^24");
     if (!dtable || (n > 0 && (!dout || !tokens)))
         return api_fail(ARCHEAD_EINVAL, "dout, tokens and dtable are required");
     if (misaligned(dout, dout_type) || misaligned(dtable, grad_type) || misaligned(tokens, ARCHEAD_F32))
