@@ -579,8 +579,9 @@ archead_status archead_fp8_matmul(int64_t M, int64_t N, int64_t K, const uint8_t
  *           scales s[b * lds + row], lds >= M, as archead_fp8_matmul reads them,
  *           or both NULL; they need d to be a multiple of 16.  y or q is required.
  * Strides lie in [d, 2^40].  h may be residual or x, and y may be x, with the same
- * type and stride; other buffers must not overlap.  Buffers are aligned to their
- * element.  eps is finite and not negative, offset finite.
+ * type and stride; otherwise a result that overlaps what is read, or another result, is
+ * refused here and below (columns of one wider matrix do not).  Buffers are aligned to
+ * their element.  eps is finite and not negative, offset finite.
  * Numerics: squares are summed in fp64; n is fp32, with three roundings (1.5 x
  * 2^-23 relative), for rows of any finite size, with eps = 0 too.  A NaN in
  * row m makes its n NaN, an infinity 0 and NaN; no other row is touched by either.  A

@@ -19,6 +19,7 @@
 #include "api_internal.hpp"
 #include "archead.h"
 #include "elements.hpp"
+#include "overlap.hpp"
 
 namespace archead {
 namespace {
@@ -717,6 +718,7 @@ template <typename T> void run_grad(const GradArgs &a, const GradWs &w, int grad
 }
 
 bool bad_type(int t) { return t != ARCHEAD_F32 && t != ARCHEAD_BF16; }
+int64_t size_of(int t) { return t == ARCHEAD_F32 ? 4 : t == ARCHEAD_BF16 ? 2 : 1; }
 bool misaligned(const void *p, int t) { return (uintptr_t)p % (t == ARCHEAD_F32 ? 4 : 2) != 0; }
 
 archead_status launched(const char *what)
@@ -765,7 +767,9 @@ extern "C" archead_status archead_embed(int64_t n, int64_t V, int64_t d, const v
         return api_fail(ARCHEAD_EINVAL, "table aligned to its element; 8-bit tables and their row strides to 16 bytes");
     if (misaligned(out, out_type) || misaligned(tokens, ARCHEAD_F32))
         return api_fail(ARCHEAD_EINVAL, "buffers must be aligned to their element");
-    if (out == table || out == tokens)
+    if (overlap({matrix_span(out, n, d, ldo, size_of(out_type))},
+                {matrix_span(table, V, d, ldt, size_of(table_type)), vector_span(tokens, 4 * n),
+                 matrix_span(f8 ? scales : nullptr, (V + kBlk - 1) / kBlk, (d + kBlk - 1) / kBlk, lds, 4)}))
         return api_fail(ARCHEAD_EINVAL, "out overlaps what is read");
     const LookArgs a{n, V, (int)d, ldt, lds, ldo, table, scales, tokens, out, scale, pad};
     hipStream_t stream = (hipStream_t)hip_stream;
@@ -811,12 +815,14 @@ extern "C" archead_status archead_embed_backward(int64_t n, int64_t V, int64_t d
         return api_fail(ARCHEAD_EINVAL, "dout, tokens and dtable are required");
     if (misaligned(dout, dout_type) || misaligned(dtable, grad_type) || misaligned(tokens, ARCHEAD_F32))
         return api_fail(ARCHEAD_EINVAL, "buffers must be aligned to their element");
-    if (dtable == dout || dtable == tokens)
-        return api_fail(ARCHEAD_EINVAL, "dtable overlaps what is read");
     if (!ws || (uintptr_t)ws % 16)
         return api_fail(ARCHEAD_EINVAL, "a 16-byte aligned workspace is required");
     if (ws_bytes < w.total)
         return api_fail(ARCHEAD_EINVAL, "the workspace is smaller than archead_embed_workspace asks for");
+    const Span grad = matrix_span(dtable, V, d, ldt, size_of(grad_type)), work = vector_span(ws, (int64_t)w.total);
+    if (overlap({grad, work}, {matrix_span(dout, n, d, ldo, size_of(dout_type)), vector_span(tokens, 4 * n)}) ||
+        overlap(grad, work))
+        return api_fail(ARCHEAD_EINVAL, "dtable or the workspace overlaps what is read, or each other");
     if (n == 0 && accumulate)
         return ARCHEAD_OK;
     char *base = (char *)ws;

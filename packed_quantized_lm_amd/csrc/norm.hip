@@ -24,6 +24,7 @@
 #include "archead.h"
 #include "e4m3.hpp"
 #include "elements.hpp"
+#include "overlap.hpp"
 
 namespace archead {
 namespace {
@@ -640,6 +641,7 @@ template <typename UT, typename HT> void run_back(const BackArgs &a, const BackP
 }
 
 bool bad_type(int t) { return t != ARCHEAD_F32 && t != ARCHEAD_BF16; }
+int64_t size_of(int t) { return t == ARCHEAD_F32 ? 4 : 2; }
 bool misaligned(const void *p, int t) { return (uintptr_t)p % (t == ARCHEAD_F32 ? 4 : 2) != 0; }
 
 archead_status check_sizes(int64_t M, int64_t d, float eps, float offset)
@@ -700,6 +702,13 @@ extern "C" archead_status archead_rms_norm(int64_t M, int64_t d, const void *x, 
         return api_fail(ARCHEAD_EINVAL, "in place, h needs the type and row stride of what it replaces");
     if (y && ((y == x && (y_type != x_type || ldy != ldx)) || y == h || y == residual))
         return api_fail(ARCHEAD_EINVAL, "y may be x, with its type and row stride, not h or residual");
+    const Span sx = matrix_span(x, M, d, ldx, size_of(x_type)), sr = matrix_span(residual, M, d, ldr, size_of(res_type)),
+               sh = matrix_span(h, M, d, ldh, size_of(res_type)), sy = matrix_span(y, M, d, ldy, size_of(y_type)),
+               sq = matrix_span(q, M, d, ldq, 1), ss = matrix_span(s, (d + kBlk - 1) / kBlk, M, lds, 4);
+    if (overlap_but_itself(sh, sx) || overlap_but_itself(sh, sr) || overlap_but_itself(sy, sx) || overlap(sy, sr) ||
+        overlap({sq, ss}, {sx, sr}) || overlap({sh, sy, sq, ss}, {vector_span(weight, d * size_of(weight_type))}) ||
+        overlap({sh, sy, sq, ss}))
+        return api_fail(ARCHEAD_EINVAL, "a result overlaps what is read, or another result");
     const NormArgs a{M, (int)d, ldx, ldr, ldh, ldy, ldq, lds, x, residual, weight, h, y, q, s, 1. / (double)d, eps, offset,
                      weight_type, y_type};
     hipStream_t stream = (hipStream_t)hip_stream;
@@ -751,6 +760,13 @@ extern "C" archead_status archead_rms_norm_backward(int64_t M, int64_t d, const 
     const BackPlan p = plan_back(M, d);
     if (ws_bytes < p.total)
         return api_fail(ARCHEAD_EINVAL, "the workspace is smaller than archead_rms_norm_workspace asks for");
+    const Span su = matrix_span(dy, M, d, ldy, size_of(dy_type)), sh = matrix_span(h, M, d, ldh, size_of(h_type)),
+               sr = matrix_span(dres, M, d, ldr, size_of(h_type)), sd = matrix_span(dh, M, d, ldd, size_of(h_type)),
+               sg = vector_span(dweight, 4 * d), sw = vector_span(weight, d * size_of(weight_type)),
+               work = vector_span(ws, (int64_t)p.total);
+    if (overlap({sd, sg, work}, {su, sh, sw}) || overlap_but_itself(sd, sr) || overlap({sg, work}, {sr}) ||
+        overlap({sd, sg, work}))
+        return api_fail(ARCHEAD_EINVAL, "a result or the workspace overlaps what is read, or another result");
     if (M == 0 && !dweight)
         return ARCHEAD_OK;
     const BackArgs a{M, (int)d, ldy, ldh, ldr, ldd, dy, h, weight, dres, dh, (float *)ws, (float4 *)((char *)ws + p.inv),

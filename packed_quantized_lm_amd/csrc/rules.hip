@@ -30,6 +30,7 @@
 #include "archead.h"
 #include "elements.hpp"
 #include "kernels.hpp"
+#include "overlap.hpp"
 
 namespace archead {
 namespace {
@@ -732,6 +733,17 @@ archead_status check_rules(const RuleArgs &a, int64_t V, int64_t L, int64_t B, i
     return ARCHEAD_OK;
 }
 
+// whether a result lies in what the rules are read from, beside the logits
+bool in_the_rules(const RuleArgs &a, std::initializer_list<Span> results)
+{
+    const int64_t lists = a.ldb == 0 ? 1 : a.M;
+    return overlap(results, {matrix_span(a.history, a.M, a.L, a.ldh, 4), vector_span(a.lengths, 4 * a.M),
+                             vector_span(a.prompts, 4 * a.M), vector_span(a.repetition, 4 * a.M),
+                             vector_span(a.frequency, 4 * a.M), vector_span(a.presence, 4 * a.M),
+                             matrix_span(a.bias_ids, lists, a.B, a.ldb, 4), matrix_span(a.bias_values, lists, a.B, a.ldb, 4),
+                             matrix_span(a.mask, a.R, (a.V + 31) / 32, a.ldm, 4), vector_span(a.mask_rows, 4 * a.M)});
+}
+
 archead_status check_ws(const RuleWs &w, const void *ws, uint64_t bytes)
 {
     if (w.total && (!ws || misaligned(ws, 16)))
@@ -808,6 +820,11 @@ extern "C" archead_status archead_adjust_logits(int64_t M, int64_t V, const void
     s = check_ws(w, ws, ws_bytes);
     if (s != ARCHEAD_OK || M == 0)
         return s;
+    const int64_t element = type == ARCHEAD_F32 ? 4 : 2;
+    const Span read = matrix_span(logits, M, V, ld, element), result = matrix_span(out, M, V, ldo, element),
+               work = vector_span(w.total ? ws : nullptr, (int64_t)w.total);
+    if (overlap_but_itself(result, read) || overlap(work, read) || overlap(result, work) || in_the_rules(a, {result, work}))
+        return api_fail(ARCHEAD_EINVAL, "out or the workspace overlaps what is read, or each other");
     a.out = out;
     a.ldo = ldo;
     lay_out(a, w, ws);
@@ -861,6 +878,12 @@ extern "C" archead_status archead_sample_logits(int64_t M, int64_t V, const void
     s = check_ws(w, ws, ws_bytes);
     if (s != ARCHEAD_OK || M == 0)
         return s;
+    const std::initializer_list<Span> results = {vector_span(values, 4 * M * K), vector_span(indices, 4 * M * K),
+                                                 vector_span(samples, 4 * M), vector_span(ws, (int64_t)w.total)};
+    if (overlap(results, {matrix_span(logits, M, V, ld, type == ARCHEAD_F32 ? 4 : 2), vector_span(temperatures, 4 * M),
+                          vector_span(u, 4 * M)}) ||
+        overlap(results) || in_the_rules(a, results))
+        return api_fail(ARCHEAD_EINVAL, "a result or the workspace overlaps what is read, or another result");
     a.K = K;
     a.part = (uint64_t *)ws;
     lay_out(a, w, ws);
