@@ -61,16 +61,6 @@ __device__ __forceinline__ void store_eight(float *p, const Eight<float> &o)
     *(f32x4e *)(p + 4) = o.b;
 }
 __device__ __forceinline__ void store_eight(uint16_t *p, const Eight<uint16_t> &o) { *(u16x8e *)p = o.a; }
-// past the caches' working set: results that nothing reads before they are evicted
-__device__ __forceinline__ void stream_eight(float *p, const Eight<float> &o)
-{
-    __builtin_nontemporal_store(o.a, (f32x4e *)p);
-    __builtin_nontemporal_store(o.b, (f32x4e *)(p + 4));
-}
-__device__ __forceinline__ void stream_eight(uint16_t *p, const Eight<uint16_t> &o)
-{
-    __builtin_nontemporal_store(o.a, (u16x8e *)p);
-}
 __device__ __forceinline__ void store_one(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_one(uint16_t *p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
 
