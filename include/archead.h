@@ -582,8 +582,9 @@ archead_status archead_fp8_matmul(int64_t M, int64_t N, int64_t K, const uint8_t
  * type and stride; otherwise a result that overlaps what is read, or another result, is
  * refused here and below (columns of one wider matrix do not).  Buffers are aligned to
  * their element.  eps is finite and not negative, offset finite.
- * Numerics: squares are summed in fp64; n is fp32, with three roundings (1.5 x
- * 2^-23 relative), for rows of any finite size, with eps = 0 too.  A NaN in
+ * Numerics: squares are summed in fp64; n is fp32, with four roundings (r, weight +
+ * offset and two products: 2 x 2^-23 relative; three, 1.5 x 2^-23, where offset is 0),
+ * for rows of any finite size, with eps = 0 too.  A NaN in
  * row m makes its n NaN, an infinity 0 and NaN; no other row is touched by either.  A
  * row of zeros with eps = 0 is 0 / 0.
  * The current device must be the one the buffers and hip_stream belong to.
