@@ -19,6 +19,7 @@
 #include "api_internal.hpp"
 #include "archead.h"
 #include "elements.hpp"
+#include "entry.hpp"
 #include "overlap.hpp"
 
 namespace archead {
@@ -717,18 +718,6 @@ template <typename T> void run_grad(const GradArgs &a, const GradWs &w, int grad
     a.d < 8 ? run_grad<true, T>(a, w, grad_type, st) : run_grad<false, T>(a, w, grad_type, st);
 }
 
-bool bad_type(int t) { return t != ARCHEAD_F32 && t != ARCHEAD_BF16; }
-int64_t size_of(int t) { return t == ARCHEAD_F32 ? 4 : t == ARCHEAD_BF16 ? 2 : 1; }
-bool misaligned(const void *p, int t) { return (uintptr_t)p % (t == ARCHEAD_F32 ? 4 : 2) != 0; }
-
-archead_status launched(const char *what)
-{
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess)
-        return api_fail(ARCHEAD_EHIP, std::string(what) + ": " + hipGetErrorString(e));
-    return ARCHEAD_OK;
-}
-
 archead_status check_sizes(int64_t n, int64_t V, int64_t d)
 {
     if (n < 0)
@@ -763,9 +752,9 @@ extern "C" archead_status archead_embed(int64_t n, int64_t V, int64_t d, const v
         return ARCHEAD_OK;
     if (!table || !tokens || !out || (f8 && !scales))
         return api_fail(ARCHEAD_EINVAL, "table, tokens, out and an 8-bit table's scales are required");
-    if (f8 ? (uintptr_t)table % 16 || ldt % 16 || misaligned(scales, ARCHEAD_F32) : misaligned(table, table_type))
+    if (f8 ? (uintptr_t)table % 16 || ldt % 16 || misaligned(scales, 4) : misaligned(table, size_of(table_type)))
         return api_fail(ARCHEAD_EINVAL, "table aligned to its element; 8-bit tables and their row strides to 16 bytes");
-    if (misaligned(out, out_type) || misaligned(tokens, ARCHEAD_F32))
+    if (misaligned(out, size_of(out_type)) || misaligned(tokens, 4))
         return api_fail(ARCHEAD_EINVAL, "buffers must be aligned to their element");
     if (overlap({matrix_span(out, n, d, ldo, size_of(out_type))},
                 {matrix_span(table, V, d, ldt, size_of(table_type)), vector_span(tokens, 4 * n),
@@ -813,7 +802,7 @@ extern "C" archead_status archead_embed_backward(int64_t n, int64_t V, int64_t d
         return api_fail(ARCHEAD_ESHAPE, "n ceil(d / 512) must be 2^26 - 4 at most, V below 2^26 - 2^24");
     if (!dtable || (n > 0 && (!dout || !tokens)))
         return api_fail(ARCHEAD_EINVAL, "dout, tokens and dtable are required");
-    if (misaligned(dout, dout_type) || misaligned(dtable, grad_type) || misaligned(tokens, ARCHEAD_F32))
+    if (misaligned(dout, size_of(dout_type)) || misaligned(dtable, size_of(grad_type)) || misaligned(tokens, 4))
         return api_fail(ARCHEAD_EINVAL, "buffers must be aligned to their element");
     if (!ws || (uintptr_t)ws % 16)
         return api_fail(ARCHEAD_EINVAL, "a 16-byte aligned workspace is required");

@@ -19,6 +19,7 @@
 #include "archead.h"
 #include "device.hpp"
 #include "e4m3.hpp"
+#include "entry.hpp"
 #include "lds_copy.hpp"
 
 namespace archead {
@@ -492,14 +493,6 @@ __global__ __launch_bounds__((BN * 2), (Tile<BM, BN>::wgs * BN / 128)) void prod
                 put4((O *)a.out + m * a.ldo + c, acc[t][n], a.N - c);
         }
     }
-}
-
-archead_status launched(const char *what)
-{
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess)
-        return api_fail(ARCHEAD_EHIP, std::string(what) + ": " + hipGetErrorString(e));
-    return ARCHEAD_OK;
 }
 
 bool bad_rows(const void *p, int64_t ld, int64_t cols) { return (uintptr_t)p % 16 || ld % 16 || ld < cols; }

@@ -32,6 +32,7 @@
 #include "api_internal.hpp"
 #include "archead.h"
 #include "device.hpp"
+#include "entry.hpp"
 
 namespace archead {
 namespace {
@@ -744,14 +745,6 @@ archead_status check_grad(int64_t V, const void *logits, int type, int64_t ld, c
         return api_fail(ARCHEAD_EINVAL, "dlogits must be aligned to its element");
     if (dlogits == logits && (grad_type != type || ldg != ld))
         return api_fail(ARCHEAD_EINVAL, "a gradient in place needs the logits' type and row stride");
-    return ARCHEAD_OK;
-}
-
-archead_status launched(const char *what)
-{
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess)
-        return api_fail(ARCHEAD_EHIP, std::string(what) + ": " + hipGetErrorString(e));
     return ARCHEAD_OK;
 }
 

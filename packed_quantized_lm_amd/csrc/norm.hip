@@ -24,6 +24,7 @@
 #include "archead.h"
 #include "e4m3.hpp"
 #include "elements.hpp"
+#include "entry.hpp"
 #include "overlap.hpp"
 
 namespace archead {
@@ -640,10 +641,6 @@ template <typename UT, typename HT> void run_back(const BackArgs &a, const BackP
                            a.d, dw);
 }
 
-bool bad_type(int t) { return t != ARCHEAD_F32 && t != ARCHEAD_BF16; }
-int64_t size_of(int t) { return t == ARCHEAD_F32 ? 4 : 2; }
-bool misaligned(const void *p, int t) { return (uintptr_t)p % (t == ARCHEAD_F32 ? 4 : 2) != 0; }
-
 archead_status check_sizes(int64_t M, int64_t d, float eps, float offset)
 {
     if (M < 0)
@@ -652,14 +649,6 @@ archead_status check_sizes(int64_t M, int64_t d, float eps, float offset)
         return api_fail(ARCHEAD_ESHAPE, "M < 2^22 and 1 <= d <= 2^20");
     if (!(eps >= 0.f) || !std::isfinite(eps) || !std::isfinite(offset))
         return api_fail(ARCHEAD_EINVAL, "eps must be finite and not negative, offset finite");
-    return ARCHEAD_OK;
-}
-
-archead_status launched(const char *what)
-{
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess)
-        return api_fail(ARCHEAD_EHIP, std::string(what) + ": " + hipGetErrorString(e));
     return ARCHEAD_OK;
 }
 
@@ -694,8 +683,8 @@ extern "C" archead_status archead_rms_norm(int64_t M, int64_t d, const void *x, 
         return ARCHEAD_OK;
     if (!x || !weight)
         return api_fail(ARCHEAD_EINVAL, "x and weight are required");
-    if (misaligned(x, x_type) || misaligned(weight, weight_type) || misaligned(y, y_type) ||
-        (residual && (misaligned(residual, res_type) || misaligned(h, res_type))) || misaligned(s, ARCHEAD_F32) ||
+    if (misaligned(x, size_of(x_type)) || misaligned(weight, size_of(weight_type)) || misaligned(y, size_of(y_type)) ||
+        (residual && (misaligned(residual, size_of(res_type)) || misaligned(h, size_of(res_type)))) || misaligned(s, 4) ||
         (uintptr_t)q % 16 || (q && ldq % 16))
         return api_fail(ARCHEAD_EINVAL, "buffers aligned to their element; q and its row stride to 16 bytes");
     if (residual && ((h == residual && ldh != ldr) || (h == x && (res_type != x_type || ldh != ldx))))
@@ -752,8 +741,8 @@ extern "C" archead_status archead_rms_norm_backward(int64_t M, int64_t d, const 
         return api_fail(ARCHEAD_EINVAL, "dh may be dres, not dy or h");
     if (dres && dres == dh && ldr != ldd)
         return api_fail(ARCHEAD_EINVAL, "in place of dres, dh needs its row stride");
-    if (misaligned(dy, dy_type) || misaligned(h, h_type) || misaligned(weight, weight_type) ||
-        misaligned(dres, h_type) || misaligned(dh, h_type) || misaligned(dweight, ARCHEAD_F32))
+    if (misaligned(dy, size_of(dy_type)) || misaligned(h, size_of(h_type)) || misaligned(weight, size_of(weight_type)) ||
+        misaligned(dres, size_of(h_type)) || misaligned(dh, size_of(h_type)) || misaligned(dweight, 4))
         return api_fail(ARCHEAD_EINVAL, "buffers must be aligned to their element");
     if (!ws || (uintptr_t)ws % 16)
         return api_fail(ARCHEAD_EINVAL, "a 16-byte aligned workspace is required");

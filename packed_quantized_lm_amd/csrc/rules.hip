@@ -29,6 +29,7 @@
 #include "api_internal.hpp"
 #include "archead.h"
 #include "elements.hpp"
+#include "entry.hpp"
 #include "kernels.hpp"
 #include "overlap.hpp"
 
@@ -695,8 +696,6 @@ void lay_out(RuleArgs &a, const RuleWs &w, void *ws)
     }
 }
 
-bool misaligned(const void *p, size_t to) { return (uintptr_t)p % to != 0; }
-
 archead_status check_rules(const RuleArgs &a, int64_t V, int64_t L, int64_t B, int type)
 {
     if (a.M < 0)
@@ -722,7 +721,7 @@ archead_status check_rules(const RuleArgs &a, int64_t V, int64_t L, int64_t B, i
         return api_fail(ARCHEAD_EINVAL, "without mask rows a mask has a row for each row of logits");
     if (a.M > 0 && !a.y)
         return api_fail(ARCHEAD_EINVAL, "logits are required");
-    if (misaligned(a.y, type == ARCHEAD_F32 ? 4 : 2))
+    if (misaligned(a.y, size_of(type)))
         return api_fail(ARCHEAD_EINVAL, "logits must be aligned to their element");
     for (const void *p : {(const void *)a.history, (const void *)a.lengths, (const void *)a.prompts,
                           (const void *)a.repetition, (const void *)a.frequency, (const void *)a.presence,
@@ -750,14 +749,6 @@ archead_status check_ws(const RuleWs &w, const void *ws, uint64_t bytes)
         return api_fail(ARCHEAD_EINVAL, "a 16-byte aligned workspace is required");
     if (bytes < w.total)
         return api_fail(ARCHEAD_EINVAL, "the workspace is smaller than archead_rules_workspace asks for");
-    return ARCHEAD_OK;
-}
-
-archead_status launched(const char *what)
-{
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess)
-        return api_fail(ARCHEAD_EHIP, std::string(what) + ": " + hipGetErrorString(e));
     return ARCHEAD_OK;
 }
 
@@ -814,13 +805,13 @@ extern "C" archead_status archead_adjust_logits(int64_t M, int64_t V, const void
         return api_fail(ARCHEAD_EINVAL, "out is required");
     if (out == logits && M > 0 && ldo != ld)
         return api_fail(ARCHEAD_EINVAL, "in place, out needs the logits' row stride");
-    if (misaligned(out, type == ARCHEAD_F32 ? 4 : 2))
+    if (misaligned(out, size_of(type)))
         return api_fail(ARCHEAD_EINVAL, "out must be aligned to its element");
     const RuleWs w = rule_ws(M, V, L, 0);
     s = check_ws(w, ws, ws_bytes);
     if (s != ARCHEAD_OK || M == 0)
         return s;
-    const int64_t element = type == ARCHEAD_F32 ? 4 : 2;
+    const int64_t element = size_of(type);
     const Span read = matrix_span(logits, M, V, ld, element), result = matrix_span(out, M, V, ldo, element),
                work = vector_span(w.total ? ws : nullptr, (int64_t)w.total);
     if (overlap_but_itself(result, read) || overlap(work, read) || overlap(result, work) || in_the_rules(a, {result, work}))
@@ -880,7 +871,7 @@ extern "C" archead_status archead_sample_logits(int64_t M, int64_t V, const void
         return s;
     const std::initializer_list<Span> results = {vector_span(values, 4 * M * K), vector_span(indices, 4 * M * K),
                                                  vector_span(samples, 4 * M), vector_span(ws, (int64_t)w.total)};
-    if (overlap(results, {matrix_span(logits, M, V, ld, type == ARCHEAD_F32 ? 4 : 2), vector_span(temperatures, 4 * M),
+    if (overlap(results, {matrix_span(logits, M, V, ld, size_of(type)), vector_span(temperatures, 4 * M),
                           vector_span(u, 4 * M)}) ||
         overlap(results) || in_the_rules(a, results))
         return api_fail(ARCHEAD_EINVAL, "a result or the workspace overlaps what is read, or another result");
