@@ -321,16 +321,6 @@ __device__ __forceinline__ void weights_of(const BackArgs &a, int q, float w[8])
     weights_of(n, q, 1.f, w);
 }
 
-// a vector's share of a row's sums of h^2 and g h
-__device__ __forceinline__ void add_sums(const float u[8], const float h[8], const float w[8], double &ss, double &c)
-{
-    for (int i = 0; i < 8; ++i) {
-        const double hd = h[i];
-        ss = __builtin_fma(hd, hd, ss);
-        c = __builtin_fma((double)(u[i] * w[i]), hd, c);
-    }
-}
-
 // Rows near the ends of fp32's range have an r, or an r^2 c beside it, that fp32 does not
 // hold.  Their u and h are multiplied by powers of two, us and hs, first, and
 //   dh = r / us (g us - (h hs) (r^2 c us / hs)),   dw's term = (u us) (h hs) (r / us / hs).
@@ -411,7 +401,7 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void norm_back_kernel(BackArgs a
         if (!kAhead)
             fetch(m);
         fetch_res(m);
-        float uv[H][8], hv[H][8];
+        float uv[H][8], hv[H][8], g[H][8];
         double ss = 0., c = 0.;
 #pragma unroll
         for (int j = 0; j < H; ++j) {
@@ -422,9 +412,13 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void norm_back_kernel(BackArgs a
             fetch(m + step); // the next row is on its way while this one is summed
 #pragma unroll
         for (int j = 0; j < H; ++j) {
-            float w[8];
-            weight(j, w);
-            add_sums(uv[j], hv[j], w, ss, c);
+            weight(j, g[j]);
+            for (int i = 0; i < 8; ++i) {
+                const double hd = hv[j][i];
+                g[j][i] *= uv[j][i];
+                ss = __builtin_fma(hd, hd, ss);
+                c = __builtin_fma((double)g[j][i], hd, c);
+            }
         }
         team_sums<T>(ss, c, red[turn]);
         const double root = inverse_root(__builtin_fma(ss, a.inv_d, (double)a.eps));
@@ -436,18 +430,18 @@ __global__ __launch_bounds__(T > 256 ? T : 256) void norm_back_kernel(BackArgs a
             for (int j = 0; j < H; ++j)
                 for (int i = 0; i < 8; ++i) {
                     uv[j][i] *= f.us;
+                    g[j][i] *= f.us;
                     hv[j][i] *= f.hs;
                 }
         }
 #pragma unroll
         for (int j = 0; j < H; ++j) {
             const int q = t + j * T;
-            float o[8] = {}, w[8];
-            weight(j, w);
+            float o[8] = {};
             if (a.dres)
                 vector_values(q, a.d, rr[j], o);
             for (int i = 0; i < 8; ++i) {
-                o[i] = __builtin_fmaf(r, __builtin_fmaf(-hv[j][i], k, uv[j][i] * w[i]), o[i]);
+                o[i] = __builtin_fmaf(r, __builtin_fmaf(-hv[j][i], k, g[j][i]), o[i]);
                 dw[j][i] = __builtin_fmaf(uv[j][i], hv[j][i] * rw, dw[j][i]);
             }
             if (q < nv)
